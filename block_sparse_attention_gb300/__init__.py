@@ -11,12 +11,24 @@ the calls raise.
     bsattn_mask_from_topk(scores, topk, use_dense_for_last_block, apply_tril)  -> mask
     bsattn_mask_from_threshold(scores, thr, use_dense_for_last_block, apply_tril) -> mask
     bsattn_num_splits_heuristic(...)                                     -> int
+
+Around them, for a paged serving loop:
+
+    bsattn_paged_plan(cached_lens, new_lens, free_pages, free_count, block_table, page_size, max_tokens)
+                                                  -> (slots, starts, seqlens, free_left)
+    bsattn_kv4_cache(num_pages, Hkv, page_size, d)                       -> Kv4Cache (4-bit pages)
+    bsattn_kv4_append(k, v, slots, cache)         bsattn_kv4_gather(slots, cache, dtype) -> (k, v)
+    bsattn_decode_paged_kv4(q, cache, cache_seqlens, block_table, block_indices=None, window=0) -> out
+    bsattn_prefill_window(q, k, v, window, sinks)                        -> out
+    bsattn_decode_window(q, k, v, cache_seqlens, window, sinks)          -> out
+    bsattn_decode_window_paged(q, k_pages, v_pages, cache_seqlens, block_table, window, sinks) -> out
 """
 from __future__ import annotations
 
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -31,6 +43,10 @@ __all__ = [
     "bsattn_set_wait_budget_ns", "bsattn_status_string", "bsattn_version", "workspace",
     "bsattn_decode_varlen_mask", "bsattn_decode_paged", "bsattn_mask_from_cumulative_threshold",
     "bsattn_decode_varlen_noalloc", "bsattn_decode_noalloc_status",
+    "BSATTN_ERR_NO_SPACE", "Kv4Cache", "bsattn_kv4_cache", "bsattn_kv4_append", "bsattn_kv4_gather",
+    "bsattn_decode_paged_kv4", "bsattn_decode_kv4_workspace_size", "bsattn_paged_plan",
+    "bsattn_prefill_window", "bsattn_decode_window", "bsattn_decode_window_paged",
+    "bsattn_decode_window_workspace_size", "call_workspace", "status_workspace",
 ]
 
 BSATTN_OK = 0
@@ -39,6 +55,7 @@ BSATTN_ERR_UNSUPPORTED = 2
 BSATTN_ERR_CUDA = 4
 BSATTN_ERR_TIMEOUT = 8
 BSATTN_ERR_BAD_INDEX = 16
+BSATTN_ERR_NO_SPACE = 32
 
 _F16, _BF16 = 0, 1
 _lock = threading.Lock()
@@ -67,6 +84,7 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
                 _build.build()
             lib = ctypes.CDLL(path)
             P, I, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+            L, F = ctypes.c_longlong, ctypes.c_float
             sig = {
                 "bsattn_status_string": ([I], ctypes.c_char_p),
                 "bsattn_version": ([], ctypes.c_char_p),
@@ -86,6 +104,16 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
                 "bsattn_set_wait_budget_ns": ([ctypes.c_ulonglong], None),
                 "bsattn_decode_varlen_noalloc": ([P, P, P, P, P, I, P, I, I, I, I, I, I, I, P], I),
                 "bsattn_decode_noalloc_status": ([P], I),
+                "bsattn_paged_plan": ([P] * 9 + [I] * 5 + [P, Z, P], I),
+                "bsattn_kv4_append": ([P, P, L, L, L, L, P, P, P, P, P, F, F, I, I, I, I, I, I, P, Z, P], I),
+                "bsattn_kv4_gather": ([P, P, P, P, P, F, F, P, P, I, I, I, I, I, I, P, Z, P], I),
+                "bsattn_decode_paged_kv4": ([P, P, P, P, P, F, F, P, P, P, I, I, P, I, I, I, I, I, I, I, I, I,
+                                             P, Z, P], I),
+                "bsattn_decode_kv4_workspace_size": ([I, I, I], Z),
+                "bsattn_prefill_window": ([P, P, P, I, I, P, I, I, I, I, I, I, P, I, P, Z, P], I),
+                "bsattn_decode_window": ([P, P, P, P, I, I, P, I, I, I, I, I, I, P, Z, P], I),
+                "bsattn_decode_window_paged": ([P, P, P, P, P, I, I, P, I, I, I, I, I, I, I, I, P, Z, P], I),
+                "bsattn_decode_window_workspace_size": ([I, I, I], Z),
             }
             for name, (args, res) in sig.items():
                 f = getattr(lib, name)
@@ -367,3 +395,326 @@ def bsattn_get_device_status(ws: torch.Tensor) -> int:
 
 def bsattn_set_wait_budget_ns(ns: int) -> None:
     load().bsattn_set_wait_budget_ns(int(ns))
+
+
+# ----------------------------------------------------------------- paged serving
+
+_STREAM_HEADER = 256 + 4 * 1024          # status word and tickets: all that has to start at zero
+
+
+def call_workspace(device, purpose: str, nbytes: int) -> torch.Tensor:
+    """A workspace for the stream decodes that no other call in flight uses: one per (stream, purpose),
+    and a new one for every call captured into a CUDA graph (graphs may be replayed side by side)."""
+    device = torch.device(device)
+    capturing = torch.cuda.is_current_stream_capturing()
+    key = (device.index, purpose, _stream(device))
+    buf = None if capturing else _ws_cache.get(key)
+    if buf is None or buf.numel() < nbytes:
+        buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        buf[:_STREAM_HEADER].zero_()
+        if not capturing:
+            _ws_cache[key] = buf
+    return buf
+
+
+_status_ws: dict = {}
+
+
+def status_workspace(device) -> torch.Tensor:
+    """The 256-byte workspace of the calls that keep only a status word in it.  They set bits of it and
+    read nothing, so all of a device's streams and graphs share it."""
+    device = torch.device(device)
+    buf = _status_ws.get(device.index)
+    if buf is None:
+        buf = torch.zeros(256, dtype=torch.uint8, device=device)
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(device).synchronize()
+            _status_ws[device.index] = buf
+    return buf
+
+
+def _same_device(**tensors):
+    dev = None
+    for name, t in tensors.items():
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if dev is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
+        dev = t.device
+    return dev
+
+
+def _contiguous(**tensors):
+    for name, t in tensors.items():
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _dtypes(dtype, **tensors):
+    for name, t in tensors.items():
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+
+
+def _shape(name, t, want):
+    if tuple(t.shape) != tuple(want):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(want)}")
+
+
+def _out(out, like):
+    if out is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    if out.device != like.device or out.dtype != like.dtype:
+        raise ValueError("out must have the queries' device and dtype")
+    _shape("out", out, like.shape)
+    return out
+
+
+def bsattn_paged_plan(cached_lens, new_lens, free_pages, free_count, block_table, page_size: int,
+                      max_tokens: int, ws=None):
+    """Block-table rows and slot map for `new_lens` tokens on top of `cached_lens`, both int32 [B].
+    free_pages int32 [n] is the free list, free_count int32 [1] how many of it are free (taken from the
+    end); block_table int32 [B, max_pages] gets the new pages.  Returns (slots int64 [max_tokens], -1
+    where there is no token; starts int32 [B + 1]; seqlens int32 [B]; free_left int32 [1])."""
+    lib = load()
+    dev = _same_device(cached_lens=cached_lens, new_lens=new_lens, free_pages=free_pages,
+                       free_count=free_count, block_table=block_table)
+    _contiguous(cached_lens=cached_lens, new_lens=new_lens, free_pages=free_pages, free_count=free_count,
+                block_table=block_table)
+    _dtypes(torch.int32, cached_lens=cached_lens, new_lens=new_lens, free_pages=free_pages,
+            free_count=free_count, block_table=block_table)
+    B = cached_lens.numel()
+    _shape("new_lens", new_lens, cached_lens.shape)
+    if cached_lens.dim() != 1 or block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("cached_lens must be [B] and block_table [B, max_pages]")
+    if free_count.numel() != 1:
+        raise ValueError("free_count must have one element")
+    with torch.cuda.device(dev):
+        slots = torch.empty(int(max_tokens), dtype=torch.int64, device=dev)
+        ints = torch.empty(2 * B + 2, dtype=torch.int32, device=dev)
+        starts, seqlens, left = ints[:B + 1], ints[B + 1:2 * B + 1], ints[2 * B + 1:]
+        if ws is None:
+            ws = status_workspace(dev)
+        rc = lib.bsattn_paged_plan(cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
+                                   free_count.data_ptr(), block_table.data_ptr(), slots.data_ptr(),
+                                   starts.data_ptr(), seqlens.data_ptr(), left.data_ptr(), B,
+                                   int(page_size), block_table.shape[1], free_pages.numel(),
+                                   int(max_tokens), ws.data_ptr(), ws.numel(), _stream(dev))
+    _check("bsattn_paged_plan", rc)
+    return slots, starts, seqlens, left
+
+
+class Kv4Cache(NamedTuple):
+    """A paged 4-bit cache: e2m1 codes [pages, Hkv, page_size, d/2] and e4m3 scales
+    [pages, Hkv, page_size, d/16] of keys and values, all uint8."""
+    k_codes: torch.Tensor
+    k_scales: torch.Tensor
+    v_codes: torch.Tensor
+    v_scales: torch.Tensor
+
+
+def bsattn_kv4_cache(num_pages: int, Hkv: int, page_size: int, d: int, device="cuda") -> Kv4Cache:
+    """A zeroed paged 4-bit cache."""
+    def make(n):
+        return torch.zeros(num_pages, Hkv, page_size, n, dtype=torch.uint8, device=device)
+    return Kv4Cache(make(d // 2), make(d // 16), make(d // 2), make(d // 16))
+
+
+def _kv4(cache):
+    c = Kv4Cache(*cache)
+    _contiguous(**c._asdict())
+    _dtypes(torch.uint8, **c._asdict())
+    if c.k_codes.dim() != 4:
+        raise ValueError("a 4-bit cache's tensors are [pages, Hkv, page_size, ...]")
+    pages, hkv, page, half = c.k_codes.shape
+    _shape("v_codes", c.v_codes, c.k_codes.shape)
+    for name in ("k_scales", "v_scales"):
+        _shape(name, getattr(c, name), (pages, hkv, page, half // 8))
+    return c, pages, hkv, page, 2 * half
+
+
+def bsattn_kv4_append(k, v, slots, cache, k_scale: float = 1.0, v_scale: float = 1.0, ws=None) -> None:
+    """Rounds k and v [T, Hkv, d] fp16|bf16 (channels contiguous, any 16-byte aligned token and head
+    strides) into the rows that slots int64 [T] names (negative: skipped; all others distinct)."""
+    lib = load()
+    c, pages, hkv, page, d = _kv4(cache)
+    dev = _same_device(k=k, v=v, slots=slots, **c._asdict())
+    _dtypes(torch.int64, slots=slots)
+    _contiguous(slots=slots)
+    if k.dim() != 3 or v.dtype != k.dtype:
+        raise ValueError("k and v must be [T, Hkv, d] of one dtype")
+    T = k.shape[0]
+    _shape("k", k, (T, hkv, d))
+    _shape("v", v, (T, hkv, d))
+    _shape("slots", slots, (T,))
+    for name, t in (("k", k), ("v", v)):
+        if T and t.stride(2) != 1:
+            raise ValueError(f"{name}'s channels must be contiguous")
+    # the stride of a dimension of one entry is never used
+    st = [t.stride(i) if t.shape[i] > 1 else 0 for t in (k, v) for i in (0, 1)]
+    with torch.cuda.device(dev):
+        if ws is None:
+            ws = status_workspace(dev)
+        rc = lib.bsattn_kv4_append(k.data_ptr(), v.data_ptr(), *st, slots.data_ptr(), *(t.data_ptr() for t in c),
+                                   float(k_scale), float(v_scale), T, hkv, pages, page, d, _dtype_code(k),
+                                   ws.data_ptr(), ws.numel(), _stream(dev))
+    _check("bsattn_kv4_append", rc)
+
+
+def bsattn_kv4_gather(slots, cache, dtype, k_scale: float = 1.0, v_scale: float = 1.0, ws=None):
+    """The rows that slots int64 [T] names, as (k, v) [T, Hkv, d] of `dtype` (negative slots: zeros)."""
+    lib = load()
+    c, pages, hkv, page, d = _kv4(cache)
+    dev = _same_device(slots=slots, **c._asdict())
+    _dtypes(torch.int64, slots=slots)
+    _contiguous(slots=slots)
+    if slots.dim() != 1:
+        raise ValueError("slots must be [T]")
+    with torch.cuda.device(dev):
+        k = torch.empty(slots.numel(), hkv, d, dtype=dtype, device=dev)
+        v = torch.empty_like(k)
+        if ws is None:
+            ws = status_workspace(dev)
+        rc = lib.bsattn_kv4_gather(slots.data_ptr(), *(t.data_ptr() for t in c), float(k_scale), float(v_scale),
+                                   k.data_ptr(), v.data_ptr(), slots.numel(), hkv, pages, page, d,
+                                   _dtype_code(k), ws.data_ptr(), ws.numel(), _stream(dev))
+    _check("bsattn_kv4_gather", rc)
+    return k, v
+
+
+def bsattn_decode_window_workspace_size(Hq: int, Hkv: int, d: int) -> int:
+    return int(load().bsattn_decode_window_workspace_size(Hq, Hkv, d))
+
+
+def bsattn_decode_kv4_workspace_size(Hq: int, Hkv: int, d: int) -> int:
+    return int(load().bsattn_decode_kv4_workspace_size(Hq, Hkv, d))
+
+
+def _decode_args(q, cache_seqlens, block_table, hkv, d):
+    if q.dim() != 3 or q.shape[2] != d:
+        raise ValueError(f"q must be [B, Hq, {d}]")
+    _contiguous(q=q, cache_seqlens=cache_seqlens)
+    _dtypes(torch.int32, cache_seqlens=cache_seqlens)
+    _shape("cache_seqlens", cache_seqlens, (q.shape[0],))
+    if block_table is not None:
+        _contiguous(block_table=block_table)
+        _dtypes(torch.int32, block_table=block_table)
+        if block_table.dim() != 2 or block_table.shape[0] != q.shape[0]:
+            raise ValueError("block_table must be [B, max_pages]")
+
+
+def bsattn_decode_paged_kv4(q, cache, cache_seqlens, block_table, block_indices=None, window: int = 0,
+                            sinks: int = 0, k_scale: float = 1.0, v_scale: float = 1.0, out=None, ws=None):
+    """One query token per sequence over a paged 4-bit cache.  q [B,Hq,d] fp16|bf16; cache_seqlens int32
+    [B]; block_table int32 [B,max_pages]; block_indices int32 [B,Hkv,max_sel] (-1 = empty) limits each kv
+    head to chosen 64-token blocks, window > 0 to the last `window` tokens and the first `sinks`."""
+    lib = load()
+    c, pages, hkv, page, d = _kv4(cache)
+    dev = _same_device(q=q, cache_seqlens=cache_seqlens, block_table=block_table, **c._asdict())
+    _decode_args(q, cache_seqlens, block_table, hkv, d)
+    B, Hq, _ = q.shape
+    max_sel, chosen = 0, None
+    if block_indices is not None:
+        _same_device(q=q, block_indices=block_indices)
+        _contiguous(block_indices=block_indices)
+        _dtypes(torch.int32, block_indices=block_indices)
+        if block_indices.dim() != 3 or tuple(block_indices.shape[:2]) != (B, hkv):
+            raise ValueError("block_indices must be [B, Hkv, max_sel]")
+        max_sel, chosen = block_indices.shape[2], block_indices.data_ptr()
+        if max_sel == 0:
+            raise ValueError("block_indices has no slots")
+    with torch.cuda.device(dev):
+        out = _out(out, q)
+        _contiguous(out=out)
+        if ws is None:
+            ws = call_workspace(dev, "decode_kv4", bsattn_decode_kv4_workspace_size(Hq, hkv, d))
+        rc = lib.bsattn_decode_paged_kv4(q.data_ptr(), *(t.data_ptr() for t in c), float(k_scale), float(v_scale),
+                                         cache_seqlens.data_ptr(), chosen, block_table.data_ptr(), int(window),
+                                         int(sinks), out.data_ptr(), B, Hq, hkv, pages, page,
+                                         block_table.shape[1], d, max_sel, _dtype_code(q), ws.data_ptr(),
+                                         ws.numel(), _stream(dev))
+    _check("bsattn_decode_paged_kv4", rc)
+    return out
+
+
+def bsattn_decode_window(q, k, v, cache_seqlens, window: int, sinks: int = 0, out=None, ws=None):
+    """One query token per sequence over the last `window` tokens and the first `sinks` of a contiguous
+    cache.  q [B,Hq,d]; k/v [B,Smax,Hkv,d] fp16|bf16 CUDA; cache_seqlens int32 [B]."""
+    lib = load()
+    dev = _same_device(q=q, k=k, v=v, cache_seqlens=cache_seqlens)
+    _contiguous(k=k, v=v)
+    if k.dim() != 4 or k.shape[0] != q.shape[0] or k.shape != v.shape:
+        raise ValueError("k and v must be [B, Smax, Hkv, d]")
+    if not (q.dtype == k.dtype == v.dtype):
+        raise TypeError("q, k, v must share a dtype")
+    _, Smax, hkv, d = k.shape
+    _decode_args(q, cache_seqlens, None, hkv, d)
+    B, Hq, _ = q.shape
+    with torch.cuda.device(dev):
+        out = _out(out, q)
+        _contiguous(out=out)
+        if ws is None:
+            ws = call_workspace(dev, "decode_window", bsattn_decode_window_workspace_size(Hq, hkv, d))
+        rc = lib.bsattn_decode_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), cache_seqlens.data_ptr(),
+                                      int(window), int(sinks), out.data_ptr(), B, Hq, hkv, Smax, d,
+                                      _dtype_code(q), ws.data_ptr(), ws.numel(), _stream(dev))
+    _check("bsattn_decode_window", rc)
+    return out
+
+
+def bsattn_decode_window_paged(q, k_pages, v_pages, cache_seqlens, block_table, window: int, sinks: int = 0,
+                               out=None, ws=None):
+    """bsattn_decode_window over a paged cache: k_pages/v_pages [num_pages,page_size,Hkv,d]; block_table
+    int32 [B,max_pages]."""
+    lib = load()
+    dev = _same_device(q=q, k_pages=k_pages, v_pages=v_pages, cache_seqlens=cache_seqlens,
+                       block_table=block_table)
+    _contiguous(k_pages=k_pages, v_pages=v_pages)
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape:
+        raise ValueError("k_pages and v_pages must be [num_pages, page_size, Hkv, d]")
+    if not (q.dtype == k_pages.dtype == v_pages.dtype):
+        raise TypeError("q, k_pages, v_pages must share a dtype")
+    pages, page, hkv, d = k_pages.shape
+    _decode_args(q, cache_seqlens, block_table, hkv, d)
+    B, Hq, _ = q.shape
+    with torch.cuda.device(dev):
+        out = _out(out, q)
+        _contiguous(out=out)
+        if ws is None:
+            ws = call_workspace(dev, "decode_window", bsattn_decode_window_workspace_size(Hq, hkv, d))
+        rc = lib.bsattn_decode_window_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                                            cache_seqlens.data_ptr(), block_table.data_ptr(), int(window),
+                                            int(sinks), out.data_ptr(), B, Hq, hkv, pages, page,
+                                            block_table.shape[1], d, _dtype_code(q), ws.data_ptr(), ws.numel(),
+                                            _stream(dev))
+    _check("bsattn_decode_window_paged", rc)
+    return out
+
+
+def bsattn_prefill_window(q, k, v, window: int, sinks: int = 0, out=None, ws=None):
+    """Causal attention with a sliding window and sinks: query row i (position p = i + Sk - Sq) sees key j
+    iff j <= p and (j < sinks or j > p - window).  q [B,Hq,Sq,d], k/v [B,Hkv,Sk,d] fp16|bf16 CUDA views
+    with contiguous channels and 16-byte aligned strides; out: as q laid out, unless given."""
+    lib = load()
+    dev = _same_device(q=q, k=k, v=v)
+    if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape or q.shape[0] != k.shape[0] or q.shape[3] != k.shape[3]:
+        raise ValueError("q must be [B, Hq, Sq, d], k and v [B, Hkv, Sk, d]")
+    if not (q.dtype == k.dtype == v.dtype):
+        raise TypeError("q, k, v must share a dtype")
+    B, Hq, Sq, d = q.shape
+    hkv, Sk = k.shape[1], k.shape[2]
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty_like(q)
+        out = _out(out, q)
+        for name, t in (("q", q), ("k", k), ("v", v), ("out", out)):
+            if t.numel() and t.stride(3) != 1:
+                raise ValueError(f"{name}'s channels must be contiguous")
+        strides = (ctypes.c_int64 * 12)(*(s for t in (q, k, v, out) for s in t.stride()[:3]))
+        if ws is None:
+            ws = status_workspace(dev)
+        rc = lib.bsattn_prefill_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), int(window), int(sinks),
+                                       out.data_ptr(), B, Hq, hkv, Sq, Sk, d, strides, _dtype_code(q),
+                                       ws.data_ptr(), ws.numel(), _stream(dev))
+    _check("bsattn_prefill_window", rc)
+    return out

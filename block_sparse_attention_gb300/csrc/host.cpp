@@ -39,6 +39,7 @@ const char* bsattn_status_string(int status) {
         {BSATTN_ERR_CUDA, "BSATTN_ERR_CUDA"},
         {BSATTN_ERR_TIMEOUT, "BSATTN_ERR_TIMEOUT"},
         {BSATTN_ERR_BAD_INDEX, "BSATTN_ERR_BAD_INDEX"},
+        {BSATTN_ERR_NO_SPACE, "BSATTN_ERR_NO_SPACE"},
     };
     int rest = status;
     for (const auto& n : names) {
@@ -225,6 +226,21 @@ int encode_3d(CUtensorMap* map, const void* base, int elem_bytes_is_2_dtype_bf16
                     CU_TENSOR_MAP_INTERLEAVE_NONE,
                     swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? BSATTN_OK : BSATTN_ERR_INVALID_ARG;
+}
+
+int encode_4d(CUtensorMap* map, const void* base, int bf16, const uint64_t (&dims)[4],
+              const uint64_t (&stride_bytes)[3], const uint32_t (&box)[4]) {
+    auto fn = encode_fn();
+    if (!fn) return BSATTN_ERR_CUDA;
+    cuuint64_t n[4] = {dims[0], dims[1], dims[2], dims[3]};
+    cuuint64_t strides[3] = {stride_bytes[0], stride_bytes[1], stride_bytes[2]};
+    cuuint32_t bx[4] = {box[0], box[1], box[2], box[3]};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                    const_cast<void*>(base), n, strides, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? BSATTN_OK : BSATTN_ERR_INVALID_ARG;
 }
 

@@ -17,6 +17,10 @@ int encode_3d(CUtensorMap* map, const void* base, int bf16, uint64_t dim0, uint6
               uint64_t dim2, uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box0,
               uint32_t box1, uint32_t box2, bool swizzle128);
 
+// The same with four dimensions, byte strides of dims 1-3, and the 128-byte swizzle.
+int encode_4d(CUtensorMap* map, const void* base, int bf16, const uint64_t (&dims)[4],
+              const uint64_t (&stride_bytes)[3], const uint32_t (&box)[4]);
+
 // SM count of the current device (0 if it cannot be queried).
 int num_sms_of_current_device();
 

@@ -1,0 +1,260 @@
+// paged_plan.cu -- block tables and slot maps for a paged cache, built on the GPU from request
+// lengths, sm_103a.
+//
+// Per call every sequence b brings new_lens[b] tokens to the cached_lens[b] it holds.  With
+//     end_b  = new_0 + ... + new_b                        (place of its tokens in the packed batch)
+//     held_b = ceil(cached_b / page), need_b = ceil((cached_b + new_b) / page)
+//     a_b    = need_b - held_b, A_b = a_0 + ... + a_b     (0 for a sequence that cannot fit)
+// sequence b takes the pages free[count - 1 - (A_b - a_b) - k], k < a_b, off the top of the free
+// list, and token t of it goes to slot table[pos / page] * page + pos % page, pos = cached_b + i.
+//
+// The work is a few bytes a sequence and 8 bytes a token, so a small call is bound by its launch
+// and by the two dependent prefix sums.  Every CTA therefore scans all sequences itself (they are
+// L2-resident and few) and keeps the results in shared memory: one launch, no workspace that two
+// calls could disturb, no CTA that waits on another.  Tokens are dealt out over the CTAs and find
+// their sequence by bisection in shared memory; a new page's number is read from the free list,
+// not from the table, so that nothing is read that another CTA writes.
+#include <climits>
+
+#include "host_internal.h"
+#include "ptx.cuh"
+
+namespace bsattn {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kPerThread = 16;
+constexpr int kMaxSeqs = kThreads * kPerThread;
+constexpr int kTokensPerCta = 4 * kThreads;     // slots a CTA writes before the grid grows
+
+struct PlanParams {
+    const int32_t* cached;
+    const int32_t* fresh;
+    const int32_t* free_pages;
+    const int32_t* free_count;
+    int32_t* table;
+    int64_t* slots;
+    int32_t* starts;
+    int32_t* lens;
+    int32_t* free_left;
+    int* status;
+    int B, page, max_pages, free_cap, max_tokens;
+};
+
+// Sums above INT_MAX stay there: the operands are not negative, so the sum is still associative.
+__device__ __forceinline__ int sat_add(int a, int b) {
+    const unsigned s = static_cast<unsigned>(a) + static_cast<unsigned>(b);
+    return s > 0x7fffffffu ? 0x7fffffff : static_cast<int>(s);
+}
+
+// Inclusive prefix sum over the CTA's threads.
+__device__ __forceinline__ int block_scan(int v, int* warp_sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v = sat_add(v, u);
+    }
+    if (lane == 31) warp_sums[warp] = v;
+    __syncthreads();
+    int before = 0;
+    if (warp > 0) {
+        int s = lane < warp ? warp_sums[lane] : 0;      // at most 16 warps
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s = sat_add(s, __shfl_xor_sync(0xffffffffu, s, o));
+        before = s;
+    }
+    __syncthreads();
+    return sat_add(before, v);
+}
+
+__global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
+    extern __shared__ int sm[];
+    __shared__ int warp_sums[kThreads / 32];
+    __shared__ int used_max;
+    int* end_of = sm;                    // [B] end of the sequence's tokens in the packed batch
+    int* first_of = sm + p.B;            // [B] its first place in the free list's order, -1 = not served
+    const int tid = threadIdx.x;
+    const int per = (p.B + kThreads - 1) / kThreads;      // <= kPerThread
+    const int b0 = tid * per;
+    int room = *p.free_count;
+    int flags = 0;
+    if (room < 0 || room > p.free_cap) {
+        flags |= BSATTN_ERR_BAD_INDEX;
+        room = room < 0 ? 0 : p.free_cap;
+    }
+    if (tid == 0) used_max = 0;
+
+    int have[kPerThread], more[kPerThread];
+    int sum = 0;
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+        const int b = b0 + k;
+        have[k] = more[k] = 0;
+        if (k < per && b < p.B) {
+            have[k] = p.cached[b];
+            more[k] = p.fresh[b];
+            sum = sat_add(sum, max(more[k], 0));
+        }
+    }
+    int end = block_scan(sum, warp_sums);
+    if (blockIdx.x == 0 && tid == kThreads - 1) {
+        p.starts[0] = 0;
+    }
+    // tokens: walk the thread's sequences forward from the tokens before them
+    int before = 0;
+    {
+        __shared__ int excl[kThreads];
+        excl[tid] = end;
+        __syncthreads();
+        before = tid > 0 ? excl[tid - 1] : 0;
+        __syncthreads();
+    }
+    int asked[kPerThread];
+    int pages = 0, at = before;
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+        const int b = b0 + k;
+        asked[k] = -1;                                    // -1: cannot be served
+        if (k < per && b < p.B) {
+            const bool sane = have[k] >= 0 && more[k] >= 0;
+            at = sat_add(at, max(more[k], 0));
+            end_of[b] = at;
+            if (!sane) {
+                flags |= BSATTN_ERR_BAD_INDEX;
+            } else {
+                const long long total = static_cast<long long>(have[k]) + more[k];
+                const long long need = (total + p.page - 1) / p.page;
+                const int held = have[k] / p.page + (have[k] % p.page != 0);
+                if (need <= p.max_pages && at <= p.max_tokens && at < INT_MAX && total <= INT_MAX) {
+                    asked[k] = static_cast<int>(need) - held;
+                    pages = sat_add(pages, asked[k]);
+                } else {
+                    flags |= BSATTN_ERR_NO_SPACE;
+                }
+            }
+        }
+    }
+    const int upto = block_scan(pages, warp_sums);
+    int first = 0;
+    {
+        __shared__ int excl[kThreads];
+        excl[tid] = upto;
+        __syncthreads();
+        first = tid > 0 ? excl[tid - 1] : 0;
+    }
+    int used = 0;
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+        const int b = b0 + k;
+        if (k < per && b < p.B) {
+            const int a = asked[k];
+            const int last = sat_add(first, max(a, 0));
+            const bool served = a >= 0 && (a == 0 || last <= room);
+            if (a >= 0 && !served) flags |= BSATTN_ERR_NO_SPACE;
+            first_of[b] = served ? first : -1;
+            if (served && a > 0) used = last;
+            first = last;
+            if (blockIdx.x == 0) {
+                p.starts[b + 1] = end_of[b];
+                p.lens[b] = served ? have[k] + more[k] : have[k];
+            }
+        }
+    }
+    if (blockIdx.x == 0) {
+        if (flags) atomicOr(p.status, flags);
+        if (used) atomicMax(&used_max, used);
+    }
+    __syncthreads();
+    if (blockIdx.x == 0 && tid == 0) *p.free_left = room - used_max;
+
+    // new table entries: a warp a sequence, the sequences dealt out over the grid
+    const int lane = tid & 31;
+    for (int b = blockIdx.x * (kThreads / 32) + (tid >> 5); b < p.B; b += gridDim.x * (kThreads / 32)) {
+        const int f = first_of[b];
+        if (f < 0) continue;
+        const int have_b = p.cached[b], more_b = p.fresh[b];
+        const int held = have_b / p.page + (have_b % p.page != 0);
+        const int need = static_cast<int>((static_cast<long long>(have_b) + more_b + p.page - 1) / p.page);
+        int32_t* row = p.table + static_cast<size_t>(b) * p.max_pages;
+        for (int c = held + lane; c < need; c += 32) row[c] = p.free_pages[room - 1 - (f + c - held)];
+    }
+
+    // slots: thread t of the grid takes tokens t, t + threads, ...
+    bool unmapped = false;
+    for (int t = blockIdx.x * kThreads + tid; t < p.max_tokens; t += gridDim.x * kThreads) {
+        int lo = 0, hi = p.B;                     // first sequence that ends after t
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (end_of[mid] > t) hi = mid;
+            else lo = mid + 1;
+        }
+        int64_t slot = -1;
+        if (lo < p.B && first_of[lo] >= 0) {
+            const int have_b = p.cached[lo];
+            const int pos = have_b + t - (lo > 0 ? end_of[lo - 1] : 0);
+            const int held = have_b / p.page + (have_b % p.page != 0);
+            const int c = pos / p.page;
+            const int page = c < held ? p.table[static_cast<size_t>(lo) * p.max_pages + c]
+                                      : p.free_pages[room - 1 - (first_of[lo] + c - held)];
+            if (page >= 0) slot = static_cast<int64_t>(page) * p.page + (pos - c * p.page);
+            else unmapped = true;
+        }
+        p.slots[t] = slot;
+        if (t > 0x7fffffff - static_cast<int>(gridDim.x) * kThreads) break;
+    }
+    if (unmapped) atomicOr(p.status, BSATTN_ERR_BAD_INDEX);
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
+}  // namespace
+}  // namespace bsattn
+
+extern "C" int bsattn_paged_plan(const int32_t* cached_lens, const int32_t* new_lens,
+                                 const int32_t* free_pages, const int32_t* free_count,
+                                 int32_t* block_table, int64_t* slots, int32_t* starts,
+                                 int32_t* seqlens, int32_t* free_left, int B, int page_size,
+                                 int max_pages_per_seq, int free_capacity, int max_tokens,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+    using namespace bsattn;
+    if (B < 0 || page_size <= 0 || max_pages_per_seq <= 0 || free_capacity < 0 || max_tokens < 0)
+        return BSATTN_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < 256 || !starts || !free_left || !free_count)
+        return BSATTN_ERR_INVALID_ARG;
+    if ((B > 0 && (!cached_lens || !new_lens || !block_table || !seqlens)) ||
+        (max_tokens > 0 && !slots) || (free_capacity > 0 && !free_pages))
+        return BSATTN_ERR_INVALID_ARG;
+    if (B > kMaxSeqs) return BSATTN_ERR_UNSUPPORTED;
+    // every CTA reads the inputs while CTA 0 writes the new lengths: no output may be an input
+    const size_t nb = sizeof(int32_t) * static_cast<size_t>(B);
+    const void* in[4] = {cached_lens, new_lens, free_pages, free_count};
+    const size_t in_bytes[4] = {nb, nb, sizeof(int32_t) * static_cast<size_t>(free_capacity), sizeof(int32_t)};
+    const void* out[5] = {block_table, slots, starts, seqlens, free_left};
+    const size_t out_bytes[5] = {nb * max_pages_per_seq, sizeof(int64_t) * static_cast<size_t>(max_tokens),
+                                 nb + sizeof(int32_t), nb, sizeof(int32_t)};
+    for (int i = 0; i < 5; ++i) {
+        for (int j = 0; j < 4; ++j)
+            if (out_bytes[i] && in_bytes[j] && overlap(out[i], out_bytes[i], in[j], in_bytes[j]))
+                return BSATTN_ERR_INVALID_ARG;
+        for (int j = i + 1; j < 5; ++j)
+            if (out_bytes[i] && out_bytes[j] && overlap(out[i], out_bytes[i], out[j], out_bytes[j]))
+                return BSATTN_ERR_INVALID_ARG;
+    }
+    PlanParams p{cached_lens, new_lens, free_pages, free_count, block_table, slots, starts, seqlens,
+                 free_left, static_cast<int*>(workspace), B, page_size, max_pages_per_seq, free_capacity,
+                 max_tokens};
+    int sms = num_sms_of_current_device();
+    if (sms <= 0) sms = 148;
+    long long grid = (static_cast<long long>(max_tokens) + kTokensPerCta - 1) / kTokensPerCta;
+    grid = grid < 1 ? 1 : (grid > sms ? sms : grid);
+    const size_t smem = 2 * nb;
+    if (smem > 32 * 1024 &&
+        cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024) != cudaSuccess)
+        return BSATTN_ERR_CUDA;
+    plan_kernel<<<static_cast<unsigned>(grid), kThreads, smem, static_cast<cudaStream_t>(stream)>>>(p);
+    return cudaGetLastError() == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
+}

@@ -1,0 +1,674 @@
+// prefill_window.cu -- causal attention with a sliding window and a few first tokens that stay
+// visible (sinks), forward, sm_103a.
+//
+// Query row i stands at position p = i + (Sk - Sq) and sees key j iff j <= p and (j < sinks or
+// j > p - window); out_i = softmax_j(q_i . k_j / sqrt(d)) v_j over those keys, 0 where there is none.
+//
+// Both products are tensor-core work: 4 d operations a visible pair, against which the reads are
+// small as long as a K/V tile serves many rows.  One CTA per SM therefore takes two 128-row query
+// tiles that see (nearly) the same keys, two query heads of a kv head at the same rows or, where
+// heads do not pair up, two neighbouring row blocks of a head, and runs them against one stream of
+// 128-key K/V tiles: half the L2 traffic of one tile a CTA, and while the softmax of one query tile
+// works the tensor core has the other's products.
+//     S_x = Q_x K^T    tcgen05.mma M=128 N=128 K=d, fp32 in TMEM (N = 128: both operands' shared
+//                      memory reads then take no longer than the products themselves)
+//     P_x              exp2 online softmax, one thread a row, written over S_x as the 16-bit type
+//     O_x += P_x V     tcgen05.mma M=128 N=d K=128, A = P_x from TMEM
+// The row maximum used is raised, and O_x rescaled, only when it grows by more than 2^8: weights stay
+// below 2^8 and the sum and O share the reference, so nothing is lost.  P is rounded to the input
+// type (the products of kind::f16 take one type); statistics, sums and O are 32-bit.
+//
+// 352 threads:
+//   warps 0-3 / 4-7   softmax and epilogue of query tile 0 / 1 (TMEM lane = row)
+//   warps 8 / 9       issue the products of query tile 0 / 1: S(0), then P V(j) and S(j + 1) in turn.
+//                     One issuer's MMAs run in order, so S(j + 1) may overwrite P(j) without a wait
+//   warp 10           TMA: Q tiles, then K and V tiles through one ring of stages
+// TMEM: S_0 0-127, S_1 128-255, O_0 256.., O_1 256 + d...  Items are dealt out round-robin, last
+// rows first (they see the most keys), so CTAs at work at one time share K/V in L2.  Every wait is
+// bounded: on expiry the CTA records BSATTN_ERR_TIMEOUT, drains what is in flight and leaves.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cmath>
+#include <type_traits>
+
+#include "host_internal.h"
+#include "ptx.cuh"
+
+namespace bsattn {
+namespace {
+
+constexpr int kThreads = 352;
+constexpr int kMmaWarp = 8;              // and 9
+constexpr int kLoadWarp = 10;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kOCol = 256;
+constexpr float kRescaleLog2 = 8.0f;
+
+template <int D>
+struct Cfg {
+    static constexpr int kStages = D == 64 ? 10 : 5;             // one 128-row tile of K or V each
+    static constexpr uint32_t kTile = 128 * D * 2;
+    static constexpr uint32_t kQ = 0;                            // two query tiles
+    static constexpr uint32_t kKV = 2 * kTile;
+    static constexpr uint32_t kBars = kKV + kStages * kTile;
+    // q_full[2] q_free[2] full[stages] empty[stages] s_full[2] p_full[2] pv_done[2] o_free[2] fin[2]
+    static constexpr uint32_t kNumBars = 4 + 2 * kStages + 10;
+    static constexpr uint32_t kMisc = kBars + 8 * kNumBars;      // tmem base, abort flag
+    static constexpr uint32_t kBytes = 1024 + kMisc + 16;
+    static_assert(kBytes <= 227 * 1024, "shared memory");
+};
+
+struct WindowParams {
+    void* out;
+    int* status;
+    long long out_b, out_h, out_s;       // element strides of out
+    int B, Hq, Hkv, Sq, Sk;
+    int window, sinks;
+    int nq;                              // 128-row query blocks
+    int by_heads;                        // 1: a pair is two heads, 0: two row blocks
+    int pairs;                           // items per (batch, pair row): head pairs, or heads
+    int rows;                            // item rows: row blocks, or pairs of them
+    int total_items;
+    float scale_log2;
+    unsigned long long budget_ns;
+};
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
+                                            int c2, int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+__device__ __forceinline__ float max3f(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+__device__ __forceinline__ float2 fma2f(float2 a, float2 b, float2 c) {
+    unsigned long long ra, rb, rc, rd;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(ra) : "f"(a.x), "f"(a.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(rb) : "f"(b.x), "f"(b.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(rc) : "f"(c.x), "f"(c.y));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(rd) : "l"(ra), "l"(rb), "l"(rc));
+    float2 d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(rd));
+    return d;
+}
+
+__device__ __forceinline__ float2 add2f(float2 a, float2 b) {
+    unsigned long long ra, rb, rd;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(ra) : "f"(a.x), "f"(a.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(rb) : "f"(b.x), "f"(b.y));
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(rd) : "l"(ra), "l"(rb));
+    float2 d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(rd));
+    return d;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    if constexpr (BF16) {
+        __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<uint32_t*>(&v);
+    } else {
+        __half2 v = __floats2half2_rn(a, b);
+        return *reinterpret_cast<uint32_t*>(&v);
+    }
+}
+
+// 32 TMEM lanes x 32 columns, one accumulator row a thread.
+__device__ __forceinline__ void tmem_ld_row32(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st_row32(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+        ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_row16(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+        "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15])
+        : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], kind::f16, by one lane of a converged warp under a guard predicate.
+__device__ __forceinline__ void mma_f16_ts_if(bool lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead ? 1u : 0u)
+        : "memory");
+}
+
+// The 128-key tiles one query tile visits: [0, sink) and [lo, hi); hi = 0: none.
+struct Tiles {
+    int head, qb;          // query head, row block (past the last one: no rows)
+    int lo, hi, sink;
+    __device__ __forceinline__ bool has(int t) const { return t < hi && (t < sink || t >= lo); }
+    __device__ __forceinline__ int count() const { return hi > 0 ? sink + hi - lo : 0; }
+};
+
+// One item: the two query tiles and the tiles their union visits.
+struct Item {
+    int b, kvh;
+    Tiles x[2];
+    int lo, hi, sink;
+    __device__ __forceinline__ int count() const { return hi > 0 ? sink + hi - lo : 0; }
+    __device__ __forceinline__ int tile(int i) const { return i < sink ? i : lo + (i - sink); }
+};
+
+__device__ __forceinline__ Tiles tiles_of(const WindowParams& p, int head, int qb) {
+    Tiles x;
+    x.head = head;
+    x.qb = qb;
+    x.lo = x.hi = x.sink = 0;
+    if (qb < p.nq) {
+        const int past = p.Sk - p.Sq;
+        const int first = qb * 128 + past, last = min(qb * 128 + 127, p.Sq - 1) + past;
+        if (last >= 0) {
+            const long long low = static_cast<long long>(first) - p.window + 1;
+            x.lo = low > 0 ? static_cast<int>(low / 128) : 0;
+            x.hi = last / 128 + 1;
+            x.sink = min(p.sinks / 128 + (p.sinks % 128 != 0), x.lo);
+        }
+    }
+    return x;
+}
+
+__device__ __forceinline__ Item item_of(const WindowParams& p, int t) {
+    // last rows first; at a row, all pairs of all batches next to each other
+    Item it;
+    const int per_row = p.B * p.pairs;
+    const int row = p.rows - 1 - t / per_row;
+    const int r = t - (t / per_row) * per_row;
+    it.b = r / p.pairs;
+    const int pair = r - it.b * p.pairs;
+    const int group = p.Hq / p.Hkv;
+    if (p.by_heads) {
+        it.kvh = 2 * pair / group;
+        it.x[0] = tiles_of(p, 2 * pair, row);
+        it.x[1] = it.x[0];
+        it.x[1].head = 2 * pair + 1;
+        it.lo = it.x[0].lo;
+        it.hi = it.x[0].hi;
+        it.sink = it.x[0].sink;
+    } else {
+        it.kvh = pair / group;
+        it.x[0] = tiles_of(p, pair, 2 * row);
+        it.x[1] = tiles_of(p, pair, 2 * row + 1);
+        // the second block is the later one: its keys start and end no earlier
+        const Tiles& a = it.x[0].hi > 0 ? it.x[0] : it.x[1];
+        it.lo = a.lo;
+        it.sink = a.sink;
+        it.hi = max(it.x[0].hi, it.x[1].hi);
+    }
+    return it;
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v, const WindowParams p) {
+    using C = Cfg<D>;
+    using T = std::conditional_t<BF16, __nv_bfloat16, __half>;
+    constexpr int kStages = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sq = sm + C::kQ;
+    uint8_t* skv = sm + C::kKV;
+    uint64_t* q_full = reinterpret_cast<uint64_t*>(sm + C::kBars);   // [2]
+    uint64_t* q_free = q_full + 2;                                    // [2]
+    uint64_t* full = q_free + 2;                                      // [stages]
+    uint64_t* empty = full + kStages;                                 // [stages] both issuers
+    uint64_t* s_full = empty + kStages;                               // [2]
+    uint64_t* p_full = s_full + 2;                                    // [2] four warps
+    uint64_t* pv_done = p_full + 2;                                   // [2]
+    uint64_t* o_free = pv_done + 2;                                   // [2] four warps
+    uint64_t* fin = o_free + 2;                                       // [2]
+    int* misc = reinterpret_cast<int*>(sm + C::kMisc);
+    volatile int* abort_flag = &misc[1];
+    int* status = p.status;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint64_t deadline = global_timer_ns() + p.budget_ns;
+
+    if (tid == 0) {
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&q_full[x], 1);
+            mbar_init(&q_free[x], 1);
+            mbar_init(&s_full[x], 1);
+            mbar_init(&p_full[x], 4);
+            mbar_init(&pv_done[x], 1);
+            mbar_init(&o_free[x], 4);
+            mbar_init(&fin[x], 1);
+        }
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 2);
+        }
+        misc[1] = 0;
+        fence_barrier_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(reinterpret_cast<uint32_t*>(&misc[0]), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = static_cast<uint32_t>(misc[0]);
+
+    if (warp == kLoadWarp) {
+        // ------------------------------------------------------------ TMA
+        if (lane == 0) {
+            tma_prefetch_desc(&tm_q);
+            tma_prefetch_desc(&tm_k);
+            tma_prefetch_desc(&tm_v);
+            int g = 0;                                   // tiles loaded, K and V counted apart
+            int nq[2] = {0, 0};                          // Q tiles loaded
+            bool ok = true;
+            auto load = [&](const CUtensorMap* map, int tile, const Item& it) {
+                const int st = g % kStages;
+                if (g >= kStages && !wait_parity(&empty[st], (g / kStages - 1) & 1, deadline, abort_flag, status))
+                    return false;
+                mbar_arrive_expect_tx(&full[st], C::kTile);
+                for (int h = 0; h < D / 64; ++h)
+                    tma_load_4d(skv + st * C::kTile + h * 16384, map, &full[st], h * 64, tile * 128, it.kvh, it.b);
+                ++g;
+                return true;
+            };
+            for (int t = blockIdx.x; ok && t < p.total_items; t += gridDim.x) {
+                const Item it = item_of(p, t);
+                const int n = it.count();
+                for (int i = 0; ok && i < n; ++i) {
+                    ok = load(&tm_k, it.tile(i), it);
+                    if (i == 0) {
+                        for (int x = 0; ok && x < 2; ++x) {
+                            if (it.x[x].hi == 0) continue;
+                            if (nq[x] > 0 && !wait_parity(&q_free[x], (nq[x] - 1) & 1, deadline, abort_flag, status)) {
+                                ok = false;
+                                break;
+                            }
+                            mbar_arrive_expect_tx(&q_full[x], C::kTile);
+                            for (int h = 0; h < D / 64; ++h)
+                                tma_load_4d(sq + x * C::kTile + h * 16384, &tm_q, &q_full[x], h * 64,
+                                            it.x[x].qb * 128, it.x[x].head, it.b);
+                            ++nq[x];
+                        }
+                    }
+                    ok = ok && load(&tm_v, it.tile(i), it);
+                }
+            }
+            if (*abort_flag) {
+                // copies in flight land before the shared memory is released
+                const uint64_t dl = global_timer_ns() + 200000000ull;
+                for (int x = 0; x < 2; ++x)
+                    if (nq[x] > 0) wait_parity_drain(&q_full[x], (nq[x] - 1) & 1, dl);
+                for (int j = max(0, g - kStages); j < g; ++j) wait_parity_drain(&full[j % kStages], (j / kStages) & 1, dl);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= kMmaWarp) {
+        // ------------------------------------------------------------ products of query tile x
+        const int x = warp - kMmaWarp;
+        const bool lead = lane == 0;
+        constexpr uint32_t idS = idesc_f16(128, 128, BF16, false);
+        constexpr uint32_t idO = idesc_f16(128, D, BF16, true);
+        const uint64_t q_desc = sdesc_sw128(smem_u32(sq + x * C::kTile), 16, 1024);
+        const uint64_t k_desc = sdesc_sw128(smem_u32(skv), 16, 1024);
+        const uint64_t v_desc = sdesc_sw128(smem_u32(skv), 16384, 1024);
+        const uint32_t ts = tbase + 128 * x, to = tbase + kOCol + D * x;
+        int g = 0;                                       // ring position (K of union tile i: g + 2 i, V: g + 2 i + 1)
+        int blk = 0, items = 0;                          // tiles and items of this query tile so far
+        bool ok = true;
+        for (int t = blockIdx.x; ok && t < p.total_items; t += gridDim.x) {
+            const Item it = item_of(p, t);
+            const Tiles me = x ? it.x[1] : it.x[0];
+            const int n = it.count();
+            // V of the tile visited last waits here until its P is written
+            int pend = -1;                               // ring position of that V, or none
+            bool first = true;
+            auto pv = [&]() {
+                const int st = pend % kStages;
+                if (!warp_wait_parity(&full[st], (pend / kStages) & 1, deadline, abort_flag, status) ||
+                    (first && items > 0 && !warp_wait_parity(&o_free[x], (items - 1) & 1, deadline, abort_flag, status)) ||
+                    !warp_wait_parity(&p_full[x], (blk - 1) & 1, deadline, abort_flag, status))
+                    return false;
+                tc_fence_after();
+                const uint64_t b0 = v_desc + static_cast<uint32_t>(st) * (C::kTile >> 4);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_f16_ts_if(lead, to, ts + 8 * kk, b0 + ((kk * 2048) >> 4), idO, (!first || kk > 0) ? 1u : 0u);
+                mma_commit_if(lead, &empty[st]);
+                mma_commit_if(lead, &pv_done[x]);
+                first = false;
+                pend = -1;
+                return true;
+            };
+            bool any = false;
+            int left = me.count();
+            for (int i = 0; ok && i < n; ++i) {
+                const int gk = g + 2 * i, st = gk % kStages;
+                if ((pend >= 0 && !pv()) ||
+                    !warp_wait_parity(&full[st], (gk / kStages) & 1, deadline, abort_flag, status)) {
+                    ok = false;
+                    break;
+                }
+                if (!me.has(it.tile(i))) {
+                    // not this query tile's: both stages are released unread, once loaded (an arrival
+                    // before that could count for the stage's use before)
+                    const int sv = (gk + 1) % kStages;
+                    mbar_arrive_if(lead, &empty[st]);
+                    if (!warp_wait_parity(&full[sv], ((gk + 1) / kStages) & 1, deadline, abort_flag, status)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_if(lead, &empty[sv]);
+                    continue;
+                }
+                if (!any) {
+                    ok = warp_wait_parity(&q_full[x], items & 1, deadline, abort_flag, status);
+                    if (!ok) break;
+                    any = true;
+                }
+                tc_fence_after();
+                const uint64_t b0 = k_desc + static_cast<uint32_t>(st) * (C::kTile >> 4);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+                    mma_f16_ss_if(lead, ts, q_desc + off, b0 + off, idS, kk > 0 ? 1u : 0u);
+                }
+                mma_commit_if(lead, &s_full[x]);
+                mma_commit_if(lead, &empty[st]);
+                if (--left == 0) mma_commit_if(lead, &q_free[x]);
+                pend = gk + 1;
+                ++blk;
+            }
+            if (ok && pend >= 0) ok = pv();
+            if (any) ++items;
+            g += 2 * n;
+        }
+        mma_commit_if(lead, &fin[x]);
+        wait_parity_drain(&fin[x], 0, global_timer_ns() + 200000000ull);
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ softmax of query tile x
+        const int x = warp >> 2;
+        const int lrow = 32 * (warp & 3) + lane;
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const uint32_t ts = tbase + lanes + 128 * x, to = tbase + lanes + kOCol + D * x;
+        const float c = p.scale_log2;
+        int blk = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; ok && t < p.total_items; t += gridDim.x) {
+            const Item it = item_of(p, t);
+            const Tiles me = x ? it.x[1] : it.x[0];
+            if (me.qb >= p.nq) continue;                 // the odd row block's missing partner
+            const int n = me.count();
+            const int row = me.qb * 128 + lrow;
+            const int pos = row + p.Sk - p.Sq;
+            T* out = reinterpret_cast<T*>(p.out) + it.b * p.out_b + me.head * p.out_h + row * p.out_s;
+            if (n == 0) {
+                if (row < p.Sq)
+                    for (int e = 0; e < D / 8; ++e) reinterpret_cast<uint4*>(out)[e] = make_uint4(0, 0, 0, 0);
+                continue;
+            }
+            // keys [lo, pos] and, below lo, those before the sinks
+            const int lo = pos >= p.window ? pos - p.window + 1 : 0;
+            float m_used = -INFINITY, l = 0.f;
+            for (int i = 0; i < n; ++i, ++blk) {
+                const int key0 = 128 * (i < me.sink ? i : me.lo + (i - me.sink));
+                if (!warp_wait_parity(&s_full[x], blk & 1, deadline, abort_flag, status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                float s[128];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) tmem_ld_row32(ts + 32 * h, reinterpret_cast<uint32_t*>(s) + 32 * h);
+                tmem_wait_ld();
+                const bool edge = key0 + 127 > pos || (key0 < lo && key0 + 128 > p.sinks);
+                if (__any_sync(0xffffffffu, edge)) {
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        // bit e: key k0 + e is visible
+                        const int k0 = key0 + 32 * h;
+                        auto below = [](int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u); };
+                        const uint32_t on = below(pos + 1 - k0) & (~below(lo - k0) | below(p.sinks - k0));
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!((on >> e) & 1u)) s[32 * h + e] = -INFINITY;
+                    }
+                }
+                float mx;
+                {
+                    float m4[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        m4[j] = max3f(s[j], s[j + 4], s[j + 8]);
+#pragma unroll
+                        for (int e = 12; e + 4 < 128; e += 8) m4[j] = max3f(m4[j], s[j + e], s[j + e + 4]);
+                        m4[j] = fmaxf(m4[j], s[j + 124]);
+                    }
+                    mx = fmaxf(max3f(m4[0], m4[1], m4[2]), m4[3]);
+                }
+                const bool grow = mx * c > m_used * c + kRescaleLog2;
+                const float m_new = grow ? mx : m_used;
+                const float alpha = grow ? ex2_approx((m_used - m_new) * c) : 1.f;
+                const bool rescale = grow && m_used != -INFINITY;
+                m_used = m_new;
+                const float mc = m_new == -INFINITY ? 0.f : m_new * c;
+                float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                                 make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t pv[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 y = fma2f(make_float2(s[32 * h + 2 * e], s[32 * h + 2 * e + 1]), make_float2(c, c),
+                                               make_float2(-mc, -mc));
+                        const float2 ev = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                        acc[e & 3] = add2f(acc[e & 3], ev);
+                        pv[e] = pack2<BF16>(ev.x, ev.y);
+                    }
+                    tmem_st_row16(ts + 16 * h, pv);
+                }
+                const float2 a2 = add2f(add2f(acc[0], acc[1]), add2f(acc[2], acc[3]));
+                l = l * alpha + (a2.x + a2.y);
+                if (__any_sync(0xffffffffu, rescale)) {
+                    // O is complete up to the tile before this one
+                    if (!warp_wait_parity(&pv_done[x], (blk - 1) & 1, deadline, abort_flag, status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t o[32];
+                        tmem_ld_row32(to + c0, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        tmem_st_row32(to + c0, o);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[x]);
+            }
+            if (!ok) break;
+            // ---- O / l to memory
+            if (!warp_wait_parity(&pv_done[x], (blk - 1) & 1, deadline, abort_flag, status)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const float inv = l == 0.f ? 0.f : 1.f / l;         // NaN stays NaN
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 32) {
+                uint32_t o[32];
+                tmem_ld_row32(to + c0, o);
+                tmem_wait_ld();
+                if (c0 + 32 == D) {
+                    // O is in registers: the next item's first P V may overwrite it
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&o_free[x]);
+                }
+                if (row < p.Sq) {
+                    uint32_t ob[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        ob[e] = l == 0.f ? 0u : pack2<BF16>(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        reinterpret_cast<uint4*>(out)[c0 / 8 + k] =
+                            make_uint4(ob[4 * k], ob[4 * k + 1], ob[4 * k + 2], ob[4 * k + 3]);
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tbase, kTmemCols);
+    }
+}
+
+// Strides (elements) of a [B, H, S, d] tensor as a tensor map wants them: a dimension of one entry may
+// carry any stride, so it gets one that is always valid.  False: not a layout the map can hold.
+bool map_strides(const int64_t* st, int B, int H, int S, int d, uint64_t (&bytes)[3]) {
+    const int64_t in[3] = {st[2], st[1], st[0]};         // rows, heads, batches
+    const int n[3] = {S, H, B};
+    for (int i = 0; i < 3; ++i) {
+        if (n[i] == 1) {
+            bytes[i] = static_cast<uint64_t>(d) * 2;
+            continue;
+        }
+        if (in[i] <= 0 || (in[i] & 7) || in[i] >= (int64_t(1) << 38)) return false;
+        bytes[i] = static_cast<uint64_t>(in[i]) * 2;
+    }
+    return true;
+}
+
+template <int D, bool BF16>
+int launch(const void* q, const void* k, const void* v, const int64_t (&st)[12], const WindowParams& prm,
+           cudaStream_t stream) {
+    uint64_t qs[3], ks[3], vs[3];
+    const int sk = prm.Sk > 0 ? prm.Sk : 1, hk = prm.Sk > 0 ? prm.Hkv : 1, bk = prm.Sk > 0 ? prm.B : 1;
+    if (!map_strides(st, prm.B, prm.Hq, prm.Sq, D, qs) || !map_strides(st + 3, bk, hk, sk, D, ks) ||
+        !map_strides(st + 6, bk, hk, sk, D, vs))
+        return BSATTN_ERR_INVALID_ARG;
+    CUtensorMap tq, tk, tv;
+    const uint64_t dq[4] = {D, uint64_t(prm.Sq), uint64_t(prm.Hq), uint64_t(prm.B)};
+    const uint64_t dk[4] = {D, uint64_t(sk), uint64_t(hk), uint64_t(bk)};
+    const uint32_t box[4] = {64, 128, 1, 1};
+    int rc = encode_4d(&tq, q, BF16, dq, qs, box);
+    if (!rc) rc = encode_4d(&tk, k, BF16, dk, ks, box);
+    if (!rc) rc = encode_4d(&tv, v, BF16, dk, vs, box);
+    if (rc) return rc;
+    auto kern = window_kernel<D, BF16>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kBytes) != cudaSuccess)
+        return BSATTN_ERR_CUDA;
+    int sms = num_sms_of_current_device();
+    if (sms <= 0) sms = 148;
+    const int grid = prm.total_items < sms ? prm.total_items : sms;
+    kern<<<static_cast<unsigned>(grid), kThreads, Cfg<D>::kBytes, stream>>>(tq, tk, tv, prm);
+    return cudaGetLastError() == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace bsattn
+
+extern "C" int bsattn_prefill_window(const void* q, const void* k, const void* v, int window, int sinks,
+                                     void* out, int B, int Hq, int Hkv, int Sq, int Sk, int d,
+                                     const int64_t* strides, bsattn_dtype dtype, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+    using namespace bsattn;
+    if (B < 0 || Hq <= 0 || Hkv <= 0 || Sq < 0 || Sk < 0 || window < 1 || sinks < 0) return BSATTN_ERR_INVALID_ARG;
+    if (Hq % Hkv) return BSATTN_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return BSATTN_ERR_UNSUPPORTED;
+    if (dtype != BSATTN_F16 && dtype != BSATTN_BF16) return BSATTN_ERR_UNSUPPORTED;
+    if (!workspace || workspace_bytes < 256) return BSATTN_ERR_INVALID_ARG;
+    if (B == 0 || Sq == 0) return BSATTN_OK;
+    if (!q || !out || !aligned16(q) || !aligned16(out)) return BSATTN_ERR_INVALID_ARG;
+    if (Sk > 0 && (!k || !v || !aligned16(k) || !aligned16(v))) return BSATTN_ERR_INVALID_ARG;
+    if (Sq > (1 << 30) || Sk > (1 << 30)) return BSATTN_ERR_UNSUPPORTED;
+    int64_t st[12];
+    if (strides) {
+        for (int i = 0; i < 12; ++i) st[i] = strides[i];
+    } else {
+        const int64_t H[4] = {Hq, Hkv, Hkv, Hq}, S[4] = {Sq, Sk, Sk, Sq};
+        for (int i = 0; i < 4; ++i) {
+            st[3 * i] = H[i] * S[i] * d;
+            st[3 * i + 1] = S[i] * d;
+            st[3 * i + 2] = d;
+        }
+    }
+    // out is written with 16-byte stores, each element once
+    const int64_t on[3] = {B, Hq, Sq};
+    for (int i = 0; i < 3; ++i)
+        if (on[i] > 1 && (st[9 + i] <= 0 || (st[9 + i] & 7))) return BSATTN_ERR_INVALID_ARG;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    WindowParams prm{};
+    prm.out = out;
+    prm.status = static_cast<int*>(workspace);
+    prm.out_b = B > 1 ? st[9] : 0;
+    prm.out_h = Hq > 1 ? st[10] : 0;
+    prm.out_s = Sq > 1 ? st[11] : 0;
+    prm.B = B;
+    prm.Hq = Hq;
+    prm.Hkv = Hkv;
+    prm.Sq = Sq;
+    prm.Sk = Sk;
+    prm.window = window;
+    prm.sinks = sinks;
+    prm.nq = (Sq + 127) / 128;
+    prm.by_heads = (Hq / Hkv) % 2 == 0;
+    prm.pairs = prm.by_heads ? Hq / 2 : Hq;
+    prm.rows = prm.by_heads ? prm.nq : (prm.nq + 1) / 2;
+    const long long items = static_cast<long long>(B) * prm.pairs * prm.rows;
+    if (items > 0x3fffffffLL) return BSATTN_ERR_UNSUPPORTED;
+    prm.total_items = static_cast<int>(items);
+    prm.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(d)));
+    prm.budget_ns = wait_budget_ns();
+    if (Sk == 0) k = v = q;                     // no row sees a key: K and V are not read, only mapped
+    const bool bf16 = dtype == BSATTN_BF16;
+    if (d == 64) return bf16 ? launch<64, true>(q, k, v, st, prm, cs) : launch<64, false>(q, k, v, st, prm, cs);
+    return bf16 ? launch<128, true>(q, k, v, st, prm, cs) : launch<128, false>(q, k, v, st, prm, cs);
+}

@@ -44,7 +44,8 @@ typedef enum {
     BSATTN_ERR_UNSUPPORTED = 2,  /* head dim / dtype / shape outside what is built */
     BSATTN_ERR_CUDA = 4,         /* a CUDA runtime / driver call failed */
     BSATTN_ERR_TIMEOUT = 8,      /* device: a bounded wait expired (the kernel bailed out) */
-    BSATTN_ERR_BAD_INDEX = 16    /* device: a block index past the sequence was skipped */
+    BSATTN_ERR_BAD_INDEX = 16,   /* device: a block index past the sequence was skipped */
+    BSATTN_ERR_NO_SPACE = 32     /* device: a request got no pages or slots (bsattn_paged_plan) */
 } bsattn_status;
 
 #define BSATTN_BLOCK 64
@@ -248,6 +249,135 @@ int bsattn_mask_from_threshold(const float* scores, int B, int H, int nq, int nk
  */
 int bsattn_mask_from_cumulative_threshold(const float* attn_sum, int B, int H, int nq, int nk,
                                           double threshold, int causal, uint8_t* mask_out);
+
+/*
+ * ---------------------------------------------------------------------------------------------
+ * Paged serving: a page plan, a 4-bit cache, and attention with a sliding window.  The calls below
+ * have no counterpart in the pages; their definitions are given in full here.
+ *
+ * Their workspaces: the plan, append, gather and window prefill use only the status word (256 bytes,
+ * 16-byte aligned); they set bits of it and read nothing, so calls may share one.  The stream decodes
+ * (bsattn_decode_window, bsattn_decode_window_paged, bsattn_decode_paged_kv4) also keep merge tickets
+ * and partial results in theirs: its first 4352 bytes must be zero before the first use, any shapes
+ * may follow one another on it, and calls that can overlap on the GPU (streams, replayed graphs) need
+ * one each.
+ */
+
+/*
+ * Block-table rows and slot map of a step, from request lengths.  Sequence b holds cached_lens[b]
+ * tokens and brings new_lens[b]; the new tokens of all sequences are packed in that order.
+ *
+ *   cached_lens, new_lens  (device) [B] int32
+ *   free_pages   (device) [free_capacity] int32: the first *free_count entries are free pages; they
+ *                are taken from the end, in the order of the sequences
+ *   free_count   (device) int32
+ *   block_table  (device) [B, max_pages_per_seq] int32, updated: the entries of new pages are written,
+ *                all others are left as they were
+ *   slots        (device) [max_tokens] int64, fully written: page * page_size + row of each packed
+ *                token's place, -1 for a token that got none and past the last token
+ *   starts       (device) [B + 1] int32: starts[b] = new_lens[0] + ... + new_lens[b - 1] (sums past
+ *                INT32_MAX stay there)
+ *   seqlens      (device) [B] int32: cached_lens[b] + new_lens[b], or cached_lens[b] if not served
+ *   free_left    (device) int32: the free pages that remain
+ * A sequence is not served (no page, slots -1, BSATTN_ERR_NO_SPACE in the status word) if its table
+ * row or `slots` is too short for it, or if it needs pages and those asked for up to and including it
+ * exceed *free_count.  A negative length is not served and counts as 0 tokens (BSATTN_ERR_BAD_INDEX);
+ * a token whose page is mapped to a negative number gets slot -1 (BSATTN_ERR_BAD_INDEX).  No output
+ * may overlap another output or an input (BSATTN_ERR_INVALID_ARG), so that a call can be repeated.
+ * page_size >= 1; B <= 8192 (else BSATTN_ERR_UNSUPPORTED).
+ */
+int bsattn_paged_plan(const int32_t* cached_lens, const int32_t* new_lens, const int32_t* free_pages,
+                      const int32_t* free_count, int32_t* block_table, int64_t* slots, int32_t* starts,
+                      int32_t* seqlens, int32_t* free_left, int B, int page_size, int max_pages_per_seq,
+                      int free_capacity, int max_tokens, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+/*
+ * The 4-bit cache.  16 consecutive channels of a token's head are a group; a group is 16 e2m1 codes
+ * c_i and one e4m3 scale s and stands for the values e2m1(c_i) * s * unit, where the unit (k_scale for
+ * all keys, v_scale for all values) is a power of two in [2^-16, 2^16].
+ *
+ *   k_codes, v_codes    (device) [num_pages, Hkv, page_size, d / 2] uint8: channel 2 i in the low half
+ *                       of byte i, channel 2 i + 1 in the high half
+ *   k_scales, v_scales  (device) [num_pages, Hkv, page_size, d / 16] uint8
+ * all 16-byte aligned.  Writing x: s = e4m3(max |x| / (6 unit)), c = e2m1(x / (s unit)), each rounded to
+ * nearest with ties to even and saturated (448, 6), c = 0 where s = 0 and for every value that rounds to
+ * 0; the bytes are those of exact arithmetic.  A group with an infinity or a NaN gets the NaN scale 0x7f and reads as NaN.
+ *
+ * Append rounds T rows of k and v, (device) [T, Hkv, d] dtype with contiguous channels and the given
+ * strides (elements, multiples of 8; any value for a dimension of one entry), into the rows that
+ * slots (device) [T] int64 names.  Negative slots are skipped; slots at or past num_pages * page_size
+ * are skipped and flagged BSATTN_ERR_BAD_INDEX; the others must be distinct.  Other rows are not
+ * touched.  Gather writes the rows that slots names to k and v, (device) [T, Hkv, d] dtype, dense,
+ * rounded to nearest; a skipped slot gives zeros, a slot may be named more than once.
+ */
+int bsattn_kv4_append(const void* k, const void* v, long long k_token_stride, long long k_head_stride,
+                      long long v_token_stride, long long v_head_stride, const int64_t* slots,
+                      uint8_t* k_codes, uint8_t* k_scales, uint8_t* v_codes, uint8_t* v_scales,
+                      float k_scale, float v_scale, int T, int Hkv, int num_pages, int page_size, int d,
+                      bsattn_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+int bsattn_kv4_gather(const int64_t* slots, const uint8_t* k_codes, const uint8_t* k_scales,
+                      const uint8_t* v_codes, const uint8_t* v_scales, float k_scale, float v_scale,
+                      void* k, void* v, int T, int Hkv, int num_pages, int page_size, int d,
+                      bsattn_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One query token per sequence over the paged 4-bit cache.  As bsattn_decode_paged: query head h of
+ * sequence b attends to kv head h / (Hq / Hkv) over the visible ones of its cache_seqlens[b] tokens,
+ * out = softmax(q . k / sqrt(d)) v, 0 where nothing is visible.  Visible are
+ *   - with block_indices (device) [B, Hkv, max_sel] int32: the tokens of the chosen 64-token blocks
+ *     (-1 = empty slot, distinct, any order; a block at or past the end is skipped and flagged
+ *     BSATTN_ERR_BAD_INDEX); window must be 0;
+ *   - with block_indices NULL and window > 0: token j with j < sinks or j >= cache_seqlens[b] - window;
+ *   - with block_indices NULL and window 0: every token.
+ * q, out (device) [B, Hq, d] dtype; block_table as in bsattn_decode_paged, page_size a multiple of 64.
+ * Tokens on pages out of range, and any past the table, are skipped and flagged BSATTN_ERR_BAD_INDEX;
+ * a negative length is flagged and taken as 0.  Masked tokens and rows past the end may hold anything.
+ * The products run in fp16 with 32-bit sums: cache values are exact there, weights are rounded to fp16.
+ * Requires Hq % Hkv == 0, Hq / Hkv <= 8, Hkv <= 1024, d in {64, 128}.  The result does not depend on
+ * the order in which CTAs run.
+ */
+int bsattn_decode_paged_kv4(const void* q, const uint8_t* k_codes, const uint8_t* k_scales,
+                            const uint8_t* v_codes, const uint8_t* v_scales, float k_scale, float v_scale,
+                            const int32_t* cache_seqlens, const int32_t* block_indices,
+                            const int32_t* block_table, int window, int sinks, void* out, int B, int Hq,
+                            int Hkv, int num_pages, int page_size, int max_pages_per_seq, int d,
+                            int max_sel, bsattn_dtype dtype, void* workspace, size_t workspace_bytes,
+                            void* stream);
+size_t bsattn_decode_kv4_workspace_size(int Hq, int Hkv, int d);
+
+/*
+ * Sliding-window decode with sinks over a 16-bit cache: as bsattn_decode_varlen (contiguous k, v
+ * [B, Smax, Hkv, d]) and bsattn_decode_paged ([num_pages, page_size, Hkv, d] and a block table), with
+ * token j of sequence b visible iff j < cache_seqlens[b] and (j < sinks or j >= cache_seqlens[b] -
+ * window), window >= 1.  A length past Smax is flagged BSATTN_ERR_BAD_INDEX and taken as Smax; bad
+ * lengths and pages otherwise as in bsattn_decode_paged_kv4, and the same limits.
+ */
+int bsattn_decode_window(const void* q, const void* k, const void* v, const int32_t* cache_seqlens,
+                         int window, int sinks, void* out, int B, int Hq, int Hkv, int Smax, int d,
+                         bsattn_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+int bsattn_decode_window_paged(const void* q, const void* k_pages, const void* v_pages,
+                               const int32_t* cache_seqlens, const int32_t* block_table, int window,
+                               int sinks, void* out, int B, int Hq, int Hkv, int num_pages, int page_size,
+                               int max_pages_per_seq, int d, bsattn_dtype dtype, void* workspace,
+                               size_t workspace_bytes, void* stream);
+size_t bsattn_decode_window_workspace_size(int Hq, int Hkv, int d);
+
+/*
+ * Causal attention with a sliding window and sinks, forward.  Query row i of Sq stands at position
+ * p = i + (Sk - Sq) and sees key j iff j <= p and (j < sinks or j > p - window); query head h reads kv
+ * head h / (Hq / Hkv); out_i = softmax_j(q_i . k_j / sqrt(d)) v_j, 0 for a row that sees no key.
+ *
+ *   q, out   (device) [B, Hq, Sq, d] dtype;  k, v (device) [B, Hkv, Sk, d] dtype; 16-byte aligned
+ *   strides  (host) 12 element strides: batch, head, row of q, of k, of v, of out (positive multiples
+ *            of 8; any value for a dimension of one entry), or NULL for dense tensors
+ * window >= 1, sinks >= 0, d in {64, 128}, any Hq % Hkv == 0.  P is rounded to dtype before the second
+ * product, which takes whole 128-key tiles: v must be finite, since a weight of 0 times an infinity is
+ * NaN (keys that a row does not see may hold anything).
+ */
+int bsattn_prefill_window(const void* q, const void* k, const void* v, int window, int sinks, void* out,
+                          int B, int Hq, int Hkv, int Sq, int Sk, int d, const int64_t* strides,
+                          bsattn_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Reads and clears the device status word at the start of `workspace` (device), after
