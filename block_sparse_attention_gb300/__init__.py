@@ -75,6 +75,8 @@ def library_path() -> str:
 def load(build_if_missing: bool = True) -> ctypes.CDLL:
     """Loads libbsattn.so (building it with nvcc first if it is missing)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.LIB
@@ -398,19 +400,35 @@ def bsattn_set_wait_budget_ns(ns: int) -> None:
 
 
 # ----------------------------------------------------------------- paged serving
+#
+# A step of a server makes these calls back to back with kernels of a few microseconds, so what the
+# binding itself takes counts.  Each call tests its arguments in one expression; only if that fails does
+# it go through them one by one for the error that says which is wrong.
 
 _STREAM_HEADER = 256 + 4 * 1024          # status word and tickets: all that has to start at zero
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_capturing = torch._C._cuda_isCurrentStreamCapturing
+_I32, _I64, _U8 = torch.int32, torch.int64, torch.uint8
+_CODES = {torch.float16: _F16, torch.bfloat16: _BF16}
+
+
+def _device_index(device) -> int:
+    if isinstance(device, int):
+        return device
+    device = torch.device(device)
+    return torch.cuda.current_device() if device.index is None else device.index
 
 
 def call_workspace(device, purpose: str, nbytes: int) -> torch.Tensor:
     """A workspace for the stream decodes that no other call in flight uses: one per (stream, purpose),
     and a new one for every call captured into a CUDA graph (graphs may be replayed side by side)."""
-    device = torch.device(device)
-    capturing = torch.cuda.is_current_stream_capturing()
-    key = (device.index, purpose, _stream(device))
+    index = _device_index(device)
+    capturing = _capturing()
+    key = (index, purpose, _raw_stream(index))
     buf = None if capturing else _ws_cache.get(key)
     if buf is None or buf.numel() < nbytes:
-        buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        buf = torch.empty(nbytes, dtype=_U8, device=torch.device("cuda", index))
         buf[:_STREAM_HEADER].zero_()
         if not capturing:
             _ws_cache[key] = buf
@@ -423,51 +441,40 @@ _status_ws: dict = {}
 def status_workspace(device) -> torch.Tensor:
     """The 256-byte workspace of the calls that keep only a status word in it.  They set bits of it and
     read nothing, so all of a device's streams and graphs share it."""
-    device = torch.device(device)
-    buf = _status_ws.get(device.index)
+    index = _device_index(device)
+    buf = _status_ws.get(index)
     if buf is None:
-        buf = torch.zeros(256, dtype=torch.uint8, device=device)
-        if not torch.cuda.is_current_stream_capturing():
-            torch.cuda.current_stream(device).synchronize()
-            _status_ws[device.index] = buf
+        buf = torch.zeros(256, dtype=_U8, device=torch.device("cuda", index))
+        if not _capturing():
+            torch.cuda.current_stream(index).synchronize()
+            _status_ws[index] = buf
     return buf
 
 
-def _same_device(**tensors):
-    dev = None
-    for name, t in tensors.items():
-        if not t.is_cuda:
+def _refuse(*tensors):
+    """Raises for the first of (name, tensor, dtype, dims, shape or None) that is not as it should be."""
+    index = tensors[0][1].get_device()
+    for name, t, dtype, dims, shape in tensors:
+        if t.get_device() < 0:
             raise ValueError(f"{name} must be a CUDA tensor")
-        if dev is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
-        dev = t.device
-    return dev
-
-
-def _contiguous(**tensors):
-    for name, t in tensors.items():
+        if t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, {tensors[0][0]} on {tensors[0][1].device}")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.dim() != dims:
+            raise ValueError(f"{name} must have {dims} dimensions, not {t.dim()}")
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
+    raise ValueError("the arguments' shapes disagree")
 
 
-def _dtypes(dtype, **tensors):
-    for name, t in tensors.items():
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-
-
-def _shape(name, t, want):
-    if tuple(t.shape) != tuple(want):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(want)}")
-
-
-def _out(out, like):
-    if out is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
-    if out.device != like.device or out.dtype != like.dtype:
-        raise ValueError("out must have the queries' device and dtype")
-    _shape("out", out, like.shape)
-    return out
+def _check_out(out, q, contiguous):
+    if out.get_device() != q.get_device() or out.dtype is not q.dtype or out.shape != q.shape:
+        raise ValueError("out must have the queries' device, dtype and shape")
+    if contiguous and not out.is_contiguous():
+        raise ValueError("out must be contiguous")
 
 
 def bsattn_paged_plan(cached_lens, new_lens, free_pages, free_count, block_table, page_size: int,
@@ -476,31 +483,34 @@ def bsattn_paged_plan(cached_lens, new_lens, free_pages, free_count, block_table
     free_pages int32 [n] is the free list, free_count int32 [1] how many of it are free (taken from the
     end); block_table int32 [B, max_pages] gets the new pages.  Returns (slots int64 [max_tokens], -1
     where there is no token; starts int32 [B + 1]; seqlens int32 [B]; free_left int32 [1])."""
-    lib = load()
-    dev = _same_device(cached_lens=cached_lens, new_lens=new_lens, free_pages=free_pages,
-                       free_count=free_count, block_table=block_table)
-    _contiguous(cached_lens=cached_lens, new_lens=new_lens, free_pages=free_pages, free_count=free_count,
-                block_table=block_table)
-    _dtypes(torch.int32, cached_lens=cached_lens, new_lens=new_lens, free_pages=free_pages,
-            free_count=free_count, block_table=block_table)
+    i = cached_lens.get_device()
     B = cached_lens.numel()
-    _shape("new_lens", new_lens, cached_lens.shape)
-    if cached_lens.dim() != 1 or block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError("cached_lens must be [B] and block_table [B, max_pages]")
-    if free_count.numel() != 1:
-        raise ValueError("free_count must have one element")
-    with torch.cuda.device(dev):
-        slots = torch.empty(int(max_tokens), dtype=torch.int64, device=dev)
-        ints = torch.empty(2 * B + 2, dtype=torch.int32, device=dev)
-        starts, seqlens, left = ints[:B + 1], ints[B + 1:2 * B + 1], ints[2 * B + 1:]
-        if ws is None:
-            ws = status_workspace(dev)
-        rc = lib.bsattn_paged_plan(cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
-                                   free_count.data_ptr(), block_table.data_ptr(), slots.data_ptr(),
-                                   starts.data_ptr(), seqlens.data_ptr(), left.data_ptr(), B,
-                                   int(page_size), block_table.shape[1], free_pages.numel(),
-                                   int(max_tokens), ws.data_ptr(), ws.numel(), _stream(dev))
-    _check("bsattn_paged_plan", rc)
+    if not (i >= 0 and new_lens.get_device() == i and free_pages.get_device() == i
+            and free_count.get_device() == i and block_table.get_device() == i
+            and cached_lens.dtype is _I32 and new_lens.dtype is _I32 and free_pages.dtype is _I32
+            and free_count.dtype is _I32 and block_table.dtype is _I32
+            and cached_lens.dim() == 1 and new_lens.shape == cached_lens.shape and free_pages.dim() == 1
+            and free_count.numel() == 1 and block_table.dim() == 2 and block_table.shape[0] == B
+            and cached_lens.is_contiguous() and new_lens.is_contiguous() and free_pages.is_contiguous()
+            and block_table.is_contiguous()):
+        _refuse(("cached_lens", cached_lens, _I32, 1, None), ("new_lens", new_lens, _I32, 1, (B,)),
+                ("free_pages", free_pages, _I32, 1, None), ("free_count", free_count, _I32, 1, (1,)),
+                ("block_table", block_table, _I32, 2, (B, *block_table.shape[1:])))
+    if _current_device() != i:
+        with torch.cuda.device(i):
+            return bsattn_paged_plan(cached_lens, new_lens, free_pages, free_count, block_table, page_size,
+                                     max_tokens, ws)
+    slots = cached_lens.new_empty(max_tokens, dtype=_I64)
+    starts, seqlens, left = cached_lens.new_empty(B + 1), torch.empty_like(cached_lens), torch.empty_like(free_count)
+    if ws is None:
+        ws = status_workspace(i)
+    rc = load().bsattn_paged_plan(cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
+                                  free_count.data_ptr(), block_table.data_ptr(), slots.data_ptr(),
+                                  starts.data_ptr(), seqlens.data_ptr(), left.data_ptr(), B, page_size,
+                                  block_table.shape[1], free_pages.numel(), max_tokens, ws.data_ptr(),
+                                  ws.numel(), _raw_stream(i))
+    if rc:
+        _check("bsattn_paged_plan", rc)
     return slots, starts, seqlens, left
 
 
@@ -516,69 +526,82 @@ class Kv4Cache(NamedTuple):
 def bsattn_kv4_cache(num_pages: int, Hkv: int, page_size: int, d: int, device="cuda") -> Kv4Cache:
     """A zeroed paged 4-bit cache."""
     def make(n):
-        return torch.zeros(num_pages, Hkv, page_size, n, dtype=torch.uint8, device=device)
+        return torch.zeros(num_pages, Hkv, page_size, n, dtype=_U8, device=device)
     return Kv4Cache(make(d // 2), make(d // 16), make(d // 2), make(d // 16))
 
 
-def _kv4(cache):
-    c = Kv4Cache(*cache)
-    _contiguous(**c._asdict())
-    _dtypes(torch.uint8, **c._asdict())
-    if c.k_codes.dim() != 4:
-        raise ValueError("a 4-bit cache's tensors are [pages, Hkv, page_size, ...]")
-    pages, hkv, page, half = c.k_codes.shape
-    _shape("v_codes", c.v_codes, c.k_codes.shape)
-    for name in ("k_scales", "v_scales"):
-        _shape(name, getattr(c, name), (pages, hkv, page, half // 8))
-    return c, pages, hkv, page, 2 * half
+def _kv4(cache, i):
+    """The shape (pages, Hkv, page_size, d / 2) of a 4-bit cache on device i, or an error."""
+    kc, ks, vc, vs = cache
+    shape = kc.shape
+    scales = ks.shape
+    if not (i >= 0 and kc.get_device() == i and ks.get_device() == i and vc.get_device() == i
+            and vs.get_device() == i and kc.dtype is _U8 and ks.dtype is _U8 and vc.dtype is _U8 and vs.dtype is _U8
+            and len(shape) == 4 and vc.shape == shape and vs.shape == scales and scales[:3] == shape[:3]
+            and len(scales) == 4 and 8 * scales[3] == shape[3] and kc.is_contiguous() and ks.is_contiguous()
+            and vc.is_contiguous() and vs.is_contiguous()):
+        small = (*shape[:3], shape[-1] // 8)
+        _refuse(("k_codes", kc, _U8, 4, None), ("k_scales", ks, _U8, 4, small), ("v_codes", vc, _U8, 4, shape),
+                ("v_scales", vs, _U8, 4, small))
+    return shape
+
+
+def _row_strides(name, t):
+    st = t.stride()
+    if st[2] != 1 and t.numel():
+        raise ValueError(f"{name}'s channels must be contiguous")
+    # the stride of a dimension of one entry is never used
+    return (st[0] if t.shape[0] > 1 else 0), (st[1] if t.shape[1] > 1 else 0)
 
 
 def bsattn_kv4_append(k, v, slots, cache, k_scale: float = 1.0, v_scale: float = 1.0, ws=None) -> None:
     """Rounds k and v [T, Hkv, d] fp16|bf16 (channels contiguous, any 16-byte aligned token and head
     strides) into the rows that slots int64 [T] names (negative: skipped; all others distinct)."""
-    lib = load()
-    c, pages, hkv, page, d = _kv4(cache)
-    dev = _same_device(k=k, v=v, slots=slots, **c._asdict())
-    _dtypes(torch.int64, slots=slots)
-    _contiguous(slots=slots)
-    if k.dim() != 3 or v.dtype != k.dtype:
-        raise ValueError("k and v must be [T, Hkv, d] of one dtype")
-    T = k.shape[0]
-    _shape("k", k, (T, hkv, d))
-    _shape("v", v, (T, hkv, d))
-    _shape("slots", slots, (T,))
-    for name, t in (("k", k), ("v", v)):
-        if T and t.stride(2) != 1:
-            raise ValueError(f"{name}'s channels must be contiguous")
-    # the stride of a dimension of one entry is never used
-    st = [t.stride(i) if t.shape[i] > 1 else 0 for t in (k, v) for i in (0, 1)]
-    with torch.cuda.device(dev):
-        if ws is None:
-            ws = status_workspace(dev)
-        rc = lib.bsattn_kv4_append(k.data_ptr(), v.data_ptr(), *st, slots.data_ptr(), *(t.data_ptr() for t in c),
-                                   float(k_scale), float(v_scale), T, hkv, pages, page, d, _dtype_code(k),
-                                   ws.data_ptr(), ws.numel(), _stream(dev))
-    _check("bsattn_kv4_append", rc)
+    i = k.get_device()
+    pages, hkv, page, half = _kv4(cache, i)
+    T = slots.numel()
+    dtype = _dtype_code(k)
+    if not (v.get_device() == i and slots.get_device() == i and v.dtype is k.dtype and slots.dtype is _I64
+            and slots.dim() == 1 and slots.is_contiguous() and k.shape == (T, hkv, 2 * half) and v.shape == k.shape):
+        _refuse(("slots", slots, _I64, 1, None), ("k", k.contiguous(), k.dtype, 3, (T, hkv, 2 * half)),
+                ("v", v.contiguous(), k.dtype, 3, (T, hkv, 2 * half)))
+    if _current_device() != i:
+        with torch.cuda.device(i):
+            return bsattn_kv4_append(k, v, slots, cache, k_scale, v_scale, ws)
+    kt, kh = _row_strides("k", k)
+    vt, vh = _row_strides("v", v)
+    if ws is None:
+        ws = status_workspace(i)
+    kc, ks, vc, vs = cache
+    rc = load().bsattn_kv4_append(k.data_ptr(), v.data_ptr(), kt, kh, vt, vh, slots.data_ptr(), kc.data_ptr(),
+                                  ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), k_scale, v_scale, T, hkv, pages,
+                                  page, 2 * half, dtype, ws.data_ptr(), ws.numel(), _raw_stream(i))
+    if rc:
+        _check("bsattn_kv4_append", rc)
 
 
 def bsattn_kv4_gather(slots, cache, dtype, k_scale: float = 1.0, v_scale: float = 1.0, ws=None):
     """The rows that slots int64 [T] names, as (k, v) [T, Hkv, d] of `dtype` (negative slots: zeros)."""
-    lib = load()
-    c, pages, hkv, page, d = _kv4(cache)
-    dev = _same_device(slots=slots, **c._asdict())
-    _dtypes(torch.int64, slots=slots)
-    _contiguous(slots=slots)
-    if slots.dim() != 1:
-        raise ValueError("slots must be [T]")
-    with torch.cuda.device(dev):
-        k = torch.empty(slots.numel(), hkv, d, dtype=dtype, device=dev)
-        v = torch.empty_like(k)
-        if ws is None:
-            ws = status_workspace(dev)
-        rc = lib.bsattn_kv4_gather(slots.data_ptr(), *(t.data_ptr() for t in c), float(k_scale), float(v_scale),
-                                   k.data_ptr(), v.data_ptr(), slots.numel(), hkv, pages, page, d,
-                                   _dtype_code(k), ws.data_ptr(), ws.numel(), _stream(dev))
-    _check("bsattn_kv4_gather", rc)
+    i = slots.get_device()
+    pages, hkv, page, half = _kv4(cache, i)
+    if not (slots.dtype is _I64 and slots.dim() == 1 and slots.is_contiguous()):
+        _refuse(("slots", slots, _I64, 1, None))
+    if dtype not in _CODES:
+        raise TypeError(f"bsattn gives fp16 or bf16 rows, not {dtype}")
+    if _current_device() != i:
+        with torch.cuda.device(i):
+            return bsattn_kv4_gather(slots, cache, dtype, k_scale, v_scale, ws)
+    T = slots.numel()
+    k = slots.new_empty((T, hkv, 2 * half), dtype=dtype)
+    v = torch.empty_like(k)
+    if ws is None:
+        ws = status_workspace(i)
+    kc, ks, vc, vs = cache
+    rc = load().bsattn_kv4_gather(slots.data_ptr(), kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(),
+                                  k_scale, v_scale, k.data_ptr(), v.data_ptr(), T, hkv, pages, page, 2 * half,
+                                  _CODES[dtype], ws.data_ptr(), ws.numel(), _raw_stream(i))
+    if rc:
+        _check("bsattn_kv4_gather", rc)
     return k, v
 
 
@@ -590,17 +613,15 @@ def bsattn_decode_kv4_workspace_size(Hq: int, Hkv: int, d: int) -> int:
     return int(load().bsattn_decode_kv4_workspace_size(Hq, Hkv, d))
 
 
-def _decode_args(q, cache_seqlens, block_table, hkv, d):
-    if q.dim() != 3 or q.shape[2] != d:
-        raise ValueError(f"q must be [B, Hq, {d}]")
-    _contiguous(q=q, cache_seqlens=cache_seqlens)
-    _dtypes(torch.int32, cache_seqlens=cache_seqlens)
-    _shape("cache_seqlens", cache_seqlens, (q.shape[0],))
-    if block_table is not None:
-        _contiguous(block_table=block_table)
-        _dtypes(torch.int32, block_table=block_table)
-        if block_table.dim() != 2 or block_table.shape[0] != q.shape[0]:
-            raise ValueError("block_table must be [B, max_pages]")
+_stream_sizes: dict = {}
+
+
+def _stream_workspace(index, purpose, size, Hq, hkv, d):
+    key = (index, purpose, Hq, hkv, d)
+    n = _stream_sizes.get(key)
+    if n is None:
+        n = _stream_sizes[key] = size(Hq, hkv, d)
+    return call_workspace(index, purpose, n)
 
 
 def bsattn_decode_paged_kv4(q, cache, cache_seqlens, block_table, block_indices=None, window: int = 0,
@@ -608,57 +629,81 @@ def bsattn_decode_paged_kv4(q, cache, cache_seqlens, block_table, block_indices=
     """One query token per sequence over a paged 4-bit cache.  q [B,Hq,d] fp16|bf16; cache_seqlens int32
     [B]; block_table int32 [B,max_pages]; block_indices int32 [B,Hkv,max_sel] (-1 = empty) limits each kv
     head to chosen 64-token blocks, window > 0 to the last `window` tokens and the first `sinks`."""
-    lib = load()
-    c, pages, hkv, page, d = _kv4(cache)
-    dev = _same_device(q=q, cache_seqlens=cache_seqlens, block_table=block_table, **c._asdict())
-    _decode_args(q, cache_seqlens, block_table, hkv, d)
-    B, Hq, _ = q.shape
+    i = q.get_device()
+    pages, hkv, page, half = _kv4(cache, i)
+    d = 2 * half
+    dtype = _dtype_code(q)
+    qs = q.shape
+    if not (len(qs) == 3 and qs[2] == d and q.is_contiguous() and cache_seqlens.get_device() == i
+            and block_table.get_device() == i and cache_seqlens.dtype is _I32 and block_table.dtype is _I32
+            and cache_seqlens.shape == qs[:1] and block_table.dim() == 2 and block_table.shape[0] == qs[0]
+            and cache_seqlens.is_contiguous() and block_table.is_contiguous()):
+        _refuse(("q", q, q.dtype, 3, (*qs[:2], d)), ("cache_seqlens", cache_seqlens, _I32, 1, qs[:1]),
+                ("block_table", block_table, _I32, 2, (qs[0], *block_table.shape[1:])))
+    B, Hq, _ = qs
     max_sel, chosen = 0, None
     if block_indices is not None:
-        _same_device(q=q, block_indices=block_indices)
-        _contiguous(block_indices=block_indices)
-        _dtypes(torch.int32, block_indices=block_indices)
-        if block_indices.dim() != 3 or tuple(block_indices.shape[:2]) != (B, hkv):
-            raise ValueError("block_indices must be [B, Hkv, max_sel]")
-        max_sel, chosen = block_indices.shape[2], block_indices.data_ptr()
-        if max_sel == 0:
-            raise ValueError("block_indices has no slots")
-    with torch.cuda.device(dev):
-        out = _out(out, q)
-        _contiguous(out=out)
-        if ws is None:
-            ws = call_workspace(dev, "decode_kv4", bsattn_decode_kv4_workspace_size(Hq, hkv, d))
-        rc = lib.bsattn_decode_paged_kv4(q.data_ptr(), *(t.data_ptr() for t in c), float(k_scale), float(v_scale),
-                                         cache_seqlens.data_ptr(), chosen, block_table.data_ptr(), int(window),
-                                         int(sinks), out.data_ptr(), B, Hq, hkv, pages, page,
-                                         block_table.shape[1], d, max_sel, _dtype_code(q), ws.data_ptr(),
-                                         ws.numel(), _stream(dev))
-    _check("bsattn_decode_paged_kv4", rc)
+        max_sel, chosen = block_indices.shape[-1], block_indices.data_ptr()
+        if not (block_indices.get_device() == i and block_indices.dtype is _I32 and block_indices.is_contiguous()
+                and block_indices.shape == (B, hkv, max_sel) and max_sel > 0):
+            _refuse(("q", q, q.dtype, 3, None), ("block_indices", block_indices, _I32, 3, (B, hkv, max(max_sel, 1))))
+    if _current_device() != i:
+        with torch.cuda.device(i):
+            return bsattn_decode_paged_kv4(q, cache, cache_seqlens, block_table, block_indices, window, sinks,
+                                           k_scale, v_scale, out, ws)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check_out(out, q, True)
+    if ws is None:
+        ws = _stream_workspace(i, "decode_kv4", bsattn_decode_kv4_workspace_size, Hq, hkv, d)
+    kc, ks, vc, vs = cache
+    rc = load().bsattn_decode_paged_kv4(q.data_ptr(), kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(),
+                                        k_scale, v_scale, cache_seqlens.data_ptr(), chosen, block_table.data_ptr(),
+                                        window, sinks, out.data_ptr(), B, Hq, hkv, pages, page,
+                                        block_table.shape[1], d, max_sel, dtype, ws.data_ptr(), ws.numel(),
+                                        _raw_stream(i))
+    if rc:
+        _check("bsattn_decode_paged_kv4", rc)
     return out
+
+
+def _window_args(q, k, v, cache_seqlens):
+    """Checks shared by the two window decodes; (device, dtype code)."""
+    i = q.get_device()
+    dtype = _dtype_code(q)
+    qs, ks = q.shape, k.shape
+    if not (i >= 0 and k.get_device() == i and v.get_device() == i and cache_seqlens.get_device() == i
+            and k.dtype is q.dtype and v.dtype is q.dtype and cache_seqlens.dtype is _I32 and len(qs) == 3
+            and len(ks) == 4 and v.shape == ks and qs[2] == ks[3] and cache_seqlens.shape == qs[:1]
+            and q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and cache_seqlens.is_contiguous()):
+        _refuse(("q", q, q.dtype, 3, None), ("k", k, q.dtype, 4, (*ks[:3], qs[-1])), ("v", v, q.dtype, 4, ks),
+                ("cache_seqlens", cache_seqlens, _I32, 1, qs[:1]))
+    return i, dtype
 
 
 def bsattn_decode_window(q, k, v, cache_seqlens, window: int, sinks: int = 0, out=None, ws=None):
     """One query token per sequence over the last `window` tokens and the first `sinks` of a contiguous
     cache.  q [B,Hq,d]; k/v [B,Smax,Hkv,d] fp16|bf16 CUDA; cache_seqlens int32 [B]."""
-    lib = load()
-    dev = _same_device(q=q, k=k, v=v, cache_seqlens=cache_seqlens)
-    _contiguous(k=k, v=v)
-    if k.dim() != 4 or k.shape[0] != q.shape[0] or k.shape != v.shape:
+    i, dtype = _window_args(q, k, v, cache_seqlens)
+    B, Hq, d = q.shape
+    if k.shape[0] != B:
         raise ValueError("k and v must be [B, Smax, Hkv, d]")
-    if not (q.dtype == k.dtype == v.dtype):
-        raise TypeError("q, k, v must share a dtype")
-    _, Smax, hkv, d = k.shape
-    _decode_args(q, cache_seqlens, None, hkv, d)
-    B, Hq, _ = q.shape
-    with torch.cuda.device(dev):
-        out = _out(out, q)
-        _contiguous(out=out)
-        if ws is None:
-            ws = call_workspace(dev, "decode_window", bsattn_decode_window_workspace_size(Hq, hkv, d))
-        rc = lib.bsattn_decode_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), cache_seqlens.data_ptr(),
-                                      int(window), int(sinks), out.data_ptr(), B, Hq, hkv, Smax, d,
-                                      _dtype_code(q), ws.data_ptr(), ws.numel(), _stream(dev))
-    _check("bsattn_decode_window", rc)
+    if _current_device() != i:
+        with torch.cuda.device(i):
+            return bsattn_decode_window(q, k, v, cache_seqlens, window, sinks, out, ws)
+    _, Smax, hkv, _ = k.shape
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check_out(out, q, True)
+    if ws is None:
+        ws = _stream_workspace(i, "decode_window", bsattn_decode_window_workspace_size, Hq, hkv, d)
+    rc = load().bsattn_decode_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), cache_seqlens.data_ptr(), window,
+                                     sinks, out.data_ptr(), B, Hq, hkv, Smax, d, dtype, ws.data_ptr(), ws.numel(),
+                                     _raw_stream(i))
+    if rc:
+        _check("bsattn_decode_window", rc)
     return out
 
 
@@ -666,55 +711,62 @@ def bsattn_decode_window_paged(q, k_pages, v_pages, cache_seqlens, block_table, 
                                out=None, ws=None):
     """bsattn_decode_window over a paged cache: k_pages/v_pages [num_pages,page_size,Hkv,d]; block_table
     int32 [B,max_pages]."""
-    lib = load()
-    dev = _same_device(q=q, k_pages=k_pages, v_pages=v_pages, cache_seqlens=cache_seqlens,
-                       block_table=block_table)
-    _contiguous(k_pages=k_pages, v_pages=v_pages)
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape:
-        raise ValueError("k_pages and v_pages must be [num_pages, page_size, Hkv, d]")
-    if not (q.dtype == k_pages.dtype == v_pages.dtype):
-        raise TypeError("q, k_pages, v_pages must share a dtype")
-    pages, page, hkv, d = k_pages.shape
-    _decode_args(q, cache_seqlens, block_table, hkv, d)
-    B, Hq, _ = q.shape
-    with torch.cuda.device(dev):
-        out = _out(out, q)
-        _contiguous(out=out)
-        if ws is None:
-            ws = call_workspace(dev, "decode_window", bsattn_decode_window_workspace_size(Hq, hkv, d))
-        rc = lib.bsattn_decode_window_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-                                            cache_seqlens.data_ptr(), block_table.data_ptr(), int(window),
-                                            int(sinks), out.data_ptr(), B, Hq, hkv, pages, page,
-                                            block_table.shape[1], d, _dtype_code(q), ws.data_ptr(), ws.numel(),
-                                            _stream(dev))
-    _check("bsattn_decode_window_paged", rc)
+    i, dtype = _window_args(q, k_pages, v_pages, cache_seqlens)
+    B, Hq, d = q.shape
+    if not (block_table.get_device() == i and block_table.dtype is _I32 and block_table.dim() == 2
+            and block_table.shape[0] == B and block_table.is_contiguous()):
+        _refuse(("q", q, q.dtype, 3, None), ("block_table", block_table, _I32, 2, (B, *block_table.shape[1:])))
+    if _current_device() != i:
+        with torch.cuda.device(i):
+            return bsattn_decode_window_paged(q, k_pages, v_pages, cache_seqlens, block_table, window, sinks, out, ws)
+    pages, page, hkv, _ = k_pages.shape
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check_out(out, q, True)
+    if ws is None:
+        ws = _stream_workspace(i, "decode_window", bsattn_decode_window_workspace_size, Hq, hkv, d)
+    rc = load().bsattn_decode_window_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                                           cache_seqlens.data_ptr(), block_table.data_ptr(), window, sinks,
+                                           out.data_ptr(), B, Hq, hkv, pages, page, block_table.shape[1], d, dtype,
+                                           ws.data_ptr(), ws.numel(), _raw_stream(i))
+    if rc:
+        _check("bsattn_decode_window_paged", rc)
     return out
+
+
+_Strides = ctypes.c_int64 * 12
 
 
 def bsattn_prefill_window(q, k, v, window: int, sinks: int = 0, out=None, ws=None):
     """Causal attention with a sliding window and sinks: query row i (position p = i + Sk - Sq) sees key j
     iff j <= p and (j < sinks or j > p - window).  q [B,Hq,Sq,d], k/v [B,Hkv,Sk,d] fp16|bf16 CUDA views
-    with contiguous channels and 16-byte aligned strides; out: as q laid out, unless given."""
-    lib = load()
-    dev = _same_device(q=q, k=k, v=v)
-    if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape or q.shape[0] != k.shape[0] or q.shape[3] != k.shape[3]:
-        raise ValueError("q must be [B, Hq, Sq, d], k and v [B, Hkv, Sk, d]")
-    if not (q.dtype == k.dtype == v.dtype):
-        raise TypeError("q, k, v must share a dtype")
+    with contiguous channels and 16-byte aligned strides; out: laid out as q is, unless given."""
+    i = q.get_device()
+    dtype = _dtype_code(q)
+    if not (i >= 0 and k.get_device() == i and v.get_device() == i and k.dtype is q.dtype and v.dtype is q.dtype
+            and q.dim() == 4 and k.dim() == 4 and v.shape == k.shape and q.shape[0] == k.shape[0]
+            and q.shape[3] == k.shape[3]):
+        _refuse(("q", q.contiguous(), q.dtype, 4, None),
+                ("k", k.contiguous(), q.dtype, 4, (q.shape[0], *k.shape[1:-1], q.shape[-1])),
+                ("v", v.contiguous(), q.dtype, 4, k.shape))
+    if _current_device() != i:
+        with torch.cuda.device(i):
+            return bsattn_prefill_window(q, k, v, window, sinks, out, ws)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check_out(out, q, False)
     B, Hq, Sq, d = q.shape
-    hkv, Sk = k.shape[1], k.shape[2]
-    with torch.cuda.device(dev):
-        if out is None:
-            out = torch.empty_like(q)
-        out = _out(out, q)
-        for name, t in (("q", q), ("k", k), ("v", v), ("out", out)):
-            if t.numel() and t.stride(3) != 1:
-                raise ValueError(f"{name}'s channels must be contiguous")
-        strides = (ctypes.c_int64 * 12)(*(s for t in (q, k, v, out) for s in t.stride()[:3]))
-        if ws is None:
-            ws = status_workspace(dev)
-        rc = lib.bsattn_prefill_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), int(window), int(sinks),
-                                       out.data_ptr(), B, Hq, hkv, Sq, Sk, d, strides, _dtype_code(q),
-                                       ws.data_ptr(), ws.numel(), _stream(dev))
-    _check("bsattn_prefill_window", rc)
+    _, hkv, Sk, _ = k.shape
+    qs, ks, vs, os_ = q.stride(), k.stride(), v.stride(), out.stride()
+    if (qs[3] != 1 or os_[3] != 1) and q.numel() or (ks[3] != 1 or vs[3] != 1) and k.numel():
+        raise ValueError("channels (the last dimension) must be contiguous")
+    if ws is None:
+        ws = status_workspace(i)
+    rc = load().bsattn_prefill_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), window, sinks, out.data_ptr(), B,
+                                      Hq, hkv, Sq, Sk, d, _Strides(*qs[:3], *ks[:3], *vs[:3], *os_[:3]), dtype,
+                                      ws.data_ptr(), ws.numel(), _raw_stream(i))
+    if rc:
+        _check("bsattn_prefill_window", rc)
     return out

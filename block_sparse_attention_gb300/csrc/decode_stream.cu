@@ -763,8 +763,9 @@ template <int D, bool BF16, bool KV4>
 int launch(const CUtensorMap& tk, const CUtensorMap& tv, const StreamParams& prm, cudaStream_t stream) {
     using R = Ring<D, KV4>;
     auto kern = stream_kernel<D, BF16, KV4>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kBytes) != cudaSuccess)
-        return BSATTN_ERR_CUDA;
+    static std::atomic<unsigned long long> raised{0};
+    const int rc = raise_smem_limit(reinterpret_cast<const void*>(kern), R::kBytes, raised);
+    if (rc) return rc;
     kern<<<static_cast<unsigned>(prm.parts) * prm.Hkv, kThreads, R::kBytes, stream>>>(tk, tv, prm);
     return cudaGetLastError() == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
 }

@@ -244,6 +244,19 @@ int encode_4d(CUtensorMap* map, const void* base, int bf16, const uint64_t (&dim
     return r == CUDA_SUCCESS ? BSATTN_OK : BSATTN_ERR_INVALID_ARG;
 }
 
+int raise_smem_limit(const void* kernel, int bytes, std::atomic<unsigned long long>& done) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return BSATTN_ERR_CUDA;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    if (bit && (done.load(std::memory_order_acquire) & bit)) return BSATTN_OK;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+        cudaGetLastError();
+        return BSATTN_ERR_CUDA;
+    }
+    done.fetch_or(bit, std::memory_order_release);
+    return BSATTN_OK;
+}
+
 int num_sms_of_current_device() {
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;

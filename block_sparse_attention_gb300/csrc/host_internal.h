@@ -1,6 +1,7 @@
 // host_internal.h -- helpers shared by the launchers (not part of the C ABI).
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -23,6 +24,10 @@ int encode_4d(CUtensorMap* map, const void* base, int bf16, const uint64_t (&dim
 
 // SM count of the current device (0 if it cannot be queried).
 int num_sms_of_current_device();
+
+// Raises a kernel's dynamic shared memory limit to `bytes` on the current device, once for each device
+// (`done` is the kernel's own record: a bit a device).  Returns a bsattn_status.
+int raise_smem_limit(const void* kernel, int bytes, std::atomic<unsigned long long>& done);
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -603,8 +603,9 @@ int launch(const void* q, const void* k, const void* v, const int64_t (&st)[12],
     if (!rc) rc = encode_4d(&tv, v, BF16, dk, vs, box);
     if (rc) return rc;
     auto kern = window_kernel<D, BF16>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kBytes) != cudaSuccess)
-        return BSATTN_ERR_CUDA;
+    static std::atomic<unsigned long long> raised{0};
+    rc = raise_smem_limit(reinterpret_cast<const void*>(kern), Cfg<D>::kBytes, raised);
+    if (rc) return rc;
     int sms = num_sms_of_current_device();
     if (sms <= 0) sms = 148;
     const int grid = prm.total_items < sms ? prm.total_items : sms;
