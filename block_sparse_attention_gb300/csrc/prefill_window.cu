@@ -18,11 +18,13 @@
 // below 2^8 and the sum and O share the reference, so nothing is lost.  P is rounded to the input
 // type (the products of kind::f16 take one type); statistics, sums and O are 32-bit.
 //
-// 352 threads:
+// 320 threads:
 //   warps 0-3 / 4-7   softmax and epilogue of query tile 0 / 1 (TMEM lane = row)
-//   warps 8 / 9       issue the products of query tile 0 / 1: S(0), then P V(j) and S(j + 1) in turn.
-//                     One issuer's MMAs run in order, so S(j + 1) may overwrite P(j) without a wait
-//   warp 10           TMA: Q tiles, then K and V tiles through one ring of stages
+//   warp 8            issues all products, in turn P V(j) and S(j + 1) of query tile 0, then of tile 1.
+//                     They run in that order: S(j + 1) may overwrite P(j) without a wait, and the two
+//                     tiles stay half a period apart, one's softmax under the other's products (an issuer
+//                     a tile let them fall in step: 4650 cycles a key tile against 2048 of products)
+//   warp 9            TMA: Q tiles, then K and V tiles through one ring of stages
 // TMEM: S_0 0-127, S_1 128-255, O_0 256.., O_1 256 + d...  Items are dealt out round-robin, last
 // rows first (they see the most keys), so CTAs at work at one time share K/V in L2.  Every wait is
 // bounded: on expiry the CTA records BSATTN_ERR_TIMEOUT, drains what is in flight and leaves.
@@ -38,9 +40,9 @@
 namespace bsattn {
 namespace {
 
-constexpr int kThreads = 352;
-constexpr int kMmaWarp = 8;              // and 9
-constexpr int kLoadWarp = 10;
+constexpr int kThreads = 320;
+constexpr int kMmaWarp = 8;
+constexpr int kLoadWarp = 9;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 256;
 constexpr float kRescaleLog2 = 8.0f;
@@ -52,8 +54,8 @@ struct Cfg {
     static constexpr uint32_t kQ = 0;                            // two query tiles
     static constexpr uint32_t kKV = 2 * kTile;
     static constexpr uint32_t kBars = kKV + kStages * kTile;
-    // q_full[2] q_free[2] full[stages] empty[stages] s_full[2] p_full[2] pv_done[2] o_free[2] fin[2]
-    static constexpr uint32_t kNumBars = 4 + 2 * kStages + 10;
+    // q_full[2] q_free[2] full[stages] empty[stages] s_full[2] p_full[2] pv_done[2] o_free[2] fin
+    static constexpr uint32_t kNumBars = 4 + 2 * kStages + 9;
     static constexpr uint32_t kMisc = kBars + 8 * kNumBars;      // tmem base, abort flag
     static constexpr uint32_t kBytes = 1024 + kMisc + 16;
     static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -251,12 +253,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* q_full = reinterpret_cast<uint64_t*>(sm + C::kBars);   // [2]
     uint64_t* q_free = q_full + 2;                                    // [2]
     uint64_t* full = q_free + 2;                                      // [stages]
-    uint64_t* empty = full + kStages;                                 // [stages] both issuers
+    uint64_t* empty = full + kStages;                                 // [stages]
     uint64_t* s_full = empty + kStages;                               // [2]
     uint64_t* p_full = s_full + 2;                                    // [2] four warps
     uint64_t* pv_done = p_full + 2;                                   // [2]
     uint64_t* o_free = pv_done + 2;                                   // [2] four warps
-    uint64_t* fin = o_free + 2;                                       // [2]
+    uint64_t* fin = o_free + 2;
     int* misc = reinterpret_cast<int*>(sm + C::kMisc);
     volatile int* abort_flag = &misc[1];
     int* status = p.status;
@@ -272,12 +274,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&p_full[x], 4);
             mbar_init(&pv_done[x], 1);
             mbar_init(&o_free[x], 4);
-            mbar_init(&fin[x], 1);
         }
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 2);
+            mbar_init(&empty[s], 1);
         }
+        mbar_init(fin, 1);
         misc[1] = 0;
         fence_barrier_init();
     }
@@ -340,88 +342,81 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp >= kMmaWarp) {
-        // ------------------------------------------------------------ products of query tile x
-        const int x = warp - kMmaWarp;
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------ products
         const bool lead = lane == 0;
         constexpr uint32_t idS = idesc_f16(128, 128, BF16, false);
         constexpr uint32_t idO = idesc_f16(128, D, BF16, true);
-        const uint64_t q_desc = sdesc_sw128(smem_u32(sq + x * C::kTile), 16, 1024);
+        const uint64_t q_desc = sdesc_sw128(smem_u32(sq), 16, 1024);
         const uint64_t k_desc = sdesc_sw128(smem_u32(skv), 16, 1024);
         const uint64_t v_desc = sdesc_sw128(smem_u32(skv), 16384, 1024);
-        const uint32_t ts = tbase + 128 * x, to = tbase + kOCol + D * x;
-        int g = 0;                                       // ring position (K of union tile i: g + 2 i, V: g + 2 i + 1)
-        int blk = 0, items = 0;                          // tiles and items of this query tile so far
+        constexpr uint32_t kTileDesc = C::kTile >> 4;
+        int g = 0;                                       // ring position: K of union tile i at g + 2 i, V after it
+        int blk[2] = {0, 0}, items[2] = {0, 0};          // tiles and items of each query tile so far
         bool ok = true;
         for (int t = blockIdx.x; ok && t < p.total_items; t += gridDim.x) {
             const Item it = item_of(p, t);
-            const Tiles me = x ? it.x[1] : it.x[0];
             const int n = it.count();
-            // V of the tile visited last waits here until its P is written
-            int pend = -1;                               // ring position of that V, or none
-            bool first = true;
-            auto pv = [&]() {
-                const int st = pend % kStages;
-                if (!warp_wait_parity(&full[st], (pend / kStages) & 1, deadline, abort_flag, status) ||
-                    (first && items > 0 && !warp_wait_parity(&o_free[x], (items - 1) & 1, deadline, abort_flag, status)) ||
-                    !warp_wait_parity(&p_full[x], (blk - 1) & 1, deadline, abort_flag, status))
-                    return false;
-                tc_fence_after();
-                const uint64_t b0 = v_desc + static_cast<uint32_t>(st) * (C::kTile >> 4);
+            int done[2] = {0, 0};                        // S issued in this item
+            bool pend[2] = {false, false};               // P of the tile before is awaited
+            // Round i: P V of tile i - 1, S of tile i, for one query tile and then the other.
+            for (int i = 0; ok && i <= n && n > 0; ++i) {
+                const int gk = g + 2 * i, gv = gk - 1;
+                const int tile = i < n ? it.tile(i) : 0;
+                const uint64_t vb = v_desc + static_cast<uint32_t>((gv + kStages) % kStages) * kTileDesc;
+                const uint64_t kb = k_desc + static_cast<uint32_t>(gk % kStages) * kTileDesc;
+                if (i > 0) ok = warp_wait_parity(&full[gv % kStages], (gv / kStages) & 1, deadline, abort_flag, status);
+                if (ok && i < n)
+                    ok = warp_wait_parity(&full[gk % kStages], (gk / kStages) & 1, deadline, abort_flag, status);
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_f16_ts_if(lead, to, ts + 8 * kk, b0 + ((kk * 2048) >> 4), idO, (!first || kk > 0) ? 1u : 0u);
-                mma_commit_if(lead, &empty[st]);
-                mma_commit_if(lead, &pv_done[x]);
-                first = false;
-                pend = -1;
-                return true;
-            };
-            bool any = false;
-            int left = me.count();
-            for (int i = 0; ok && i < n; ++i) {
-                const int gk = g + 2 * i, st = gk % kStages;
-                if ((pend >= 0 && !pv()) ||
-                    !warp_wait_parity(&full[st], (gk / kStages) & 1, deadline, abort_flag, status)) {
-                    ok = false;
-                    break;
-                }
-                if (!me.has(it.tile(i))) {
-                    // not this query tile's: both stages are released unread, once loaded (an arrival
-                    // before that could count for the stage's use before)
-                    const int sv = (gk + 1) % kStages;
-                    mbar_arrive_if(lead, &empty[st]);
-                    if (!warp_wait_parity(&full[sv], ((gk + 1) / kStages) & 1, deadline, abort_flag, status)) {
-                        ok = false;
-                        break;
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t ts = tbase + 128 * x, to = tbase + kOCol + D * x;
+                    if (ok && pend[x]) {
+                        const bool first = done[x] == 1;
+                        if ((first && items[x] > 1 &&
+                             !warp_wait_parity(&o_free[x], items[x] & 1, deadline, abort_flag, status)) ||
+                            !warp_wait_parity(&p_full[x], (blk[x] - 1) & 1, deadline, abort_flag, status)) {
+                            ok = false;
+                        } else {
+                            tc_fence_after();
+#pragma unroll
+                            for (int kk = 0; kk < 8; ++kk)
+                                mma_f16_ts_if(lead, to, ts + 8 * kk, vb + ((kk * 2048) >> 4), idO,
+                                              (!first || kk > 0) ? 1u : 0u);
+                            mma_commit_if(lead, &pv_done[x]);
+                            pend[x] = false;
+                        }
                     }
-                    mbar_arrive_if(lead, &empty[sv]);
-                    continue;
-                }
-                if (!any) {
-                    ok = warp_wait_parity(&q_full[x], items & 1, deadline, abort_flag, status);
-                    if (!ok) break;
-                    any = true;
-                }
-                tc_fence_after();
-                const uint64_t b0 = k_desc + static_cast<uint32_t>(st) * (C::kTile >> 4);
+                    if (ok && i < n && it.x[x].has(tile)) {
+                        if (done[x] == 0) {
+                            ok = warp_wait_parity(&q_full[x], items[x] & 1, deadline, abort_flag, status);
+                            ++items[x];
+                        }
+                        if (ok) {
+                            tc_fence_after();
+                            const uint64_t qb = q_desc + x * kTileDesc;
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-                    mma_f16_ss_if(lead, ts, q_desc + off, b0 + off, idS, kk > 0 ? 1u : 0u);
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+                                mma_f16_ss_if(lead, ts, qb + off, kb + off, idS, kk > 0 ? 1u : 0u);
+                            }
+                            mma_commit_if(lead, &s_full[x]);
+                            pend[x] = true;
+                            ++blk[x];
+                            if (++done[x] == it.x[x].count()) mma_commit_if(lead, &q_free[x]);
+                        }
+                    }
                 }
-                mma_commit_if(lead, &s_full[x]);
-                mma_commit_if(lead, &empty[st]);
-                if (--left == 0) mma_commit_if(lead, &q_free[x]);
-                pend = gk + 1;
-                ++blk;
+                if (ok) {
+                    // both stages of this round are read once everything issued so far is done
+                    if (i > 0) mma_commit_if(lead, &empty[gv % kStages]);
+                    if (i < n) mma_commit_if(lead, &empty[gk % kStages]);
+                }
             }
-            if (ok && pend >= 0) ok = pv();
-            if (any) ++items;
             g += 2 * n;
         }
-        mma_commit_if(lead, &fin[x]);
-        wait_parity_drain(&fin[x], 0, global_timer_ns() + 200000000ull);
+        mma_commit_if(lead, fin);
+        wait_parity_drain(fin, 0, global_timer_ns() + 200000000ull);
         __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax of query tile x
@@ -461,12 +456,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_wait_ld();
                 const bool edge = key0 + 127 > pos || (key0 < lo && key0 + 128 > p.sinks);
                 if (__any_sync(0xffffffffu, edge)) {
+                    // 32 keys at a time, as most of them are visible to all of a warp's rows or to none
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
-                        // bit e: key k0 + e is visible
                         const int k0 = key0 + 32 * h;
                         auto below = [](int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u); };
+                        // bit e: key k0 + e is visible
                         const uint32_t on = below(pos + 1 - k0) & (~below(lo - k0) | below(p.sinks - k0));
+                        if (__all_sync(0xffffffffu, on == 0xffffffffu)) continue;
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             if (!((on >> e) & 1u)) s[32 * h + e] = -INFINITY;
