@@ -54,7 +54,7 @@ struct Cfg {
     static constexpr uint32_t kQ = 0;                            // two query tiles
     static constexpr uint32_t kKV = 2 * kTile;
     static constexpr uint32_t kBars = kKV + kStages * kTile;
-    // q_full[2] q_free[2] full[stages] empty[stages] s_full[2] p_full[2] pv_done[2] o_free[2] fin
+    // q_full[2] q_free[2] full[stages] empty[stages] s_full[2] p_full[2] o_full[2] o_free[2] fin
     static constexpr uint32_t kNumBars = 4 + 2 * kStages + 9;
     static constexpr uint32_t kMisc = kBars + 8 * kNumBars;      // tmem base, abort flag
     static constexpr uint32_t kBytes = 1024 + kMisc + 16;
@@ -256,8 +256,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* empty = full + kStages;                                 // [stages]
     uint64_t* s_full = empty + kStages;                               // [2]
     uint64_t* p_full = s_full + 2;                                    // [2] four warps
-    uint64_t* pv_done = p_full + 2;                                   // [2]
-    uint64_t* o_free = pv_done + 2;                                   // [2] four warps
+    uint64_t* o_full = p_full + 2;                                    // [2] an item's last P V
+    uint64_t* o_free = o_full + 2;                                    // [2] four warps
     uint64_t* fin = o_free + 2;
     int* misc = reinterpret_cast<int*>(sm + C::kMisc);
     volatile int* abort_flag = &misc[1];
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&q_free[x], 1);
             mbar_init(&s_full[x], 1);
             mbar_init(&p_full[x], 4);
-            mbar_init(&pv_done[x], 1);
+            mbar_init(&o_full[x], 1);
             mbar_init(&o_free[x], 4);
         }
         for (int s = 0; s < kStages; ++s) {
@@ -359,7 +359,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int n = it.count();
             int done[2] = {0, 0};                        // S issued in this item
             bool pend[2] = {false, false};               // P of the tile before is awaited
-            // Round i: P V of tile i - 1, S of tile i, for one query tile and then the other.
+            // Round i: P V of tile i - 1, S of tile i, for one query tile and then the other.  A commit takes
+            // its turn among the products (some 200 cycles), so there is only S's: the softmax warps pass
+            // on what it says about the stages, Q and O.
             for (int i = 0; ok && i <= n && n > 0; ++i) {
                 const int gk = g + 2 * i, gv = gk - 1;
                 const int tile = i < n ? it.tile(i) : 0;
@@ -383,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int kk = 0; kk < 8; ++kk)
                                 mma_f16_ts_if(lead, to, ts + 8 * kk, vb + ((kk * 2048) >> 4), idO,
                                               (!first || kk > 0) ? 1u : 0u);
-                            mma_commit_if(lead, &pv_done[x]);
+                            if (done[x] == it.x[x].count()) mma_commit_if(lead, &o_full[x]);
                             pend[x] = false;
                         }
                     }
@@ -403,14 +405,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mma_commit_if(lead, &s_full[x]);
                             pend[x] = true;
                             ++blk[x];
-                            if (++done[x] == it.x[x].count()) mma_commit_if(lead, &q_free[x]);
+                            ++done[x];
                         }
                     }
-                }
-                if (ok) {
-                    // both stages of this round are read once everything issued so far is done
-                    if (i > 0) mma_commit_if(lead, &empty[gv % kStages]);
-                    if (i < n) mma_commit_if(lead, &empty[gk % kStages]);
                 }
             }
             g += 2 * n;
@@ -425,17 +422,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t ts = tbase + lanes + 128 * x, to = tbase + lanes + kOCol + D * x;
         const float c = p.scale_log2;
-        int blk = 0;
+        int blk = 0, items = 0, g = 0;
         bool ok = true;
         for (int t = blockIdx.x; ok && t < p.total_items; t += gridDim.x) {
             const Item it = item_of(p, t);
             const Tiles me = x ? it.x[1] : it.x[0];
-            if (me.qb >= p.nq) continue;                 // the odd row block's missing partner
             const int n = me.count();
+            const int g0 = g;                            // ring position of the item's first K tile
+            g += 2 * it.count();
+            // S of a tile is there: its K tile has been read by this query tile, and V of the tile before.
+            // Tile 1's products come last in a round, so it gives the stages back, or tile 0 where tile 1
+            // does not visit the tile.
+            int v_read = -1;                             // stage of the V tile read next, if it is ours to give back
+            auto give_back = [&](int tile, bool last) {
+                if (v_read >= 0) mbar_arrive(&empty[v_read]);
+                v_read = -1;
+                if (x == 1 || !it.x[1].has(tile)) {
+                    const int at = g0 + 2 * (tile < it.sink ? tile : it.sink + tile - it.lo);
+                    mbar_arrive(&empty[at % kStages]);
+                    v_read = (at + 1) % kStages;
+                }
+                if (last) mbar_arrive(&q_free[x]);
+            };
             const int row = me.qb * 128 + lrow;
             const int pos = row + p.Sk - p.Sq;
             T* out = reinterpret_cast<T*>(p.out) + it.b * p.out_b + me.head * p.out_h + row * p.out_s;
             if (n == 0) {
+                // no key, or (the partner of an odd last row block) no row
                 if (row < p.Sq)
                     for (int e = 0; e < D / 8; ++e) reinterpret_cast<uint4*>(out)[e] = make_uint4(0, 0, 0, 0);
                 continue;
@@ -444,12 +457,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int lo = pos >= p.window ? pos - p.window + 1 : 0;
             float m_used = -INFINITY, l = 0.f;
             for (int i = 0; i < n; ++i, ++blk) {
-                const int key0 = 128 * (i < me.sink ? i : me.lo + (i - me.sink));
+                const int tile = i < me.sink ? i : me.lo + (i - me.sink);
+                const int key0 = 128 * tile;
                 if (!warp_wait_parity(&s_full[x], blk & 1, deadline, abort_flag, status)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
+                if ((warp & 3) == 0 && lane == 0) give_back(tile, i == n - 1);
+                __syncwarp();
                 float s[128];
 #pragma unroll
                 for (int h = 0; h < 4; ++h) tmem_ld_row32(ts + 32 * h, reinterpret_cast<uint32_t*>(s) + 32 * h);
@@ -505,12 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float2 a2 = add2f(add2f(acc[0], acc[1]), add2f(acc[2], acc[3]));
                 l = l * alpha + (a2.x + a2.y);
                 if (__any_sync(0xffffffffu, rescale)) {
-                    // O is complete up to the tile before this one
-                    if (!warp_wait_parity(&pv_done[x], (blk - 1) & 1, deadline, abort_flag, status)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
+                    // O holds every tile before this one: their P V ran before this tile's S
 #pragma unroll 1
                     for (int c0 = 0; c0 < D; c0 += 32) {
                         uint32_t o[32];
@@ -528,11 +539,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
             // ---- O / l to memory
-            if (!warp_wait_parity(&pv_done[x], (blk - 1) & 1, deadline, abort_flag, status)) {
+            if (!warp_wait_parity(&o_full[x], items & 1, deadline, abort_flag, status)) {
                 ok = false;
                 break;
             }
+            ++items;
             tc_fence_after();
+            if ((warp & 3) == 0 && lane == 0 && v_read >= 0) mbar_arrive(&empty[v_read]);
+            __syncwarp();
             const float inv = l == 0.f ? 0.f : 1.f / l;         // NaN stays NaN
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
