@@ -18,13 +18,14 @@
 // below 2^8 and the sum and O share the reference, so nothing is lost.  P is rounded to the input
 // type (the products of kind::f16 take one type); statistics, sums and O are 32-bit.
 //
-// 320 threads:
+// 352 threads:
 //   warps 0-3 / 4-7   softmax and epilogue of query tile 0 / 1 (TMEM lane = row)
-//   warp 8            issues all products, in turn P V(j) and S(j + 1) of query tile 0, then of tile 1.
-//                     They run in that order: S(j + 1) may overwrite P(j) without a wait, and the two
-//                     tiles stay half a period apart, one's softmax under the other's products (an issuer
-//                     a tile let them fall in step: 4650 cycles a key tile against 2048 of products)
-//   warp 9            TMA: Q tiles, then K and V tiles through one ring of stages
+//   warps 8 / 9       issue the products of query tile 0 / 1, P V(j) and S(j + 1) in turn.  One issuer's
+//                     products run in order: S(j + 1) may overwrite P(j) without a wait
+//   warp 10           TMA: Q tiles, then K and V tiles through one ring of stages
+// The two issuers take turns, a P V and an S each, which keeps the query tiles half a period apart, one's
+// softmax under the other's products; left alone they fall into step and stay there (4500 cycles a round).
+// All other waits of an issuer lie before its turn, where they overlap the other's products.
 // TMEM: S_0 0-127, S_1 128-255, O_0 256.., O_1 256 + d...  Items are dealt out round-robin, last
 // rows first (they see the most keys), so CTAs at work at one time share K/V in L2.  Every wait is
 // bounded: on expiry the CTA records BSATTN_ERR_TIMEOUT, drains what is in flight and leaves.
@@ -40,9 +41,9 @@
 namespace bsattn {
 namespace {
 
-constexpr int kThreads = 320;
-constexpr int kMmaWarp = 8;
-constexpr int kLoadWarp = 9;
+constexpr int kThreads = 352;
+constexpr int kMmaWarp = 8;              // and 9
+constexpr int kLoadWarp = 10;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 256;
 constexpr float kRescaleLog2 = 8.0f;
@@ -54,8 +55,8 @@ struct Cfg {
     static constexpr uint32_t kQ = 0;                            // two query tiles
     static constexpr uint32_t kKV = 2 * kTile;
     static constexpr uint32_t kBars = kKV + kStages * kTile;
-    // q_full[2] q_free[2] full[stages] empty[stages] s_full[2] p_full[2] o_full[2] o_free[2] fin
-    static constexpr uint32_t kNumBars = 4 + 2 * kStages + 9;
+    // q_full[2] q_free[2] full[stages] empty[stages] s_full[2] p_full[2] o_full[2] o_free[2] fin[2] turn[2]
+    static constexpr uint32_t kNumBars = 4 + 2 * kStages + 12;
     static constexpr uint32_t kMisc = kBars + 8 * kNumBars;      // tmem base, abort flag
     static constexpr uint32_t kBytes = 1024 + kMisc + 16;
     static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -253,12 +254,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* q_full = reinterpret_cast<uint64_t*>(sm + C::kBars);   // [2]
     uint64_t* q_free = q_full + 2;                                    // [2]
     uint64_t* full = q_free + 2;                                      // [stages]
-    uint64_t* empty = full + kStages;                                 // [stages]
+    uint64_t* empty = full + kStages;                                 // [stages] both query tiles
     uint64_t* s_full = empty + kStages;                               // [2]
     uint64_t* p_full = s_full + 2;                                    // [2] four warps
     uint64_t* o_full = p_full + 2;                                    // [2] an item's last P V
     uint64_t* o_free = o_full + 2;                                    // [2] four warps
-    uint64_t* fin = o_free + 2;
+    uint64_t* fin = o_free + 2;                                       // [2]
+    uint64_t* turn = fin + 2;                                         // [2] the other has issued
     int* misc = reinterpret_cast<int*>(sm + C::kMisc);
     volatile int* abort_flag = &misc[1];
     int* status = p.status;
@@ -274,12 +276,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&p_full[x], 4);
             mbar_init(&o_full[x], 1);
             mbar_init(&o_free[x], 4);
+            mbar_init(&fin[x], 1);
+            mbar_init(&turn[x], 1);
         }
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&empty[s], 2);
         }
-        mbar_init(fin, 1);
         misc[1] = 0;
         fence_barrier_init();
     }
@@ -342,78 +345,83 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp == kMmaWarp) {
-        // ------------------------------------------------------------ products
+    } else if (warp >= kMmaWarp) {
+        // ------------------------------------------------------------ products of query tile x
+        const int x = warp - kMmaWarp;
         const bool lead = lane == 0;
         constexpr uint32_t idS = idesc_f16(128, 128, BF16, false);
         constexpr uint32_t idO = idesc_f16(128, D, BF16, true);
-        const uint64_t q_desc = sdesc_sw128(smem_u32(sq), 16, 1024);
+        const uint64_t q_desc = sdesc_sw128(smem_u32(sq + x * C::kTile), 16, 1024);
         const uint64_t k_desc = sdesc_sw128(smem_u32(skv), 16, 1024);
         const uint64_t v_desc = sdesc_sw128(smem_u32(skv), 16384, 1024);
         constexpr uint32_t kTileDesc = C::kTile >> 4;
+        const uint32_t ts = tbase + 128 * x, to = tbase + kOCol + D * x;
         int g = 0;                                       // ring position: K of union tile i at g + 2 i, V after it
-        int blk[2] = {0, 0}, items[2] = {0, 0};          // tiles and items of each query tile so far
+        int blk = 0, items = 0, rounds = 0;              // tiles, items and rounds of this query tile so far
         bool ok = true;
         for (int t = blockIdx.x; ok && t < p.total_items; t += gridDim.x) {
             const Item it = item_of(p, t);
-            const int n = it.count();
-            int done[2] = {0, 0};                        // S issued in this item
-            bool pend[2] = {false, false};               // P of the tile before is awaited
-            // Round i: P V of tile i - 1, S of tile i, for one query tile and then the other.  A commit takes
-            // its turn among the products (some 200 cycles), so there is only S's: the softmax warps pass
-            // on what it says about the stages, Q and O.
+            const Tiles me = x ? it.x[1] : it.x[0];
+            const int n = it.count(), mine = me.count();
+            int done = 0;                                // S issued in this item
+            int pend = -1;                               // ring position of the V that awaits its P
+            // Round i: P V of the tile before, S of tile i.  A commit takes its turn among the products, so
+            // there is only S's and the last P V's: the softmax warps pass on what it says about the stages
+            // and Q.
+            // Every stage is waited for in turn, visited or not: a parity tells two of its uses apart, no more.
             for (int i = 0; ok && i <= n && n > 0; ++i) {
-                const int gk = g + 2 * i, gv = gk - 1;
-                const int tile = i < n ? it.tile(i) : 0;
-                const uint64_t vb = v_desc + static_cast<uint32_t>((gv + kStages) % kStages) * kTileDesc;
-                const uint64_t kb = k_desc + static_cast<uint32_t>(gk % kStages) * kTileDesc;
-                if (i > 0) ok = warp_wait_parity(&full[gv % kStages], (gv / kStages) & 1, deadline, abort_flag, status);
-                if (ok && i < n)
-                    ok = warp_wait_parity(&full[gk % kStages], (gk / kStages) & 1, deadline, abort_flag, status);
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const uint32_t ts = tbase + 128 * x, to = tbase + kOCol + D * x;
-                    if (ok && pend[x]) {
-                        const bool first = done[x] == 1;
-                        if ((first && items[x] > 1 &&
-                             !warp_wait_parity(&o_free[x], items[x] & 1, deadline, abort_flag, status)) ||
-                            !warp_wait_parity(&p_full[x], (blk[x] - 1) & 1, deadline, abort_flag, status)) {
-                            ok = false;
-                        } else {
-                            tc_fence_after();
-#pragma unroll
-                            for (int kk = 0; kk < 8; ++kk)
-                                mma_f16_ts_if(lead, to, ts + 8 * kk, vb + ((kk * 2048) >> 4), idO,
-                                              (!first || kk > 0) ? 1u : 0u);
-                            if (done[x] == it.x[x].count()) mma_commit_if(lead, &o_full[x]);
-                            pend[x] = false;
-                        }
-                    }
-                    if (ok && i < n && it.x[x].has(tile)) {
-                        if (done[x] == 0) {
-                            ok = warp_wait_parity(&q_full[x], items[x] & 1, deadline, abort_flag, status);
-                            ++items[x];
-                        }
-                        if (ok) {
-                            tc_fence_after();
-                            const uint64_t qb = q_desc + x * kTileDesc;
-#pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk) {
-                                const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-                                mma_f16_ss_if(lead, ts, qb + off, kb + off, idS, kk > 0 ? 1u : 0u);
-                            }
-                            mma_commit_if(lead, &s_full[x]);
-                            pend[x] = true;
-                            ++blk[x];
-                            ++done[x];
-                        }
+                const int gk = g + 2 * i, sk = gk % kStages;
+                const bool visit = i < n && me.has(it.tile(i));
+                if (i > 0)
+                    ok = warp_wait_parity(&full[(gk - 1) % kStages], ((gk - 1) / kStages) & 1, deadline, abort_flag, status);
+                if (ok && i < n) ok = warp_wait_parity(&full[sk], (gk / kStages) & 1, deadline, abort_flag, status);
+                if (!ok) break;
+                if (pend >= 0) {
+                    if ((done == 1 && items > 1 &&
+                         !warp_wait_parity(&o_free[x], items & 1, deadline, abort_flag, status)) ||
+                        !warp_wait_parity(&p_full[x], (blk - 1) & 1, deadline, abort_flag, status)) {
+                        ok = false;
+                        break;
                     }
                 }
+                // tile 0's round comes after tile 1's round before, tile 1's after tile 0's
+                if (rounds + x > 0 && !warp_wait_parity(&turn[x], (rounds + x + 1) & 1, deadline, abort_flag, status)) {
+                    ok = false;
+                    break;
+                }
+                ++rounds;
+                tc_fence_after();
+                if (pend >= 0) {
+                    const uint64_t vb = v_desc + static_cast<uint32_t>(pend % kStages) * kTileDesc;
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        mma_f16_ts_if(lead, to, ts + 8 * kk, vb + ((kk * 2048) >> 4), idO, (done > 1 || kk > 0) ? 1u : 0u);
+                    if (done == mine) mma_commit_if(lead, &o_full[x]);
+                    pend = -1;
+                }
+                if (visit) {
+                    if (done == 0) {
+                        ok = warp_wait_parity(&q_full[x], items & 1, deadline, abort_flag, status);
+                        if (!ok) break;
+                        ++items;
+                    }
+                    const uint64_t kb = k_desc + static_cast<uint32_t>(sk) * kTileDesc;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+                        mma_f16_ss_if(lead, ts, q_desc + off, kb + off, idS, kk > 0 ? 1u : 0u);
+                    }
+                    mma_commit_if(lead, &s_full[x]);
+                    pend = gk + 1;
+                    ++blk;
+                    ++done;
+                }
+                mbar_arrive_if(lead, &turn[1 - x]);
             }
             g += 2 * n;
         }
-        mma_commit_if(lead, fin);
-        wait_parity_drain(fin, 0, global_timer_ns() + 200000000ull);
+        mma_commit_if(lead, &fin[x]);
+        wait_parity_drain(&fin[x], 0, global_timer_ns() + 200000000ull);
         __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax of query tile x
@@ -430,20 +438,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int n = me.count();
             const int g0 = g;                            // ring position of the item's first K tile
             g += 2 * it.count();
-            // S of a tile is there: its K tile has been read by this query tile, and V of the tile before.
-            // Tile 1's products come last in a round, so it gives the stages back, or tile 0 where tile 1
-            // does not visit the tile.
-            int v_read = -1;                             // stage of the V tile read next, if it is ours to give back
-            auto give_back = [&](int tile, bool last) {
-                if (v_read >= 0) mbar_arrive(&empty[v_read]);
-                v_read = -1;
-                if (x == 1 || !it.x[1].has(tile)) {
-                    const int at = g0 + 2 * (tile < it.sink ? tile : it.sink + tile - it.lo);
-                    mbar_arrive(&empty[at % kStages]);
-                    v_read = (at + 1) % kStages;
+            // Both query tiles give every stage back.  One that this tile does not visit goes back unread, but
+            // only once it is loaded: an arrival before that could count for the stage's use before.
+            const bool speaks = (warp & 3) == 0 && lane == 0;
+            auto skip_to = [&](int i, int& next) {
+                for (; next < i; ++next) {
+                    const int at = g0 + 2 * next;
+                    for (int j = at; j < at + 2; ++j) {
+                        if (!wait_parity(&full[j % kStages], (j / kStages) & 1, deadline, abort_flag, status)) return;
+                        mbar_arrive(&empty[j % kStages]);
+                    }
                 }
-                if (last) mbar_arrive(&q_free[x]);
             };
+            const int n_union = it.count();
+            int next = 0;                                // union tile this query tile has not dealt with yet
+            int v_read = -1;                             // stage of the V tile to give back when it is read
             const int row = me.qb * 128 + lrow;
             const int pos = row + p.Sk - p.Sq;
             T* out = reinterpret_cast<T*>(p.out) + it.b * p.out_b + me.head * p.out_h + row * p.out_s;
@@ -451,6 +460,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // no key, or (the partner of an odd last row block) no row
                 if (row < p.Sq)
                     for (int e = 0; e < D / 8; ++e) reinterpret_cast<uint4*>(out)[e] = make_uint4(0, 0, 0, 0);
+                if (speaks) skip_to(n_union, next);
+                __syncwarp();
                 continue;
             }
             // keys [lo, pos] and, below lo, those before the sinks
@@ -459,12 +470,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < n; ++i, ++blk) {
                 const int tile = i < me.sink ? i : me.lo + (i - me.sink);
                 const int key0 = 128 * tile;
+                const int u = tile < it.sink ? tile : it.sink + tile - it.lo;
+                if (speaks) skip_to(u, next);
+                __syncwarp();
                 if (!warp_wait_parity(&s_full[x], blk & 1, deadline, abort_flag, status)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                if ((warp & 3) == 0 && lane == 0) give_back(tile, i == n - 1);
+                if (speaks) {
+                    // S of this tile is there: its K tile has been read, and V of the tile before
+                    if (v_read >= 0) mbar_arrive(&empty[v_read]);
+                    const int at = g0 + 2 * u;
+                    mbar_arrive(&empty[at % kStages]);
+                    v_read = (at + 1) % kStages;
+                    next = u + 1;
+                    if (i == n - 1) mbar_arrive(&q_free[x]);
+                }
                 __syncwarp();
                 float s[128];
 #pragma unroll
@@ -545,7 +567,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ++items;
             tc_fence_after();
-            if ((warp & 3) == 0 && lane == 0 && v_read >= 0) mbar_arrive(&empty[v_read]);
+            if (speaks) {
+                mbar_arrive(&empty[v_read]);
+                skip_to(n_union, next);
+            }
             __syncwarp();
             const float inv = l == 0.f ? 0.f : 1.f / l;         // NaN stays NaN
 #pragma unroll 1
