@@ -163,6 +163,15 @@ __device__ __forceinline__ void tmem_st_row16(uint32_t taddr, const uint32_t* r)
         : "memory");
 }
 
+// A value that is the same in all lanes, in a form the compiler knows to be so: descriptors and TMEM
+// addresses made from it stay in uniform registers.  An MMA then takes one issue slot or two instead of a
+// dozen, which decides its rate when the softmax warps contend for the slots: 64 cycles an M128 N128 K16
+// MMA against 71 alone and 110 beside a warp that issues every cycle.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ uint64_t uniform(uint64_t v) {
+    return static_cast<uint64_t>(uniform(static_cast<uint32_t>(v >> 32))) << 32 | uniform(static_cast<uint32_t>(v));
+}
+
 // D[tmem] (+)= A[tmem] * B[smem], kind::f16, by one lane of a converged warp under a guard predicate.
 __device__ __forceinline__ void mma_f16_ts_if(bool lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                               uint32_t idesc, uint32_t accumulate) {
@@ -347,15 +356,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp >= kMmaWarp) {
         // ------------------------------------------------------------ products of query tile x
-        const int x = warp - kMmaWarp;
-        const bool lead = lane == 0;
+        const int x = static_cast<int>(uniform(static_cast<uint32_t>(warp - kMmaWarp)));
+        const bool lead = elect_one_sync();
         constexpr uint32_t idS = idesc_f16(128, 128, BF16, false);
         constexpr uint32_t idO = idesc_f16(128, D, BF16, true);
-        const uint64_t q_desc = sdesc_sw128(smem_u32(sq + x * C::kTile), 16, 1024);
+        const uint64_t q_desc = uniform(sdesc_sw128(smem_u32(sq + x * C::kTile), 16, 1024));
         const uint64_t k_desc = sdesc_sw128(smem_u32(skv), 16, 1024);
         const uint64_t v_desc = sdesc_sw128(smem_u32(skv), 16384, 1024);
         constexpr uint32_t kTileDesc = C::kTile >> 4;
-        const uint32_t ts = tbase + 128 * x, to = tbase + kOCol + D * x;
+        const uint32_t ts = uniform(tbase + 128 * x), to = uniform(tbase + kOCol + D * x);
         int g = 0;                                       // ring position: K of union tile i at g + 2 i, V after it
         int blk = 0, items = 0, rounds = 0;              // tiles, items and rounds of this query tile so far
         bool ok = true;
@@ -392,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++rounds;
                 tc_fence_after();
                 if (pend >= 0) {
-                    const uint64_t vb = v_desc + static_cast<uint32_t>(pend % kStages) * kTileDesc;
+                    const uint64_t vb = uniform(v_desc + static_cast<uint32_t>(pend % kStages) * kTileDesc);
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
                         mma_f16_ts_if(lead, to, ts + 8 * kk, vb + ((kk * 2048) >> 4), idO, (done > 1 || kk > 0) ? 1u : 0u);
@@ -405,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!ok) break;
                         ++items;
                     }
-                    const uint64_t kb = k_desc + static_cast<uint32_t>(sk) * kTileDesc;
+                    const uint64_t kb = uniform(k_desc + static_cast<uint32_t>(sk) * kTileDesc);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
