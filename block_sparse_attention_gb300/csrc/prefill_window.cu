@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Tiles me = x ? it.x[1] : it.x[0];
             const int n = it.count(), mine = me.count();
             int done = 0;                                // S issued in this item
-            int pend = -1;                               // ring position of the V that awaits its P
+            bool pend = false;                           // the tile before awaits its P V
             // Round i: P V of the tile before, S of tile i.  A commit takes its turn among the products, so
             // there is only S's and the last P V's: the softmax warps pass on what it says about the stages
             // and Q.
@@ -385,13 +385,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = warp_wait_parity(&full[(gk - 1) % kStages], ((gk - 1) / kStages) & 1, deadline, abort_flag, status);
                 if (ok && i < n) ok = warp_wait_parity(&full[sk], (gk / kStages) & 1, deadline, abort_flag, status);
                 if (!ok) break;
-                if (pend >= 0) {
-                    if ((done == 1 && items > 1 &&
-                         !warp_wait_parity(&o_free[x], items & 1, deadline, abort_flag, status)) ||
-                        !warp_wait_parity(&p_full[x], (blk - 1) & 1, deadline, abort_flag, status)) {
+                const uint64_t vb = uniform(v_desc + static_cast<uint32_t>((gk + kStages - 1) % kStages) * kTileDesc);
+                const uint64_t kb = uniform(k_desc + static_cast<uint32_t>(sk) * kTileDesc);
+                if (visit && done == 0) {
+                    if (!warp_wait_parity(&q_full[x], items & 1, deadline, abort_flag, status)) {
                         ok = false;
                         break;
                     }
+                    ++items;
                 }
                 // tile 0's round comes after tile 1's round before, tile 1's after tile 0's
                 if (rounds + x > 0 && !warp_wait_parity(&turn[x], (rounds + x + 1) & 1, deadline, abort_flag, status)) {
@@ -399,29 +400,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 ++rounds;
+                if (pend) {
+                    if ((done == 1 && items > 1 &&
+                         !warp_wait_parity(&o_free[x], items & 1, deadline, abort_flag, status)) ||
+                        !warp_wait_parity(&p_full[x], (blk - 1) & 1, deadline, abort_flag, status)) {
+                        ok = false;
+                        break;
+                    }
+                }
                 tc_fence_after();
-                if (pend >= 0) {
-                    const uint64_t vb = uniform(v_desc + static_cast<uint32_t>(pend % kStages) * kTileDesc);
+                if (pend) {
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
                         mma_f16_ts_if(lead, to, ts + 8 * kk, vb + ((kk * 2048) >> 4), idO, (done > 1 || kk > 0) ? 1u : 0u);
                     if (done == mine) mma_commit_if(lead, &o_full[x]);
-                    pend = -1;
+                    pend = false;
                 }
                 if (visit) {
-                    if (done == 0) {
-                        ok = warp_wait_parity(&q_full[x], items & 1, deadline, abort_flag, status);
-                        if (!ok) break;
-                        ++items;
-                    }
-                    const uint64_t kb = uniform(k_desc + static_cast<uint32_t>(sk) * kTileDesc);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
                         mma_f16_ss_if(lead, ts, q_desc + off, kb + off, idS, kk > 0 ? 1u : 0u);
                     }
                     mma_commit_if(lead, &s_full[x]);
-                    pend = gk + 1;
+                    pend = true;
                     ++blk;
                     ++done;
                 }
