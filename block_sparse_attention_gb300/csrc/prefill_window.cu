@@ -18,14 +18,15 @@
 // below 2^8 and the sum and O share the reference, so nothing is lost.  P is rounded to the input
 // type (the products of kind::f16 take one type); statistics, sums and O are 32-bit.
 //
-// 352 threads:
+// 384 threads:
 //   warps 0-3 / 4-7   softmax and epilogue of query tile 0 / 1 (TMEM lane = row)
 //   warps 8 / 9       issue the products of query tile 0 / 1, P V(j) and S(j + 1) in turn.  One issuer's
 //                     products run in order: S(j + 1) may overwrite P(j) without a wait
-//   warp 10           TMA: Q tiles, then K and V tiles through one ring of stages
+//   warp 10           TMA: Q tiles, then K and V tiles through one ring of stages (warp 11 idles)
+// P is handed over in two halves of 64 keys, so that half of P V runs under the rest of the softmax.
 // The two issuers take turns, a P V and an S each, which keeps the query tiles half a period apart, one's
 // softmax under the other's products; left alone they fall into step and stay there (4500 cycles a round).
-// All other waits of an issuer lie before its turn, where they overlap the other's products.
+// All other waits of an issuer come before the one for P, where they overlap the softmax.
 // TMEM: S_0 0-127, S_1 128-255, O_0 256.., O_1 256 + d...  Items are dealt out round-robin, last
 // rows first (they see the most keys), so CTAs at work at one time share K/V in L2.  Every wait is
 // bounded: on expiry the CTA records BSATTN_ERR_TIMEOUT, drains what is in flight and leaves.
@@ -41,9 +42,10 @@
 namespace bsattn {
 namespace {
 
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;
 constexpr int kMmaWarp = 8;              // and 9
 constexpr int kLoadWarp = 10;
+constexpr int kRegsSoftmax = 208, kRegsOther = 88;       // registers a thread: two warpgroups, and the third
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 256;
 constexpr float kRescaleLog2 = 8.0f;
@@ -55,8 +57,8 @@ struct Cfg {
     static constexpr uint32_t kQ = 0;                            // two query tiles
     static constexpr uint32_t kKV = 2 * kTile;
     static constexpr uint32_t kBars = kKV + kStages * kTile;
-    // q_full[2] q_free[2] full[stages] empty[stages] s_full[2] p_full[2] o_full[2] o_free[2] fin[2] turn[2]
-    static constexpr uint32_t kNumBars = 4 + 2 * kStages + 12;
+    // q_full[2] q_free[2] full[stages] empty[stages] s_full[2] p_half[2] p_full[2] o_full[2] o_free[2] fin[2] turn[2]
+    static constexpr uint32_t kNumBars = 4 + 2 * kStages + 14;
     static constexpr uint32_t kMisc = kBars + 8 * kNumBars;      // tmem base, abort flag
     static constexpr uint32_t kBytes = 1024 + kMisc + 16;
     static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -265,7 +267,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* full = q_free + 2;                                      // [stages]
     uint64_t* empty = full + kStages;                                 // [stages] both query tiles
     uint64_t* s_full = empty + kStages;                               // [2]
-    uint64_t* p_full = s_full + 2;                                    // [2] four warps
+    uint64_t* p_half = s_full + 2;                                    // [2] four warps: P of the first 64 keys
+    uint64_t* p_full = p_half + 2;                                    // [2] four warps
     uint64_t* o_full = p_full + 2;                                    // [2] an item's last P V
     uint64_t* o_free = o_full + 2;                                    // [2] four warps
     uint64_t* fin = o_free + 2;                                       // [2]
@@ -282,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&q_full[x], 1);
             mbar_init(&q_free[x], 1);
             mbar_init(&s_full[x], 1);
+            mbar_init(&p_half[x], 4);
             mbar_init(&p_full[x], 4);
             mbar_init(&o_full[x], 1);
             mbar_init(&o_free[x], 4);
@@ -304,137 +308,152 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tbase = static_cast<uint32_t>(misc[0]);
 
-    if (warp == kLoadWarp) {
-        // ------------------------------------------------------------ TMA
-        if (lane == 0) {
-            tma_prefetch_desc(&tm_q);
-            tma_prefetch_desc(&tm_k);
-            tma_prefetch_desc(&tm_v);
-            int g = 0;                                   // tiles loaded, K and V counted apart
-            int nq[2] = {0, 0};                          // Q tiles loaded
+    // The softmax keeps a row of 128 scores a thread: its two warpgroups take 208 of the registers that the
+    // launch gave, the third is left 88.  (launch() has checked that the launch gave that many.)
+    if (warp >= kMmaWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+        if (warp == kLoadWarp) {
+            // ------------------------------------------------------------ TMA
+            if (lane == 0) {
+                tma_prefetch_desc(&tm_q);
+                tma_prefetch_desc(&tm_k);
+                tma_prefetch_desc(&tm_v);
+                int g = 0;                                   // tiles loaded, K and V counted apart
+                int nq[2] = {0, 0};                          // Q tiles loaded
+                bool ok = true;
+                auto load = [&](const CUtensorMap* map, int tile, const Item& it) {
+                    const int st = g % kStages;
+                    if (g >= kStages && !wait_parity(&empty[st], (g / kStages - 1) & 1, deadline, abort_flag, status))
+                        return false;
+                    mbar_arrive_expect_tx(&full[st], C::kTile);
+                    for (int h = 0; h < D / 64; ++h)
+                        tma_load_4d(skv + st * C::kTile + h * 16384, map, &full[st], h * 64, tile * 128, it.kvh, it.b);
+                    ++g;
+                    return true;
+                };
+                for (int t = blockIdx.x; ok && t < p.total_items; t += gridDim.x) {
+                    const Item it = item_of(p, t);
+                    const int n = it.count();
+                    for (int i = 0; ok && i < n; ++i) {
+                        ok = load(&tm_k, it.tile(i), it);
+                        if (i == 0) {
+                            for (int x = 0; ok && x < 2; ++x) {
+                                if (it.x[x].hi == 0) continue;
+                                if (nq[x] > 0 && !wait_parity(&q_free[x], (nq[x] - 1) & 1, deadline, abort_flag, status)) {
+                                    ok = false;
+                                    break;
+                                }
+                                mbar_arrive_expect_tx(&q_full[x], C::kTile);
+                                for (int h = 0; h < D / 64; ++h)
+                                    tma_load_4d(sq + x * C::kTile + h * 16384, &tm_q, &q_full[x], h * 64,
+                                                it.x[x].qb * 128, it.x[x].head, it.b);
+                                ++nq[x];
+                            }
+                        }
+                        ok = ok && load(&tm_v, it.tile(i), it);
+                    }
+                }
+                if (*abort_flag) {
+                    // copies in flight land before the shared memory is released
+                    const uint64_t dl = global_timer_ns() + 200000000ull;
+                    for (int x = 0; x < 2; ++x)
+                        if (nq[x] > 0) wait_parity_drain(&q_full[x], (nq[x] - 1) & 1, dl);
+                    for (int j = max(0, g - kStages); j < g; ++j) wait_parity_drain(&full[j % kStages], (j / kStages) & 1, dl);
+                }
+            }
+            __syncwarp();
+        } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+            // ------------------------------------------------------------ products of query tile x
+            const int x = static_cast<int>(uniform(static_cast<uint32_t>(warp - kMmaWarp)));
+            const bool lead = elect_one_sync();
+            constexpr uint32_t idS = idesc_f16(128, 128, BF16, false);
+            constexpr uint32_t idO = idesc_f16(128, D, BF16, true);
+            const uint64_t q_desc = uniform(sdesc_sw128(smem_u32(sq + x * C::kTile), 16, 1024));
+            const uint64_t k_desc = sdesc_sw128(smem_u32(skv), 16, 1024);
+            const uint64_t v_desc = sdesc_sw128(smem_u32(skv), 16384, 1024);
+            constexpr uint32_t kTileDesc = C::kTile >> 4;
+            const uint32_t ts = uniform(tbase + 128 * x), to = uniform(tbase + kOCol + D * x);
+            int g = 0;                                       // ring position: K of union tile i at g + 2 i, V after it
+            int blk = 0, items = 0, rounds = 0;              // tiles, items and rounds of this query tile so far
             bool ok = true;
-            auto load = [&](const CUtensorMap* map, int tile, const Item& it) {
-                const int st = g % kStages;
-                if (g >= kStages && !wait_parity(&empty[st], (g / kStages - 1) & 1, deadline, abort_flag, status))
-                    return false;
-                mbar_arrive_expect_tx(&full[st], C::kTile);
-                for (int h = 0; h < D / 64; ++h)
-                    tma_load_4d(skv + st * C::kTile + h * 16384, map, &full[st], h * 64, tile * 128, it.kvh, it.b);
-                ++g;
-                return true;
-            };
             for (int t = blockIdx.x; ok && t < p.total_items; t += gridDim.x) {
                 const Item it = item_of(p, t);
-                const int n = it.count();
-                for (int i = 0; ok && i < n; ++i) {
-                    ok = load(&tm_k, it.tile(i), it);
-                    if (i == 0) {
-                        for (int x = 0; ok && x < 2; ++x) {
-                            if (it.x[x].hi == 0) continue;
-                            if (nq[x] > 0 && !wait_parity(&q_free[x], (nq[x] - 1) & 1, deadline, abort_flag, status)) {
-                                ok = false;
-                                break;
-                            }
-                            mbar_arrive_expect_tx(&q_full[x], C::kTile);
-                            for (int h = 0; h < D / 64; ++h)
-                                tma_load_4d(sq + x * C::kTile + h * 16384, &tm_q, &q_full[x], h * 64,
-                                            it.x[x].qb * 128, it.x[x].head, it.b);
-                            ++nq[x];
+                const Tiles me = x ? it.x[1] : it.x[0];
+                const int n = it.count(), mine = me.count();
+                int done = 0;                                // S issued in this item
+                bool pend = false;                           // the tile before awaits its P V
+                // Round i: P V of the tile before, S of tile i.  A commit takes its turn among the products, so
+                // there is only S's and the last P V's: the softmax warps pass on what it says about the stages
+                // and Q.
+                // Every stage is waited for in turn, visited or not: a parity tells two of its uses apart, no more.
+                for (int i = 0; ok && i <= n && n > 0; ++i) {
+                    const int gk = g + 2 * i, sk = gk % kStages;
+                    const bool visit = i < n && me.has(it.tile(i));
+                    if (i > 0)
+                        ok = warp_wait_parity(&full[(gk - 1) % kStages], ((gk - 1) / kStages) & 1, deadline, abort_flag, status);
+                    if (ok && i < n) ok = warp_wait_parity(&full[sk], (gk / kStages) & 1, deadline, abort_flag, status);
+                    if (!ok) break;
+                    const uint64_t vb = uniform(v_desc + static_cast<uint32_t>((gk + kStages - 1) % kStages) * kTileDesc);
+                    const uint64_t kb = uniform(k_desc + static_cast<uint32_t>(sk) * kTileDesc);
+                    if (visit && done == 0) {
+                        if (!warp_wait_parity(&q_full[x], items & 1, deadline, abort_flag, status)) {
+                            ok = false;
+                            break;
+                        }
+                        ++items;
+                    }
+                    // tile 0's round comes after tile 1's round before, tile 1's after tile 0's
+                    if (rounds + x > 0 && !warp_wait_parity(&turn[x], (rounds + x + 1) & 1, deadline, abort_flag, status)) {
+                        ok = false;
+                        break;
+                    }
+                    ++rounds;
+                    if (pend) {
+                        if ((done == 1 && items > 1 &&
+                             !warp_wait_parity(&o_free[x], items & 1, deadline, abort_flag, status)) ||
+                            !warp_wait_parity(&p_half[x], (blk - 1) & 1, deadline, abort_flag, status)) {
+                            ok = false;
+                            break;
+                        }
+                        // the first half of P V runs under the second half of the softmax
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_f16_ts_if(lead, to, ts + 8 * kk, vb + ((kk * 2048) >> 4), idO, (done > 1 || kk > 0) ? 1u : 0u);
+                        if (!warp_wait_parity(&p_full[x], (blk - 1) & 1, deadline, abort_flag, status)) {
+                            ok = false;
+                            break;
                         }
                     }
-                    ok = ok && load(&tm_v, it.tile(i), it);
-                }
-            }
-            if (*abort_flag) {
-                // copies in flight land before the shared memory is released
-                const uint64_t dl = global_timer_ns() + 200000000ull;
-                for (int x = 0; x < 2; ++x)
-                    if (nq[x] > 0) wait_parity_drain(&q_full[x], (nq[x] - 1) & 1, dl);
-                for (int j = max(0, g - kStages); j < g; ++j) wait_parity_drain(&full[j % kStages], (j / kStages) & 1, dl);
-            }
-        }
-        __syncwarp();
-    } else if (warp >= kMmaWarp) {
-        // ------------------------------------------------------------ products of query tile x
-        const int x = static_cast<int>(uniform(static_cast<uint32_t>(warp - kMmaWarp)));
-        const bool lead = elect_one_sync();
-        constexpr uint32_t idS = idesc_f16(128, 128, BF16, false);
-        constexpr uint32_t idO = idesc_f16(128, D, BF16, true);
-        const uint64_t q_desc = uniform(sdesc_sw128(smem_u32(sq + x * C::kTile), 16, 1024));
-        const uint64_t k_desc = sdesc_sw128(smem_u32(skv), 16, 1024);
-        const uint64_t v_desc = sdesc_sw128(smem_u32(skv), 16384, 1024);
-        constexpr uint32_t kTileDesc = C::kTile >> 4;
-        const uint32_t ts = uniform(tbase + 128 * x), to = uniform(tbase + kOCol + D * x);
-        int g = 0;                                       // ring position: K of union tile i at g + 2 i, V after it
-        int blk = 0, items = 0, rounds = 0;              // tiles, items and rounds of this query tile so far
-        bool ok = true;
-        for (int t = blockIdx.x; ok && t < p.total_items; t += gridDim.x) {
-            const Item it = item_of(p, t);
-            const Tiles me = x ? it.x[1] : it.x[0];
-            const int n = it.count(), mine = me.count();
-            int done = 0;                                // S issued in this item
-            bool pend = false;                           // the tile before awaits its P V
-            // Round i: P V of the tile before, S of tile i.  A commit takes its turn among the products, so
-            // there is only S's and the last P V's: the softmax warps pass on what it says about the stages
-            // and Q.
-            // Every stage is waited for in turn, visited or not: a parity tells two of its uses apart, no more.
-            for (int i = 0; ok && i <= n && n > 0; ++i) {
-                const int gk = g + 2 * i, sk = gk % kStages;
-                const bool visit = i < n && me.has(it.tile(i));
-                if (i > 0)
-                    ok = warp_wait_parity(&full[(gk - 1) % kStages], ((gk - 1) / kStages) & 1, deadline, abort_flag, status);
-                if (ok && i < n) ok = warp_wait_parity(&full[sk], (gk / kStages) & 1, deadline, abort_flag, status);
-                if (!ok) break;
-                const uint64_t vb = uniform(v_desc + static_cast<uint32_t>((gk + kStages - 1) % kStages) * kTileDesc);
-                const uint64_t kb = uniform(k_desc + static_cast<uint32_t>(sk) * kTileDesc);
-                if (visit && done == 0) {
-                    if (!warp_wait_parity(&q_full[x], items & 1, deadline, abort_flag, status)) {
-                        ok = false;
-                        break;
-                    }
-                    ++items;
-                }
-                // tile 0's round comes after tile 1's round before, tile 1's after tile 0's
-                if (rounds + x > 0 && !warp_wait_parity(&turn[x], (rounds + x + 1) & 1, deadline, abort_flag, status)) {
-                    ok = false;
-                    break;
-                }
-                ++rounds;
-                if (pend) {
-                    if ((done == 1 && items > 1 &&
-                         !warp_wait_parity(&o_free[x], items & 1, deadline, abort_flag, status)) ||
-                        !warp_wait_parity(&p_full[x], (blk - 1) & 1, deadline, abort_flag, status)) {
-                        ok = false;
-                        break;
-                    }
-                }
-                tc_fence_after();
-                if (pend) {
+                    tc_fence_after();
+                    if (pend) {
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        mma_f16_ts_if(lead, to, ts + 8 * kk, vb + ((kk * 2048) >> 4), idO, (done > 1 || kk > 0) ? 1u : 0u);
-                    if (done == mine) mma_commit_if(lead, &o_full[x]);
-                    pend = false;
-                }
-                if (visit) {
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-                        mma_f16_ss_if(lead, ts, q_desc + off, kb + off, idS, kk > 0 ? 1u : 0u);
+                        for (int kk = 4; kk < 8; ++kk)
+                            mma_f16_ts_if(lead, to, ts + 8 * kk, vb + ((kk * 2048) >> 4), idO, (done > 1 || kk > 0) ? 1u : 0u);
+                        if (done == mine) mma_commit_if(lead, &o_full[x]);
+                        pend = false;
                     }
-                    mma_commit_if(lead, &s_full[x]);
-                    pend = true;
-                    ++blk;
-                    ++done;
+                    if (visit) {
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+                            mma_f16_ss_if(lead, ts, q_desc + off, kb + off, idS, kk > 0 ? 1u : 0u);
+                        }
+                        mma_commit_if(lead, &s_full[x]);
+                        pend = true;
+                        ++blk;
+                        ++done;
+                    }
+                    mbar_arrive_if(lead, &turn[1 - x]);
                 }
-                mbar_arrive_if(lead, &turn[1 - x]);
+                g += 2 * n;
             }
-            g += 2 * n;
+            mma_commit_if(lead, &fin[x]);
+            wait_parity_drain(&fin[x], 0, global_timer_ns() + 200000000ull);
+            __syncwarp();
         }
-        mma_commit_if(lead, &fin[x]);
-        wait_parity_drain(&fin[x], 0, global_timer_ns() + 200000000ull);
-        __syncwarp();
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         // ------------------------------------------------------------ softmax of query tile x
         const int x = warp >> 2;
         const int lrow = 32 * (warp & 3) + lane;
@@ -536,6 +555,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool rescale = grow && m_used != -INFINITY;
                 m_used = m_new;
                 const float mc = m_new == -INFINITY ? 0.f : m_new * c;
+                if (__any_sync(0xffffffffu, rescale)) {
+                    // O holds every tile before this one: their P V ran before this tile's S
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t o[32];
+                        tmem_ld_row32(to + c0, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        tmem_st_row32(to + c0, o);
+                    }
+                }
                 float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                                  make_float2(0.f, 0.f)};
 #pragma unroll
@@ -550,21 +581,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         pv[e] = pack2<BF16>(ev.x, ev.y);
                     }
                     tmem_st_row16(ts + 16 * h, pv);
+                    if (h == 1) {
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&p_half[x]);
+                    }
                 }
                 const float2 a2 = add2f(add2f(acc[0], acc[1]), add2f(acc[2], acc[3]));
                 l = l * alpha + (a2.x + a2.y);
-                if (__any_sync(0xffffffffu, rescale)) {
-                    // O holds every tile before this one: their P V ran before this tile's S
-#pragma unroll 1
-                    for (int c0 = 0; c0 < D; c0 += 32) {
-                        uint32_t o[32];
-                        tmem_ld_row32(to + c0, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                        tmem_st_row32(to + c0, o);
-                    }
-                }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -653,6 +678,13 @@ int launch(const void* q, const void* k, const void* v, const int64_t (&st)[12],
     static std::atomic<unsigned long long> raised{0};
     rc = raise_smem_limit(reinterpret_cast<const void*>(kern), Cfg<D>::kBytes, raised);
     if (rc) return rc;
+    // the warpgroups' register shares come out of the launch's: with fewer, the larger ones would never come
+    static const bool enough = [kern] {
+        cudaFuncAttributes a{};
+        return cudaFuncGetAttributes(&a, kern) == cudaSuccess &&
+               a.numRegs * kThreads >= 128 * (2 * kRegsSoftmax + kRegsOther);
+    }();
+    if (!enough) return BSATTN_ERR_CUDA;
     int sms = num_sms_of_current_device();
     if (sms <= 0) sms = 148;
     const int grid = prm.total_items < sms ? prm.total_items : sms;
