@@ -48,6 +48,7 @@ constexpr int kMaxTickets = 1024;
 // exp2 is taken of x - max + 12: weights up to 4096, so that a weight 2^-24 of the largest is
 // still a normal fp16 number and 2^-36 the smallest one
 constexpr float kWeightLog2 = 12.f;
+constexpr int kBatch = 16;                // pieces joined in one trip to L2
 
 struct StreamParams {
     const void* q;
@@ -83,7 +84,7 @@ struct Ring {
     static constexpr uint32_t kK = KV4 ? kCodes + kScales : kTok * D * 2;
     static constexpr uint32_t kStage = 2 * kK;
     static constexpr uint32_t kRing = kStages * kStage;          // of one warp
-    static constexpr int kRow = D + 8;                           // padded row of the joining scratch
+    static constexpr int kRow = D + 4;                           // padded row of the joining scratch
     static constexpr uint32_t kJoinWarp = (16 + 8 * kRow) * 4;   // m[8], l[8], O[8][kRow]
     static constexpr uint32_t kMain = kWarps * (kRing > kJoinWarp ? kRing : kJoinWarp);
     static constexpr uint32_t kBars = (kMain + 15) & ~15u;       // full[warp][stage]
@@ -285,57 +286,6 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
         const int lo = p.window > 0 && !p.chosen ? max(0, s.len - p.window) : 0;
         const int sinks = p.window > 0 && !p.chosen ? p.sinks : 0;
 
-        // ---------------------------------------------------------------- queries
-        // lane holds the four channels of head lane/4 that its K registers hold in each k16 step
-        uint32_t qb[D / 16][2];
-        float c0 = p.score_log2, c1 = p.score_log2;       // of heads 2 (lane % 4) + {0, 1}
-        {
-            const T* qg = reinterpret_cast<const T*>(p.q) + (static_cast<size_t>(b) * p.Hq + g * G) * D;
-            const int hq = lane >> 2, j = lane & 3;
-            const bool on = hq < G;
-            if constexpr (KV4) {
-                float top = 0.f;
-                uint4 raw[D / 32];
-#pragma unroll
-                for (int w = 0; w < D / 32; ++w) {
-                    raw[w] = on ? *reinterpret_cast<const uint4*>(qg + hq * D + j * (D / 4) + 8 * w)
-                                : make_uint4(0, 0, 0, 0);
-                    const uint32_t r[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 f = unpack2<BF16>(r[e]);
-                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-                    }
-                }
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                // a power of two brings the head's largest query value into [1, 2): fp16 then holds
-                // bf16 values exactly, but for those 2^-17 of the largest and less (off by 2^-25 of it)
-                const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-                const bool scaled = top > 0.f && e > -126 && e < 127;
-                const float down = scaled ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 1.f;
-                const float up = scaled ? __uint_as_float(static_cast<uint32_t>(127 + e) << 23) : 1.f;
-#pragma unroll
-                for (int w = 0; w < D / 32; ++w) {
-                    const uint32_t r[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
-#pragma unroll
-                    for (int e2 = 0; e2 < 4; ++e2) {
-                        const float2 f = unpack2<BF16>(r[e2]);
-                        qb[2 * w + (e2 >> 1)][e2 & 1] = pack2<false>(f.x * down, f.y * down);
-                    }
-                }
-                c0 *= __shfl_sync(0xffffffffu, up, 8 * j);
-                c1 *= __shfl_sync(0xffffffffu, up, 8 * j + 4);
-            } else {
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const T* src = qg + hq * D + kk * 16 + 2 * j;
-                    qb[kk][0] = on ? *reinterpret_cast<const uint32_t*>(src) : 0u;
-                    qb[kk][1] = on ? *reinterpret_cast<const uint32_t*>(src + 8) : 0u;
-                }
-            }
-        }
-
         // ---------------------------------------------------------------- feeding
         // Unit k of this warp in this piece.  Lane L looks unit (k & ~31) + L up, 32 at a time.
         int look_key = 0, look_row = -1, look_page = 0;
@@ -405,6 +355,60 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
                 }
             }
         };
+        // the first copies are on their way before the queries are read: both take a trip to memory
+        const int base_seq = seq;
+        for (int k = 0; k < kStages && k < mine; ++k) issue(k);
+
+        // ---------------------------------------------------------------- queries
+        // lane holds the four channels of head lane/4 that its K registers hold in each k16 step
+        uint32_t qb[D / 16][2];
+        float c0 = p.score_log2, c1 = p.score_log2;       // of heads 2 (lane % 4) + {0, 1}
+        {
+            const T* qg = reinterpret_cast<const T*>(p.q) + (static_cast<size_t>(b) * p.Hq + g * G) * D;
+            const int hq = lane >> 2, j = lane & 3;
+            const bool on = hq < G;
+            if constexpr (KV4) {
+                float top = 0.f;
+                uint4 raw[D / 32];
+#pragma unroll
+                for (int w = 0; w < D / 32; ++w) {
+                    raw[w] = on ? *reinterpret_cast<const uint4*>(qg + hq * D + j * (D / 4) + 8 * w)
+                                : make_uint4(0, 0, 0, 0);
+                    const uint32_t r[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 f = unpack2<BF16>(r[e]);
+                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
+                }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // a power of two brings the head's largest query value into [1, 2): fp16 then holds
+                // bf16 values exactly, but for those 2^-17 of the largest and less (off by 2^-25 of it)
+                const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+                const bool scaled = top > 0.f && e > -126 && e < 127;
+                const float down = scaled ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 1.f;
+                const float up = scaled ? __uint_as_float(static_cast<uint32_t>(127 + e) << 23) : 1.f;
+#pragma unroll
+                for (int w = 0; w < D / 32; ++w) {
+                    const uint32_t r[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
+#pragma unroll
+                    for (int e2 = 0; e2 < 4; ++e2) {
+                        const float2 f = unpack2<BF16>(r[e2]);
+                        qb[2 * w + (e2 >> 1)][e2 & 1] = pack2<false>(f.x * down, f.y * down);
+                    }
+                }
+                c0 *= __shfl_sync(0xffffffffu, up, 8 * j);
+                c1 *= __shfl_sync(0xffffffffu, up, 8 * j + 4);
+            } else {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const T* src = qg + hq * D + kk * 16 + 2 * j;
+                    qb[kk][0] = on ? *reinterpret_cast<const uint32_t*>(src) : 0u;
+                    qb[kk][1] = on ? *reinterpret_cast<const uint32_t*>(src + 8) : 0u;
+                }
+            }
+        }
 
         // ---------------------------------------------------------------- the warp's units
         float o[D / 16][4];
@@ -415,8 +419,6 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
         // K row r8 of a tile is token r8 with the pairs (2,3) and (6,7) swapped: the V loads of a lane
         // quad then fall on rows of both parities, halving their bank conflicts
         const int tok_r = r8 ^ ((r8 >> 1) & 1);
-        const int base_seq = seq;
-        for (int k = 0; k < kStages && k < mine; ++k) issue(k);
         for (int k = 0; k < mine; ++k) {
             const int at = base_seq + k, st = at % kStages;
             if (!warp_wait_parity(&full[st], (at / kStages) & 1, deadline, abort_flag, p.status)) {
@@ -617,13 +619,19 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
             }
 #pragma unroll
             for (int mt = 0; mt < D / 16; ++mt) {
-                // 4 bits: lane row r8 stands for channels r8 D/8 + 2 mt + {0, 1}
-                const int d0 = KV4 ? r8 * (D / 8) + 2 * mt : mt * 16 + r8;
-                const int d1 = KV4 ? d0 + 1 : d0 + 8;
-                mw[16 + h0 * R::kRow + d0] = o[mt][0];
-                mw[16 + (h0 + 1) * R::kRow + d0] = o[mt][1];
-                mw[16 + h0 * R::kRow + d1] = o[mt][2];
-                mw[16 + (h0 + 1) * R::kRow + d1] = o[mt][3];
+                if constexpr (KV4) {
+                    // lane row r8 stands for channels r8 D/8 + 2 mt + {0, 1}; they are kept at 16 mt + 2 r8, so
+                    // that a store's eight rows lie next to each other
+                    *reinterpret_cast<float2*>(mw + 16 + h0 * R::kRow + 16 * mt + 2 * r8) = make_float2(o[mt][0], o[mt][2]);
+                    *reinterpret_cast<float2*>(mw + 16 + (h0 + 1) * R::kRow + 16 * mt + 2 * r8) =
+                        make_float2(o[mt][1], o[mt][3]);
+                } else {
+                    const int d0 = mt * 16 + r8;
+                    mw[16 + h0 * R::kRow + d0] = o[mt][0];
+                    mw[16 + (h0 + 1) * R::kRow + d0] = o[mt][1];
+                    mw[16 + h0 * R::kRow + d0 + 8] = o[mt][2];
+                    mw[16 + (h0 + 1) * R::kRow + d0 + 8] = o[mt][3];
+                }
             }
         }
         __syncthreads();
@@ -645,7 +653,16 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
                 // a warp without a finite score has l = 0, or NaN if it met one: either way it counts
                 const float mw = join[w * kW + row];
                 const float wt = mw == -INFINITY ? 1.f : ex2_approx(mw - ref);
-                const float4 ov = *reinterpret_cast<const float4*>(join + w * kW + 16 + row * R::kRow + 4 * c4);
+                const float* ow = join + w * kW + 16 + row * R::kRow;
+                float4 ov;
+                if constexpr (KV4) {
+                    const int r = 4 * c4 / (D / 8), mt = (4 * c4 % (D / 8)) / 2;
+                    const float2 lo2 = *reinterpret_cast<const float2*>(ow + 16 * mt + 2 * r);
+                    const float2 hi2 = *reinterpret_cast<const float2*>(ow + 16 * mt + 16 + 2 * r);
+                    ov = make_float4(lo2.x, lo2.y, hi2.x, hi2.y);
+                } else {
+                    ov = *reinterpret_cast<const float4*>(ow + 4 * c4);
+                }
                 num.x += wt * ov.x;
                 num.y += wt * ov.y;
                 num.z += wt * ov.z;
@@ -679,16 +696,16 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
             }
             __syncthreads();
             if (misc[1]) {
-                // read through L2 (an SM's L1 may hold an earlier call's lines), eight pieces at a time
+                // read through L2 (an SM's L1 may hold an earlier call's lines), kBatch pieces at a time
                 for (int e = tid; e < G * (D / 4); e += kThreads) {
                     const int row = e / (D / 4), c4 = e % (D / 4);
                     float M = -INFINITY, den = 0.f;
                     float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int c8 = 0; c8 < count; c8 += 8) {
-                        float lv[8];
-                        float4 ov[8];
+                    for (int c8 = 0; c8 < count; c8 += kBatch) {
+                        float lv[kBatch];
+                        float4 ov[kBatch];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
+                        for (int k = 0; k < kBatch; ++k) {
                             const int c = c_first + c8 + k;
                             const size_t sl = (static_cast<size_t>(c) * 2 + (c == c_first ? 1 : 0)) * p.Hkv + g;
                             const bool in = c <= c_last;
@@ -698,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
                         }
                         float Mc = M;
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) Mc = fmaxf(Mc, lv[k]);
+                        for (int k = 0; k < kBatch; ++k) Mc = fmaxf(Mc, lv[k]);
                         const float ref = Mc == -INFINITY ? 0.f : Mc;
                         const float r = ex2_approx(M - ref);
                         num.x *= r;
@@ -707,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
                         num.w *= r;
                         den *= r;
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
+                        for (int k = 0; k < kBatch; ++k) {
                             const float wt = ex2_approx(lv[k] - ref);
                             num.x += wt * ov[k].x;
                             num.y += wt * ov[k].y;
