@@ -8,13 +8,12 @@
 //
 // Each K/V byte is used once, by the G <= 8 query heads of its kv head, so HBM bandwidth bounds
 // this, and everything is arranged around equal shares of bytes in flight:
-//   * The visible tokens of a sequence are cut into units (32 tokens at 4 bits, 16 at 16 bits: both
-//     4-8 KB of K and V).  All sequences' units, end to end, are cut into equal parts, one CTA for
+//   * The visible tokens of a sequence are cut into units (64 tokens at 4 bits, 32 at 16 bits).  All sequences' units, end to end, are cut into equal parts, one CTA for
 //     each (part, kv head), as many as fit the GPU at once: ragged lengths leave no CTA longer than
 //     another.  A CTA finds its part with one pass over the lengths.  The kv heads of a part run next
 //     to each other, so that neighbouring rows of a 16-bit cache are read at about the same time.
 //   * Each of a CTA's four warps takes every fourth unit and feeds itself: lane 0 issues the copies of
-//     a unit into the warp's own ring of stages (TMA boxes with a 128-byte swizzle at 16 bits; plain
+//     its K and then its V into the warp's own ring of stages (TMA boxes with a 128-byte swizzle at 16 bits; plain
 //     bulk copies at 4 bits, where a unit of a head is contiguous), with an mbarrier for each stage.
 //     No producer warp, and warps wait for nothing but their own data.
 //   * The products are transposed, so that the G <= 8 heads are the n = 8 side of mma.sync m16n8k16:
@@ -76,13 +75,12 @@ struct StreamParams {
 // joining of the four warps' results reuses the rings once they are drained.
 template <int D, bool KV4>
 struct Ring {
-    static constexpr int kTok = KV4 ? 32 : 16;                   // tokens of a unit
-    static constexpr int kStages = 3;
-    static constexpr int kCtas = KV4 ? 4 : 2;                    // resident CTAs per SM
+    static constexpr int kTok = KV4 ? 64 : 32;                   // tokens of a unit
+    static constexpr int kStages = D == 128 ? (KV4 ? 3 : 3) : 6;             // a stage holds K or V of a unit
+    static constexpr int kCtas = KV4 ? 3 : 2;                    // resident CTAs per SM
     static constexpr uint32_t kCodes = kTok * D / 2;             // 4 bits: codes, then scales
     static constexpr uint32_t kScales = kTok * D / kGroup4;
-    static constexpr uint32_t kK = KV4 ? kCodes + kScales : kTok * D * 2;
-    static constexpr uint32_t kStage = 2 * kK;
+    static constexpr uint32_t kStage = KV4 ? kCodes + kScales : kTok * D * 2;
     static constexpr uint32_t kRing = kStages * kStage;          // of one warp
     static constexpr int kRow = D + 4;                           // padded row of the joining scratch
     static constexpr uint32_t kJoinWarp = (16 + 8 * kRow) * 4;   // m[8], l[8], O[8][kRow]
@@ -253,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
     // parts of a multiple of four units (one a warp), four rounds at least: a shorter part would cost
     // more in joining than it gains
     long long chunk = (total + p.parts - 1) / p.parts;
-    chunk = max((chunk + kWarps - 1) / kWarps * kWarps, 4ll * kWarps);
+    chunk = max((chunk + kWarps - 1) / kWarps * kWarps, 2ll * kWarps);
     const long long x0 = part * chunk, x1 = min(x0 + chunk, total);
     if (x0 >= total) return;                       // the whole CTA: x0 and total are the same for all
     if (upto - sum <= x0 && x0 < upto) {
@@ -323,8 +321,10 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
                 look_row = key;
             }
         };
-        auto issue = [&](int k) {
-            if ((k & 31) == 0) look_up(k);
+        // Half h is K of unit h / 2 if h is even, its V if it is odd.
+        auto issue = [&](int h) {
+            const int k = h >> 1;
+            if ((h & 63) == 0) look_up(k);
             const int row = __shfl_sync(0xffffffffu, look_row, k & 31);
             const int page = __shfl_sync(0xffffffffu, look_page, k & 31);
             const int key = __shfl_sync(0xffffffffu, look_key, k & 31);
@@ -333,31 +333,26 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
             if (lane == 0) {
                 key0_of[st] = row < 0 ? -1 : key;
                 if (row < 0) {
-                    mbar_arrive(&full[st]);                         // nothing to load: the stage is skipped
+                    mbar_arrive(&full[st]);                         // nothing to load: the unit is skipped
                 } else {
                     uint8_t* dst = ring + st * R::kStage;
                     mbar_arrive_expect_tx(&full[st], R::kStage);
                     if constexpr (KV4) {
                         const size_t at = (static_cast<size_t>(page) * p.Hkv + g) * p.page_size + row;
-                        bulk_load(dst, p.kc + at * (D / 2), R::kCodes, &full[st]);
-                        bulk_load(dst + R::kCodes, p.ks + at * (D / kGroup4), R::kScales, &full[st]);
-                        bulk_load(dst + R::kK, p.vc + at * (D / 2), R::kCodes, &full[st]);
-                        bulk_load(dst + R::kK + R::kCodes, p.vs + at * (D / kGroup4), R::kScales, &full[st]);
+                        bulk_load(dst, (h & 1 ? p.vc : p.kc) + at * (D / 2), R::kCodes, &full[st]);
+                        bulk_load(dst + R::kCodes, (h & 1 ? p.vs : p.ks) + at * (D / kGroup4), R::kScales, &full[st]);
                     } else {
                         const int r = (p.table ? page * p.page_size : page * p.Smax) + row;
 #pragma unroll
-                        for (int h = 0; h < D / 64; ++h)
-                            tma_load_3d(dst + h * (kTok * 128), &tm_k, &full[st], h * 64, g, r);
-#pragma unroll
-                        for (int h = 0; h < D / 64; ++h)
-                            tma_load_3d(dst + R::kK + h * (kTok * 128), &tm_v, &full[st], h * 64, g, r);
+                        for (int c = 0; c < D / 64; ++c)
+                            tma_load_3d(dst + c * (kTok * 128), h & 1 ? &tm_v : &tm_k, &full[st], c * 64, g, r);
                     }
                 }
             }
         };
         // the first copies are on their way before the queries are read: both take a trip to memory
         const int base_seq = seq;
-        for (int k = 0; k < kStages && k < mine; ++k) issue(k);
+        for (int h = 0; h < kStages && h < 2 * mine; ++h) issue(h);
 
         // ---------------------------------------------------------------- queries
         // lane holds the four channels of head lane/4 that its K registers hold in each k16 step
@@ -419,16 +414,31 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
         // K row r8 of a tile is token r8 with the pairs (2,3) and (6,7) swapped: the V loads of a lane
         // quad then fall on rows of both parities, halving their bank conflicts
         const int tok_r = r8 ^ ((r8 >> 1) & 1);
-        for (int k = 0; k < mine; ++k) {
-            const int at = base_seq + k, st = at % kStages;
+        // Waits for half h and returns its stage; issues half h + kStages into it once it is read.
+        auto arrived = [&](int h) -> uint8_t* {
+            const int at = base_seq + h, st = at % kStages;
             if (!warp_wait_parity(&full[st], (at / kStages) & 1, deadline, abort_flag, p.status)) {
                 ok = false;
-                break;
+                return nullptr;
             }
             __syncwarp();
-            const int key0 = key0_of[st];
-            if (key0 >= 0) {
-                uint8_t* stage = ring + st * R::kStage;
+            return ring + st * R::kStage;
+        };
+        auto consumed = [&](int h) {
+            __syncwarp();
+            if (h + kStages < 2 * mine) issue(h + kStages);
+        };
+        for (int k = 0; k < mine; ++k) {
+            uint8_t* stage = arrived(2 * k);
+            if (!stage) break;
+            const int key0 = key0_of[(base_seq + 2 * k) % kStages];
+            if (key0 < 0) {
+                consumed(2 * k);
+                if (!arrived(2 * k + 1)) break;
+                consumed(2 * k + 1);
+                continue;
+            }
+            {
                 // tokens [key0, key0 + kTok): visible [max(lo, 0), len) and [0, sinks)
                 const bool edge = key0 + kTok > s.len || (key0 < lo && key0 + kTok > sinks);
                 auto seen = [&](int t) { return t < s.len && (t >= lo || t < sinks); };
@@ -475,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
                         for (int kk = 0; kk < D / 16; ++kk) {
                             const int col = kk * 16 + (mat >> 1) * 8;
                             uint32_t a[4];
-                            ldsm4(kbase + (col >> 6) * (kTok * 128) + sw128_offset((mat & 1) * 8 + (lane & 7), col & 63), a);
+                            ldsm4(kbase + (col >> 6) * (kTok * 128) + sw128_offset(16 * mt + (mat & 1) * 8 + (lane & 7), col & 63), a);
                             mma16816<kBf>(sc, a, qb[kk][0], qb[kk][1]);
                         }
                     }
@@ -489,6 +499,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
                         if (!seen(ta + 8)) x[mt][2] = x[mt][3] = -INFINITY;
                     }
                 }
+                consumed(2 * k);
                 float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
                 for (int mt = 0; mt < kTiles; ++mt) {
@@ -518,18 +529,25 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
                 }
                 const float z0 = m0 == -INFINITY ? 0.f : m0 - kWeightLog2;
                 const float z1 = m1 == -INFINITY ? 0.f : m1 - kWeightLog2;
+                uint32_t pb[kTiles][2];
 #pragma unroll
                 for (int mt = 0; mt < kTiles; ++mt) {
                     const float p0 = ex2_approx(x[mt][0] - z0), p1 = ex2_approx(x[mt][1] - z1);
                     const float p2 = ex2_approx(x[mt][2] - z0), p3 = ex2_approx(x[mt][3] - z1);
                     l0 += p0 + p2;
                     l1 += p1 + p3;
-                    const uint32_t pb0 = transpose8x8(pack2<kBf>(p0, p1));
-                    const uint32_t pb1 = transpose8x8(pack2<kBf>(p2, p3));
+                    pb[mt][0] = transpose8x8(pack2<kBf>(p0, p1));
+                    pb[mt][1] = transpose8x8(pack2<kBf>(p2, p3));
+                }
+                stage = arrived(2 * k + 1);
+                if (!stage) break;
+#pragma unroll
+                for (int mt = 0; mt < kTiles; ++mt) {
+                    const uint32_t pb0 = pb[mt][0], pb1 = pb[mt][1];
                     if constexpr (KV4) {
                         // tokens 2 j4, 2 j4 + 1 and eight further, as K's rows name them
                         const int ta = 16 * mt + (2 * j4 ^ (j4 & 1)), tb = 16 * mt + ((2 * j4 + 1) ^ (j4 & 1));
-                        const uint8_t* vc = stage + R::kK;
+                        const uint8_t* vc = stage;
                         const uint8_t* vs = vc + R::kCodes;
                         const int gi = D == 128 ? r8 : r8 >> 1;
                         uint32_t e8[4] = {vs[ta * (D / 16) + gi], vs[tb * (D / 16) + gi], vs[(ta + 8) * (D / 16) + gi],
@@ -542,13 +560,17 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
                             if (!seen(key0 + tb + 8)) e8[3] = 0;
                         }
                         const uint32_t sx = e4m3x2_to_f16(e8[0] | e8[1] << 8), sy = e4m3x2_to_f16(e8[2] | e8[3] << 8);
+                        uint32_t v4[4][D / 64];                     // four tokens' D / 8 channels
+                        const int rows[4] = {ta, tb, ta + 8, tb + 8};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint8_t* src = vc + rows[e] * (D / 2) + r8 * (D / 16);
+                            if constexpr (D == 128) *reinterpret_cast<uint2*>(v4[e]) = *reinterpret_cast<const uint2*>(src);
+                            else v4[e][0] = *reinterpret_cast<const uint32_t*>(src);
+                        }
 #pragma unroll
                         for (int w = 0; w < D / 64; ++w) {
-                            const int off = r8 * (D / 16) + 4 * w;
-                            const uint32_t u0 = *reinterpret_cast<const uint32_t*>(vc + ta * (D / 2) + off);
-                            const uint32_t u1 = *reinterpret_cast<const uint32_t*>(vc + tb * (D / 2) + off);
-                            const uint32_t u2 = *reinterpret_cast<const uint32_t*>(vc + (ta + 8) * (D / 2) + off);
-                            const uint32_t u3 = *reinterpret_cast<const uint32_t*>(vc + (tb + 8) * (D / 2) + off);
+                            const uint32_t u0 = v4[0][w], u1 = v4[1][w], u2 = v4[2][w], u3 = v4[3][w];
                             // byte i of ev / od: the even / odd channel of byte i, of two tokens
                             uint32_t ev0[4], od0[4], ev1[4], od1[4];
                             constexpr uint32_t kLow = 0x0f0f0f0fu;
@@ -564,33 +586,32 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
                             }
                         }
                     } else {
-                        if (edge) {
+                        if (edge && mt == 0) {
                             // tokens that are not visible may hold anything: zero their V rows, so that
                             // a weight of 0 cannot meet a NaN
                             for (int e = lane; e < kTok * (D / 8); e += 32) {
                                 const int r = e / (D / 8), col = (e % (D / 8)) * 8;
                                 if (!seen(key0 + r))
-                                    *reinterpret_cast<uint4*>(stage + R::kK + (col >> 6) * (kTok * 128) +
+                                    *reinterpret_cast<uint4*>(stage + (col >> 6) * (kTok * 128) +
                                                               sw128_offset(r, col & 63)) = make_uint4(0, 0, 0, 0);
                             }
                             fence_proxy_async_smem();
                             __syncwarp();
                         }
-                        const uint32_t vbase = smem_u32(stage) + R::kK;
+                        const uint32_t vbase = smem_u32(stage);
                         const int mat = lane >> 3;
 #pragma unroll
                         for (int dt = 0; dt < D / 16; ++dt) {
                             const int col = dt * 16 + (mat & 1) * 8;
                             uint32_t a[4];
                             ldsm4_t(vbase + (col >> 6) * (kTok * 128) +
-                                        sw128_offset((mat >> 1) * 8 + (lane & 7), col & 63), a);
+                                        sw128_offset(16 * mt + (mat >> 1) * 8 + (lane & 7), col & 63), a);
                             mma16816<kBf>(o[dt], a, pb0, pb1);
                         }
                     }
                 }
+                consumed(2 * k + 1);
             }
-            __syncwarp();
-            if (k + kStages < mine) issue(k + kStages);
         }
         if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.status, BSATTN_ERR_BAD_INDEX);
         if (!ok) {
@@ -823,8 +844,8 @@ int decode_stream(StreamParams prm, const void* k16, const void* v16, int d, bsa
         const uint64_t rows = prm.table ? static_cast<uint64_t>(prm.num_pages) * prm.page_size
                                         : static_cast<uint64_t>(prm.B) * prm.Smax;
         const uint64_t row_bytes = uint64_t(prm.Hkv) * d * 2;
-        int rc = encode_3d(&tk, k16, bf16, d, prm.Hkv, rows, d * 2ull, row_bytes, 64, 1, 16, true);
-        rc |= encode_3d(&tv, v16, bf16, d, prm.Hkv, rows, d * 2ull, row_bytes, 64, 1, 16, true);
+        int rc = encode_3d(&tk, k16, bf16, d, prm.Hkv, rows, d * 2ull, row_bytes, 64, 1, Ring<128, false>::kTok, true);
+        rc |= encode_3d(&tv, v16, bf16, d, prm.Hkv, rows, d * 2ull, row_bytes, 64, 1, Ring<128, false>::kTok, true);
         if (rc) return rc;
         if (d == 64) return bf16 ? launch<64, true, false>(tk, tv, prm, st) : launch<64, false, false>(tk, tv, prm, st);
         return bf16 ? launch<128, true, false>(tk, tv, prm, st) : launch<128, false, false>(tk, tv, prm, st);
