@@ -47,7 +47,7 @@ constexpr int kMaxTickets = 1024;
 // exp2 is taken of x - max + 12: weights up to 4096, so that a weight 2^-24 of the largest is
 // still a normal fp16 number and 2^-36 the smallest one
 constexpr float kWeightLog2 = 12.f;
-constexpr int kBatch = 16;                // pieces joined in one trip to L2
+constexpr int kBatch = 12;                // pieces joined in one trip to L2
 
 struct StreamParams {
     const void* q;
