@@ -406,9 +406,10 @@ def bsattn_set_wait_budget_ns(ns: int) -> None:
 # it go through them one by one for the error that says which is wrong.
 
 _STREAM_HEADER = 256 + 4 * 1024          # status word and tickets: all that has to start at zero
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
-_capturing = torch._C._cuda_isCurrentStreamCapturing
+# the calls behind torch.cuda's own (absent from a CPU-only torch, which has no CUDA tensors to pass)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None)
 _I32, _I64, _U8 = torch.int32, torch.int64, torch.uint8
 _CODES = {torch.float16: _F16, torch.bfloat16: _BF16}
 
@@ -470,6 +471,22 @@ def _refuse(*tensors):
     raise ValueError("the arguments' shapes disagree")
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
+def _int(v) -> int:
+    """v as a C int (ctypes would cut larger values off)."""
+    v = int(v)
+    if not -_INT_MAX <= v <= _INT_MAX:
+        raise ValueError(f"{v} does not fit 32 bits")
+    return v
+
+
+def _span(window, sinks):
+    """A window and sinks as C ints: past 2^31 - 1 tokens there is nothing more to see."""
+    return max(min(int(window), _INT_MAX), -1), max(min(int(sinks), _INT_MAX), -1)
+
+
 def _check_out(out, q, contiguous):
     if out.get_device() != q.get_device() or out.dtype is not q.dtype or out.shape != q.shape:
         raise ValueError("out must have the queries' device, dtype and shape")
@@ -500,7 +517,8 @@ def bsattn_paged_plan(cached_lens, new_lens, free_pages, free_count, block_table
         with torch.cuda.device(i):
             return bsattn_paged_plan(cached_lens, new_lens, free_pages, free_count, block_table, page_size,
                                      max_tokens, ws)
-    slots = cached_lens.new_empty(max_tokens, dtype=_I64)
+    page_size, max_tokens = _int(page_size), _int(max_tokens)
+    slots = cached_lens.new_empty(max(max_tokens, 0), dtype=_I64)
     starts, seqlens, left = cached_lens.new_empty(B + 1), torch.empty_like(cached_lens), torch.empty_like(free_count)
     if ws is None:
         ws = status_workspace(i)
@@ -574,8 +592,8 @@ def bsattn_kv4_append(k, v, slots, cache, k_scale: float = 1.0, v_scale: float =
         ws = status_workspace(i)
     kc, ks, vc, vs = cache
     rc = load().bsattn_kv4_append(k.data_ptr(), v.data_ptr(), kt, kh, vt, vh, slots.data_ptr(), kc.data_ptr(),
-                                  ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), k_scale, v_scale, T, hkv, pages,
-                                  page, 2 * half, dtype, ws.data_ptr(), ws.numel(), _raw_stream(i))
+                                  ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), float(k_scale), float(v_scale), T, hkv,
+                                  pages, page, 2 * half, dtype, ws.data_ptr(), ws.numel(), _raw_stream(i))
     if rc:
         _check("bsattn_kv4_append", rc)
 
@@ -598,7 +616,7 @@ def bsattn_kv4_gather(slots, cache, dtype, k_scale: float = 1.0, v_scale: float 
         ws = status_workspace(i)
     kc, ks, vc, vs = cache
     rc = load().bsattn_kv4_gather(slots.data_ptr(), kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(),
-                                  k_scale, v_scale, k.data_ptr(), v.data_ptr(), T, hkv, pages, page, 2 * half,
+                                  float(k_scale), float(v_scale), k.data_ptr(), v.data_ptr(), T, hkv, pages, page, 2 * half,
                                   _CODES[dtype], ws.data_ptr(), ws.numel(), _raw_stream(i))
     if rc:
         _check("bsattn_kv4_gather", rc)
@@ -641,6 +659,7 @@ def bsattn_decode_paged_kv4(q, cache, cache_seqlens, block_table, block_indices=
         _refuse(("q", q, q.dtype, 3, (*qs[:2], d)), ("cache_seqlens", cache_seqlens, _I32, 1, qs[:1]),
                 ("block_table", block_table, _I32, 2, (qs[0], *block_table.shape[1:])))
     B, Hq, _ = qs
+    window, sinks = _span(window, sinks)
     max_sel, chosen = 0, None
     if block_indices is not None:
         max_sel, chosen = block_indices.shape[-1], block_indices.data_ptr()
@@ -659,7 +678,7 @@ def bsattn_decode_paged_kv4(q, cache, cache_seqlens, block_table, block_indices=
         ws = _stream_workspace(i, "decode_kv4", bsattn_decode_kv4_workspace_size, Hq, hkv, d)
     kc, ks, vc, vs = cache
     rc = load().bsattn_decode_paged_kv4(q.data_ptr(), kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(),
-                                        k_scale, v_scale, cache_seqlens.data_ptr(), chosen, block_table.data_ptr(),
+                                        float(k_scale), float(v_scale), cache_seqlens.data_ptr(), chosen, block_table.data_ptr(),
                                         window, sinks, out.data_ptr(), B, Hq, hkv, pages, page,
                                         block_table.shape[1], d, max_sel, dtype, ws.data_ptr(), ws.numel(),
                                         _raw_stream(i))
@@ -693,6 +712,7 @@ def bsattn_decode_window(q, k, v, cache_seqlens, window: int, sinks: int = 0, ou
         with torch.cuda.device(i):
             return bsattn_decode_window(q, k, v, cache_seqlens, window, sinks, out, ws)
     _, Smax, hkv, _ = k.shape
+    window, sinks = _span(window, sinks)
     if out is None:
         out = torch.empty_like(q)
     else:
@@ -720,6 +740,7 @@ def bsattn_decode_window_paged(q, k_pages, v_pages, cache_seqlens, block_table, 
         with torch.cuda.device(i):
             return bsattn_decode_window_paged(q, k_pages, v_pages, cache_seqlens, block_table, window, sinks, out, ws)
     pages, page, hkv, _ = k_pages.shape
+    window, sinks = _span(window, sinks)
     if out is None:
         out = torch.empty_like(q)
     else:
@@ -759,6 +780,7 @@ def bsattn_prefill_window(q, k, v, window: int, sinks: int = 0, out=None, ws=Non
         _check_out(out, q, False)
     B, Hq, Sq, d = q.shape
     _, hkv, Sk, _ = k.shape
+    window, sinks = _span(window, sinks)
     qs, ks, vs, os_ = q.stride(), k.stride(), v.stride(), out.stride()
     if (qs[3] != 1 or os_[3] != 1) and q.numel() or (ks[3] != 1 or vs[3] != 1) and k.numel():
         raise ValueError("channels (the last dimension) must be contiguous")

@@ -218,7 +218,7 @@ int check(const Kv4Params& p, int num_pages, int d, bsattn_dtype dtype, const vo
     if (p.T < 0 || p.Hkv <= 0 || num_pages <= 0 || p.page <= 0) return BSATTN_ERR_INVALID_ARG;
     if (d != 64 && d != 128) return BSATTN_ERR_UNSUPPORTED;
     if (dtype != BSATTN_F16 && dtype != BSATTN_BF16) return BSATTN_ERR_UNSUPPORTED;
-    if (p.Hkv > (1 << 20)) return BSATTN_ERR_UNSUPPORTED;
+    if (p.Hkv > (1 << 20) || p.T > (1 << 30)) return BSATTN_ERR_UNSUPPORTED;
     if (!unit_ok4(p.k_unit) || !unit_ok4(p.v_unit)) return BSATTN_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < 256) return BSATTN_ERR_INVALID_ARG;
     if (p.T == 0) return BSATTN_OK;

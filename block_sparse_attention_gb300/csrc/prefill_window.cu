@@ -278,7 +278,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int* status = p.status;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint64_t deadline = global_timer_ns() + p.budget_ns;
+    // of the waits of an item: a call over long sequences may itself take longer than a wait's budget
+    uint64_t deadline = global_timer_ns() + p.budget_ns;
 
     if (tid == 0) {
         for (int x = 0; x < 2; ++x) {
@@ -333,6 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 for (int t = blockIdx.x; ok && t < p.total_items; t += gridDim.x) {
                     const Item it = item_of(p, t);
+                    deadline = global_timer_ns() + p.budget_ns;
                     const int n = it.count();
                     for (int i = 0; ok && i < n; ++i) {
                         ok = load(&tm_k, it.tile(i), it);
@@ -378,6 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int t = blockIdx.x; ok && t < p.total_items; t += gridDim.x) {
                 const Item it = item_of(p, t);
+                deadline = global_timer_ns() + p.budget_ns;
                 const Tiles me = x ? it.x[1] : it.x[0];
                 const int n = it.count(), mine = me.count();
                 int done = 0;                                // S issued in this item
@@ -464,6 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int t = blockIdx.x; ok && t < p.total_items; t += gridDim.x) {
             const Item it = item_of(p, t);
+            deadline = global_timer_ns() + p.budget_ns;
             const Tiles me = x ? it.x[1] : it.x[0];
             const int n = me.count();
             const int g0 = g;                            // ring position of the item's first K tile
@@ -720,10 +724,10 @@ extern "C" int bsattn_prefill_window(const void* q, const void* k, const void* v
             st[3 * i + 2] = d;
         }
     }
-    // out is written with 16-byte stores, each element once
+    // out is written with 16-byte stores, each element once: its rows must not overlap
     const int64_t on[3] = {B, Hq, Sq};
     for (int i = 0; i < 3; ++i)
-        if (on[i] > 1 && (st[9 + i] <= 0 || (st[9 + i] & 7))) return BSATTN_ERR_INVALID_ARG;
+        if (on[i] > 1 && (st[9 + i] < d || (st[9 + i] & 7))) return BSATTN_ERR_INVALID_ARG;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     WindowParams prm{};
     prm.out = out;

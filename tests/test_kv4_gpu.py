@@ -449,3 +449,46 @@ def test_serving_loop(bsa):
     q = _rand(1, Hq, 40, d, dtype=BF16, seed=1)
     kk, vv = pk.transpose(0, 1)[None], pv.transpose(0, 1)[None]
     ref.check(bsa.bsattn_prefill_window(q, kk, vv, 90, 4), *ref.window_prefill(q, kk, vv, 90, 4))
+
+
+def test_cache_rows_past_32_bit_offsets(bsa):
+    """Pages whose codes lie past 2^32 bytes: append, gather and decode at the cache's far end."""
+    Hkv, d, page = 8, 128, 64
+    pages = (1 << 32) // (Hkv * page * d // 2) + 4
+    codes = [torch.empty(pages, Hkv, page, d // 2, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scales = [torch.empty(pages, Hkv, page, d // 16, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    cache = bsa.Kv4Cache(codes[0], scales[0], codes[1], scales[1])
+    table = torch.tensor([[pages - 1, 1, pages - 2]], dtype=torch.int32, device="cuda")
+    j = torch.arange(150, device="cuda")
+    slots = table[0].long()[j // page] * page + j % page
+    k, v = _rand(150, Hkv, d, dtype=BF16, seed=1), _rand(150, Hkv, d, dtype=BF16, seed=2)
+    bsa.bsattn_kv4_append(k, v, slots, cache)
+    gk, gv = bsa.bsattn_kv4_gather(slots, cache, BF16)
+    assert torch.equal(gk.double(), ref.dequantise(*ref.quantise(k, 1.0), 1.0))
+    q = _rand(1, 16, d, dtype=BF16, seed=3)
+    n = torch.tensor([150], dtype=torch.int32, device="cuda")
+    got = bsa.bsattn_decode_paged_kv4(q, cache, n, table)
+    ref.check(got, *ref.decode(q, _Held([gk.double()], [gv.double()]), [150], lambda b, g, m: ref.windowed(m, m, 0, "cuda"), F16))
+
+
+def test_sizes_that_do_not_fit_are_refused(bsa):
+    cache, table = _cache4([70], 2, 64, 64, seed=1)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    with pytest.raises(ValueError):
+        bsa.bsattn_paged_plan(i32([0]), i32([1]), i32([3]), i32([1]), table, 2 ** 32 + 64, 8)
+    with pytest.raises(bsa.BsattnError):
+        bsa.bsattn_paged_plan(i32([0]), i32([1]), i32([3]), i32([1]), table, 64, -1)
+    with pytest.raises(TypeError):
+        bsa.bsattn_kv4_gather(torch.zeros(1, dtype=torch.int64, device="cuda"), cache, torch.float32)
+    q = _rand(1, 4, 64, dtype=F16, seed=2)
+    for bad in (dict(block_indices=i32([[[0], [0]]]), window=3), dict(k_scale=0.7)):
+        with pytest.raises(bsa.BsattnError):
+            bsa.bsattn_decode_paged_kv4(q, cache, i32([70]), table, **bad)
+    for bad in (dict(block_indices=i32([[[0]]])), dict(block_indices=torch.zeros(1, 2, 0, dtype=torch.int32, device="cuda")),
+                dict(out=q[:, :2])):
+        with pytest.raises(ValueError):
+            bsa.bsattn_decode_paged_kv4(q, cache, i32([70]), table, **bad)
+    with pytest.raises(ValueError):
+        bsa.bsattn_decode_paged_kv4(q, cache[:2] + (cache[3], cache[2]), i32([70]), table)
+    want = bsa.bsattn_decode_paged_kv4(q, cache, i32([70]), table)
+    assert torch.equal(want, bsa.bsattn_decode_paged_kv4(q, cache, i32([70]), table, window=2 ** 40, sinks=2 ** 33))

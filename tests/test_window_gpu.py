@@ -369,3 +369,61 @@ def test_a_wait_that_expires_is_reported(bsa, B):
     got = bsa.bsattn_decode_window(q[:, :, 0].contiguous(), kd, vd, n, 4000, 0, ws=ws)
     assert bsa.bsattn_get_device_status(ws) == 0
     ref.check(got[:1], *want)
+
+
+def test_wait_budget_is_not_the_calls(bsa):
+    """A call that takes longer than a wait's budget, with no wait that does: 2.5 ms against 1 ms."""
+    q = _rand(4, 32, 16384, 128, dtype=BF16, seed=1)
+    k, v = _rand(4, 8, 16384, 128, dtype=BF16, seed=2), _rand(4, 8, 16384, 128, dtype=BF16, seed=3)
+    want = bsa.bsattn_prefill_window(q, k, v, 4096, 4)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    bsa.bsattn_set_wait_budget_ns(1_000_000)
+    try:
+        got = bsa.bsattn_prefill_window(q, k, v, 4096, 4, ws=ws)
+        assert bsa.bsattn_get_device_status(ws) == 0
+    finally:
+        bsa.bsattn_set_wait_budget_ns(2_000_000_000)
+    assert torch.equal(got, want)
+
+
+def test_windows_past_32_bits(bsa):
+    """A window or a number of sinks larger than any length is all of it, however it is written."""
+    q = _rand(1, 2, 150, 64, dtype=F16, seed=1)
+    k, v = _rand(1, 2, 150, 64, dtype=F16, seed=2), _rand(1, 2, 150, 64, dtype=F16, seed=3)
+    want = bsa.bsattn_prefill_window(q, k, v, 150, 0)
+    for window, sinks in ((2 ** 31 - 1, 0), (2 ** 32 + 5, 0), (2 ** 40, 2 ** 40), (1, 2 ** 32 + 1)):
+        assert torch.equal(want, bsa.bsattn_prefill_window(q, k, v, window, sinks))
+    n = torch.tensor([150], dtype=torch.int32, device="cuda")
+    args = (q[:, :, -1].contiguous(), k.transpose(1, 2).contiguous(), v.transpose(1, 2).contiguous(), n)
+    want = bsa.bsattn_decode_window(*args, 150, 0)
+    for window, sinks in ((2 ** 31 - 1, 0), (2 ** 32 + 5, 0), (1, 2 ** 32 + 1)):
+        assert torch.equal(want, bsa.bsattn_decode_window(*args, window, sinks))
+    with pytest.raises(bsa.BsattnError):
+        bsa.bsattn_decode_window(*args, -2 ** 40, 0)
+
+
+def test_in_place_output(bsa):
+    """The output may be the queries: every query row is read before its output is written."""
+    q = _rand(2, 6, 500, 128, dtype=BF16, seed=1)
+    k, v = _rand(2, 3, 700, 128, dtype=BF16, seed=2), _rand(2, 3, 700, 128, dtype=BF16, seed=3)
+    want = bsa.bsattn_prefill_window(q, k, v, 100, 3)
+    bsa.bsattn_prefill_window(q, k, v, 100, 3, out=q)
+    assert torch.equal(q, want)
+    lens = [9000, 40]
+    kp, vp, table = _paged(lens, 2, 64, BF16, 64, seed=4)
+    q = _rand(2, 8, 64, dtype=BF16, seed=5)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    want = bsa.bsattn_decode_window_paged(q, kp, vp, n, table, 8000, 4)
+    bsa.bsattn_decode_window_paged(q, kp, vp, n, table, 8000, 4, out=q)
+    assert torch.equal(q, want)
+
+
+def test_prefill_rows_past_32_bit_offsets(bsa):
+    """Batches 2^32 elements apart, heads 2^26, rows 2^20: offsets that only 64 bits hold."""
+    shape, stride = (2, 4, 40, 64), (1 << 32, 1 << 26, 1 << 20, 1)
+    room = torch.empty((1 << 32) + (1 << 28), dtype=F16, device="cuda")
+    q, out = (torch.as_strided(room, shape, stride, at) for at in (0, 128))
+    q.copy_(_rand(*shape, dtype=F16, seed=1))
+    k, v = _rand(2, 2, 40, 64, dtype=F16, seed=2), _rand(2, 2, 40, 64, dtype=F16, seed=3)
+    bsa.bsattn_prefill_window(q, k, v, 9, 1, out=out)
+    ref.check(out, *ref.window_prefill(q, k, v, 9, 1))
