@@ -76,7 +76,10 @@ struct StreamParams {
 template <int D, bool KV4>
 struct Ring {
     static constexpr int kTok = KV4 ? 64 : 32;                   // tokens of a unit
-    static constexpr int kStages = D == 128 ? (KV4 ? 3 : 3) : 6;             // a stage holds K or V of a unit
+    // A stage holds K or V of a unit; two a warp.  With three, 196 KB an SM in flight at 16 bits instead of
+    // 131, 192 sequences with a 4096 window took 430 us against 410: DRAM serves fewer streams better.  At
+    // 4 bits the conversions bound the kernel and it made no difference (139 us against 138).
+    static constexpr int kStages = 2 * (128 / D);
     static constexpr int kCtas = KV4 ? 3 : 2;                    // resident CTAs per SM
     static constexpr uint32_t kCodes = kTok * D / 2;             // 4 bits: codes, then scales
     static constexpr uint32_t kScales = kTok * D / kGroup4;
@@ -87,10 +90,11 @@ struct Ring {
     static constexpr uint32_t kMain = kWarps * (kRing > kJoinWarp ? kRing : kJoinWarp);
     static constexpr uint32_t kBars = (kMain + 15) & ~15u;       // full[warp][stage]
     static constexpr uint32_t kKey0 = kBars + 8 * kWarps * kStages;
-    static constexpr uint32_t kMisc = kKey0 + 4 * kWarps * kStages;
+    static constexpr uint32_t kMisc = (kKey0 + 4 * kWarps * kStages + 15) & ~15u;   // holds 8-byte values
     static constexpr uint32_t kSlack = KV4 ? 0 : 1024;           // room to align the base up for the swizzle
     static constexpr uint32_t kBytes = kSlack + kMisc + 64;
     static_assert(KV4 || kStage % 1024 == 0, "swizzled tiles start on 1024 bytes");
+    static_assert(kStage % 16 == 0 && kJoinWarp % 16 == 0 && kBars % 8 == 0 && kMisc % 16 == 0, "alignment");
 };
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
