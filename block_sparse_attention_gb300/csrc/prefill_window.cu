@@ -9,7 +9,8 @@
 // tiles that see (nearly) the same keys, two query heads of a kv head at the same rows or, where
 // heads do not pair up, two neighbouring row blocks of a head, and runs them against one stream of
 // 128-key K/V tiles: half the L2 traffic of one tile a CTA, and while the softmax of one query tile
-// works the tensor core has the other's products.
+// works the tensor core has the other's products.  With no more query tiles than SMs both are the same
+// tile instead, each over every second of its key tiles; their O and sums are joined at the end.
 //     S_x = Q_x K^T    tcgen05.mma M=128 N=128 K=d, fp32 in TMEM (N = 128: both operands' shared
 //                      memory reads then take no longer than the products themselves)
 //     P_x              exp2 online softmax, one thread a row, written over S_x as the 16-bit type
@@ -57,12 +58,18 @@ struct Cfg {
     static constexpr uint32_t kQ = 0;                            // two query tiles
     static constexpr uint32_t kKV = 2 * kTile;
     static constexpr uint32_t kBars = kKV + kStages * kTile;
-    // q_full[2] q_free[2] full[stages] empty[stages] s_full[2] p_half[2] p_full[2] o_full[2] o_free[2] fin[2] turn[2]
-    static constexpr uint32_t kNumBars = 4 + 2 * kStages + 14;
-    static constexpr uint32_t kMisc = kBars + 8 * kNumBars;      // tmem base, abort flag
-    static constexpr uint32_t kBytes = 1024 + kMisc + 16;
+    // q_full[2] q_free[2] full[stages] empty[stages] s_full[2] p_half[2] p_full[2] o_full[2] o_free[2] fin[2] turn[2] joined
+    static constexpr uint32_t kNumBars = 4 + 2 * kStages + 15;
+    static constexpr uint32_t kMisc = (kBars + 8 * kNumBars + 15) & ~15u;   // tmem base, abort flag
+    static constexpr uint32_t kHalf = kMisc + 16;                // (m, l) of query tile 1's rows
+    static constexpr uint32_t kBytes = 1024 + kHalf + 128 * 8;
     static_assert(kBytes <= 227 * 1024, "shared memory");
 };
+
+// What the two query tiles of an item are: two heads of a kv head at the same rows, two neighbouring row
+// blocks of a head, or one tile whose keys are shared out between them.  (The last has kernels of its own:
+// decided at run time it would cost the other two 2 % at d = 64.)
+enum Pairing { kHeads, kRows, kSplit };
 
 struct WindowParams {
     void* out;
@@ -71,10 +78,10 @@ struct WindowParams {
     int B, Hq, Hkv, Sq, Sk;
     int window, sinks;
     int nq;                              // 128-row query blocks
-    int by_heads;                        // 1: a pair is two heads, 0: two row blocks
-    int pairs;                           // items per (batch, pair row): head pairs, or heads
+    int pairing;                         // what an item's two query tiles are
+    int pairs;                           // items per (batch, item row): head pairs, or heads
     int rows;                            // item rows: row blocks, or pairs of them
-    int total_items;
+    int total_items, sms;
     float scale_log2;
     unsigned long long budget_ns;
 };
@@ -190,17 +197,33 @@ __device__ __forceinline__ void mma_f16_ts_if(bool lead, uint32_t d_tmem, uint32
 struct Tiles {
     int head, qb;          // query head, row block (past the last one: no rows)
     int lo, hi, sink;
-    __device__ __forceinline__ bool has(int t) const { return t < hi && (t < sink || t >= lo); }
+    __device__ __forceinline__ int tile(int i) const { return i < sink ? i : lo + (i - sink); }
     __device__ __forceinline__ int count() const { return hi > 0 ? sink + hi - lo : 0; }
 };
 
-// One item: the two query tiles and the tiles their union visits.
+// One item: the two query tiles and the tiles their union visits.  SPLIT: both are one query tile, which
+// visits that union, tile 0 the even positions in it and tile 1 the odd ones.
+template <bool SPLIT>
 struct Item {
     int b, kvh;
-    Tiles x[2];
-    int lo, hi, sink;
-    __device__ __forceinline__ int count() const { return hi > 0 ? sink + hi - lo : 0; }
-    __device__ __forceinline__ int tile(int i) const { return i < sink ? i : lo + (i - sink); }
+    Tiles x[2], both;
+    __device__ __forceinline__ int count() const { return both.count(); }
+    __device__ __forceinline__ int tile(int i) const { return both.tile(i); }
+    __device__ __forceinline__ int count(int w) const {
+        if (SPLIT) return (both.count() + 1 - w) / 2;
+        return w ? x[1].count() : x[0].count();
+    }
+    // whether query tile w visits position i, which holds tile t
+    __device__ __forceinline__ bool has(int w, int i, int t) const {
+        if (SPLIT) return (i & 1) == w;
+        const Tiles& me = w ? x[1] : x[0];
+        return t < me.hi && (t < me.sink || t >= me.lo);
+    }
+    // position of the m-th tile of query tile w, which is t
+    __device__ __forceinline__ int at(int w, int m, int t) const {
+        if (SPLIT) return 2 * m + w;
+        return t < both.sink ? t : both.sink + t - both.lo;
+    }
 };
 
 __device__ __forceinline__ Tiles tiles_of(const WindowParams& p, int head, int qb) {
@@ -221,37 +244,37 @@ __device__ __forceinline__ Tiles tiles_of(const WindowParams& p, int head, int q
     return x;
 }
 
-__device__ __forceinline__ Item item_of(const WindowParams& p, int t) {
+template <bool SPLIT>
+__device__ __forceinline__ Item<SPLIT> item_of(const WindowParams& p, int t) {
     // last rows first; at a row, all pairs of all batches next to each other
-    Item it;
+    Item<SPLIT> it;
     const int per_row = p.B * p.pairs;
     const int row = p.rows - 1 - t / per_row;
     const int r = t - (t / per_row) * per_row;
     it.b = r / p.pairs;
     const int pair = r - it.b * p.pairs;
     const int group = p.Hq / p.Hkv;
-    if (p.by_heads) {
+    if (!SPLIT && p.pairing == kHeads) {
         it.kvh = 2 * pair / group;
         it.x[0] = tiles_of(p, 2 * pair, row);
         it.x[1] = it.x[0];
         it.x[1].head = 2 * pair + 1;
-        it.lo = it.x[0].lo;
-        it.hi = it.x[0].hi;
-        it.sink = it.x[0].sink;
-    } else {
+        it.both = it.x[0];
+    } else if (!SPLIT) {
         it.kvh = pair / group;
         it.x[0] = tiles_of(p, pair, 2 * row);
         it.x[1] = tiles_of(p, pair, 2 * row + 1);
         // the second block is the later one: its keys start and end no earlier
-        const Tiles& a = it.x[0].hi > 0 ? it.x[0] : it.x[1];
-        it.lo = a.lo;
-        it.sink = a.sink;
-        it.hi = max(it.x[0].hi, it.x[1].hi);
+        it.both = it.x[0].hi > 0 ? it.x[0] : it.x[1];
+        it.both.hi = max(it.x[0].hi, it.x[1].hi);
+    } else {
+        it.kvh = pair / group;
+        it.both = it.x[0] = it.x[1] = tiles_of(p, pair, row);
     }
     return it;
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     window_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const WindowParams p) {
@@ -273,7 +296,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* o_free = o_full + 2;                                    // [2] four warps
     uint64_t* fin = o_free + 2;                                       // [2]
     uint64_t* turn = fin + 2;                                         // [2] the other has issued
+    uint64_t* joined = turn + 2;                                      // four warps: query tile 1's (m, l)
     int* misc = reinterpret_cast<int*>(sm + C::kMisc);
+    float2* half_ml = reinterpret_cast<float2*>(sm + C::kHalf);
     volatile int* abort_flag = &misc[1];
     int* status = p.status;
 
@@ -293,6 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&fin[x], 1);
             mbar_init(&turn[x], 1);
         }
+        mbar_init(joined, 4);
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 2);
@@ -322,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int g = 0;                                   // tiles loaded, K and V counted apart
                 int nq[2] = {0, 0};                          // Q tiles loaded
                 bool ok = true;
-                auto load = [&](const CUtensorMap* map, int tile, const Item& it) {
+                auto load = [&](const CUtensorMap* map, int tile, const Item<SPLIT>& it) {
                     const int st = g % kStages;
                     if (g >= kStages && !wait_parity(&empty[st], (g / kStages - 1) & 1, deadline, abort_flag, status))
                         return false;
@@ -333,14 +359,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return true;
                 };
                 for (int t = blockIdx.x; ok && t < p.total_items; t += gridDim.x) {
-                    const Item it = item_of(p, t);
+                    const Item<SPLIT> it = item_of<SPLIT>(p, t);
                     deadline = global_timer_ns() + p.budget_ns;
                     const int n = it.count();
                     for (int i = 0; ok && i < n; ++i) {
                         ok = load(&tm_k, it.tile(i), it);
                         if (i == 0) {
                             for (int x = 0; ok && x < 2; ++x) {
-                                if (it.x[x].hi == 0) continue;
+                                if (it.count(x) == 0) continue;
                                 if (nq[x] > 0 && !wait_parity(&q_free[x], (nq[x] - 1) & 1, deadline, abort_flag, status)) {
                                     ok = false;
                                     break;
@@ -379,10 +405,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             int blk = 0, items = 0, rounds = 0;              // tiles, items and rounds of this query tile so far
             bool ok = true;
             for (int t = blockIdx.x; ok && t < p.total_items; t += gridDim.x) {
-                const Item it = item_of(p, t);
+                const Item<SPLIT> it = item_of<SPLIT>(p, t);
                 deadline = global_timer_ns() + p.budget_ns;
-                const Tiles me = x ? it.x[1] : it.x[0];
-                const int n = it.count(), mine = me.count();
+                const int n = it.count(), mine = it.count(x);
                 int done = 0;                                // S issued in this item
                 bool pend = false;                           // the tile before awaits its P V
                 // Round i: P V of the tile before, S of tile i.  A commit takes its turn among the products, so
@@ -391,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Every stage is waited for in turn, visited or not: a parity tells two of its uses apart, no more.
                 for (int i = 0; ok && i <= n && n > 0; ++i) {
                     const int gk = g + 2 * i, sk = gk % kStages;
-                    const bool visit = i < n && me.has(it.tile(i));
+                    const bool visit = i < n && it.has(x, i, it.tile(i));
                     if (i > 0)
                         ok = warp_wait_parity(&full[(gk - 1) % kStages], ((gk - 1) / kStages) & 1, deadline, abort_flag, status);
                     if (ok && i < n) ok = warp_wait_parity(&full[sk], (gk / kStages) & 1, deadline, abort_flag, status);
@@ -466,10 +491,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         int blk = 0, items = 0, g = 0;
         bool ok = true;
         for (int t = blockIdx.x; ok && t < p.total_items; t += gridDim.x) {
-            const Item it = item_of(p, t);
+            const Item<SPLIT> it = item_of<SPLIT>(p, t);
             deadline = global_timer_ns() + p.budget_ns;
             const Tiles me = x ? it.x[1] : it.x[0];
-            const int n = me.count();
+            const int n = it.count(x);
             const int g0 = g;                            // ring position of the item's first K tile
             g += 2 * it.count();
             // Both query tiles give every stage back.  One that this tile does not visit goes back unread, but
@@ -490,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row = me.qb * 128 + lrow;
             const int pos = row + p.Sk - p.Sq;
             T* out = reinterpret_cast<T*>(p.out) + it.b * p.out_b + me.head * p.out_h + row * p.out_s;
-            if (n == 0) {
+            if (n == 0 && !SPLIT) {
                 // no key, or (the partner of an odd last row block) no row
                 if (row < p.Sq)
                     for (int e = 0; e < D / 8; ++e) reinterpret_cast<uint4*>(out)[e] = make_uint4(0, 0, 0, 0);
@@ -502,9 +527,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int lo = pos >= p.window ? pos - p.window + 1 : 0;
             float m_used = -INFINITY, l = 0.f;
             for (int i = 0; i < n; ++i, ++blk) {
-                const int tile = i < me.sink ? i : me.lo + (i - me.sink);
+                const int tile = SPLIT ? it.tile(2 * i + x) : me.tile(i);
                 const int key0 = 128 * tile;
-                const int u = tile < it.sink ? tile : it.sink + tile - it.lo;
+                const int u = it.at(x, i, tile);
                 if (speaks) skip_to(u, next);
                 __syncwarp();
                 if (!warp_wait_parity(&s_full[x], blk & 1, deadline, abort_flag, status)) {
@@ -601,23 +626,61 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
             // ---- O / l to memory
-            if (!warp_wait_parity(&o_full[x], items & 1, deadline, abort_flag, status)) {
+            if ((!SPLIT || n > 0) && !warp_wait_parity(&o_full[x], items & 1, deadline, abort_flag, status)) {
                 ok = false;
                 break;
             }
-            ++items;
+            if (!SPLIT || n > 0) ++items;
             tc_fence_after();
             if (speaks) {
-                mbar_arrive(&empty[v_read]);
+                if (!SPLIT || n > 0) mbar_arrive(&empty[v_read]);
                 skip_to(n_union, next);
             }
             __syncwarp();
+            float scale0 = 1.f, scale1 = 0.f;
+            if (SPLIT) {
+                // query tile 0's threads join both halves of a row: tile 1's O is in the same TMEM lane.  (A CTA
+                // has one item then, so nothing overwrites it.)
+                if (x == 1) {
+                    half_ml[lrow] = make_float2(m_used, l);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(joined);
+                    continue;
+                }
+                if (!warp_wait_parity(joined, 0, deadline, abort_flag, status) ||
+                    (it.count(1) > 0 && !warp_wait_parity(&o_full[1], 0, deadline, abort_flag, status))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const float2 other = half_ml[lrow];
+                const float top = fmaxf(m_used, other.x);
+                const float ref = top == -INFINITY ? 0.f : top;
+                // a half without a finite score has l = 0, or NaN if it met one: either way it counts
+                scale0 = m_used == -INFINITY ? 1.f : ex2_approx((m_used - ref) * c);
+                scale1 = other.x == -INFINITY ? 1.f : ex2_approx((other.x - ref) * c);
+                l = l * scale0 + other.y * scale1;
+            }
+            const bool two = SPLIT && it.count(1) > 0;
             const float inv = l == 0.f ? 0.f : 1.f / l;         // NaN stays NaN
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
                 uint32_t o[32];
                 tmem_ld_row32(to + c0, o);
                 tmem_wait_ld();
+                if (SPLIT && n == 0) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0u;
+                }
+                if (two) {
+                    uint32_t o1[32];
+                    tmem_ld_row32(to + D + c0, o1);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = __float_as_uint(__uint_as_float(o[e]) * scale0 + __uint_as_float(o1[e]) * scale1);
+                }
                 if (c0 + 32 == D) {
                     // O is in registers: the next item's first P V may overwrite it
                     tc_fence_before();
@@ -662,7 +725,7 @@ bool map_strides(const int64_t* st, int B, int H, int S, int d, uint64_t (&bytes
     return true;
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool SPLIT>
 int launch(const void* q, const void* k, const void* v, const int64_t (&st)[12], const WindowParams& prm,
            cudaStream_t stream) {
     uint64_t qs[3], ks[3], vs[3];
@@ -678,7 +741,7 @@ int launch(const void* q, const void* k, const void* v, const int64_t (&st)[12],
     if (!rc) rc = encode_4d(&tk, k, BF16, dk, ks, box);
     if (!rc) rc = encode_4d(&tv, v, BF16, dk, vs, box);
     if (rc) return rc;
-    auto kern = window_kernel<D, BF16>;
+    auto kern = window_kernel<D, BF16, SPLIT>;
     static std::atomic<unsigned long long> raised{0};
     rc = raise_smem_limit(reinterpret_cast<const void*>(kern), Cfg<D>::kBytes, raised);
     if (rc) return rc;
@@ -689,9 +752,7 @@ int launch(const void* q, const void* k, const void* v, const int64_t (&st)[12],
                a.numRegs * kThreads >= 128 * (2 * kRegsSoftmax + kRegsOther);
     }();
     if (!enough) return BSATTN_ERR_CUDA;
-    int sms = num_sms_of_current_device();
-    if (sms <= 0) sms = 148;
-    const int grid = prm.total_items < sms ? prm.total_items : sms;
+    const int grid = prm.total_items < prm.sms ? prm.total_items : prm.sms;
     kern<<<static_cast<unsigned>(grid), kThreads, Cfg<D>::kBytes, stream>>>(tq, tk, tv, prm);
     return cudaGetLastError() == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
 }
@@ -743,16 +804,38 @@ extern "C" int bsattn_prefill_window(const void* q, const void* k, const void* v
     prm.window = window;
     prm.sinks = sinks;
     prm.nq = (Sq + 127) / 128;
-    prm.by_heads = (Hq / Hkv) % 2 == 0;
-    prm.pairs = prm.by_heads ? Hq / 2 : Hq;
-    prm.rows = prm.by_heads ? prm.nq : (prm.nq + 1) / 2;
+    // Where there is an SM for every query tile, both tiles of a CTA are the same one, each with half of its
+    // keys (257 rows of 8 heads after 8192 cached tokens, window 1024: 20.8 us against 23.7).
+    int sms = num_sms_of_current_device();
+    if (sms <= 0) sms = 148;
+    if (static_cast<long long>(B) * Hq * prm.nq <= sms) {
+        prm.pairing = kSplit;
+        prm.pairs = Hq;
+        prm.rows = prm.nq;
+    } else if ((Hq / Hkv) % 2 == 0) {
+        prm.pairing = kHeads;
+        prm.pairs = Hq / 2;
+        prm.rows = prm.nq;
+    } else {
+        prm.pairing = kRows;
+        prm.pairs = Hq;
+        prm.rows = (prm.nq + 1) / 2;
+    }
     const long long items = static_cast<long long>(B) * prm.pairs * prm.rows;
     if (items > 0x3fffffffLL) return BSATTN_ERR_UNSUPPORTED;
     prm.total_items = static_cast<int>(items);
+    prm.sms = sms;
     prm.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(d)));
     prm.budget_ns = wait_budget_ns();
     if (Sk == 0) k = v = q;                     // no row sees a key: K and V are not read, only mapped
     const bool bf16 = dtype == BSATTN_BF16;
-    if (d == 64) return bf16 ? launch<64, true>(q, k, v, st, prm, cs) : launch<64, false>(q, k, v, st, prm, cs);
-    return bf16 ? launch<128, true>(q, k, v, st, prm, cs) : launch<128, false>(q, k, v, st, prm, cs);
+    const auto run = [&](auto dim, auto split) {
+        constexpr int D = decltype(dim)::value;
+        constexpr bool SPLIT = decltype(split)::value;
+        return bf16 ? launch<D, true, SPLIT>(q, k, v, st, prm, cs) : launch<D, false, SPLIT>(q, k, v, st, prm, cs);
+    };
+    using D64 = std::integral_constant<int, 64>;
+    using D128 = std::integral_constant<int, 128>;
+    if (prm.pairing == kSplit) return d == 64 ? run(D64{}, std::true_type{}) : run(D128{}, std::true_type{});
+    return d == 64 ? run(D64{}, std::false_type{}) : run(D128{}, std::false_type{});
 }

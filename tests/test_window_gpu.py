@@ -52,6 +52,25 @@ def test_prefill_many_items_a_cta(bsa):
     _prefill(bsa, 2, 9, 3, 2950, 2950, 64, F16, 333, 200, seed=4)
 
 
+@pytest.mark.parametrize("d,dtype", [(64, F16), (128, BF16)])
+@pytest.mark.parametrize("heads", [(2, 1), (3, 3), (60, 12)])
+def test_prefill_few_and_many_query_tiles(bsa, heads, d, dtype):
+    """The same lengths with few query tiles (a tile's keys shared out within a CTA) and with many."""
+    for Sq, Sk, window, sinks in ((200, 900, 300, 4), (130, 2000, 5000, 0), (256, 1500, 100, 700), (300, 140, 64, 3),
+                                  (1, 700, 640, 129), (129, 129, 1, 0)):
+        _prefill(bsa, 1, *heads, Sq, Sk, d, dtype, window, sinks, seed=Sq)
+
+
+def test_prefill_nan_reaches_its_row_from_either_half(bsa):
+    q = _rand(1, 1, 100, 128, dtype=BF16, seed=1)
+    k, v = _rand(1, 1, 1000, 128, dtype=BF16, seed=2), _rand(1, 1, 1000, 128, dtype=BF16, seed=3)
+    for at in (3, 950):                                         # in the first half of the keys, in the second
+        bad = k.clone()
+        bad[0, 0, at] = float("nan")
+        got = bsa.bsattn_prefill_window(q, bad, v, 2000, 0)
+        assert torch.equal(got.isnan().any(-1)[0, 0], torch.arange(900, 1000, device="cuda") >= at)
+
+
 def test_prefill_large_scores_rescale(bsa):
     """Scores that keep growing along a row: the reference maximum moves and O is rescaled."""
     q = _rand(1, 2, 600, 128, dtype=F16, seed=9)
