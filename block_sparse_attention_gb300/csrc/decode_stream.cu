@@ -8,14 +8,15 @@
 //
 // Each K/V byte is used once, by the G <= 8 query heads of its kv head, so HBM bandwidth bounds
 // this, and everything is arranged around equal shares of bytes in flight:
-//   * The visible tokens of a sequence are cut into units (64 tokens at 4 bits, 32 at 16 bits).  All sequences' units, end to end, are cut into equal parts, one CTA for
-//     each (part, kv head), as many as fit the GPU at once: ragged lengths leave no CTA longer than
-//     another.  A CTA finds its part with one pass over the lengths.  The kv heads of a part run next
-//     to each other, so that neighbouring rows of a 16-bit cache are read at about the same time.
+//   * The visible tokens of a sequence are cut into units (64 tokens at 4 bits, 32 at 16 bits).  All
+//     sequences' units, end to end, are cut into equal parts, one CTA for each (part, kv head), as many as
+//     fit the GPU at once: ragged lengths leave no CTA longer than another.  A CTA finds its part with one
+//     pass over the lengths.  The kv heads of a part run next to each other, so that neighbouring rows of a
+//     16-bit cache are read at about the same time.
 //   * Each of a CTA's four warps takes every fourth unit and feeds itself: lane 0 issues the copies of
-//     its K and then its V into the warp's own ring of stages (TMA boxes with a 128-byte swizzle at 16 bits; plain
-//     bulk copies at 4 bits, where a unit of a head is contiguous), with an mbarrier for each stage.
-//     No producer warp, and warps wait for nothing but their own data.
+//     its K and then its V into the warp's own ring of stages (TMA boxes with a 128-byte swizzle at 16
+//     bits; plain bulk copies at 4 bits, where a unit of a head is contiguous), with an mbarrier for each
+//     stage.  No producer warp, and warps wait for nothing but their own data.
 //   * The products are transposed, so that the G <= 8 heads are the n = 8 side of mma.sync m16n8k16:
 //     S^T [16 tokens x 8] = K Q^T and O^T [d x 8] += V^T P^T, P moving from the first product's
 //     accumulators to the second's operand by an in-register 8x8 transpose.
@@ -81,6 +82,7 @@ struct Ring {
     // 4 bits the conversions bound the kernel and it made no difference (139 us against 138).
     static constexpr int kStages = 2 * (128 / D);
     static constexpr int kCtas = KV4 ? 3 : 2;                    // resident CTAs per SM
+    static constexpr int kSpare = 128 / kTok * kWarps;           // 128 tokens a warp
     static constexpr uint32_t kCodes = kTok * D / 2;             // 4 bits: codes, then scales
     static constexpr uint32_t kScales = kTok * D / kGroup4;
     static constexpr uint32_t kStage = KV4 ? kCodes + kScales : kTok * D * 2;
@@ -205,10 +207,11 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
     uint8_t* ring = sm + warp * R::kRing;
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + R::kBars) + warp * kStages;
     int* key0_of = reinterpret_cast<int*>(sm + R::kKey0) + warp * kStages;
-    int* misc = reinterpret_cast<int*>(sm + R::kMisc);      // [0] abort [1] last [2] b [4..] warp sums
-    long long* start = reinterpret_cast<long long*>(misc + 4);          // [0] units before b
+    int* misc = reinterpret_cast<int*>(sm + R::kMisc);      // [0] abort [1] last [2] b [3] b's first part
+    long long* start = reinterpret_cast<long long*>(misc + 4);          // units [0] before b, [1] up to its end
     volatile int* abort_flag = &misc[0];
     __shared__ long long warp_sums[kWarps];
+    __shared__ int warp_parts[kWarps];
 
     const int part = blockIdx.x / p.Hkv, g = blockIdx.x - part * p.Hkv;
     const int G = p.Hq / p.Hkv;
@@ -252,26 +255,70 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
         if (w < warp) upto += warp_sums[w];
         total += warp_sums[w];
     }
-    // parts of a multiple of four units (one a warp), four rounds at least: a shorter part would cost
+    // parts of a multiple of four units (one a warp), two rounds at least: a shorter part would cost
     // more in joining than it gains
-    long long chunk = (total + p.parts - 1) / p.parts;
-    chunk = max((chunk + kWarps - 1) / kWarps * kWarps, 2ll * kWarps);
-    const long long x0 = part * chunk, x1 = min(x0 + chunk, total);
-    if (x0 >= total) return;                       // the whole CTA: x0 and total are the same for all
-    if (upto - sum <= x0 && x0 < upto) {
-        int b = tid * per;
-        long long before = upto - sum;
-        for (;; ++b) {
-            const int n = span_of<kTok>(p, b).n;
-            if (x0 < before + n) break;
-            before += n;
+    const auto part_of = [&](long long n) {
+        const long long c = (total + n - 1) / n;
+        return max((c + kWarps - 1) / kWarps * kWarps, 2ll * kWarps);
+    };
+    long long chunk = part_of(p.parts);
+    // A part that ends one sequence and begins another does both one after the other, with all their
+    // latencies: 4 to 5 us.  Where it makes the parts no more than kSpare units longer, every sequence is
+    // cut for itself: ceil(n_b / chunk) parts each, p.parts in all or fewer with this chunk.  (32 query
+    // heads, 8 kv heads, d = 128: 2 sequences of 1500 tokens 17.4 -> 11.7 us at 4 bits, 14.3 -> 10.0 us at
+    // 16; 8 of 9000 31.2 -> 26.1 us; done whatever the parts grow by, 32 of 9000 would take 118 us, not 73.)
+    bool apart = false;
+    if (p.B <= kThreads && p.B < p.parts) {
+        const long long longer = part_of(p.parts - p.B);
+        apart = longer - chunk <= R::kSpare;
+        if (apart) chunk = longer;
+    }
+    long long x0 = part * chunk;
+    if (apart) {
+        // thread t has sequence t's units
+        const int n = static_cast<int>((sum + chunk - 1) / chunk);
+        int parts_upto = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, parts_upto, o);
+            if (lane >= o) parts_upto += u;
         }
-        misc[2] = b;
-        start[0] = before;
+        if (lane == 31) warp_parts[warp] = parts_upto;
+        __syncthreads();
+        int parts = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) parts_upto += warp_parts[w];
+            parts += warp_parts[w];
+        }
+        if (part >= parts) return;                 // the whole CTA
+        if (parts_upto - n <= part && part < parts_upto) {
+            misc[2] = tid;
+            misc[3] = parts_upto - n;
+            start[0] = upto - sum;
+            start[1] = upto;
+        }
+    } else {
+        if (x0 >= total) return;                   // the whole CTA: x0 and total are the same for all
+        if (upto - sum <= x0 && x0 < upto) {
+            int b = tid * per;
+            long long before = upto - sum;
+            for (;; ++b) {
+                const int n = span_of<kTok>(p, b).n;
+                if (x0 < before + n) break;
+                before += n;
+            }
+            misc[2] = b;
+            start[0] = before;
+            start[1] = total;
+        }
     }
     __syncthreads();
     int b = misc[2];
     long long before = start[0];
+    const int first = misc[3];
+    if (apart) x0 = before + (part - first) * chunk;
+    const long long x1 = min(x0 + chunk, start[1]);
 
     int seq = 0;                                   // units this warp has issued, over all pieces
     bool ok = true;
@@ -710,14 +757,18 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
         }
         if (!whole) {
             // ------------------------------------------------------------ joining the pieces
-            const int c_first = static_cast<int>(before / chunk);
-            const int c_last = static_cast<int>((before + s.n - 1) / chunk);
+            const int c_first = apart ? first : static_cast<int>(before / chunk);
+            const int c_last = apart ? first + static_cast<int>((s.n - 1) / chunk)
+                                     : static_cast<int>((before + s.n - 1) / chunk);
             const int count = c_last - c_first + 1;
             __syncthreads();
             if (tid == 0) {
-                __threadfence();
-                misc[1] = atomicAdd(&p.tickets[c_first * p.Hkv + g], 1) == count - 1;
-                if (misc[1]) __threadfence();
+                int before_me;
+                asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
+                             : "=r"(before_me)
+                             : "l"(&p.tickets[c_first * p.Hkv + g])
+                             : "memory");
+                misc[1] = before_me == count - 1;
             }
             __syncthreads();
             if (misc[1]) {

@@ -332,6 +332,16 @@ def test_decode_many_sequences(bsa):
     _decode4(bsa, torch.randint(0, 200, (700,), generator=g).tolist(), 4, 2, 64, F16, 64, seed=8)
 
 
+@pytest.mark.parametrize("B", [2, 20, 56, 57, 58, 127, 128, 129])
+def test_decode_batches_about_the_number_of_parts(bsa, B):
+    """Sequences cut for themselves (few of them, or long parts) and end to end, with empty ones among them."""
+    for n, d in ((70, 64), (900, 128)):
+        lens = [0 if b % 7 == 3 else n + 53 * (b % 5) for b in range(B)]
+        got, _ = _decode4(bsa, lens, 8, 8, d, BF16, 64, seed=B + n)
+        assert all(got[b].abs().max() == 0 for b in range(B) if lens[b] == 0)
+    _decode4(bsa, [0] * B, 8, 8, 64, F16, 64, seed=B)
+
+
 def test_decode_chosen_blocks(bsa):
     lens = [1000, 64, 0, 3333]
     g = torch.Generator().manual_seed(4)

@@ -279,6 +279,19 @@ def test_decode_many_sequences(bsa):
     ref.check(got, *ref.decode(q, _Rows(k, v, table), lens, lambda b, g, m: ref.windowed(m, 90, 3, "cuda"), F16))
 
 
+@pytest.mark.parametrize("B", [2, 20, 37, 38, 39, 127, 128, 129])
+def test_decode_batches_about_the_number_of_parts(bsa, B):
+    """Sequences cut for themselves (few of them, or long parts) and end to end, with empty ones among them."""
+    for n, window, d in ((70, 40, 64), (900, 600, 128)):
+        lens = [0 if b % 7 == 3 else n + 53 * (b % 5) for b in range(B)]
+        k, v, table = _paged(lens, 8, d, BF16, 64, seed=B + n)
+        q = _rand(B, 8, d, dtype=BF16, seed=B)
+        got = bsa.bsattn_decode_window_paged(q, k, v, torch.tensor(lens, dtype=torch.int32, device="cuda"), table,
+                                             window, 5)
+        ref.check(got, *ref.decode(q, _Rows(k, v, table), lens, lambda b, g, m: ref.windowed(m, window, 5, "cuda"), BF16))
+        assert all(got[b].abs().max() == 0 for b in range(B) if lens[b] == 0)
+
+
 def test_decode_flags_bad_pages_and_lengths(bsa):
     lens = [200, 200, 200]
     k, v, table = _paged(lens, 2, 128, BF16, 64, seed=3)
