@@ -82,6 +82,7 @@ struct Ring {
     // 4 bits the conversions bound the kernel and it made no difference (139 us against 138).
     static constexpr int kStages = 2 * (128 / D);
     static constexpr int kCtas = KV4 ? 3 : 2;                    // resident CTAs per SM
+    static constexpr int kLeast = 64 / kTok * kWarps;            // units of a part: 64 tokens a warp
     static constexpr int kSpare = 128 / kTok * kWarps;           // 128 tokens a warp
     static constexpr uint32_t kCodes = kTok * D / 2;             // 4 bits: codes, then scales
     static constexpr uint32_t kScales = kTok * D / kGroup4;
@@ -255,17 +256,18 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
         if (w < warp) upto += warp_sums[w];
         total += warp_sums[w];
     }
-    // parts of a multiple of four units (one a warp), two rounds at least: a shorter part would cost
-    // more in joining than it gains
+    // parts of a multiple of four units (one a warp), 64 tokens a warp at least: one round at 4 bits (two
+    // would take 11.6 us for 1500 tokens, one takes 10.3), two at 16 bits (with one, 200 tokens took 8.5 us
+    // instead of 8.0 and 700 8.8 instead of 9.6: joining costs what the shorter loop gains)
     const auto part_of = [&](long long n) {
         const long long c = (total + n - 1) / n;
-        return max((c + kWarps - 1) / kWarps * kWarps, 2ll * kWarps);
+        return max((c + kWarps - 1) / kWarps * kWarps, static_cast<long long>(R::kLeast));
     };
     long long chunk = part_of(p.parts);
     // A part that ends one sequence and begins another does both one after the other, with all their
     // latencies: 4 to 5 us.  Where it makes the parts no more than kSpare units longer, every sequence is
     // cut for itself: ceil(n_b / chunk) parts each, p.parts in all or fewer with this chunk.  (32 query
-    // heads, 8 kv heads, d = 128: 2 sequences of 1500 tokens 17.4 -> 11.7 us at 4 bits, 14.3 -> 10.0 us at
+    // heads, 8 kv heads, d = 128: 2 sequences of 1500 tokens 17.4 -> 11.6 us at 4 bits, 14.3 -> 10.0 us at
     // 16; 8 of 9000 31.2 -> 26.1 us; done whatever the parts grow by, 32 of 9000 would take 118 us, not 73.)
     bool apart = false;
     if (p.B <= kThreads && p.B < p.parts) {
