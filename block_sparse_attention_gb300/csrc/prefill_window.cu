@@ -21,13 +21,22 @@
 //
 // 384 threads:
 //   warps 0-3 / 4-7   softmax and epilogue of query tile 0 / 1 (TMEM lane = row)
-//   warps 8 / 9       issue the products of query tile 0 / 1, P V(j) and S(j + 1) in turn.  One issuer's
-//                     products run in order: S(j + 1) may overwrite P(j) without a wait
+//   warps 8 / 9       issue the products of query tile 0 / 1, P V(j) and S(j + 1) in turn, j counting on
+//                     from one item to the next.  One issuer's products run in order: S(j + 1) may
+//                     overwrite P(j) without a wait
 //   warp 10           TMA: Q tiles, then K and V tiles through one ring of stages (warp 11 idles)
 // P is handed over in two halves of 64 keys, so that half of P V runs under the rest of the softmax.
 // The two issuers take turns, a P V and an S each, which keeps the query tiles half a period apart, one's
 // softmax under the other's products; left alone they fall into step and stay there (4500 cycles a round).
 // All other waits of an issuer come before the one for P, where they overlap the softmax.
+//
+// What bounds it, d = 128: the tensor core, in use 70 % of the time (the rest is the hand-over from S to P
+// and back, in part under the other query tile's products).  32 heads over 8 kv heads, 16384 tokens, window
+// 4096, bf16: 652 us, 1476 TFLOP/s.  d = 64: the softmax of a tile, 1600 cycles against 1024 of products,
+// and what an item starts and ends with (11 key tiles an item there: S of the next item under the epilogue
+// and the next item worked out while the last P V runs took 220 us to 213).  4 x 16 heads, 8191 tokens,
+// window 1024, fp16: 213 us, 606 TFLOP/s.
+//
 // TMEM: S_0 0-127, S_1 128-255, O_0 256.., O_1 256 + d...  Items are dealt out round-robin, last
 // rows first (they see the most keys), so CTAs at work at one time share K/V in L2.  Every wait is
 // bounded: on expiry the CTA records BSATTN_ERR_TIMEOUT, drains what is in flight and leaves.
@@ -401,80 +410,88 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t v_desc = sdesc_sw128(smem_u32(skv), 16384, 1024);
             constexpr uint32_t kTileDesc = C::kTile >> 4;
             const uint32_t ts = uniform(tbase + 128 * x), to = uniform(tbase + kOCol + D * x);
-            int g = 0;                                       // ring position: K of union tile i at g + 2 i, V after it
-            int blk = 0, items = 0, rounds = 0;              // tiles, items and rounds of this query tile so far
+            int g = 0;                                       // ring position: K of tile i of all items' at 2 i, V after it
+            int blk = 0, items = 0, outs = 0, rounds = 0;    // tiles, items (S begun, O begun) and rounds so far
+            bool pend = false, begins = false, ends = false; // a tile awaits its P V, which begins / ends its O
+            bool passed = false;                             // the tile before is not this query tile's
             bool ok = true;
+            // One round: P V of the tile before, be it of the item before, and S of the tile at position g, if
+            // there is one and this query tile visits it.  A commit takes its turn among the products, so there
+            // is only S's and the last P V's: the softmax warps pass on what it says about the stages and Q.
+            // Every stage is waited for in turn, visited or not: a parity tells two of its uses apart, no more.
+            // A stage that this query tile does not read it gives back here, but only once it is loaded: an arrival
+            // before that could count for the stage's use before.
+            // Of the waits, none is for anything that follows from this round: K of position g takes the stage
+            // of position g - 5 or an earlier one, which the softmax gave back for a round before.
+            auto round = [&](bool tile, bool visit, bool first, bool last) {
+                const int sk = g % kStages;
+                if (g > 0 && !warp_wait_parity(&full[(g - 1) % kStages], ((g - 1) / kStages) & 1, deadline, abort_flag, status))
+                    return false;
+                if (passed) mbar_arrive_if(lead, &empty[(g - 1) % kStages]);
+                if (tile && !warp_wait_parity(&full[sk], (g / kStages) & 1, deadline, abort_flag, status)) return false;
+                passed = tile && !visit;
+                if (passed) mbar_arrive_if(lead, &empty[sk]);
+                const uint64_t vb = uniform(v_desc + static_cast<uint32_t>((g + kStages - 1) % kStages) * kTileDesc);
+                const uint64_t kb = uniform(k_desc + static_cast<uint32_t>(sk) * kTileDesc);
+                if (visit && first) {
+                    if (!warp_wait_parity(&q_full[x], items & 1, deadline, abort_flag, status)) return false;
+                    ++items;
+                }
+                // tile 0's round comes after tile 1's round before, tile 1's after tile 0's
+                if (rounds + x > 0 && !warp_wait_parity(&turn[x], (rounds + x + 1) & 1, deadline, abort_flag, status))
+                    return false;
+                ++rounds;
+                if (pend) {
+                    if (begins) {
+                        if (outs > 0 && !warp_wait_parity(&o_free[x], (outs - 1) & 1, deadline, abort_flag, status))
+                            return false;
+                        ++outs;
+                    }
+                    if (!warp_wait_parity(&p_half[x], (blk - 1) & 1, deadline, abort_flag, status)) return false;
+                    // the first half of P V runs under the second half of the softmax
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_f16_ts_if(lead, to, ts + 8 * kk, vb + ((kk * 2048) >> 4), idO, (!begins || kk > 0) ? 1u : 0u);
+                    if (!warp_wait_parity(&p_full[x], (blk - 1) & 1, deadline, abort_flag, status)) return false;
+                }
+                tc_fence_after();
+                if (pend) {
+#pragma unroll
+                    for (int kk = 4; kk < 8; ++kk)
+                        mma_f16_ts_if(lead, to, ts + 8 * kk, vb + ((kk * 2048) >> 4), idO, 1u);
+                    if (ends) mma_commit_if(lead, &o_full[x]);
+                    pend = false;
+                }
+                if (visit) {
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+                        mma_f16_ss_if(lead, ts, q_desc + off, kb + off, idS, kk > 0 ? 1u : 0u);
+                    }
+                    mma_commit_if(lead, &s_full[x]);
+                    ++blk;
+                    pend = true;
+                    begins = first;
+                    ends = last;
+                }
+                mbar_arrive_if(lead, &turn[1 - x]);
+                return true;
+            };
             for (int t = blockIdx.x; ok && t < p.total_items; t += gridDim.x) {
                 const Item<SPLIT> it = item_of<SPLIT>(p, t);
                 deadline = global_timer_ns() + p.budget_ns;
                 const int n = it.count(), mine = it.count(x);
                 int done = 0;                                // S issued in this item
-                bool pend = false;                           // the tile before awaits its P V
-                // Round i: P V of the tile before, S of tile i.  A commit takes its turn among the products, so
-                // there is only S's and the last P V's: the softmax warps pass on what it says about the stages
-                // and Q.
-                // Every stage is waited for in turn, visited or not: a parity tells two of its uses apart, no more.
-                for (int i = 0; ok && i <= n && n > 0; ++i) {
-                    const int gk = g + 2 * i, sk = gk % kStages;
-                    const bool visit = i < n && it.has(x, i, it.tile(i));
-                    if (i > 0)
-                        ok = warp_wait_parity(&full[(gk - 1) % kStages], ((gk - 1) / kStages) & 1, deadline, abort_flag, status);
-                    if (ok && i < n) ok = warp_wait_parity(&full[sk], (gk / kStages) & 1, deadline, abort_flag, status);
-                    if (!ok) break;
-                    const uint64_t vb = uniform(v_desc + static_cast<uint32_t>((gk + kStages - 1) % kStages) * kTileDesc);
-                    const uint64_t kb = uniform(k_desc + static_cast<uint32_t>(sk) * kTileDesc);
-                    if (visit && done == 0) {
-                        if (!warp_wait_parity(&q_full[x], items & 1, deadline, abort_flag, status)) {
-                            ok = false;
-                            break;
-                        }
-                        ++items;
-                    }
-                    // tile 0's round comes after tile 1's round before, tile 1's after tile 0's
-                    if (rounds + x > 0 && !warp_wait_parity(&turn[x], (rounds + x + 1) & 1, deadline, abort_flag, status)) {
-                        ok = false;
-                        break;
-                    }
-                    ++rounds;
-                    if (pend) {
-                        if ((done == 1 && items > 1 &&
-                             !warp_wait_parity(&o_free[x], items & 1, deadline, abort_flag, status)) ||
-                            !warp_wait_parity(&p_half[x], (blk - 1) & 1, deadline, abort_flag, status)) {
-                            ok = false;
-                            break;
-                        }
-                        // the first half of P V runs under the second half of the softmax
-                        tc_fence_after();
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_f16_ts_if(lead, to, ts + 8 * kk, vb + ((kk * 2048) >> 4), idO, (done > 1 || kk > 0) ? 1u : 0u);
-                        if (!warp_wait_parity(&p_full[x], (blk - 1) & 1, deadline, abort_flag, status)) {
-                            ok = false;
-                            break;
-                        }
-                    }
-                    tc_fence_after();
-                    if (pend) {
-#pragma unroll
-                        for (int kk = 4; kk < 8; ++kk)
-                            mma_f16_ts_if(lead, to, ts + 8 * kk, vb + ((kk * 2048) >> 4), idO, (done > 1 || kk > 0) ? 1u : 0u);
-                        if (done == mine) mma_commit_if(lead, &o_full[x]);
-                        pend = false;
-                    }
-                    if (visit) {
-#pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-                            mma_f16_ss_if(lead, ts, q_desc + off, kb + off, idS, kk > 0 ? 1u : 0u);
-                        }
-                        mma_commit_if(lead, &s_full[x]);
-                        pend = true;
-                        ++blk;
-                        ++done;
-                    }
-                    mbar_arrive_if(lead, &turn[1 - x]);
+                for (int i = 0; ok && i < n; ++i, g += 2) {
+                    const bool visit = it.has(x, i, it.tile(i));
+                    ok = round(true, visit, done == 0, done == mine - 1);
+                    done += visit;
                 }
-                g += 2 * n;
+            }
+            if (ok) {
+                deadline = global_timer_ns() + p.budget_ns;
+                round(false, false, false, false);
             }
             mma_commit_if(lead, &fin[x]);
             wait_parity_drain(&fin[x], 0, global_timer_ns() + 200000000ull);
@@ -490,27 +507,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float c = p.scale_log2;
         int blk = 0, items = 0, g = 0;
         bool ok = true;
+        Item<SPLIT> it = item_of<SPLIT>(p, blockIdx.x);
         for (int t = blockIdx.x; ok && t < p.total_items; t += gridDim.x) {
-            const Item<SPLIT> it = item_of<SPLIT>(p, t);
-            deadline = global_timer_ns() + p.budget_ns;
             const Tiles me = x ? it.x[1] : it.x[0];
             const int n = it.count(x);
             const int g0 = g;                            // ring position of the item's first K tile
             g += 2 * it.count();
-            // Both query tiles give every stage back.  One that this tile does not visit goes back unread, but
-            // only once it is loaded: an arrival before that could count for the stage's use before.
             const bool speaks = (warp & 3) == 0 && lane == 0;
-            auto skip_to = [&](int i, int& next) {
-                for (; next < i; ++next) {
-                    const int at = g0 + 2 * next;
-                    for (int j = at; j < at + 2; ++j) {
-                        if (!wait_parity(&full[j % kStages], (j / kStages) & 1, deadline, abort_flag, status)) return;
-                        mbar_arrive(&empty[j % kStages]);
-                    }
-                }
-            };
-            const int n_union = it.count();
-            int next = 0;                                // union tile this query tile has not dealt with yet
             int v_read = -1;                             // stage of the V tile to give back when it is read
             const int row = me.qb * 128 + lrow;
             const int pos = row + p.Sk - p.Sq;
@@ -519,8 +522,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // no key, or (the partner of an odd last row block) no row
                 if (row < p.Sq)
                     for (int e = 0; e < D / 8; ++e) reinterpret_cast<uint4*>(out)[e] = make_uint4(0, 0, 0, 0);
-                if (speaks) skip_to(n_union, next);
-                __syncwarp();
+                it = item_of<SPLIT>(p, t + gridDim.x);
+                deadline = global_timer_ns() + p.budget_ns;
                 continue;
             }
             // keys [lo, pos] and, below lo, those before the sinks
@@ -530,8 +533,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int tile = SPLIT ? it.tile(2 * i + x) : me.tile(i);
                 const int key0 = 128 * tile;
                 const int u = it.at(x, i, tile);
-                if (speaks) skip_to(u, next);
-                __syncwarp();
                 if (!warp_wait_parity(&s_full[x], blk & 1, deadline, abort_flag, status)) {
                     ok = false;
                     break;
@@ -543,7 +544,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int at = g0 + 2 * u;
                     mbar_arrive(&empty[at % kStages]);
                     v_read = (at + 1) % kStages;
-                    next = u + 1;
                     if (i == n - 1) mbar_arrive(&q_free[x]);
                 }
                 __syncwarp();
@@ -625,6 +625,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(&p_full[x]);
             }
             if (!ok) break;
+            // the next item (past the last one: unused) is worked out while the last P V runs
+            const Item<SPLIT> after = item_of<SPLIT>(p, t + gridDim.x);
+            deadline = global_timer_ns() + p.budget_ns;
             // ---- O / l to memory
             if ((!SPLIT || n > 0) && !warp_wait_parity(&o_full[x], items & 1, deadline, abort_flag, status)) {
                 ok = false;
@@ -632,10 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!SPLIT || n > 0) ++items;
             tc_fence_after();
-            if (speaks) {
-                if (!SPLIT || n > 0) mbar_arrive(&empty[v_read]);
-                skip_to(n_union, next);
-            }
+            if (speaks && (!SPLIT || n > 0)) mbar_arrive(&empty[v_read]);
             __syncwarp();
             float scale0 = 1.f, scale1 = 0.f;
             if (SPLIT) {
@@ -698,6 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             make_uint4(ob[4 * k], ob[4 * k + 1], ob[4 * k + 2], ob[4 * k + 3]);
                 }
             }
+            it = after;
         }
     }
 
