@@ -26,6 +26,15 @@
 //     channels of four tokens (8 bytes each): wide shared-memory loads, one or two scales for each.
 //   * A piece of a (sequence, kv head) that is not whole goes to the workspace as (O / l, log-sum-exp);
 //     the last CTA to finish (atomic ticket) joins the pieces in a fixed order.
+//
+// What bounds it, 32 query heads over 8 kv heads, d = 128, bf16:
+//   16 bits, 192 sequences with a 4096 window (2.94 GB): 407 us, 7.2 TB/s, all that HBM gives a reader.
+//   4 bits, 16 sequences of 8k-64k tokens (715 MB): 139 us, 5.1 TB/s.  Bound by turning codes into fp16
+//     operands (issue slots 57 %, ALU 48 %): 111 us without the arithmetic, 135 us without the copies.
+//   Short calls are a chain of latencies: 8 sequences with a 1024 window (34 MB) 11.6 us, one sequence of
+//     16385 tokens at 4 bits (19 MB) 15.6 us.  Of those, 1.1 us go to finding the part, 0.9 to the table,
+//     0.8 to the first copy, 4 to two units a warp, 1.6 to the pieces and the ticket, 3 to joining 33 pieces,
+//     and 2.5 to the launch.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -12,7 +12,9 @@
 //
 // Gather is the way back: code * s * u rounded to the output type.
 //
-// Both move each byte once and are bound by memory: 2 bytes a channel one way, 0.5625 the other.
+// Both move each byte once and are bound by memory: 2 bytes a channel one way, 0.5625 the other.  65521
+// rows of 8 heads, d = 128, keys and values (344 MB each way): append 58 us and gather 57 us, 5.9 and 6.1
+// TB/s; 61 rows: both in 4.8 us.
 // A warp takes a token, so that the slot's division is made once a token.  On the way in a lane takes
 // a group, two of keys and two of values at a time (128 bytes a lane in flight); on the way out half a
 // group, so that a warp's 16-byte stores are contiguous, four of each.  Writing whole groups out, two

@@ -13,7 +13,8 @@
 // L2-resident and few) and keeps the results in shared memory: one launch, no workspace that two
 // calls could disturb, no CTA that waits on another.  Tokens are dealt out over the CTAs and find
 // their sequence by bisection in shared memory; a new page's number is read from the free list, not
-// from the table, so that nothing is read that another CTA writes.
+// from the table, so that nothing is read that another CTA writes.  A step of 8 sequences takes 4.6 us,
+// a tick of 2000 with 493k slots (4 MB written) 9.9 us: the launch, one trip to L2 and the scans.
 #include <climits>
 
 #include "host_internal.h"
