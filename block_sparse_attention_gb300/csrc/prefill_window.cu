@@ -34,8 +34,8 @@
 // and back, in part under the other query tile's products).  32 heads over 8 kv heads, 16384 tokens, window
 // 4096, bf16: 652 us, 1476 TFLOP/s.  d = 64: the softmax of a tile, 1600 cycles against 1024 of products,
 // and what an item starts and ends with (11 key tiles an item there: S of the next item under the epilogue
-// and the next item worked out while the last P V runs took 220 us to 213).  4 x 16 heads, 8191 tokens,
-// window 1024, fp16: 213 us, 606 TFLOP/s.
+// and the next item worked out while the last P V runs took 220 us to 213, the look at O for
+// NaN 213 to 218).  4 x 16 heads, 8191 tokens, window 1024, fp16: 218 us, 592 TFLOP/s.
 //
 // TMEM: S_0 0-127, S_1 128-255, O_0 256.., O_1 256 + d...  Items are dealt out round-robin, last
 // rows first (they see the most keys), so CTAs at work at one time share K/V in L2.  Every wait is
@@ -84,6 +84,10 @@ struct WindowParams {
     void* out;
     int* status;
     long long out_b, out_h, out_s;       // element strides of out
+    const void* q;                       // what the tensor maps show, for rows that are worked out again
+    const void* k;
+    const void* v;
+    long long q_b, q_h, q_s, k_b, k_h, k_s, v_b, v_h, v_s;
     int B, Hq, Hkv, Sq, Sk;
     int window, sinks;
     int nq;                              // 128-row query blocks
@@ -281,6 +285,88 @@ __device__ __forceinline__ Item<SPLIT> item_of(const WindowParams& p, int t) {
         it.both = it.x[0] = it.x[1] = tiles_of(p, pair, row);
     }
     return it;
+}
+
+// P V takes all 128 keys of a tile, those that a row does not see with weight 0, and 0 times an infinity or
+// a NaN is NaN.  Where V holds one in a tile that a row sees in part, rows come out NaN that do not see it.
+// Those are found by their O, and worked out again by a warp each, over the keys that they see; a row that
+// does see one is left as it is.  (Looking V over before the product instead, in partly seen tiles alone,
+// cost calls without any 8 to 24 %; the look at O costs 0 to 3 %.)
+
+// The keys that a row sees, from its own back, then the sinks.
+struct Seen {
+    int pos, near, n;
+    __device__ __forceinline__ Seen(const WindowParams& p, int row) {
+        pos = row + p.Sk - p.Sq;
+        const int lo = pos >= p.window ? pos - p.window + 1 : 0;
+        near = pos + 1 - lo;
+        n = near + min(p.sinks, lo);
+    }
+    __device__ __forceinline__ int key(int i) const { return i < near ? pos - i : i - near; }
+};
+
+template <bool BF16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+    if constexpr (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    else return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// Whether a row sees an infinity or a NaN in V.
+template <int D, bool BF16>
+__device__ __noinline__ bool row_meets_spoilt(const WindowParams& p, int b, int head, int row) {
+    const int lane = threadIdx.x & 31, kvh = head / (p.Hq / p.Hkv);
+    const uint16_t* v = static_cast<const uint16_t*>(p.v) + b * p.v_b + kvh * p.v_h;
+    const Seen seen(p, row);
+    for (int i0 = 0; i0 < seen.n; i0 += 32) {
+        float sum = 0.f;
+        if (i0 + lane < seen.n) {
+            const uint32_t* r = reinterpret_cast<const uint32_t*>(v + seen.key(i0 + lane) * p.v_s);
+            for (int e = 0; e < D / 2; ++e) {
+                const float2 f = unpack2<BF16>(r[e]);
+                sum += f.x * 0.f + f.y * 0.f;
+            }
+        }
+        if (__any_sync(0xffffffffu, sum != 0.f)) return true;
+    }
+    return false;
+}
+
+// A row's output over the keys that it sees, m and 1 / l being known.
+template <int D, bool BF16>
+__device__ __noinline__ void mend_row(const WindowParams& p, int b, int head, int row, float m, float inv) {
+    constexpr int kPairs = D / 64;                               // of channels, a lane's
+    const int lane = threadIdx.x & 31, kvh = head / (p.Hq / p.Hkv);
+    const uint16_t* q = static_cast<const uint16_t*>(p.q) + b * p.q_b + head * p.q_h + row * p.q_s;
+    const uint16_t* k = static_cast<const uint16_t*>(p.k) + b * p.k_b + kvh * p.k_h;
+    const uint16_t* v = static_cast<const uint16_t*>(p.v) + b * p.v_b + kvh * p.v_h + 2 * kPairs * lane;
+    const Seen seen(p, row);
+    float2 o[kPairs] = {};
+    for (int i0 = 0; i0 < seen.n; i0 += 32) {
+        float w = 0.f;
+        if (i0 + lane < seen.n) {
+            const uint32_t* r = reinterpret_cast<const uint32_t*>(k + seen.key(i0 + lane) * p.k_s);
+            float dot = 0.f;
+            for (int e = 0; e < D / 2; ++e) {
+                const float2 a = unpack2<BF16>(r[e]), f = unpack2<BF16>(reinterpret_cast<const uint32_t*>(q)[e]);
+                dot += a.x * f.x + a.y * f.y;
+            }
+            w = unpack2<BF16>(pack2<BF16>(ex2_approx((dot - m) * p.scale_log2), 0.f)).x;
+        }
+        for (int e = 0; e < 32 && i0 + e < seen.n; ++e) {
+            const float we = __shfl_sync(0xffffffffu, w, e);
+            const uint32_t* r = reinterpret_cast<const uint32_t*>(v + seen.key(i0 + e) * p.v_s);
+#pragma unroll
+            for (int c = 0; c < kPairs; ++c) {
+                const float2 f = unpack2<BF16>(r[c]);
+                o[c].x += we * f.x;
+                o[c].y += we * f.y;
+            }
+        }
+    }
+    uint16_t* out = static_cast<uint16_t*>(p.out) + b * p.out_b + head * p.out_h + row * p.out_s + 2 * kPairs * lane;
+    __syncwarp();                                                // out may be q: all lanes have read it
+#pragma unroll
+    for (int c = 0; c < kPairs; ++c) reinterpret_cast<uint32_t*>(out)[c] = pack2<BF16>(o[c].x * inv, o[c].y * inv);
 }
 
 template <int D, bool BF16, bool SPLIT>
@@ -661,42 +747,58 @@ __global__ void __launch_bounds__(kThreads, 1)
                 scale0 = m_used == -INFINITY ? 1.f : ex2_approx((m_used - ref) * c);
                 scale1 = other.x == -INFINITY ? 1.f : ex2_approx((other.x - ref) * c);
                 l = l * scale0 + other.y * scale1;
+                m_used = top;
             }
             const bool two = SPLIT && it.count(1) > 0;
             const float inv = l == 0.f ? 0.f : 1.f / l;         // NaN stays NaN
-#pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 32) {
-                uint32_t o[32];
-                tmem_ld_row32(to + c0, o);
-                tmem_wait_ld();
-                if (SPLIT && n == 0) {
+            uint32_t o[D];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = 0u;
+            for (int c0 = 0; c0 < D; c0 += 32) tmem_ld_row32(to + c0, o + c0);
+            tmem_wait_ld();
+            if (SPLIT) {
+                if (n == 0) {
+#pragma unroll
+                    for (int e = 0; e < D; ++e) o[e] = 0u;
                 }
                 if (two) {
-                    uint32_t o1[32];
-                    tmem_ld_row32(to + D + c0, o1);
-                    tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        o[e] = __float_as_uint(__uint_as_float(o[e]) * scale0 + __uint_as_float(o1[e]) * scale1);
-                }
-                if (c0 + 32 == D) {
-                    // O is in registers: the next item's first P V may overwrite it
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&o_free[x]);
-                }
-                if (row < p.Sq) {
-                    uint32_t ob[16];
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t o1[32];
+                        tmem_ld_row32(to + D + c0, o1);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        ob[e] = l == 0.f ? 0u : pack2<BF16>(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        reinterpret_cast<uint4*>(out)[c0 / 8 + k] =
-                            make_uint4(ob[4 * k], ob[4 * k + 1], ob[4 * k + 2], ob[4 * k + 3]);
+                        for (int e = 0; e < 32; ++e)
+                            o[c0 + e] = __float_as_uint(__uint_as_float(o[c0 + e]) * scale0 + __uint_as_float(o1[e]) * scale1);
+                    }
                 }
+            }
+            // O is in registers: the next item's first P V may overwrite it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&o_free[x]);
+            float spoilt = 0.f;
+#pragma unroll
+            for (int e = 0; e < D; ++e) spoilt += __uint_as_float(o[e]) * 0.f;
+            // (a NaN in l is the row's own: of a score)
+            uint32_t rows = __ballot_sync(0xffffffffu, spoilt != 0.f && l > 0.f && row < p.Sq), mend = 0u;
+            for (; rows != 0u; rows &= rows - 1) {
+                const int at = __ffs(rows) - 1;
+                if (!row_meets_spoilt<D, BF16>(p, it.b, me.head, row - lane + at)) mend |= 1u << at;
+            }
+            if (row < p.Sq && !(mend >> lane & 1u)) {
+#pragma unroll
+                for (int c0 = 0; c0 < D; c0 += 8) {
+                    uint32_t ob[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        ob[e] = l == 0.f ? 0u : pack2<BF16>(__uint_as_float(o[c0 + 2 * e]) * inv, __uint_as_float(o[c0 + 2 * e + 1]) * inv);
+                    reinterpret_cast<uint4*>(out)[c0 / 8] = make_uint4(ob[0], ob[1], ob[2], ob[3]);
+                }
+            }
+            for (; mend != 0u; mend &= mend - 1) {
+                const int at = __ffs(mend) - 1;
+                mend_row<D, BF16>(p, it.b, me.head, row - lane + at, __shfl_sync(0xffffffffu, m_used, at),
+                                  __shfl_sync(0xffffffffu, inv, at));
             }
             it = after;
         }
@@ -793,10 +895,23 @@ extern "C" int bsattn_prefill_window(const void* q, const void* k, const void* v
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     WindowParams prm{};
     prm.out = out;
+    prm.q = q;
+    prm.k = k;
+    prm.v = v;
+    const auto stride = [&](int at, int entries) -> long long { return entries > 1 ? st[at] : 0; };
+    prm.q_b = stride(0, B);
+    prm.q_h = stride(1, Hq);
+    prm.q_s = stride(2, Sq);
+    prm.k_b = stride(3, B);
+    prm.k_h = stride(4, Hkv);
+    prm.k_s = stride(5, Sk);
+    prm.v_b = stride(6, B);
+    prm.v_h = stride(7, Hkv);
+    prm.v_s = stride(8, Sk);
     prm.status = static_cast<int*>(workspace);
-    prm.out_b = B > 1 ? st[9] : 0;
-    prm.out_h = Hq > 1 ? st[10] : 0;
-    prm.out_s = Sq > 1 ? st[11] : 0;
+    prm.out_b = stride(9, B);
+    prm.out_h = stride(10, Hq);
+    prm.out_s = stride(11, Sq);
     prm.B = B;
     prm.Hq = Hq;
     prm.Hkv = Hkv;
@@ -806,7 +921,7 @@ extern "C" int bsattn_prefill_window(const void* q, const void* k, const void* v
     prm.sinks = sinks;
     prm.nq = (Sq + 127) / 128;
     // Where there is an SM for every query tile, both tiles of a CTA are the same one, each with half of its
-    // keys (257 rows of 8 heads after 8192 cached tokens, window 1024: 20.8 us against 23.7).
+    // keys (257 rows of 8 heads after 8192 cached tokens, window 1024: 21.5 us against 23.7).
     int sms = num_sms_of_current_device();
     if (sms <= 0) sms = 148;
     if (static_cast<long long>(B) * Hq * prm.nq <= sms) {

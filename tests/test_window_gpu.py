@@ -122,6 +122,32 @@ def test_prefill_masked_keys_do_not_matter(bsa):
     assert torch.equal(a, bsa.bsattn_prefill_window(q, k2, v2, 40, 4))
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(2, 1), (3, 3), (64, 16)])
+@pytest.mark.parametrize("d,dtype", [(64, F16), (128, BF16)])
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), float("-inf")])
+def test_prefill_values_a_row_does_not_see_do_not_matter(bsa, Hq, Hkv, d, dtype, what):
+    """Infinities and NaN in V reach the rows that see their key, all of those and no others."""
+    S, window, sinks = 777, 200, 3
+    q = _rand(1, Hq, S, d, dtype=dtype, seed=1)
+    k, v = _rand(1, Hkv, S, d, dtype=dtype, seed=2), _rand(1, Hkv, S, d, dtype=dtype, seed=3)
+    want, bound = ref.window_prefill(q, k, v, window, sinks)
+    j, p = torch.arange(S, device="cuda"), torch.arange(S, device="cuda")[:, None]
+    sees = (j <= p) & ((j < sinks) | (j > p - window))
+    for keys in ([500], [1], [127, 128], [640, 700, 776], list(range(600, S)), list(range(0, 300))):
+        bad = v.clone()
+        bad[:, :, keys, 5:9] = what
+        got = bsa.bsattn_prefill_window(q, k, bad, window, sinks)
+        hit = sees[:, keys].any(-1)
+        ref.check(got[:, :, ~hit], want[:, :, ~hit], bound[:, :, ~hit])
+        assert not got[:, :, hit, 5:9].isfinite().any()
+    qv = q.transpose(1, 2).contiguous().transpose(1, 2)                 # strided, and over the queries
+    kv, bad = k.transpose(1, 2).contiguous().transpose(1, 2), v.transpose(1, 2).contiguous().transpose(1, 2)
+    bad[:, :, 700] = what
+    bsa.bsattn_prefill_window(qv, kv, bad, window, sinks, out=qv)
+    ref.check(qv[:, :, :700], want[:, :, :700], bound[:, :, :700])
+    assert not qv[:, :, 700:].isfinite().any()
+
+
 def test_prefill_nan_query_is_not_hidden(bsa):
     q = _rand(1, 2, 70, 64, dtype=F16, seed=1)
     k, v = _rand(1, 2, 70, 64, dtype=F16, seed=2), _rand(1, 2, 70, 64, dtype=F16, seed=3)
