@@ -518,8 +518,10 @@ def bsattn_paged_plan(cached_lens, new_lens, free_pages, free_count, block_table
             return bsattn_paged_plan(cached_lens, new_lens, free_pages, free_count, block_table, page_size,
                                      max_tokens, ws)
     page_size, max_tokens = _int(page_size), _int(max_tokens)
-    slots = cached_lens.new_empty(max(max_tokens, 0), dtype=_I64)
-    starts, seqlens, left = cached_lens.new_empty(B + 1), torch.empty_like(cached_lens), torch.empty_like(free_count)
+    device = cached_lens.device
+    slots = torch.empty(max(max_tokens, 0), dtype=_I64, device=device)
+    starts = torch.empty(B + 1, dtype=_I32, device=device)
+    seqlens, left = torch.empty_like(cached_lens), torch.empty_like(free_count)
     if ws is None:
         ws = status_workspace(i)
     rc = load().bsattn_paged_plan(cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
@@ -610,7 +612,7 @@ def bsattn_kv4_gather(slots, cache, dtype, k_scale: float = 1.0, v_scale: float 
         with torch.cuda.device(i):
             return bsattn_kv4_gather(slots, cache, dtype, k_scale, v_scale, ws)
     T = slots.numel()
-    k = slots.new_empty((T, hkv, 2 * half), dtype=dtype)
+    k = torch.empty((T, hkv, 2 * half), dtype=dtype, device=slots.device)
     v = torch.empty_like(k)
     if ws is None:
         ws = status_workspace(i)

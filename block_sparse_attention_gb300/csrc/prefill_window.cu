@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Every stage is waited for in turn, visited or not: a parity tells two of its uses apart, no more.
             // A stage that this query tile does not read it gives back here, but only once it is loaded: an arrival
             // before that could count for the stage's use before.
-            // Of the waits, none is for anything that follows from this round: K of position g takes the stage
+            // None of the waits waits for what comes after its own round: K of position g takes the stage
             // of position g - 5 or an earlier one, which the softmax gave back for a round before.
             auto round = [&](bool tile, bool visit, bool first, bool last) {
                 const int sk = g % kStages;
