@@ -122,7 +122,7 @@ def test_prefill_masked_keys_do_not_matter(bsa):
     assert torch.equal(a, bsa.bsattn_prefill_window(q, k2, v2, 40, 4))
 
 
-@pytest.mark.parametrize("Hq,Hkv", [(2, 1), (3, 3), (64, 16)])
+@pytest.mark.parametrize("Hq,Hkv", [(2, 1), (3, 3), (64, 16), (30, 30)])
 @pytest.mark.parametrize("d,dtype", [(64, F16), (128, BF16)])
 @pytest.mark.parametrize("what", [float("nan"), float("inf"), float("-inf")])
 def test_prefill_values_a_row_does_not_see_do_not_matter(bsa, Hq, Hkv, d, dtype, what):
