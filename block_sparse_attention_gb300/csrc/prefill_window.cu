@@ -10,7 +10,8 @@
 // heads do not pair up, two neighbouring row blocks of a head, and runs them against one stream of
 // 128-key K/V tiles: half the L2 traffic of one tile a CTA, and while the softmax of one query tile
 // works the tensor core has the other's products.  With no more query tiles than SMs both are the same
-// tile instead, each over every second of its key tiles; their O and sums are joined at the end.
+// tile instead, each over every second of its key tiles, without turns; their O and sums are joined at the
+// end.
 //     S_x = Q_x K^T    tcgen05.mma M=128 N=128 K=d, fp32 in TMEM (N = 128: both operands' shared
 //                      memory reads then take no longer than the products themselves)
 //     P_x              exp2 online softmax, one thread a row, written over S_x as the 16-bit type
@@ -553,88 +554,140 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t v_desc = sdesc_sw128(smem_u32(skv), 16384, 1024);
             constexpr uint32_t kTileDesc = C::kTile >> 4;
             const uint32_t ts = uniform(tbase + 128 * x), to = uniform(tbase + kOCol + D * x);
-            int g = 0;                                       // ring position: K of tile i of all items' at 2 i, V after it
-            int blk = 0, items = 0, outs = 0, rounds = 0;    // tiles, items (S begun, O begun) and rounds so far
-            bool pend = false, begins = false, ends = false; // a tile awaits its P V, which begins / ends its O
-            bool passed = false;                             // the tile before is not this query tile's
-            bool ok = true;
-            // One round: P V of the tile before, be it of the item before, and S of the tile at position g, if
-            // there is one and this query tile visits it.  A commit takes its turn among the products, so there
-            // is only S's and the last P V's: the softmax warps pass on what it says about the stages and Q.
-            // Every stage is waited for in turn, visited or not: a parity tells two of its uses apart, no more.
-            // A stage that this query tile does not read it gives back here, but only once it is loaded: an arrival
-            // before that could count for the stage's use before.
-            // None of the waits waits for what comes after its own round: K of position g takes the stage
-            // of position g - 5 or an earlier one, which the softmax gave back for a round before.
-            auto round = [&](bool tile, bool visit, bool first, bool last) {
-                const int sk = g % kStages;
-                if (g > 0 && !warp_wait_parity(&full[(g - 1) % kStages], ((g - 1) / kStages) & 1, deadline, abort_flag, status))
-                    return false;
-                if (passed) mbar_arrive_if(lead, &empty[(g - 1) % kStages]);
-                if (tile && !warp_wait_parity(&full[sk], (g / kStages) & 1, deadline, abort_flag, status)) return false;
-                passed = tile && !visit;
-                if (passed) mbar_arrive_if(lead, &empty[sk]);
-                const uint64_t vb = uniform(v_desc + static_cast<uint32_t>((g + kStages - 1) % kStages) * kTileDesc);
-                const uint64_t kb = uniform(k_desc + static_cast<uint32_t>(sk) * kTileDesc);
-                if (visit && first) {
-                    if (!warp_wait_parity(&q_full[x], items & 1, deadline, abort_flag, status)) return false;
-                    ++items;
-                }
-                // tile 0's round comes after tile 1's round before, tile 1's after tile 0's
-                if (rounds + x > 0 && !warp_wait_parity(&turn[x], (rounds + x + 1) & 1, deadline, abort_flag, status))
-                    return false;
-                ++rounds;
-                if (pend) {
-                    if (begins) {
-                        if (outs > 0 && !warp_wait_parity(&o_free[x], (outs - 1) & 1, deadline, abort_flag, status))
-                            return false;
-                        ++outs;
+            if constexpr (SPLIT) {
+                // One item, key tiles taken alternately: neither query tile waits for the other.  Every stage is
+                // waited for in turn, the other's too, which are given back here as they are not read.  V is given
+                // back by the product itself: the ring holds no more than five tiles, and the next K tiles
+                // wait for its place.
+                // Nothing waits for a later tile: K of tile i takes the place of V of tile i - 3 or an earlier
+                // one, V that of K of tile i - 2.
+                const Item<SPLIT> it = item_of<SPLIT>(p, blockIdx.x);
+                const int n = it.count();
+                int blk = 0;                                 // S issued
+                bool ok = it.count(x) == 0 || warp_wait_parity(&q_full[x], 0, deadline, abort_flag, status);
+                for (int i = 0; ok && i < n; ++i) {
+                    const int sk = 2 * i % kStages, sv = (2 * i + 1) % kStages;
+                    ok = warp_wait_parity(&full[sk], (2 * i / kStages) & 1, deadline, abort_flag, status);
+                    if (!ok) break;
+                    const bool mine = (i & 1) == x;
+                    if (mine) {
+                        const uint64_t kb = uniform(k_desc + static_cast<uint32_t>(sk) * kTileDesc);
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+                            mma_f16_ss_if(lead, ts, q_desc + off, kb + off, idS, kk > 0 ? 1u : 0u);
+                        }
+                        mma_commit_if(lead, &s_full[x]);
+                        ++blk;
+                    } else {
+                        mbar_arrive_if(lead, &empty[sk]);
                     }
-                    if (!warp_wait_parity(&p_half[x], (blk - 1) & 1, deadline, abort_flag, status)) return false;
-                    // the first half of P V runs under the second half of the softmax
+                    ok = warp_wait_parity(&full[sv], ((2 * i + 1) / kStages) & 1, deadline, abort_flag, status);
+                    if (!ok) break;
+                    if (!mine) mbar_arrive_if(lead, &empty[sv]);
+                    // P V of the last tile of its own, once the other's after it is passed
+                    const int own = mine ? i : i - 1;
+                    if (own < 0 || (mine && i + 1 < n)) continue;
+                    const uint32_t so = static_cast<uint32_t>(2 * own + 1) % kStages;
+                    const uint64_t vb = uniform(v_desc + so * kTileDesc);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        ok = ok && warp_wait_parity(half ? &p_full[x] : &p_half[x], (blk - 1) & 1, deadline, abort_flag, status);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+                            mma_f16_ts_if(lead, to, ts + 8 * kk, vb + ((kk * 2048) >> 4), idO, (blk > 1 || kk > 0) ? 1u : 0u);
+                    }
+                    if (!ok) break;
+                    if (blk == it.count(x)) mma_commit_if(lead, &o_full[x]);
+                    mma_commit_if(lead, &empty[so]);
+                }
+            } else {
+                int g = 0;                                       // ring position: K of tile i of all items' at 2 i, V after it
+                int blk = 0, items = 0, outs = 0, rounds = 0;    // tiles, items (S begun, O begun) and rounds so far
+                bool pend = false, begins = false, ends = false; // a tile awaits its P V, which begins / ends its O
+                bool passed = false;                             // the tile before is not this query tile's
+                bool ok = true;
+                // One round: P V of the tile before, be it of the item before, and S of the tile at position g, if
+                // there is one and this query tile visits it.  A commit takes its turn among the products, so there
+                // is only S's and the last P V's: the softmax warps pass on what it says about the stages and Q.
+                // Every stage is waited for in turn, visited or not: a parity tells two of its uses apart, no more.
+                // A stage that this query tile does not read it gives back here, but only once it is loaded: an arrival
+                // before that could count for the stage's use before.
+                // None of the waits waits for what comes after its own round: K of position g takes the stage
+                // of position g - 5 or an earlier one, which the softmax gave back for a round before.
+                auto round = [&](bool tile, bool visit, bool first, bool last) {
+                    const int sk = g % kStages;
+                    if (g > 0 && !warp_wait_parity(&full[(g - 1) % kStages], ((g - 1) / kStages) & 1, deadline, abort_flag, status))
+                        return false;
+                    if (passed) mbar_arrive_if(lead, &empty[(g - 1) % kStages]);
+                    if (tile && !warp_wait_parity(&full[sk], (g / kStages) & 1, deadline, abort_flag, status)) return false;
+                    passed = tile && !visit;
+                    if (passed) mbar_arrive_if(lead, &empty[sk]);
+                    const uint64_t vb = uniform(v_desc + static_cast<uint32_t>((g + kStages - 1) % kStages) * kTileDesc);
+                    const uint64_t kb = uniform(k_desc + static_cast<uint32_t>(sk) * kTileDesc);
+                    if (visit && first) {
+                        if (!warp_wait_parity(&q_full[x], items & 1, deadline, abort_flag, status)) return false;
+                        ++items;
+                    }
+                    // tile 0's round comes after tile 1's round before, tile 1's after tile 0's
+                    if (rounds + x > 0 && !warp_wait_parity(&turn[x], (rounds + x + 1) & 1, deadline, abort_flag, status))
+                        return false;
+                    ++rounds;
+                    if (pend) {
+                        if (begins) {
+                            if (outs > 0 && !warp_wait_parity(&o_free[x], (outs - 1) & 1, deadline, abort_flag, status))
+                                return false;
+                            ++outs;
+                        }
+                        if (!warp_wait_parity(&p_half[x], (blk - 1) & 1, deadline, abort_flag, status)) return false;
+                        // the first half of P V runs under the second half of the softmax
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_f16_ts_if(lead, to, ts + 8 * kk, vb + ((kk * 2048) >> 4), idO, (!begins || kk > 0) ? 1u : 0u);
+                        if (!warp_wait_parity(&p_full[x], (blk - 1) & 1, deadline, abort_flag, status)) return false;
+                    }
                     tc_fence_after();
+                    if (pend) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_f16_ts_if(lead, to, ts + 8 * kk, vb + ((kk * 2048) >> 4), idO, (!begins || kk > 0) ? 1u : 0u);
-                    if (!warp_wait_parity(&p_full[x], (blk - 1) & 1, deadline, abort_flag, status)) return false;
-                }
-                tc_fence_after();
-                if (pend) {
-#pragma unroll
-                    for (int kk = 4; kk < 8; ++kk)
-                        mma_f16_ts_if(lead, to, ts + 8 * kk, vb + ((kk * 2048) >> 4), idO, 1u);
-                    if (ends) mma_commit_if(lead, &o_full[x]);
-                    pend = false;
-                }
-                if (visit) {
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-                        mma_f16_ss_if(lead, ts, q_desc + off, kb + off, idS, kk > 0 ? 1u : 0u);
+                        for (int kk = 4; kk < 8; ++kk)
+                            mma_f16_ts_if(lead, to, ts + 8 * kk, vb + ((kk * 2048) >> 4), idO, 1u);
+                        if (ends) mma_commit_if(lead, &o_full[x]);
+                        pend = false;
                     }
-                    mma_commit_if(lead, &s_full[x]);
-                    ++blk;
-                    pend = true;
-                    begins = first;
-                    ends = last;
+                    if (visit) {
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+                            mma_f16_ss_if(lead, ts, q_desc + off, kb + off, idS, kk > 0 ? 1u : 0u);
+                        }
+                        mma_commit_if(lead, &s_full[x]);
+                        ++blk;
+                        pend = true;
+                        begins = first;
+                        ends = last;
+                    }
+                    mbar_arrive_if(lead, &turn[1 - x]);
+                    return true;
+                };
+                for (int t = blockIdx.x; ok && t < p.total_items; t += gridDim.x) {
+                    const Item<SPLIT> it = item_of<SPLIT>(p, t);
+                    deadline = global_timer_ns() + p.budget_ns;
+                    const int n = it.count(), mine = it.count(x);
+                    int done = 0;                                // S issued in this item
+                    for (int i = 0; ok && i < n; ++i, g += 2) {
+                        const bool visit = it.has(x, i, it.tile(i));
+                        ok = round(true, visit, done == 0, done == mine - 1);
+                        done += visit;
+                    }
                 }
-                mbar_arrive_if(lead, &turn[1 - x]);
-                return true;
-            };
-            for (int t = blockIdx.x; ok && t < p.total_items; t += gridDim.x) {
-                const Item<SPLIT> it = item_of<SPLIT>(p, t);
-                deadline = global_timer_ns() + p.budget_ns;
-                const int n = it.count(), mine = it.count(x);
-                int done = 0;                                // S issued in this item
-                for (int i = 0; ok && i < n; ++i, g += 2) {
-                    const bool visit = it.has(x, i, it.tile(i));
-                    ok = round(true, visit, done == 0, done == mine - 1);
-                    done += visit;
+                if (ok) {
+                    deadline = global_timer_ns() + p.budget_ns;
+                    round(false, false, false, false);
                 }
-            }
-            if (ok) {
-                deadline = global_timer_ns() + p.budget_ns;
-                round(false, false, false, false);
             }
             mma_commit_if(lead, &fin[x]);
             wait_parity_drain(&fin[x], 0, global_timer_ns() + 200000000ull);
@@ -683,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 if (speaks) {
                     // S of this tile is there: its K tile has been read, and V of the tile before
-                    if (v_read >= 0) mbar_arrive(&empty[v_read]);
+                    if (!SPLIT && v_read >= 0) mbar_arrive(&empty[v_read]);
                     const int at = g0 + 2 * u;
                     mbar_arrive(&empty[at % kStages]);
                     v_read = (at + 1) % kStages;
@@ -777,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!SPLIT || n > 0) ++items;
             tc_fence_after();
-            if (speaks && (!SPLIT || n > 0)) mbar_arrive(&empty[v_read]);
+            if (!SPLIT && speaks) mbar_arrive(&empty[v_read]);
             __syncwarp();
             float scale0 = 1.f, scale1 = 0.f;
             if (SPLIT) {
@@ -978,7 +1031,7 @@ extern "C" int bsattn_prefill_window(const void* q, const void* k, const void* v
     prm.sinks = sinks;
     prm.nq = (Sq + 127) / 128;
     // Where there is an SM for every query tile, both tiles of a CTA are the same one, each with half of its
-    // keys (257 rows of 8 heads after 8192 cached tokens, window 1024: 21.4 us against 23.7).
+    // keys (257 rows of 8 heads after 8192 cached tokens, window 1024: 17.8 us against 23.7).
     int sms = num_sms_of_current_device();
     if (sms <= 0) sms = 148;
     if (static_cast<long long>(B) * Hq * prm.nq <= sms) {
