@@ -484,6 +484,8 @@ def _int(v) -> int:
 
 def _span(window, sinks):
     """A window and sinks as C ints: past 2^31 - 1 tokens there is nothing more to see."""
+    if type(window) is int and type(sinks) is int and 0 <= window <= _INT_MAX and 0 <= sinks <= _INT_MAX:
+        return window, sinks
     return max(min(int(window), _INT_MAX), -1), max(min(int(sinks), _INT_MAX), -1)
 
 
@@ -783,14 +785,16 @@ def bsattn_prefill_window(q, k, v, window: int, sinks: int = 0, out=None, ws=Non
     B, Hq, Sq, d = q.shape
     _, hkv, Sk, _ = k.shape
     window, sinks = _span(window, sinks)
-    qs, ks, vs, os_ = q.stride(), k.stride(), v.stride(), out.stride()
-    if (qs[3] != 1 or os_[3] != 1) and q.numel() or (ks[3] != 1 or vs[3] != 1) and k.numel():
-        raise ValueError("channels (the last dimension) must be contiguous")
+    strides = None
+    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and out.is_contiguous()):
+        qs, ks, vs, os_ = q.stride(), k.stride(), v.stride(), out.stride()
+        if (qs[3] != 1 or os_[3] != 1) and q.numel() or (ks[3] != 1 or vs[3] != 1) and k.numel():
+            raise ValueError("channels (the last dimension) must be contiguous")
+        strides = _Strides(*qs[:3], *ks[:3], *vs[:3], *os_[:3])
     if ws is None:
         ws = status_workspace(i)
     rc = load().bsattn_prefill_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), window, sinks, out.data_ptr(), B,
-                                      Hq, hkv, Sq, Sk, d, _Strides(*qs[:3], *ks[:3], *vs[:3], *os_[:3]), dtype,
-                                      ws.data_ptr(), ws.numel(), _raw_stream(i))
+                                      Hq, hkv, Sq, Sk, d, strides, dtype, ws.data_ptr(), ws.numel(), _raw_stream(i))
     if rc:
         _check("bsattn_prefill_window", rc)
     return out
