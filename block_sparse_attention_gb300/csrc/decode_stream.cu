@@ -333,6 +333,10 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
 
     int seq = 0;                                   // units this warp has issued, over all pieces
     bool ok = true;
+    // After a wait that expired the CTA goes through the rest of its pieces without reading anything and
+    // hands each over as NaN: every ticket is taken, so that the workspace is ready for the next call, and
+    // no row comes out that lacks a piece and does not show it.
+    bool lost = false;
     for (long long x = x0; x < x1;) {
         const Span s = span_of<kTok>(p, b);
         if (s.n == 0) {
@@ -341,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
         }
         const int i0 = static_cast<int>(x - before);
         const int i1 = static_cast<int>(min(static_cast<long long>(s.n), x1 - before));
-        const int mine = i1 - i0 > warp ? (i1 - i0 - warp + kWarps - 1) / kWarps : 0;
+        const int mine = i1 - i0 > warp && !lost ? (i1 - i0 - warp + kWarps - 1) / kWarps : 0;
         // tokens [lo, hi) and those before `sinks` are visible
         const int lo = p.window > 0 && !p.chosen ? max(0, s.len - p.window) : 0;
         const int sinks = p.window > 0 && !p.chosen ? p.sinks : 0;
@@ -688,7 +692,8 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
             l1 += __shfl_xor_sync(0xffffffffu, l1, w);
         }
         __syncthreads();                            // every warp's ring is drained
-        if (*abort_flag) return;                    // the whole CTA: nobody raises it until the next piece
+        lost = *abort_flag != 0;                    // the same in the whole CTA: nobody raises it until the next piece
+        if (lost) l0 = l1 = __int_as_float(0x7fffffff);
 
         // ---------------------------------------------------------------- joining the four warps
         {

@@ -22,7 +22,8 @@
  *     read (and cleared) with bsattn_get_device_status().
  *   - Workspaces must be zero-filled once before their first use; every call leaves them
  *     ready for the next call (counters are reset by the kernels themselves).  After a
- *     call reports BSATTN_ERR_TIMEOUT the workspace must be zero-filled again.
+ *     call reports BSATTN_ERR_TIMEOUT the workspace must be zero-filled again, but for the
+ *     paged-serving calls at the end of this file.
  *   - Block size is 64 tokens (bsattn_prefill_bs also takes 128-token prefill masks);
  *     head dimension d is 64 or 128; dtype fp16 or bf16.
  */
@@ -260,7 +261,8 @@ int bsattn_mask_from_cumulative_threshold(const float* attn_sum, int B, int H, i
  * (bsattn_decode_window, bsattn_decode_window_paged, bsattn_decode_paged_kv4) also keep merge tickets
  * and partial results in theirs: its first 4352 bytes must be zero before the first use, any shapes
  * may follow one another on it, and calls that can overlap on the GPU (streams, replayed graphs) need
- * one each.
+ * one each.  A stream decode that reports BSATTN_ERR_TIMEOUT leaves its tickets at zero too (the
+ * workspace need not be zero-filled again), and every row that lacks some of its tokens is NaN.
  */
 
 /*

@@ -1,0 +1,76 @@
+"""What the paged-serving calls leave behind: workspaces, status words and outputs after waits that expired,
+calls that follow one another, arguments at the edge of what the header allows."""
+import pytest
+import torch
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
+
+F16, BF16 = torch.float16, torch.bfloat16
+BUDGET = 2_000_000_000                     # the default
+HEADER, TICKETS = 256, 4 * 1024
+
+
+@pytest.fixture(scope="module")
+def bsa():
+    import block_sparse_attention_gb300 as m
+    m.load()
+    return m
+
+
+def _rand(*shape, dtype, seed, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def _decodes(bsa, lens, d=128, Hq=8, Hkv=8):
+    """name -> (call(ws=None) over these lengths, workspace size), all over pages in order."""
+    B, pages = len(lens), -(-max(lens) // 64)
+    table = torch.arange(B * pages, dtype=torch.int32, device="cuda").view(B, pages)
+    k, v = (_rand(B * pages, 64, Hkv, d, dtype=BF16, seed=s) for s in (1, 2))
+    q, n = _rand(B, Hq, d, dtype=BF16, seed=3), _i32(lens)
+    cache = bsa.bsattn_kv4_cache(B * pages, Hkv, 64, d)
+    bsa.bsattn_kv4_append(k.flatten(0, 1), v.flatten(0, 1), torch.arange(B * pages * 64, device="cuda"), cache)
+    flat = [x.view(B, pages * 64, Hkv, d) for x in (k, v)]
+    size = bsa.bsattn_decode_window_workspace_size(Hq, Hkv, d)
+    return {"paged": (lambda ws=None: bsa.bsattn_decode_window_paged(q, k, v, n, table, max(lens), 0, ws=ws), size),
+            "contiguous": (lambda ws=None: bsa.bsattn_decode_window(q, *flat, n, max(lens), 0, ws=ws), size),
+            "kv4": (lambda ws=None: bsa.bsattn_decode_paged_kv4(q, cache, n, table, ws=ws),
+                    bsa.bsattn_decode_kv4_workspace_size(Hq, Hkv, d))}
+
+
+@pytest.mark.parametrize("kind", ["paged", "contiguous", "kv4"])
+@pytest.mark.parametrize("lens", [[4000] * 64, [9000, 40, 0, 700]])
+def test_calls_after_an_expired_wait(bsa, kind, lens):
+    """Waits that expire in some CTAs and not in others leave the workspace ready for the next call, the
+    binding's own one too; a row is right or NaN in every channel, whatever the budget."""
+    call, size = _decodes(bsa, lens)[kind]
+    want = call()
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    seen = 0
+    try:
+        for budget in (0, 200, 500, 1000, 2000, 5000, 20000, 100000):
+            bsa.bsattn_set_wait_budget_ns(budget)
+            for _ in range(3):
+                call()
+                got = call(ws)
+                status = bsa.bsattn_get_device_status(ws)
+                seen |= status
+                assert status in (0, bsa.BSATTN_ERR_TIMEOUT)
+                assert not ws[HEADER:HEADER + TICKETS].any()
+                lost = got.isnan().all(-1)
+                assert torch.equal(got[~lost], want[~lost])
+                assert status or not lost.any()
+    finally:
+        bsa.bsattn_set_wait_budget_ns(BUDGET)
+    # A first poll may itself last until the data is there, and at 4 bits, where the arithmetic is the longer
+    # side, it does; 1 GB of 16-bit rows asked for at once takes longer.
+    if len(lens) == 64 and kind != "kv4":
+        assert seen
+    assert torch.equal(call(), want)
+    assert torch.equal(call(ws), want)
+    assert bsa.bsattn_get_device_status(ws) == 0
