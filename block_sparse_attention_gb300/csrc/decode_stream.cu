@@ -116,6 +116,27 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                  : "memory");
 }
 
+// warp_wait_parity with a budget that runs from the wait's own first poll: a call over a long cache may
+// itself take longer than any of its waits may.
+__device__ __forceinline__ bool warp_wait_within(uint64_t* bar, uint32_t parity, uint64_t budget_ns,
+                                                 volatile int* abort_flag, int* status) {
+    if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+    bool ok = true;
+    uint64_t deadline = 0;
+    for (uint32_t spins = 0; !mbar_try_wait(bar, parity); ++spins) {
+        if ((spins & 63u) != 0) continue;           // the clock is read after the first poll and every 64th
+        const uint64_t now = global_timer_ns();
+        if (spins == 0) deadline = now + budget_ns;
+        if (*abort_flag || now >= deadline) {
+            if (!*abort_flag) atomicOr(status, BSATTN_ERR_TIMEOUT);
+            *abort_flag = 1;
+            ok = false;
+            break;
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
 template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     if constexpr (BF16) {
@@ -225,7 +246,6 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
 
     const int part = blockIdx.x / p.Hkv, g = blockIdx.x - part * p.Hkv;
     const int G = p.Hq / p.Hkv;
-    const uint64_t deadline = global_timer_ns() + p.budget_ns;
 
     if (lane == 0)
         for (int s = 0; s < kStages; ++s) mbar_init(&full[s], 1);
@@ -483,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
         // Waits for half h and returns its stage; issues half h + kStages into it once it is read.
         auto arrived = [&](int h) -> uint8_t* {
             const int at = base_seq + h, st = at % kStages;
-            if (!warp_wait_parity(&full[st], (at / kStages) & 1, deadline, abort_flag, p.status)) {
+            if (!warp_wait_within(&full[st], (at / kStages) & 1, p.budget_ns, abort_flag, p.status)) {
                 ok = false;
                 return nullptr;
             }

@@ -393,7 +393,9 @@ int bsattn_get_device_status(void* workspace, void* stream);
 /*
  * Budget, in nanoseconds, of every bounded wait inside the kernels launched after this
  * call (default 2e9).  Exists so tests can make a wait expire on purpose and check that
- * the kernel reports BSATTN_ERR_TIMEOUT and leaves the context usable.
+ * the kernel reports BSATTN_ERR_TIMEOUT and leaves the context usable.  It runs from the
+ * start of the wait in the stream decodes, of the item in bsattn_prefill_window, of the
+ * CTA in the other kernels.
  */
 void bsattn_set_wait_budget_ns(unsigned long long ns);
 

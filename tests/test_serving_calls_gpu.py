@@ -74,3 +74,30 @@ def test_calls_after_an_expired_wait(bsa, kind, lens):
     assert torch.equal(call(), want)
     assert torch.equal(call(ws), want)
     assert bsa.bsattn_get_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("kind", ["paged", "kv4"])
+def test_wait_budget_is_not_the_decodes(bsa, kind):
+    """A decode that takes longer than a wait's budget, with no wait that does: 64 sequences of 65536 tokens
+    over the pages of four of them, a millisecond or more against a quarter of one."""
+    B, Hkv, d, pages = 64, 8, 128, 1024
+    k, v = (_rand(4 * pages, 64, Hkv, d, dtype=BF16, seed=s) for s in (1, 2))
+    table = torch.arange(4 * pages, dtype=torch.int32, device="cuda").view(4, pages).repeat(B // 4, 1)
+    q, n = _rand(B, 32, d, dtype=BF16, seed=3), _i32([64 * pages] * B)
+    if kind == "kv4":
+        cache = bsa.bsattn_kv4_cache(4 * pages, Hkv, 64, d)
+        bsa.bsattn_kv4_append(k.flatten(0, 1), v.flatten(0, 1), torch.arange(4 * pages * 64, device="cuda"), cache)
+        size = bsa.bsattn_decode_kv4_workspace_size(32, Hkv, d)
+        call = lambda ws: bsa.bsattn_decode_paged_kv4(q, cache, n, table, ws=ws)  # noqa: E731
+    else:
+        size = bsa.bsattn_decode_window_workspace_size(32, Hkv, d)
+        call = lambda ws: bsa.bsattn_decode_window_paged(q, k, v, n, table, 64 * pages, 0, ws=ws)  # noqa: E731
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    want = call(ws)
+    bsa.bsattn_set_wait_budget_ns(250_000)
+    try:
+        got = call(ws)
+        assert bsa.bsattn_get_device_status(ws) == 0
+    finally:
+        bsa.bsattn_set_wait_budget_ns(BUDGET)
+    assert torch.equal(got, want)
