@@ -392,7 +392,8 @@ def bsattn_mask_from_threshold(scores, threshold: float, use_dense_for_last_bloc
 
 def bsattn_get_device_status(ws: torch.Tensor) -> int:
     """Reads and clears the device status word of a workspace (syncs its stream)."""
-    return int(load().bsattn_get_device_status(ws.data_ptr(), _stream(ws.device)))
+    with torch.cuda.device(ws.device):
+        return int(load().bsattn_get_device_status(ws.data_ptr(), _stream(ws.device)))
 
 
 def bsattn_set_wait_budget_ns(ns: int) -> None:

@@ -804,8 +804,9 @@ extern "C" int bsattn_decode_varlen_noalloc(const void* q, const void* k, const 
 }
 
 // The status word of the allocation-free decode sits at the start of the scratch array, where
-// the workspace of the other decode entry points keeps its own: read and cleared the same way,
-// after synchronising the stream (a 4-byte copy to a host word; nothing is allocated).
+// the workspace of the other decode entry points keeps its own: read after synchronising the
+// stream (a 4-byte copy to a host word) and cleared by a memset: nothing is allocated, no code
+// loaded, and calls on the array do not overlap the reading.
 extern "C" int bsattn_decode_noalloc_status(void* stream) {
     using namespace bsattn;
     int cur = 0, sdev = 0;
@@ -815,5 +816,13 @@ extern "C" int bsattn_decode_noalloc_status(void* stream) {
     void* scratch = nullptr;
     const int rc = noalloc_scratch(&scratch);
     if (rc) return rc;
-    return bsattn_get_device_status(scratch, stream);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int word = 0;
+    if (cudaMemcpyAsync(&word, scratch, sizeof(int), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess)
+        return BSATTN_ERR_CUDA;
+    if (word != 0 && (cudaMemsetAsync(scratch, 0, sizeof(int), st) != cudaSuccess ||
+                      cudaStreamSynchronize(st) != cudaSuccess))
+        return BSATTN_ERR_CUDA;
+    return word;
 }

@@ -66,10 +66,7 @@ int bsattn_get_device_status(void* workspace, void* stream) {
     if (cudaMemcpyAsync(&word, workspace, sizeof(int), cudaMemcpyDeviceToHost, st) != cudaSuccess)
         return BSATTN_ERR_CUDA;
     if (cudaStreamSynchronize(st) != cudaSuccess) return BSATTN_ERR_CUDA;
-    if (word != 0) {
-        if (cudaMemsetAsync(workspace, 0, sizeof(int), st) != cudaSuccess) return BSATTN_ERR_CUDA;
-        if (cudaStreamSynchronize(st) != cudaSuccess) return BSATTN_ERR_CUDA;
-    }
+    if (word != 0 && bsattn::clear_status_bits(workspace, word, st) != BSATTN_OK) return BSATTN_ERR_CUDA;
     return word;
 }
 

@@ -22,6 +22,9 @@ int encode_3d(CUtensorMap* map, const void* base, int bf16, uint64_t dim0, uint6
 int encode_4d(CUtensorMap* map, const void* base, int bf16, const uint64_t (&dims)[4],
               const uint64_t (&stride_bytes)[3], const uint32_t (&box)[4]);
 
+// Clears `bits` of a device status word and synchronises the stream (status.cu).  Returns a bsattn_status.
+int clear_status_bits(void* word, int bits, cudaStream_t st);
+
 // SM count of the current device (0 if it cannot be queried).
 int num_sms_of_current_device();
 

@@ -257,7 +257,8 @@ int bsattn_mask_from_cumulative_threshold(const float* attn_sum, int B, int H, i
  * have no counterpart in the pages; their definitions are given in full here.
  *
  * Their workspaces: the plan, append, gather and window prefill use only the status word (256 bytes,
- * 16-byte aligned); they set bits of it and read nothing, so calls may share one.  The stream decodes
+ * 16-byte aligned); they set bits of it and read nothing, so calls may share one (the status is then
+ * that of all of them).  The stream decodes
  * (bsattn_decode_window, bsattn_decode_window_paged, bsattn_decode_paged_kv4) also keep merge tickets
  * and partial results in theirs: its first 4352 bytes must be zero before the first use, any shapes
  * may follow one another on it, and calls that can overlap on the GPU (streams, replayed graphs) need
@@ -386,7 +387,9 @@ int bsattn_prefill_window(const void* q, const void* k, const void* v, int windo
 /*
  * Reads and clears the device status word at the start of `workspace` (device), after
  * synchronising `stream`.  Returns the OR of the BSATTN_ERR_* bits the kernels recorded
- * since the last read (0 = none), or BSATTN_ERR_CUDA if the read itself failed.
+ * since the last read (0 = none), or BSATTN_ERR_CUDA if the read itself failed.  Only the
+ * bits returned are cleared: one that a call on another stream sets meanwhile is returned
+ * by the next read.  Where several calls share a workspace a bit may be of any of them.
  */
 int bsattn_get_device_status(void* workspace, void* stream);
 

@@ -101,3 +101,22 @@ def test_wait_budget_is_not_the_decodes(bsa, kind):
     finally:
         bsa.bsattn_set_wait_budget_ns(BUDGET)
     assert torch.equal(got, want)
+
+
+def test_status_bits_set_while_the_word_is_read(bsa):
+    """Calls on other streams may set bits of a shared word between its reading and its clearing: what one
+    reading does not return the next one does."""
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    word, side = ws.view(torch.int32)[:1], torch.cuda.Stream()
+    cached, new, free, count, table = _i32([0]), _i32([5]), _i32([0]), _i32([0]), _i32([[-1]])
+    both = bsa.BSATTN_ERR_BAD_INDEX | bsa.BSATTN_ERR_NO_SPACE
+    for r in range(400):
+        word.fill_(bsa.BSATTN_ERR_BAD_INDEX)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(1 + 400 * r)                  # some time in the 80 us from here on
+            bsa.bsattn_paged_plan(cached, new, free, count, table, 64, 5, ws=ws)         # no page for it
+        first = bsa.bsattn_get_device_status(ws)
+        side.synchronize()
+        assert first | bsa.bsattn_get_device_status(ws) == both, f"{first} after {400 * r} cycles"
+    assert bsa.bsattn_get_device_status(ws) == 0
