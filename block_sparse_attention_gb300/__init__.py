@@ -46,7 +46,7 @@ __all__ = [
     "BSATTN_ERR_NO_SPACE", "Kv4Cache", "bsattn_kv4_cache", "bsattn_kv4_append", "bsattn_kv4_gather",
     "bsattn_decode_paged_kv4", "bsattn_decode_kv4_workspace_size", "bsattn_paged_plan",
     "bsattn_prefill_window", "bsattn_decode_window", "bsattn_decode_window_paged",
-    "bsattn_decode_window_workspace_size", "call_workspace", "status_workspace",
+    "bsattn_decode_window_workspace_size", "call_workspace", "status_workspace", "bsattn_set_status_word",
 ]
 
 BSATTN_OK = 0
@@ -104,6 +104,7 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
                 "bsattn_decode_paged": ([P, P, P, P, P, P, I, P, I, I, I, I, I, I, I, I, I, P, Z, P], I),
                 "bsattn_mask_from_cumulative_threshold": ([P, I, I, I, I, ctypes.c_double, I, P], I),
                 "bsattn_set_wait_budget_ns": ([ctypes.c_ulonglong], None),
+                "bsattn_set_status_word": ([P], I),
                 "bsattn_decode_varlen_noalloc": ([P, P, P, P, P, I, P, I, I, I, I, I, I, I, P], I),
                 "bsattn_decode_noalloc_status": ([P], I),
                 "bsattn_paged_plan": ([P] * 9 + [I] * 5 + [P, Z, P], I),
@@ -400,6 +401,12 @@ def bsattn_set_wait_budget_ns(ns: int) -> None:
     load().bsattn_set_wait_budget_ns(int(ns))
 
 
+def bsattn_set_status_word(ws) -> None:
+    """Makes this thread's paged-serving calls record what they find in the first word of `ws` and not in
+    their workspaces; None ends that."""
+    _check("bsattn_set_status_word", load().bsattn_set_status_word(None if ws is None else ws.data_ptr()))
+
+
 # ----------------------------------------------------------------- paged serving
 #
 # A step of a server makes these calls back to back with kernels of a few microseconds, so what the
@@ -424,17 +431,33 @@ def _device_index(device) -> int:
 
 def call_workspace(device, purpose: str, nbytes: int) -> torch.Tensor:
     """A workspace for the stream decodes that no other call in flight uses: one per (stream, purpose),
-    and a new one for every call captured into a CUDA graph (graphs may be replayed side by side)."""
+    "decode_kv4" or "decode_window", and a new one for every call captured into a CUDA graph (graphs may be
+    replayed side by side).  With nbytes 0 outside a capture, the one that such calls on the current stream
+    use, for bsattn_get_device_status; what captured calls find is in status_workspace(device)."""
     index = _device_index(device)
     capturing = _capturing()
     key = (index, purpose, _raw_stream(index))
     buf = None if capturing else _ws_cache.get(key)
     if buf is None or buf.numel() < nbytes:
-        buf = torch.empty(nbytes, dtype=_U8, device=torch.device("cuda", index))
+        buf = torch.empty(max(nbytes, _STREAM_HEADER), dtype=_U8, device=torch.device("cuda", index))
         buf[:_STREAM_HEADER].zero_()
         if not capturing:
             _ws_cache[key] = buf
+            status_workspace(index)                 # there by the time that a warmed-up call is captured
     return buf
+
+
+def _to_status_workspace(f, index):
+    """f, recording in the device's status word: a captured call's own workspace goes back to the graph's
+    pool, where nobody can read it after a replay."""
+    def call(*args):
+        lib = load()
+        lib.bsattn_set_status_word(status_workspace(index).data_ptr())
+        try:
+            return f(*args)
+        finally:
+            lib.bsattn_set_status_word(None)
+    return call
 
 
 _status_ws: dict = {}
@@ -442,7 +465,9 @@ _status_ws: dict = {}
 
 def status_workspace(device) -> torch.Tensor:
     """The 256-byte workspace of the calls that keep only a status word in it.  They set bits of it and
-    read nothing, so all of a device's streams and graphs share it."""
+    read nothing, so all of a device's streams and graphs share it; bsattn_get_device_status of it returns
+    what any of them has found.  It is made by the first such call, decode or call of this function on the
+    device; a call captured before that records in a word of its own that cannot be read."""
     index = _device_index(device)
     buf = _status_ws.get(index)
     if buf is None:
@@ -679,14 +704,15 @@ def bsattn_decode_paged_kv4(q, cache, cache_seqlens, block_table, block_indices=
         out = torch.empty_like(q)
     else:
         _check_out(out, q, True)
+    f = load().bsattn_decode_paged_kv4
     if ws is None:
         ws = _stream_workspace(i, "decode_kv4", bsattn_decode_kv4_workspace_size, Hq, hkv, d)
+        if _capturing():
+            f = _to_status_workspace(f, i)
     kc, ks, vc, vs = cache
-    rc = load().bsattn_decode_paged_kv4(q.data_ptr(), kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(),
-                                        float(k_scale), float(v_scale), cache_seqlens.data_ptr(), chosen, block_table.data_ptr(),
-                                        window, sinks, out.data_ptr(), B, Hq, hkv, pages, page,
-                                        block_table.shape[1], d, max_sel, dtype, ws.data_ptr(), ws.numel(),
-                                        _raw_stream(i))
+    rc = f(q.data_ptr(), kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), float(k_scale), float(v_scale),
+           cache_seqlens.data_ptr(), chosen, block_table.data_ptr(), window, sinks, out.data_ptr(), B, Hq, hkv, pages,
+           page, block_table.shape[1], d, max_sel, dtype, ws.data_ptr(), ws.numel(), _raw_stream(i))
     if rc:
         _check("bsattn_decode_paged_kv4", rc)
     return out
@@ -722,11 +748,13 @@ def bsattn_decode_window(q, k, v, cache_seqlens, window: int, sinks: int = 0, ou
         out = torch.empty_like(q)
     else:
         _check_out(out, q, True)
+    f = load().bsattn_decode_window
     if ws is None:
         ws = _stream_workspace(i, "decode_window", bsattn_decode_window_workspace_size, Hq, hkv, d)
-    rc = load().bsattn_decode_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), cache_seqlens.data_ptr(), window,
-                                     sinks, out.data_ptr(), B, Hq, hkv, Smax, d, dtype, ws.data_ptr(), ws.numel(),
-                                     _raw_stream(i))
+        if _capturing():
+            f = _to_status_workspace(f, i)
+    rc = f(q.data_ptr(), k.data_ptr(), v.data_ptr(), cache_seqlens.data_ptr(), window, sinks, out.data_ptr(), B, Hq, hkv,
+           Smax, d, dtype, ws.data_ptr(), ws.numel(), _raw_stream(i))
     if rc:
         _check("bsattn_decode_window", rc)
     return out
@@ -750,12 +778,14 @@ def bsattn_decode_window_paged(q, k_pages, v_pages, cache_seqlens, block_table, 
         out = torch.empty_like(q)
     else:
         _check_out(out, q, True)
+    f = load().bsattn_decode_window_paged
     if ws is None:
         ws = _stream_workspace(i, "decode_window", bsattn_decode_window_workspace_size, Hq, hkv, d)
-    rc = load().bsattn_decode_window_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-                                           cache_seqlens.data_ptr(), block_table.data_ptr(), window, sinks,
-                                           out.data_ptr(), B, Hq, hkv, pages, page, block_table.shape[1], d, dtype,
-                                           ws.data_ptr(), ws.numel(), _raw_stream(i))
+        if _capturing():
+            f = _to_status_workspace(f, i)
+    rc = f(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), cache_seqlens.data_ptr(), block_table.data_ptr(),
+           window, sinks, out.data_ptr(), B, Hq, hkv, pages, page, block_table.shape[1], d, dtype, ws.data_ptr(),
+           ws.numel(), _raw_stream(i))
     if rc:
         _check("bsattn_decode_window_paged", rc)
     return out

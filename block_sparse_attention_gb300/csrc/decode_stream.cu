@@ -923,7 +923,7 @@ int decode_stream(StreamParams prm, const void* k16, const void* v16, int d, bsa
     if (workspace_bytes < w.total || !aligned16(workspace)) return BSATTN_ERR_INVALID_ARG;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     prm.parts = parts;
-    prm.status = reinterpret_cast<int*>(ws);
+    prm.status = status_word(ws);
     prm.tickets = reinterpret_cast<int*>(ws + w.tickets);
     prm.lse_part = reinterpret_cast<float*>(ws + w.lse);
     prm.o_part = reinterpret_cast<float*>(ws + w.opart);

@@ -20,10 +20,12 @@
 namespace {
 std::atomic<unsigned long long> g_wait_budget_ns{2000000000ull};
 thread_local std::string g_status_text;
+thread_local void* g_status_word = nullptr;
 }  // namespace
 
 namespace bsattn {
 unsigned long long wait_budget_ns() { return g_wait_budget_ns.load(); }
+int* status_word(void* workspace) { return static_cast<int*>(g_status_word ? g_status_word : workspace); }
 }  // namespace bsattn
 
 extern "C" {
@@ -58,6 +60,12 @@ const char* bsattn_status_string(int status) {
 }
 
 void bsattn_set_wait_budget_ns(unsigned long long ns) { g_wait_budget_ns.store(ns); }
+
+int bsattn_set_status_word(void* word) {
+    if (!bsattn::aligned16(word)) return BSATTN_ERR_INVALID_ARG;
+    g_status_word = word;
+    return BSATTN_OK;
+}
 
 int bsattn_get_device_status(void* workspace, void* stream) {
     if (!workspace) return BSATTN_ERR_INVALID_ARG;

@@ -11,6 +11,10 @@ namespace bsattn {
 // Budget of every bounded device wait, set by bsattn_set_wait_budget_ns.
 unsigned long long wait_budget_ns();
 
+// Where a paged-serving call records what its kernel finds: the word that this thread has set with
+// bsattn_set_status_word, else the one at the start of the call's workspace.
+int* status_word(void* workspace);
+
 // Encodes a 3-D tiled TMA descriptor over 16-bit elements (bf16 if `bf16`, else fp16):
 // dims {dim0 (innermost), dim1, dim2}, byte strides of dims 1 and 2, box {box0, box1, box2},
 // optional 128-byte swizzle, zero fill out of bounds.  Returns a bsattn_status.

@@ -244,7 +244,7 @@ extern "C" int bsattn_kv4_append(const void* k, const void* v, long long k_token
     using namespace bsattn;
     Kv4Params p{k, v, k_token_stride, k_head_stride, v_token_stride, v_head_stride, slots, k_codes,
                 k_scales, v_codes, v_scales, k_scale, v_scale, T, Hkv, page_size,
-                static_cast<long long>(num_pages) * page_size, static_cast<int*>(workspace)};
+                static_cast<long long>(num_pages) * page_size, status_word(workspace)};
     const int rc = check(p, num_pages, d, dtype, workspace, workspace_bytes);
     if (rc || T == 0) return rc;
     if ((k_token_stride | k_head_stride | v_token_stride | v_head_stride) & 7) return BSATTN_ERR_INVALID_ARG;
@@ -271,7 +271,7 @@ extern "C" int bsattn_kv4_gather(const int64_t* slots, const uint8_t* k_codes, c
     using namespace bsattn;
     Kv4Params p{k, v, 0, 0, 0, 0, slots, const_cast<uint8_t*>(k_codes), const_cast<uint8_t*>(k_scales),
                 const_cast<uint8_t*>(v_codes), const_cast<uint8_t*>(v_scales), k_scale, v_scale, T, Hkv,
-                page_size, static_cast<long long>(num_pages) * page_size, static_cast<int*>(workspace)};
+                page_size, static_cast<long long>(num_pages) * page_size, status_word(workspace)};
     const int rc = check(p, num_pages, d, dtype, workspace, workspace_bytes);
     if (rc || T == 0) return rc;
     const unsigned grid = (static_cast<unsigned>(T) + kWarps - 1) / kWarps;

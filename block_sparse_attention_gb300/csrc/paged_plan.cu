@@ -280,7 +280,7 @@ extern "C" int bsattn_paged_plan(const int32_t* cached_lens, const int32_t* new_
                 return BSATTN_ERR_INVALID_ARG;
     }
     PlanParams p{cached_lens, new_lens, free_pages, free_count, block_table, slots, starts, seqlens,
-                 free_left, static_cast<int*>(workspace), B, page_size, max_pages_per_seq, free_capacity,
+                 free_left, status_word(workspace), B, page_size, max_pages_per_seq, free_capacity,
                  max_tokens};
     int sms = num_sms_of_current_device();
     if (sms <= 0) sms = 148;

@@ -1018,7 +1018,7 @@ extern "C" int bsattn_prefill_window(const void* q, const void* k, const void* v
     prm.v_b = stride(6, B);
     prm.v_h = stride(7, Hkv);
     prm.v_s = stride(8, Sk);
-    prm.status = static_cast<int*>(workspace);
+    prm.status = status_word(workspace);
     prm.out_b = stride(9, B);
     prm.out_h = stride(10, Hq);
     prm.out_s = stride(11, Sq);

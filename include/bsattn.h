@@ -394,6 +394,14 @@ int bsattn_prefill_window(const void* q, const void* k, const void* v, int windo
 int bsattn_get_device_status(void* workspace, void* stream);
 
 /*
+ * Makes the paged-serving calls that this host thread makes from now on record what their kernels
+ * find in the 4 bytes at `word` (device, 16-byte aligned, zero; read like a workspace's) and not at
+ * the start of their workspace; NULL ends that.  For calls captured into a graph whose workspace
+ * is not the caller's to read afterwards.
+ */
+int bsattn_set_status_word(void* word);
+
+/*
  * Budget, in nanoseconds, of every bounded wait inside the kernels launched after this
  * call (default 2e9).  Exists so tests can make a wait expire on purpose and check that
  * the kernel reports BSATTN_ERR_TIMEOUT and leaves the context usable.  It runs from the

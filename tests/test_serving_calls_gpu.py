@@ -120,3 +120,57 @@ def test_status_bits_set_while_the_word_is_read(bsa):
         side.synchronize()
         assert first | bsa.bsattn_get_device_status(ws) == both, f"{first} after {400 * r} cycles"
     assert bsa.bsattn_get_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("kind", ["plan", "append", "gather", "prefill", "paged", "contiguous", "kv4"])
+def test_status_of_captured_calls(bsa, kind):
+    """What captured calls without a workspace argument find is read from the device's status word, after
+    every replay."""
+    dev = torch.device("cuda", torch.cuda.current_device())
+    word = bsa.status_workspace(dev)
+    bsa.bsattn_get_device_status(word)
+    x = _rand(2, 2, 64, dtype=BF16, seed=1)
+    cache = bsa.bsattn_kv4_cache(2, 2, 64, 64)
+    past = torch.tensor([5, 2 ** 40], device="cuda")        # a slot past the cache
+    k, v = _rand(2, 64, 2, 64, dtype=BF16, seed=2), _rand(2, 64, 2, 64, dtype=BF16, seed=3)
+    n, table, far = _i32([100, 60]), _i32([[0, 7], [1, 1]]), _i32([100, 60])         # there is no page 7
+    p = _rand(64, 8, 4000, 64, dtype=BF16, seed=4)
+    calls = {
+        "plan": lambda: bsa.bsattn_paged_plan(_zero, _zero, _zero, _zero, _table, 64, 4),
+        "append": lambda: bsa.bsattn_kv4_append(x, x, past, cache),
+        "gather": lambda: bsa.bsattn_kv4_gather(past, cache, BF16),
+        "prefill": lambda: bsa.bsattn_prefill_window(p, p, p, 4000),
+        "paged": lambda: bsa.bsattn_decode_window_paged(x, k, v, n, table, 100),
+        "contiguous": lambda: bsa.bsattn_decode_window(x, k, v, far, 10),
+        "kv4": lambda: bsa.bsattn_decode_paged_kv4(x, cache, n, table),
+    }
+    _zero, _table = _i32([-1]), _i32([[0]])                 # a negative length
+    want = bsa.BSATTN_ERR_TIMEOUT if kind == "prefill" else bsa.BSATTN_ERR_BAD_INDEX
+    graph = torch.cuda.CUDAGraph()
+    try:
+        if kind == "prefill":                               # a budget is taken when the call is made
+            bsa.bsattn_set_wait_budget_ns(0)
+        with torch.cuda.graph(graph):
+            calls[kind]()
+    finally:
+        bsa.bsattn_set_wait_budget_ns(BUDGET)
+    assert bsa.bsattn_get_device_status(word) == 0
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert bsa.bsattn_get_device_status(word) == want
+        assert bsa.bsattn_get_device_status(word) == 0
+
+
+def test_a_workspace_given_to_a_captured_call_has_its_status(bsa):
+    x, k = _rand(1, 2, 64, dtype=BF16, seed=1), _rand(1, 64, 2, 64, dtype=BF16, seed=2)
+    ws = torch.zeros(bsa.bsattn_decode_window_workspace_size(2, 2, 64), dtype=torch.uint8, device="cuda")
+    word, n = bsa.status_workspace(x.device), _i32([65])
+    bsa.bsattn_get_device_status(word)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        bsa.bsattn_decode_window(x, k, k, n, 10, ws=ws)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert bsa.bsattn_get_device_status(word) == 0
+    assert bsa.bsattn_get_device_status(ws) == bsa.BSATTN_ERR_BAD_INDEX
