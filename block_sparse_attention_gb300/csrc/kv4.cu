@@ -222,7 +222,7 @@ int check(const Kv4Params& p, int num_pages, int d, bsattn_dtype dtype, const vo
     if (dtype != BSATTN_F16 && dtype != BSATTN_BF16) return BSATTN_ERR_UNSUPPORTED;
     if (p.Hkv > (1 << 20) || p.T > (1 << 30)) return BSATTN_ERR_UNSUPPORTED;
     if (!unit_ok4(p.k_unit) || !unit_ok4(p.v_unit)) return BSATTN_ERR_INVALID_ARG;
-    if (!workspace || workspace_bytes < 256) return BSATTN_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < 256 || !aligned16(workspace)) return BSATTN_ERR_INVALID_ARG;
     if (p.T == 0) return BSATTN_OK;
     if (!p.k || !p.v || !p.slots || !p.kc || !p.ks || !p.vc || !p.vs) return BSATTN_ERR_INVALID_ARG;
     if (!aligned16(p.k) || !aligned16(p.v) || !aligned16(p.kc) || !aligned16(p.ks) || !aligned16(p.vc) ||

@@ -258,7 +258,7 @@ extern "C" int bsattn_paged_plan(const int32_t* cached_lens, const int32_t* new_
     using namespace bsattn;
     if (B < 0 || page_size <= 0 || max_pages_per_seq <= 0 || free_capacity < 0 || max_tokens < 0)
         return BSATTN_ERR_INVALID_ARG;
-    if (!workspace || workspace_bytes < 256 || !starts || !free_left || !free_count)
+    if (!workspace || workspace_bytes < 256 || !aligned16(workspace) || !starts || !free_left || !free_count)
         return BSATTN_ERR_INVALID_ARG;
     if ((B > 0 && (!cached_lens || !new_lens || !block_table || !seqlens)) ||
         (max_tokens > 0 && !slots) || (free_capacity > 0 && !free_pages))

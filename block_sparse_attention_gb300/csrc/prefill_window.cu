@@ -982,7 +982,7 @@ extern "C" int bsattn_prefill_window(const void* q, const void* k, const void* v
     if (Hq % Hkv) return BSATTN_ERR_INVALID_ARG;
     if (d != 64 && d != 128) return BSATTN_ERR_UNSUPPORTED;
     if (dtype != BSATTN_F16 && dtype != BSATTN_BF16) return BSATTN_ERR_UNSUPPORTED;
-    if (!workspace || workspace_bytes < 256) return BSATTN_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < 256 || !aligned16(workspace)) return BSATTN_ERR_INVALID_ARG;
     if (B == 0 || Sq == 0) return BSATTN_OK;
     if (!q || !out || !aligned16(q) || !aligned16(out)) return BSATTN_ERR_INVALID_ARG;
     if (Sk > 0 && (!k || !v || !aligned16(k) || !aligned16(v))) return BSATTN_ERR_INVALID_ARG;

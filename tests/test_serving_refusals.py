@@ -1,0 +1,54 @@
+"""More argument checks of the paged-serving entry points: what they must not launch a kernel for."""
+import ctypes
+
+import pytest
+
+import block_sparse_attention_gb300 as bsa
+
+X = 1 << 20          # an aligned address that is never read
+INVALID = bsa.BSATTN_ERR_INVALID_ARG
+
+
+def _call(name, **kw):
+    """An entry point's return value with addresses that are never read, but for what kw changes."""
+    lib = bsa.load()
+    args = {
+        "plan": dict(cached=X, new=2 * X, free=3 * X, count=4 * X, table=5 * X, slots=6 * X, starts=7 * X, lens=8 * X,
+                     left=9 * X, B=4, page=64, max_pages=8, cap=16, tokens=8, ws=10 * X, wsb=256, stream=None),
+        "append": dict(k=X, v=2 * X, kt=256, kh=128, vt=256, vh=128, slots=3 * X, kc=4 * X, ks=5 * X, vc=6 * X,
+                       vs=7 * X, ku=1.0, vu=1.0, T=3, Hkv=2, pages=4, page=64, d=128, dtype=1, ws=8 * X, wsb=256,
+                       stream=None),
+        "gather": dict(slots=X, kc=2 * X, ks=3 * X, vc=4 * X, vs=5 * X, ku=1.0, vu=1.0, k=6 * X, v=7 * X, T=3, Hkv=2,
+                       pages=4, page=64, d=128, dtype=1, ws=8 * X, wsb=256, stream=None),
+        "prefill": dict(q=X, k=2 * X, v=3 * X, window=8, sinks=0, out=4 * X, B=2, Hq=4, Hkv=2, Sq=64, Sk=64, d=128,
+                        strides=None, dtype=1, ws=5 * X, wsb=256, stream=None),
+        "kv4": dict(q=X, kc=2 * X, ks=3 * X, vc=4 * X, vs=5 * X, ku=1.0, vu=1.0, lens=6 * X, idx=None, table=7 * X,
+                    window=0, sinks=0, out=8 * X, B=1, Hq=8, Hkv=2, pages=4, page=64, max_pages=4, d=128, max_sel=0,
+                    dtype=1, ws=9 * X, wsb=1 << 30, stream=None),
+        "paged": dict(q=X, k=2 * X, v=3 * X, lens=4 * X, table=5 * X, window=8, sinks=0, out=6 * X, B=1, Hq=8, Hkv=2,
+                      pages=4, page=64, max_pages=4, d=128, dtype=1, ws=7 * X, wsb=1 << 30, stream=None),
+        "contiguous": dict(q=X, k=2 * X, v=3 * X, lens=4 * X, window=8, sinks=0, out=5 * X, B=1, Hq=8, Hkv=2, Smax=64,
+                           d=128, dtype=1, ws=6 * X, wsb=1 << 30, stream=None),
+    }[name]
+    assert not set(kw) - set(args)
+    args.update(kw)
+    if args.get("strides") is not None:
+        args["strides"] = (ctypes.c_int64 * 12)(*args["strides"])
+    f = {"plan": lib.bsattn_paged_plan, "append": lib.bsattn_kv4_append, "gather": lib.bsattn_kv4_gather,
+         "prefill": lib.bsattn_prefill_window, "kv4": lib.bsattn_decode_paged_kv4,
+         "paged": lib.bsattn_decode_window_paged, "contiguous": lib.bsattn_decode_window}[name]
+    return f(*args.values())
+
+
+@pytest.mark.parametrize("name", ["plan", "append", "gather", "prefill", "kv4", "paged", "contiguous"])
+@pytest.mark.parametrize("off", [1, 2, 4, 8])
+def test_workspace_alignment(name, off):
+    """A status word at an odd address would be a misaligned atomic once a bit is set."""
+    assert _call(name, ws=40 * X + off) == INVALID
+
+
+@pytest.mark.parametrize("off", [1, 4, 8])
+def test_status_word_alignment(off):
+    lib = bsa.load()
+    assert lib.bsattn_set_status_word(X + off) == INVALID
+    assert lib.bsattn_set_status_word(None) == bsa.BSATTN_OK
