@@ -522,6 +522,11 @@ def _check_out(out, q, contiguous):
         raise ValueError("out must be contiguous")
 
 
+def _check_ws(ws, index):
+    if ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous tensor on the device of the call's other tensors")
+
+
 def bsattn_paged_plan(cached_lens, new_lens, free_pages, free_count, block_table, page_size: int,
                       max_tokens: int, ws=None):
     """Block-table rows and slot map for `new_lens` tokens on top of `cached_lens`, both int32 [B].
@@ -552,6 +557,8 @@ def bsattn_paged_plan(cached_lens, new_lens, free_pages, free_count, block_table
     seqlens, left = torch.empty_like(cached_lens), torch.empty_like(free_count)
     if ws is None:
         ws = status_workspace(i)
+    else:
+        _check_ws(ws, i)
     rc = load().bsattn_paged_plan(cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
                                   free_count.data_ptr(), block_table.data_ptr(), slots.data_ptr(),
                                   starts.data_ptr(), seqlens.data_ptr(), left.data_ptr(), B, page_size,
@@ -620,6 +627,8 @@ def bsattn_kv4_append(k, v, slots, cache, k_scale: float = 1.0, v_scale: float =
     vt, vh = _row_strides("v", v)
     if ws is None:
         ws = status_workspace(i)
+    else:
+        _check_ws(ws, i)
     kc, ks, vc, vs = cache
     rc = load().bsattn_kv4_append(k.data_ptr(), v.data_ptr(), kt, kh, vt, vh, slots.data_ptr(), kc.data_ptr(),
                                   ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), float(k_scale), float(v_scale), T, hkv,
@@ -644,6 +653,8 @@ def bsattn_kv4_gather(slots, cache, dtype, k_scale: float = 1.0, v_scale: float 
     v = torch.empty_like(k)
     if ws is None:
         ws = status_workspace(i)
+    else:
+        _check_ws(ws, i)
     kc, ks, vc, vs = cache
     rc = load().bsattn_kv4_gather(slots.data_ptr(), kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(),
                                   float(k_scale), float(v_scale), k.data_ptr(), v.data_ptr(), T, hkv, pages, page, 2 * half,
@@ -709,6 +720,8 @@ def bsattn_decode_paged_kv4(q, cache, cache_seqlens, block_table, block_indices=
         ws = _stream_workspace(i, "decode_kv4", bsattn_decode_kv4_workspace_size, Hq, hkv, d)
         if _capturing():
             f = _to_status_workspace(f, i)
+    else:
+        _check_ws(ws, i)
     kc, ks, vc, vs = cache
     rc = f(q.data_ptr(), kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), float(k_scale), float(v_scale),
            cache_seqlens.data_ptr(), chosen, block_table.data_ptr(), window, sinks, out.data_ptr(), B, Hq, hkv, pages,
@@ -753,6 +766,8 @@ def bsattn_decode_window(q, k, v, cache_seqlens, window: int, sinks: int = 0, ou
         ws = _stream_workspace(i, "decode_window", bsattn_decode_window_workspace_size, Hq, hkv, d)
         if _capturing():
             f = _to_status_workspace(f, i)
+    else:
+        _check_ws(ws, i)
     rc = f(q.data_ptr(), k.data_ptr(), v.data_ptr(), cache_seqlens.data_ptr(), window, sinks, out.data_ptr(), B, Hq, hkv,
            Smax, d, dtype, ws.data_ptr(), ws.numel(), _raw_stream(i))
     if rc:
@@ -783,6 +798,8 @@ def bsattn_decode_window_paged(q, k_pages, v_pages, cache_seqlens, block_table, 
         ws = _stream_workspace(i, "decode_window", bsattn_decode_window_workspace_size, Hq, hkv, d)
         if _capturing():
             f = _to_status_workspace(f, i)
+    else:
+        _check_ws(ws, i)
     rc = f(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), cache_seqlens.data_ptr(), block_table.data_ptr(),
            window, sinks, out.data_ptr(), B, Hq, hkv, pages, page, block_table.shape[1], d, dtype, ws.data_ptr(),
            ws.numel(), _raw_stream(i))
@@ -824,6 +841,8 @@ def bsattn_prefill_window(q, k, v, window: int, sinks: int = 0, out=None, ws=Non
         strides = _Strides(*qs[:3], *ks[:3], *vs[:3], *os_[:3])
     if ws is None:
         ws = status_workspace(i)
+    else:
+        _check_ws(ws, i)
     rc = load().bsattn_prefill_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), window, sinks, out.data_ptr(), B,
                                       Hq, hkv, Sq, Sk, d, strides, dtype, ws.data_ptr(), ws.numel(), _raw_stream(i))
     if rc:

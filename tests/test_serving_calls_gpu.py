@@ -174,3 +174,32 @@ def test_a_workspace_given_to_a_captured_call_has_its_status(bsa):
     torch.cuda.synchronize()
     assert bsa.bsattn_get_device_status(word) == 0
     assert bsa.bsattn_get_device_status(ws) == bsa.BSATTN_ERR_BAD_INDEX
+
+
+def _every_call(bsa):
+    x, k = _rand(1, 2, 64, dtype=BF16, seed=1), _rand(1, 64, 2, 64, dtype=BF16, seed=2)
+    cache, slots, n, table = bsa.bsattn_kv4_cache(1, 2, 64, 64), torch.zeros(1, dtype=torch.int64, device="cuda"), \
+        _i32([64]), _i32([[0]])
+    return [lambda ws: bsa.bsattn_paged_plan(_i32([0]), _i32([1]), _i32([0]), _i32([1]), _i32([[-1]]), 64, 1, ws=ws),
+            lambda ws: bsa.bsattn_kv4_append(x, x, slots, cache, ws=ws),
+            lambda ws: bsa.bsattn_kv4_gather(slots, cache, F16, ws=ws),
+            lambda ws: bsa.bsattn_prefill_window(k, k, k, 8, ws=ws),
+            lambda ws: bsa.bsattn_decode_window(x, k, k, n, 8, ws=ws),
+            lambda ws: bsa.bsattn_decode_window_paged(x, k, k, n, table, 8, ws=ws),
+            lambda ws: bsa.bsattn_decode_paged_kv4(x, cache, n, table, ws=ws)]
+
+
+@pytest.mark.parametrize("call", range(7))
+def test_workspaces_that_the_kernels_could_not_write_are_refused(bsa, call):
+    size = bsa.bsattn_decode_window_workspace_size(2, 2, 64) + bsa.bsattn_decode_kv4_workspace_size(2, 2, 64)
+    f = _every_call(bsa)[call]
+    for ws in (torch.zeros(size, dtype=torch.uint8),                                      # host memory
+               torch.zeros(1, dtype=torch.uint8, device="cuda").expand(size),             # one byte
+               torch.zeros(2, size, dtype=torch.uint8, device="cuda").t()):
+        with pytest.raises(ValueError):
+            f(ws)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    with pytest.raises(bsa.BsattnError):
+        f(ws[1:])
+    f(ws)
+    assert bsa.bsattn_get_device_status(ws) == 0
