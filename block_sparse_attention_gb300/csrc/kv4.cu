@@ -247,7 +247,9 @@ extern "C" int bsattn_kv4_append(const void* k, const void* v, long long k_token
                 static_cast<long long>(num_pages) * page_size, status_word(workspace)};
     const int rc = check(p, num_pages, d, dtype, workspace, workspace_bytes);
     if (rc || T == 0) return rc;
-    if ((k_token_stride | k_head_stride | v_token_stride | v_head_stride) & 7) return BSATTN_ERR_INVALID_ARG;
+    // the stride of a dimension of one entry is never used
+    if ((T > 1 && ((k_token_stride | v_token_stride) & 7)) || (Hkv > 1 && ((k_head_stride | v_head_stride) & 7)))
+        return BSATTN_ERR_INVALID_ARG;
     p.k_unit = 1.f / k_scale;                      // a power of two: exact
     p.v_unit = 1.f / v_scale;
     const unsigned grid = (static_cast<unsigned>(T) + kWarps - 1) / kWarps;

@@ -203,3 +203,18 @@ def test_workspaces_that_the_kernels_could_not_write_are_refused(bsa, call):
         f(ws[1:])
     f(ws)
     assert bsa.bsattn_get_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("T,H,token,head", [(1, 2, 255, None), (3, 1, None, 4), (1, 1, -7, 1)])
+def test_append_takes_any_stride_of_a_dimension_of_one(bsa, T, H, token, head):
+    d, lib = 64, bsa.load()
+    k, v = _rand(T, H, d, dtype=F16, seed=1), _rand(T, H, d, dtype=F16, seed=2)
+    slots, ws = torch.arange(T, device="cuda"), torch.zeros(256, dtype=torch.uint8, device="cuda")
+    want, got = bsa.bsattn_kv4_cache(1, H, 64, d), bsa.bsattn_kv4_cache(1, H, 64, d)
+    bsa.bsattn_kv4_append(k, v, slots, want)
+    token, head = H * d if token is None else token, d if head is None else head
+    rc = lib.bsattn_kv4_append(k.data_ptr(), v.data_ptr(), token, head, token, head, slots.data_ptr(),
+                               *(x.data_ptr() for x in got), 1.0, 1.0, T, H, 1, 64, d, 0, ws.data_ptr(), 256,
+                               torch.cuda.current_stream().cuda_stream)
+    assert rc == bsa.BSATTN_OK
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
