@@ -49,6 +49,7 @@
 
 #include "host_internal.h"
 #include "ptx.cuh"
+#include "strided.h"
 
 namespace bsattn {
 namespace {
@@ -998,10 +999,22 @@ extern "C" int bsattn_prefill_window(const void* q, const void* k, const void* v
             st[3 * i + 2] = d;
         }
     }
-    // out is written with 16-byte stores, each element once: its rows must not overlap
+    // out is written with 16-byte stores while other CTAs still read q, k and v: its rows must not share
+    // memory with one another, with k or v, or with q unless it is q itself (a row block of q has been read
+    // when its outputs are written)
     const int64_t on[3] = {B, Hq, Sq};
     for (int i = 0; i < 3; ++i)
         if (on[i] > 1 && (st[9 + i] < d || (st[9 + i] & 7))) return BSATTN_ERR_INVALID_ARG;
+    const auto tensor = [&](const void* base, int heads, int rows, int at) {
+        return Strided{base, {B, heads, rows}, {st[at], st[at + 1], st[at + 2]}};
+    };
+    const Strided to = tensor(out, Hq, Sq, 9), from[3] = {tensor(q, Hq, Sq, 0), tensor(k, Hkv, Sk, 3), tensor(v, Hkv, Sk, 6)};
+    if (overlaps_itself(to, d)) return BSATTN_ERR_INVALID_ARG;
+    for (int i = 0; i < (Sk > 0 ? 3 : 1); ++i) {
+        for (int e = 0; e < 3; ++e)
+            if (from[i].n[e] > 1 && from[i].stride[e] <= 0) return BSATTN_ERR_INVALID_ARG;
+        if (!(i == 0 && to.same_as(from[0])) && overlap(to, from[i], d)) return BSATTN_ERR_INVALID_ARG;
+    }
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     WindowParams prm{};
     prm.out = out;

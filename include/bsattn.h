@@ -377,8 +377,9 @@ size_t bsattn_decode_window_workspace_size(int Hq, int Hkv, int d);
  * window >= 1, sinks >= 0, d in {64, 128}, any Hq % Hkv == 0.  P is rounded to dtype before the second
  * product.  What stands at keys that a row does not see has no effect on it, infinities and NaN
  * included; a row that sees one in v may be NaN in every channel.  (Rows that share a 128-key tile with
- * one that they do not see are worked out again, which takes longer.)  out may be q itself.  The wait
- * budget is that of an item (128 or 256 rows), not of the whole call.
+ * one that they do not see are worked out again, which takes longer.)  out may be q itself, with q's
+ * strides; otherwise its rows share no memory with q, k, v or one another (BSATTN_ERR_INVALID_ARG).  The
+ * wait budget is that of an item (128 or 256 rows), not of the whole call.
  */
 int bsattn_prefill_window(const void* q, const void* k, const void* v, int window, int sinks, void* out,
                           int B, int Hq, int Hkv, int Sq, int Sk, int d, const int64_t* strides,

@@ -218,3 +218,21 @@ def test_append_takes_any_stride_of_a_dimension_of_one(bsa, T, H, token, head):
                                torch.cuda.current_stream().cuda_stream)
     assert rc == bsa.BSATTN_OK
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("heads", [(4, 2), (3, 3)])
+def test_prefill_outputs_between_their_inputs(bsa, heads):
+    """Views of one buffer: the queries overwritten in place, and an output in a column of its own."""
+    (Hq, Hkv), B, S, d = heads, 2, 300, 64
+    fused = _rand(B, S, 2 * Hq + 2 * Hkv, d, dtype=BF16, seed=1)
+    q, k, v, out = (x.transpose(1, 2) for x in fused.split((Hq, Hkv, Hkv, Hq), 2))
+    want = bsa.bsattn_prefill_window(q.contiguous(), k.contiguous(), v.contiguous(), 100, 3)
+    before = fused.clone()
+    bsa.bsattn_prefill_window(q, k, v, 100, 3, out=out)
+    assert torch.equal(out, want) and torch.equal(fused[:, :, :Hq + 2 * Hkv], before[:, :, :Hq + 2 * Hkv])
+    bsa.bsattn_prefill_window(q, k, v, 100, 3, out=q)
+    assert torch.equal(q, want) and torch.equal(fused[:, :, Hq:Hq + 2 * Hkv], before[:, :, Hq:Hq + 2 * Hkv])
+    with pytest.raises(bsa.BsattnError):
+        bsa.bsattn_prefill_window(q, k, v, 100, 3, out=fused[:, :, 1:Hq + 1].transpose(1, 2))
+    with pytest.raises(bsa.BsattnError):
+        bsa.bsattn_prefill_window(q, k, v, 100, 3, out=fused[:, :, :1].transpose(1, 2).expand(B, Hq, S, d))

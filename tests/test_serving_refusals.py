@@ -52,3 +52,35 @@ def test_status_word_alignment(off):
     lib = bsa.load()
     assert lib.bsattn_set_status_word(X + off) == INVALID
     assert lib.bsattn_set_status_word(None) == bsa.BSATTN_OK
+
+
+def _strides(*tensors):
+    return [s for t in tensors for s in t]
+
+
+# [2, 4 or 2, 64, 128] dense, as the entry point's own layout
+Q, KV = (4 * 64 * 128, 64 * 128, 128), (2 * 64 * 128, 64 * 128, 128)
+ROWS_FIRST = (4 * 64 * 128, 128, 4 * 128)                     # [B, S, H, d] seen as [B, H, S, d]
+Q_BYTES, KV_BYTES = 2 * 2 * 4 * 64 * 128, 2 * 2 * 2 * 64 * 128
+
+
+@pytest.mark.parametrize("out", [
+    (4 * 64 * 128, 128, 128),                                  # a head's rows over the next head's
+    (4 * 64 * 128, 64 * 128 - 128, 128),                       # the last row of a head over the next one's first
+    (128, 64 * 128, 128),                                      # batches over rows
+    (4 * 64 * 128, 160, 2 * 160 + 64),                         # heads 0 and 2 a row apart, over each other
+])
+def test_prefill_window_refuses_an_output_over_itself(out):
+    assert _call("prefill", strides=_strides(Q, KV, KV, out)) == INVALID
+
+
+@pytest.mark.parametrize("kw", [
+    dict(out=2 * X), dict(out=3 * X),                          # k, v
+    dict(out=2 * X + KV_BYTES - 16), dict(out=3 * X - Q_BYTES + 16),       # by 16 bytes
+    dict(out=X + 256), dict(out=X - 16),                       # q, not where it is
+    dict(out=X, strides=_strides(Q, KV, KV, ROWS_FIRST)),      # q in another order
+    dict(out=2 * X + 64 * 128 * 2 * 2, strides=_strides(Q, (4 * 64 * 128, 64 * 128, 128), KV, Q)),
+    dict(B=1, Hq=1, Hkv=1, Sq=1, Sk=1, out=3 * X + 128),
+])
+def test_prefill_window_refuses_an_output_over_its_inputs(kw):
+    assert _call("prefill", **kw) == INVALID
