@@ -917,6 +917,17 @@ int decode_stream(StreamParams prm, const void* k16, const void* v16, int d, bsa
         return cudaMemsetAsync(prm.out, 0, static_cast<size_t>(prm.B) * prm.Hq * d * 2, st) == cudaSuccess
                    ? BSATTN_OK
                    : BSATTN_ERR_CUDA;
+    // a CTA writes its rows while others still read: out may be q itself, whose rows have then been read
+    const size_t out_bytes = static_cast<size_t>(prm.B) * prm.Hq * d * 2;
+    const size_t rows = prm.table ? static_cast<size_t>(prm.num_pages) * prm.page_size
+                                  : static_cast<size_t>(prm.B) * prm.Smax;
+    const size_t values = rows * prm.Hkv * d;
+    if ((prm.out != prm.q && overlap(prm.out, out_bytes, prm.q, out_bytes)) ||
+        (kv4 && (overlap(prm.out, out_bytes, prm.kc, values / 2) || overlap(prm.out, out_bytes, prm.vc, values / 2) ||
+                 overlap(prm.out, out_bytes, prm.ks, values / kGroup4) ||
+                 overlap(prm.out, out_bytes, prm.vs, values / kGroup4))) ||
+        (!kv4 && (overlap(prm.out, out_bytes, k16, 2 * values) || overlap(prm.out, out_bytes, v16, 2 * values))))
+        return BSATTN_ERR_INVALID_ARG;
     const int parts = parts_of(prm.Hkv, kv4 ? Ring<128, true>::kCtas : Ring<128, false>::kCtas);
     if (static_cast<long long>(parts) * prm.Hkv > kMaxTickets) return BSATTN_ERR_UNSUPPORTED;
     const WsLayout w = ws_layout(prm.Hq, prm.Hkv, d, parts);
@@ -932,8 +943,6 @@ int decode_stream(StreamParams prm, const void* k16, const void* v16, int d, bsa
     const bool bf16 = dtype == BSATTN_BF16;
     CUtensorMap tk{}, tv{};
     if (!kv4) {
-        const uint64_t rows = prm.table ? static_cast<uint64_t>(prm.num_pages) * prm.page_size
-                                        : static_cast<uint64_t>(prm.B) * prm.Smax;
         const uint64_t row_bytes = uint64_t(prm.Hkv) * d * 2;
         int rc = encode_3d(&tk, k16, bf16, d, prm.Hkv, rows, d * 2ull, row_bytes, 64, 1, Ring<128, false>::kTok, true);
         rc |= encode_3d(&tv, v16, bf16, d, prm.Hkv, rows, d * 2ull, row_bytes, 64, 1, Ring<128, false>::kTok, true);

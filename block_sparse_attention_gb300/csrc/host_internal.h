@@ -2,6 +2,7 @@
 #pragma once
 
 #include <atomic>
+#include <cstddef>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -37,6 +38,12 @@ int num_sms_of_current_device();
 int raise_smem_limit(const void* kernel, int bytes, std::atomic<unsigned long long>& done);
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Whether na bytes at a and nb bytes at b share any.
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return na && nb && x < y + nb && y < x + na;
+}
 
 // The 128-row prefill for a 128-token block mask (prefill128.cu).  Arguments are checked by the
 // caller; returns BSATTN_ERR_UNSUPPORTED when the mask rows do not fit its shared memory.

@@ -241,11 +241,6 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
     if (unmapped) atomicOr(p.status, BSATTN_ERR_BAD_INDEX);
 }
 
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
-}
-
 }  // namespace
 }  // namespace bsattn
 
@@ -273,10 +268,10 @@ extern "C" int bsattn_paged_plan(const int32_t* cached_lens, const int32_t* new_
                                  nb + sizeof(int32_t), nb, sizeof(int32_t)};
     for (int i = 0; i < 5; ++i) {
         for (int j = 0; j < 4; ++j)
-            if (out_bytes[i] && in_bytes[j] && overlap(out[i], out_bytes[i], in[j], in_bytes[j]))
+            if (overlap(out[i], out_bytes[i], in[j], in_bytes[j]))
                 return BSATTN_ERR_INVALID_ARG;
         for (int j = i + 1; j < 5; ++j)
-            if (out_bytes[i] && out_bytes[j] && overlap(out[i], out_bytes[i], out[j], out_bytes[j]))
+            if (overlap(out[i], out_bytes[i], out[j], out_bytes[j]))
                 return BSATTN_ERR_INVALID_ARG;
     }
     PlanParams p{cached_lens, new_lens, free_pages, free_count, block_table, slots, starts, seqlens,

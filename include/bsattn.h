@@ -337,8 +337,9 @@ int bsattn_kv4_gather(const int64_t* slots, const uint8_t* k_codes, const uint8_
  * Tokens on pages out of range, and any past the table, are skipped and flagged BSATTN_ERR_BAD_INDEX;
  * a negative length is flagged and taken as 0.  Masked tokens and rows past the end may hold anything.
  * The products run in fp16 with 32-bit sums: cache values are exact there, weights are rounded to fp16.
- * Requires Hq % Hkv == 0, Hq / Hkv <= 8, Hkv <= 1024, d in {64, 128}.  The result does not depend on
- * the order in which CTAs run.
+ * Requires Hq % Hkv == 0, Hq / Hkv <= 8, Hkv <= 1024, d in {64, 128}.  out may be q itself; otherwise it
+ * shares no memory with q or the cache (BSATTN_ERR_INVALID_ARG).  The result does not depend on the
+ * order in which CTAs run.
  */
 int bsattn_decode_paged_kv4(const void* q, const uint8_t* k_codes, const uint8_t* k_scales,
                             const uint8_t* v_codes, const uint8_t* v_scales, float k_scale, float v_scale,

@@ -84,3 +84,15 @@ def test_prefill_window_refuses_an_output_over_itself(out):
 ])
 def test_prefill_window_refuses_an_output_over_its_inputs(kw):
     assert _call("prefill", **kw) == INVALID
+
+
+@pytest.mark.parametrize("name", ["kv4", "paged", "contiguous"])
+@pytest.mark.parametrize("tensor,off", [("q", 256), ("q", -16), ("k", 0), ("v", 0), ("k", -16), ("v", 16384 - 16)])
+def test_stream_decodes_refuse_an_output_over_their_inputs(name, tensor, off):
+    """Another CTA may still read what one has overwritten; only q itself is read before it is."""
+    at = dict(q=X, k=2 * X, v=4 * X if name == "kv4" else 3 * X)[tensor]
+    assert _call(name, B=4, out=at + off) == INVALID
+
+
+def test_kv4_decode_refuses_an_output_over_its_scales():
+    assert _call("kv4", out=3 * X) == INVALID and _call("kv4", out=5 * X + 64) == INVALID
