@@ -38,6 +38,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cfloat>
 #include <cmath>
 #include <type_traits>
 
@@ -465,11 +466,12 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 // a power of two brings the head's largest query value into [1, 2): fp16 then holds
-                // bf16 values exactly, but for those 2^-17 of the largest and less (off by 2^-25 of it)
-                const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-                const bool scaled = top > 0.f && e > -126 && e < 127;
-                const float down = scaled ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 1.f;
-                const float up = scaled ? __uint_as_float(static_cast<uint32_t>(127 + e) << 23) : 1.f;
+                // bf16 values exactly, but for those 2^-17 of the largest and less (off by 2^-25 of it).  At
+                // the ends of bf16's range it gets into [2, 4) or below 1, as the power and its inverse have to
+                // be normal 32-bit numbers; an infinite factor would turn a score of 0 into NaN.
+                const int e = max(min(static_cast<int>(__float_as_uint(top) >> 23) - 127, 126), -126);
+                const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 #pragma unroll
                 for (int w = 0; w < D / 32; ++w) {
                     const uint32_t r[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
@@ -479,8 +481,8 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
                         qb[2 * w + (e2 >> 1)][e2 & 1] = pack2<false>(f.x * down, f.y * down);
                     }
                 }
-                c0 *= __shfl_sync(0xffffffffu, up, 8 * j);
-                c1 *= __shfl_sync(0xffffffffu, up, 8 * j + 4);
+                c0 = fminf(c0 * __shfl_sync(0xffffffffu, up, 8 * j), FLT_MAX);
+                c1 = fminf(c1 * __shfl_sync(0xffffffffu, up, 8 * j + 4), FLT_MAX);
             } else {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {

@@ -236,3 +236,29 @@ def test_prefill_outputs_between_their_inputs(bsa, heads):
         bsa.bsattn_prefill_window(q, k, v, 100, 3, out=fused[:, :, 1:Hq + 1].transpose(1, 2))
     with pytest.raises(bsa.BsattnError):
         bsa.bsattn_prefill_window(q, k, v, 100, 3, out=fused[:, :, :1].transpose(1, 2).expand(B, Hq, S, d))
+
+
+@pytest.mark.parametrize("unit,size", [(2.0 ** -16, 2.0 ** 126), (2.0 ** -16, 2.0 ** 127), (2.0 ** -16, 3.3e38),
+                                       (2.0 ** -16, -3.3e38), (1.0, 2.0 ** -126), (1.0, 2.0 ** -133),
+                                       (2.0 ** 16, 2.0 ** 126), (2.0 ** 16, -3.3e38)])
+def test_kv4_decode_queries_of_any_finite_size(bsa, unit, size):
+    """bf16 queries up to the type's ends.  Only token 5's key is not 0: with a large query of its sign it takes
+    all, with one of the other sign the rest share; a tiny query's scores are 0 to 32 bits, all weights 1."""
+    d, n = 64, 9
+    cache = bsa.bsattn_kv4_cache(1, 1, 64, d)
+    v = _rand(64, 1, d, dtype=BF16, seed=1)
+    bsa.bsattn_kv4_append(torch.zeros_like(v), v, torch.arange(64, device="cuda"), cache)
+    if unit <= 1:                                                       # above, the score has no 32-bit value
+        cache.k_codes[0, 0, 5, 0], cache.k_scales[0, 0, 5, 0] = 2, 1    # 1 * 2^-9 * unit in channel 0
+    _, values = bsa.bsattn_kv4_gather(torch.arange(n, device="cuda"), cache, F16)
+    q = torch.zeros(1, 1, d, dtype=BF16, device="cuda")
+    q[..., 0] = size
+    got = bsa.bsattn_decode_paged_kv4(q, cache, _i32([n]), _i32([[0]]), k_scale=unit)[0, 0].double()
+    values = values[:, 0].double()
+    weight = torch.ones(n, dtype=torch.float64, device="cuda")
+    if abs(size) > 1 and unit <= 1:
+        weight[torch.arange(n, device="cuda") != 5 if size > 0 else 5] = 0
+    want = weight @ values / weight.sum()
+    # one rounding to bf16; weights of 2^12 are exact in fp16, sums of n values and one quotient in 32 bits
+    bound = torch.finfo(BF16).eps / 2 * want.abs() + (n + 8) * 2.0 ** -23 * (weight @ values.abs()) / weight.sum()
+    assert bool(((got - want).abs() <= bound).all())
