@@ -404,7 +404,10 @@ def bsattn_set_wait_budget_ns(ns: int) -> None:
 def bsattn_set_status_word(ws) -> None:
     """Makes this thread's paged-serving calls record what they find in the first word of `ws` and not in
     their workspaces; None ends that."""
+    if ws is not None and not (ws.is_cuda and ws.is_contiguous() and ws.numel() * ws.element_size() >= 4):
+        raise ValueError("ws must be a contiguous CUDA tensor of 4 bytes or more")
     _check("bsattn_set_status_word", load().bsattn_set_status_word(None if ws is None else ws.data_ptr()))
+    _own_word.ws = ws                              # kept alive
 
 
 # ----------------------------------------------------------------- paged serving
@@ -457,10 +460,11 @@ def _to_status_workspace(f, index):
             return f(*args)
         finally:
             lib.bsattn_set_status_word(None)
-    return call
+    return f if getattr(_own_word, "ws", None) is not None else call
 
 
 _status_ws: dict = {}
+_own_word = threading.local()                      # .ws: what the thread has set with bsattn_set_status_word
 
 
 def status_workspace(device) -> torch.Tensor:

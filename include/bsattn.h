@@ -370,7 +370,8 @@ size_t bsattn_decode_window_workspace_size(int Hq, int Hkv, int d);
 /*
  * Causal attention with a sliding window and sinks, forward.  Query row i of Sq stands at position
  * p = i + (Sk - Sq) and sees key j iff j <= p and (j < sinks or j > p - window); query head h reads kv
- * head h / (Hq / Hkv); out_i = softmax_j(q_i . k_j / sqrt(d)) v_j, 0 for a row that sees no key.
+ * head h / (Hq / Hkv); out_i = softmax_j(q_i . k_j / sqrt(d)) v_j, 0 for a row that sees no key
+ * (and for one all of whose scores are -infinity; so in the decodes above).
  *
  *   q, out   (device) [B, Hq, Sq, d] dtype;  k, v (device) [B, Hkv, Sk, d] dtype; 16-byte aligned
  *   strides  (host) 12 element strides: batch, head, row of q, of k, of v, of out (positive multiples

@@ -262,3 +262,25 @@ def test_kv4_decode_queries_of_any_finite_size(bsa, unit, size):
     # one rounding to bf16; weights of 2^12 are exact in fp16, sums of n values and one quotient in 32 bits
     bound = torch.finfo(BF16).eps / 2 * want.abs() + (n + 8) * 2.0 ** -23 * (weight @ values.abs()) / weight.sum()
     assert bool(((got - want).abs() <= bound).all())
+
+
+def test_a_status_word_that_the_caller_has_set_stays_set(bsa):
+    x, k, n = _rand(1, 2, 64, dtype=BF16, seed=1), _rand(1, 64, 2, 64, dtype=BF16, seed=2), _i32([65])
+    default, mine = bsa.status_workspace(x.device), torch.zeros(256, dtype=torch.uint8, device="cuda")
+    bsa.bsattn_get_device_status(default)
+    graph = torch.cuda.CUDAGraph()
+    bsa.bsattn_set_status_word(mine)
+    try:
+        with torch.cuda.graph(graph):
+            bsa.bsattn_decode_window(x, k, k, n, 10)
+        graph.replay()
+        assert bsa.bsattn_get_device_status(mine) == bsa.BSATTN_ERR_BAD_INDEX
+        bsa.bsattn_decode_window(x, k, k, n, 10)
+        assert bsa.bsattn_get_device_status(mine) == bsa.BSATTN_ERR_BAD_INDEX
+    finally:
+        bsa.bsattn_set_status_word(None)
+    assert bsa.bsattn_get_device_status(default) == 0
+    ws = torch.zeros(bsa.bsattn_decode_window_workspace_size(2, 2, 64), dtype=torch.uint8, device="cuda")
+    bsa.bsattn_decode_window(x, k, k, n, 10, ws=ws)
+    assert bsa.bsattn_get_device_status(ws) == bsa.BSATTN_ERR_BAD_INDEX
+    assert bsa.bsattn_get_device_status(mine) == 0
