@@ -437,8 +437,10 @@ def call_workspace(device, purpose: str, nbytes: int) -> torch.Tensor:
     "decode_kv4" or "decode_window", and a new one for every call captured into a CUDA graph (graphs may be
     replayed side by side).  With nbytes 0 outside a capture, the one that such calls on the current stream
     use, for bsattn_get_device_status; what captured calls find is in status_workspace(device)."""
-    index = _device_index(device)
-    capturing = _capturing()
+    return _call_workspace(_device_index(device), purpose, nbytes, _capturing())
+
+
+def _call_workspace(index, purpose, nbytes, capturing):
     key = (index, purpose, _raw_stream(index))
     buf = None if capturing else _ws_cache.get(key)
     if buf is None or buf.numel() < nbytes:
@@ -679,12 +681,14 @@ def bsattn_decode_kv4_workspace_size(Hq: int, Hkv: int, d: int) -> int:
 _stream_sizes: dict = {}
 
 
-def _stream_workspace(index, purpose, size, Hq, hkv, d):
+def _stream_workspace(f, index, purpose, size, Hq, hkv, d):
+    """(workspace, f as to be called with it) of a call that is given none."""
     key = (index, purpose, Hq, hkv, d)
     n = _stream_sizes.get(key)
     if n is None:
         n = _stream_sizes[key] = size(Hq, hkv, d)
-    return call_workspace(index, purpose, n)
+    capturing = _capturing()
+    return _call_workspace(index, purpose, n, capturing), _to_status_workspace(f, index) if capturing else f
 
 
 def bsattn_decode_paged_kv4(q, cache, cache_seqlens, block_table, block_indices=None, window: int = 0,
@@ -721,9 +725,7 @@ def bsattn_decode_paged_kv4(q, cache, cache_seqlens, block_table, block_indices=
         _check_out(out, q, True)
     f = load().bsattn_decode_paged_kv4
     if ws is None:
-        ws = _stream_workspace(i, "decode_kv4", bsattn_decode_kv4_workspace_size, Hq, hkv, d)
-        if _capturing():
-            f = _to_status_workspace(f, i)
+        ws, f = _stream_workspace(f, i, "decode_kv4", bsattn_decode_kv4_workspace_size, Hq, hkv, d)
     else:
         _check_ws(ws, i)
     kc, ks, vc, vs = cache
@@ -767,9 +769,7 @@ def bsattn_decode_window(q, k, v, cache_seqlens, window: int, sinks: int = 0, ou
         _check_out(out, q, True)
     f = load().bsattn_decode_window
     if ws is None:
-        ws = _stream_workspace(i, "decode_window", bsattn_decode_window_workspace_size, Hq, hkv, d)
-        if _capturing():
-            f = _to_status_workspace(f, i)
+        ws, f = _stream_workspace(f, i, "decode_window", bsattn_decode_window_workspace_size, Hq, hkv, d)
     else:
         _check_ws(ws, i)
     rc = f(q.data_ptr(), k.data_ptr(), v.data_ptr(), cache_seqlens.data_ptr(), window, sinks, out.data_ptr(), B, Hq, hkv,
@@ -799,9 +799,7 @@ def bsattn_decode_window_paged(q, k_pages, v_pages, cache_seqlens, block_table, 
         _check_out(out, q, True)
     f = load().bsattn_decode_window_paged
     if ws is None:
-        ws = _stream_workspace(i, "decode_window", bsattn_decode_window_workspace_size, Hq, hkv, d)
-        if _capturing():
-            f = _to_status_workspace(f, i)
+        ws, f = _stream_workspace(f, i, "decode_window", bsattn_decode_window_workspace_size, Hq, hkv, d)
     else:
         _check_ws(ws, i)
     rc = f(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), cache_seqlens.data_ptr(), block_table.data_ptr(),

@@ -73,13 +73,31 @@ inline bool overlap(const Strided& a, const Strided& b, int d) {
         if (a.n[i] > 1) add_term(t, terms, a.stride[i], 0, a.n[i] - 1);
         if (b.n[i] > 1) add_term(t, terms, b.stride[i], 1 - b.n[i], 0);
     }
-    const Wide bytes = static_cast<Wide>(reinterpret_cast<uintptr_t>(a.base)) - reinterpret_cast<uintptr_t>(b.base);
-    return reaches_sorted(t, terms, bytes / 2, d);
+    const Wide at = (static_cast<Wide>(reinterpret_cast<uintptr_t>(a.base)) - reinterpret_cast<uintptr_t>(b.base)) / 2;
+    Wide low = at, high = at;                     // most tensors lie apart as a whole
+    for (int i = 0; i < terms; ++i) {
+        low += t[i].stride * t[i].lo;
+        high += t[i].stride * t[i].hi;
+    }
+    return high > -d && low < d && reaches_sorted(t, terms, at, d);
 }
 
 // Whether two of a's rows share an element.
 inline bool overlaps_itself(const Strided& a, int d) {
     using namespace strided_detail;
+    // most are nested: each stride at least the extent of all smaller ones
+    Term all[3];
+    int dims = 0;
+    for (int i = 0; i < 3; ++i)
+        if (a.n[i] > 1) all[dims++] = {a.stride[i], 0, a.n[i] - 1};
+    std::sort(all, all + dims, [](const Term& x, const Term& y) { return x.stride < y.stride; });
+    Wide extent = d;
+    bool nested = true;
+    for (int i = 0; i < dims; ++i) {
+        nested = nested && all[i].stride >= extent;
+        extent += all[i].stride * all[i].hi;
+    }
+    if (nested) return false;
     // the difference of two rows: dimension `first` is the first that differs, and taken to be positive
     for (int first = 0; first < 3; ++first) {
         if (a.n[first] <= 1) continue;
