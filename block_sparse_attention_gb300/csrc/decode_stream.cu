@@ -20,6 +20,8 @@
 //   * The products are transposed, so that the G <= 8 heads are the n = 8 side of mma.sync m16n8k16:
 //     S^T [16 tokens x 8] = K Q^T and O^T [d x 8] += V^T P^T, P moving from the first product's
 //     accumulators to the second's operand by an in-register 8x8 transpose.
+//     Weights are rounded to the type of the product, the cache's or, at 4 bits, fp16; their sum and O are
+//     32-bit.
 //   * At 4 bits an operand register is one conversion of a code pair and one product with its scale,
 //     exact in fp16.  Which channel (K) or token (V) a matrix index stands for is free as long as
 //     both factors agree, so K gives each lane 32 consecutive channels of a token (16 bytes) and V 16
@@ -28,11 +30,11 @@
 //     the last CTA to finish (atomic ticket) joins the pieces in a fixed order.
 //
 // What bounds it, 32 query heads over 8 kv heads, d = 128, bf16:
-//   16 bits, 192 sequences with a 4096 window (2.94 GB): 407 us, 7.2 TB/s, all that HBM gives a reader.
-//   4 bits, 16 sequences of 8k-64k tokens (715 MB): 139 us, 5.1 TB/s.  Bound by turning codes into fp16
-//     operands (issue slots 57 %, ALU 48 %): 111 us without the arithmetic, 135 us without the copies.
-//   Short calls are a chain of latencies: 8 sequences with a 1024 window (34 MB) 11.6 us, one sequence of
-//     16385 tokens at 4 bits (19 MB) 15.6 us.  Of those, 1.1 us go to finding the part, 0.9 to the table,
+//   16 bits, 192 sequences with a 4096 window (2.94 GB): 410 us, 7.2 TB/s, all that HBM gives a reader.
+//   4 bits, 16 sequences of 8k-64k tokens (715 MB): 138 us, 5.2 TB/s; 64 with a 4096 window and 64 sinks (286
+//     MB) 69 us, 4.1 TB/s.  Bound by turning codes into fp16 operands (issue slots 57 %, ALU 48 %): 111 us without the arithmetic, 135 us without the copies.
+//   Short calls are a chain of latencies: 8 sequences with a 1024 window (34 MB) 11.4 us, one sequence of
+//     16385 tokens at 4 bits (19 MB) 15.4 us.  Of those, 1.1 us go to finding the part, 0.9 to the table,
 //     0.8 to the first copy, 4 to two units a warp, 1.6 to the pieces and the ticket, 3 to joining 33 pieces,
 //     and 2.5 to the launch.
 #include <cuda_bf16.h>

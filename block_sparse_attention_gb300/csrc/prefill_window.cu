@@ -31,12 +31,18 @@
 // softmax under the other's products; left alone they fall into step and stay there (4500 cycles a round).
 // All other waits of an issuer come before the one for P, where they overlap the softmax.
 //
-// What bounds it, d = 128: the tensor core, in use 70 % of the time (the rest is the hand-over from S to P
+// What bounds it, d = 128: the tensor core, in use 67 % of the time (the rest is the hand-over from S to P
 // and back, in part under the other query tile's products).  32 heads over 8 kv heads, 16384 tokens, window
-// 4096, bf16: 667 us, 1443 TFLOP/s.  d = 64: the softmax of a tile, 1600 cycles against 1024 of products,
-// and what an item starts and ends with (11 key tiles an item there: S of the next item under the epilogue
-// and the next item worked out while the last P V runs took 220 us to 213, the look at O for
-// NaN 213 to 216).  4 x 16 heads, 8191 tokens, window 1024, fp16: 216 us, 598 TFLOP/s.
+// 4096, bf16: 660 us, 1459 TFLOP/s, in short runs, 700 us when run for seconds.
+// d = 64: one query tile's chain.  P is written over S, so its next S comes after its P V: S, hand-over,
+// softmax, hand-over and P V follow one another, and only the other query tile's chain runs beside them.  A
+// round (a key tile of both) takes some 2700 cycles against 1024 of products (4 x 16 heads, 8191 tokens,
+// window 1024, fp16: 210 us, 616 TFLOP/s; the busiest CTA has 14 items and 144 rounds).  Clock stamps, which
+// stretch a round to 3200, find of the 3560 cycles from one tile of a warp to its next: 870 waiting for S,
+// 300 TMEM loads, 450 masking (250 where nothing is masked), 300 maximum, 1120 exponentials and P, 520 for
+// the change of items.  Without sinks, which cost a whole key tile of 11 there, it takes 178 us for 202 (N(0, 1)
+// inputs).  S of the next item under the epilogue and the next item worked out while the last P V runs took
+// 220 us to 213, the look at O for NaN 213 to 216.
 //
 // TMEM: S_0 0-127, S_1 128-255, O_0 256.., O_1 256 + d...  Items are dealt out round-robin, last
 // rows first (they see the most keys), so CTAs at work at one time share K/V in L2.  Every wait is
@@ -295,7 +301,7 @@ __device__ __forceinline__ Item<SPLIT> item_of(const WindowParams& p, int t) {
 // values taken for 0; a row that does see one is left as it is.  Keys are taken from the last one back, as a
 // padded end, where all rows see such values, is then done with at once.  (Looking V over before the product
 // instead, in partly seen tiles alone, cost calls without any 8 to 24 %; the look at O costs 1 to 3 %.  4 x 16
-// heads of 8191 tokens, the last 1000 all NaN: 474 us against 227 for the call alone.)
+// heads of 8191 tokens, window 1024, N(0, 1) inputs, V's last 1000 all NaN: 448 us against 202.)
 template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     if constexpr (BF16) {
@@ -1044,7 +1050,7 @@ extern "C" int bsattn_prefill_window(const void* q, const void* k, const void* v
     prm.sinks = sinks;
     prm.nq = (Sq + 127) / 128;
     // Where there is an SM for every query tile, both tiles of a CTA are the same one, each with half of its
-    // keys (257 rows of 8 heads after 8192 cached tokens, window 1024: 17.8 us against 23.7).
+    // keys (257 rows of 8 heads after 8192 cached tokens, window 1024: 15.5 us against 23.7).
     int sms = num_sms_of_current_device();
     if (sms <= 0) sms = 148;
     if (static_cast<long long>(B) * Hq * prm.nq <= sms) {
