@@ -398,8 +398,8 @@ int bsattn_get_device_status(void* workspace, void* stream);
 
 /*
  * Makes the paged-serving calls that this host thread makes from now on record what their kernels
- * find in the 4 bytes at `word` (device, 16-byte aligned, zero; read like a workspace's) and not at
- * the start of their workspace; NULL ends that.  For calls captured into a graph whose workspace
+ * find in the 4 bytes at `word` (memory of the device they run on, 16-byte aligned, zero; read like a
+ * workspace's) and not at the start of their workspace; NULL ends that.  For calls captured into a graph whose workspace
  * is not the caller's to read afterwards.
  */
 int bsattn_set_status_word(void* word);
