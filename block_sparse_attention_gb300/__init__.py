@@ -22,6 +22,15 @@ Around them, for a paged serving loop:
     bsattn_prefill_window(q, k, v, window, sinks)                        -> out
     bsattn_decode_window(q, k, v, cache_seqlens, window, sinks)          -> out
     bsattn_decode_window_paged(q, k_pages, v_pages, cache_seqlens, block_table, window, sinks) -> out
+    bsattn_decode_shared(q, k_pages, v_pages, prefix_lens, prefix_table, group_starts, cache_seqlens, block_table)
+                                                  -> out (a prefix that sequences share is read once)
+
+The block mask or the block indices that the sparse calls take, made on the GPU from the queries and keys:
+
+    bsattn_mask_from_qk(q, k, topk, is_causal, sinks=1, recent=1)         -> block_mask of a prompt
+    bsattn_block_index(num_pages, Hkv, page_size, d)                     -> BlockIndex (8-bit block summaries)
+    bsattn_index_update(k_pages, cache_seqlens, new_lens, block_table, index)
+    bsattn_decode_select(q, index, cache_seqlens, block_table, max_sel, sinks=1, recent=1) -> block_indices
 """
 from __future__ import annotations
 
@@ -46,7 +55,9 @@ __all__ = [
     "BSATTN_ERR_NO_SPACE", "Kv4Cache", "bsattn_kv4_cache", "bsattn_kv4_append", "bsattn_kv4_gather",
     "bsattn_decode_paged_kv4", "bsattn_decode_kv4_workspace_size", "bsattn_paged_plan",
     "bsattn_prefill_window", "bsattn_decode_window", "bsattn_decode_window_paged",
-    "bsattn_decode_window_workspace_size", "call_workspace", "status_workspace", "bsattn_set_status_word",
+    "bsattn_decode_shared", "bsattn_decode_shared_workspace_size", "bsattn_mask_from_qk",
+    "bsattn_mask_from_qk_workspace_size", "BlockIndex", "bsattn_block_index", "bsattn_index_update",
+    "bsattn_decode_select", "bsattn_decode_window_workspace_size", "call_workspace", "status_workspace", "bsattn_set_status_word",
 ]
 
 BSATTN_OK = 0
@@ -117,6 +128,12 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
                 "bsattn_decode_window": ([P, P, P, P, I, I, P, I, I, I, I, I, I, P, Z, P], I),
                 "bsattn_decode_window_paged": ([P, P, P, P, P, I, I, P, I, I, I, I, I, I, I, I, P, Z, P], I),
                 "bsattn_decode_window_workspace_size": ([I, I, I], Z),
+                "bsattn_index_update": ([P] * 6 + [I] * 7 + [P, Z, P], I),
+                "bsattn_decode_select": ([P] * 5 + [I, I, P] + [I] * 9 + [P, Z, P], I),
+                "bsattn_mask_from_qk": ([P, P, I, I, I, I, I, P] + [I] * 6 + [P, I, P, Z, P], I),
+                "bsattn_mask_from_qk_workspace_size": ([I] * 6, Z),
+                "bsattn_decode_shared": ([P] * 9 + [I] * 10 + [P, Z, P], I),
+                "bsattn_decode_shared_workspace_size": ([I] * 5, Z),
             }
             for name, (args, res) in sig.items():
                 f = getattr(lib, name)
@@ -434,7 +451,7 @@ def _device_index(device) -> int:
 
 def call_workspace(device, purpose: str, nbytes: int) -> torch.Tensor:
     """A workspace for the stream decodes that no other call in flight uses: one per (stream, purpose),
-    "decode_kv4" or "decode_window", and a new one for every call captured into a CUDA graph (graphs may be
+    "decode_kv4", "decode_window" or "decode_shared", and a new one for every call captured into a CUDA graph (graphs may be
     replayed side by side).  With nbytes 0 outside a capture, the one that such calls on the current stream
     use, for bsattn_get_device_status; what captured calls find is in status_workspace(device)."""
     return _call_workspace(_device_index(device), purpose, nbytes, _capturing())
@@ -849,4 +866,193 @@ def bsattn_prefill_window(q, k, v, window: int, sinks: int = 0, out=None, ws=Non
                                       Hq, hkv, Sq, Sk, d, strides, dtype, ws.data_ptr(), ws.numel(), _raw_stream(i))
     if rc:
         _check("bsattn_prefill_window", rc)
+    return out
+
+
+def bsattn_decode_shared_workspace_size(B: int, P: int, Hq: int, Hkv: int, d: int) -> int:
+    return int(load().bsattn_decode_shared_workspace_size(B, P, Hq, Hkv, d))
+
+
+def bsattn_decode_shared(q, k_pages, v_pages, prefix_lens, prefix_table, group_starts, cache_seqlens, block_table,
+                         out=None, ws=None):
+    """One query token per sequence over a prefix that sequences share and the sequence's own tokens.
+    q [B,Hq,d]; k_pages/v_pages [num_pages,page_size,Hkv,d] fp16|bf16 CUDA; prefix_lens int32 [P];
+    prefix_table int32 [P,max_pages_per_prefix]; group_starts int32 [P+1]: sequences group_starts[p] to
+    group_starts[p+1] share prefix p; cache_seqlens int32 [B] and block_table int32 [B,max_pages] are of the
+    sequences' own tokens."""
+    i, dtype = _window_args(q, k_pages, v_pages, cache_seqlens)
+    B, Hq, d = q.shape
+    P = prefix_lens.numel()
+    if not (block_table.get_device() == i and prefix_lens.get_device() == i and prefix_table.get_device() == i
+            and group_starts.get_device() == i and block_table.dtype is _I32 and prefix_lens.dtype is _I32
+            and prefix_table.dtype is _I32 and group_starts.dtype is _I32 and block_table.dim() == 2
+            and block_table.shape[0] == B and prefix_lens.dim() == 1 and prefix_table.dim() == 2
+            and prefix_table.shape[0] == P and group_starts.shape == (P + 1,) and block_table.is_contiguous()
+            and prefix_lens.is_contiguous() and prefix_table.is_contiguous() and group_starts.is_contiguous()):
+        _refuse(("q", q, q.dtype, 3, None), ("prefix_lens", prefix_lens, _I32, 1, None),
+                ("prefix_table", prefix_table, _I32, 2, (P, *prefix_table.shape[1:])),
+                ("group_starts", group_starts, _I32, 1, (P + 1,)),
+                ("block_table", block_table, _I32, 2, (B, *block_table.shape[1:])))
+    if _current_device() != i:
+        with torch.cuda.device(i):
+            return bsattn_decode_shared(q, k_pages, v_pages, prefix_lens, prefix_table, group_starts, cache_seqlens,
+                                        block_table, out, ws)
+    pages, page, hkv, _ = k_pages.shape
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check_out(out, q, True)
+    f = load().bsattn_decode_shared
+    if ws is None:
+        capturing = _capturing()
+        ws = _call_workspace(i, "decode_shared", bsattn_decode_shared_workspace_size(B, P, Hq, hkv, d), capturing)
+        if capturing:
+            f = _to_status_workspace(f, i)
+    else:
+        _check_ws(ws, i)
+    rc = f(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), prefix_lens.data_ptr(), prefix_table.data_ptr(),
+           group_starts.data_ptr(), cache_seqlens.data_ptr(), block_table.data_ptr(), out.data_ptr(), B, P, Hq, hkv,
+           pages, page, prefix_table.shape[1], block_table.shape[1], d, dtype, ws.data_ptr(), ws.numel(), _raw_stream(i))
+    if rc:
+        _check("bsattn_decode_shared", rc)
+    return out
+
+
+# ----------------------------------------------------------------- choosing blocks
+
+
+class BlockIndex(NamedTuple):
+    """8-bit summaries of the 64-token blocks of a paged cache's keys: codes int8 [pages, page_size/64, Hkv, d]
+    and scales fp32 [pages, page_size/64, Hkv]; a block's mean is codes * scale."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+
+def bsattn_block_index(num_pages: int, Hkv: int, page_size: int, d: int, device="cuda") -> BlockIndex:
+    """A zeroed index for a cache [num_pages, page_size, Hkv, d]."""
+    if page_size <= 0 or page_size % 64:
+        raise ValueError("page_size must be a multiple of 64")
+    shape = (num_pages, page_size // 64, Hkv)
+    return BlockIndex(torch.zeros(*shape, d, dtype=torch.int8, device=device),
+                      torch.zeros(*shape, dtype=torch.float32, device=device))
+
+
+def _index(index, i, lens, table):
+    """The shape (pages, blocks of a page, Hkv, d) of an index on device i, or an error; lens and table with it."""
+    codes, scales = index
+    shape = codes.shape
+    if not (i >= 0 and codes.get_device() == i and scales.get_device() == i and lens.get_device() == i
+            and table.get_device() == i and codes.dtype is torch.int8 and scales.dtype is torch.float32
+            and lens.dtype is _I32 and table.dtype is _I32 and len(shape) == 4 and scales.shape == shape[:3]
+            and lens.dim() == 1 and table.dim() == 2 and table.shape[0] == lens.shape[0] and codes.is_contiguous()
+            and scales.is_contiguous() and lens.is_contiguous() and table.is_contiguous()):
+        _refuse(("codes", codes, torch.int8, 4, None), ("scales", scales, torch.float32, 3, shape[:3]),
+                ("cache_seqlens", lens, _I32, 1, None),
+                ("block_table", table, _I32, 2, (lens.numel(), *table.shape[1:])))
+    return shape
+
+
+def bsattn_index_update(k_pages, cache_seqlens, new_lens, block_table, index, ws=None) -> None:
+    """Summarises again each 64-token block that holds one of a sequence's last new_lens tokens, from the rows in
+    the cache.  k_pages [num_pages,page_size,Hkv,d] fp16|bf16 CUDA; cache_seqlens (with the new tokens) and
+    new_lens int32 [B]; block_table int32 [B,max_pages]; index: a BlockIndex."""
+    i = k_pages.get_device()
+    dtype = _dtype_code(k_pages)
+    pages, per, hkv, d = _index(index, i, cache_seqlens, block_table)
+    if not (k_pages.shape == (pages, 64 * per, hkv, d) and k_pages.is_contiguous() and new_lens.get_device() == i
+            and new_lens.dtype is _I32 and new_lens.shape == cache_seqlens.shape and new_lens.is_contiguous()):
+        _refuse(("k_pages", k_pages, k_pages.dtype, 4, (pages, 64 * per, hkv, d)),
+                ("new_lens", new_lens, _I32, 1, cache_seqlens.shape))
+    if _current_device() != i:
+        with torch.cuda.device(i):
+            return bsattn_index_update(k_pages, cache_seqlens, new_lens, block_table, index, ws)
+    if ws is None:
+        ws = status_workspace(i)
+    else:
+        _check_ws(ws, i)
+    rc = load().bsattn_index_update(k_pages.data_ptr(), cache_seqlens.data_ptr(), new_lens.data_ptr(),
+                                    block_table.data_ptr(), index[0].data_ptr(), index[1].data_ptr(),
+                                    cache_seqlens.shape[0], hkv, pages, 64 * per, block_table.shape[1], d, dtype,
+                                    ws.data_ptr(), ws.numel(), _raw_stream(i))
+    if rc:
+        _check("bsattn_index_update", rc)
+
+
+def bsattn_decode_select(q, index, cache_seqlens, block_table, max_sel: int, sinks: int = 1, recent: int = 1,
+                         out=None, ws=None):
+    """The key blocks of one query token per sequence: the first `sinks`, the last `recent` and those with the
+    highest scores, max_sel in all.  q [B,Hq,d] fp16|bf16 CUDA; index: a BlockIndex; cache_seqlens int32 [B];
+    block_table int32 [B,max_pages].  Returns int32 [B,Hkv,max_sel], rising, -1 where there is none."""
+    i = q.get_device()
+    dtype = _dtype_code(q)
+    pages, per, hkv, d = _index(index, i, cache_seqlens, block_table)
+    B = cache_seqlens.shape[0]
+    if not (q.dim() == 3 and q.shape[0] == B and q.shape[2] == d and q.is_contiguous()):
+        _refuse(("q", q, q.dtype, 3, (B, *q.shape[1:-1], d)), ("codes", index[0], torch.int8, 4, None))
+    if _current_device() != i:
+        with torch.cuda.device(i):
+            return bsattn_decode_select(q, index, cache_seqlens, block_table, max_sel, sinks, recent, out, ws)
+    max_sel, sinks, recent = _int(max_sel), _int(sinks), _int(recent)
+    if out is None:
+        out = torch.empty((B, hkv, max(max_sel, 0)), dtype=_I32, device=q.device)
+    elif not (out.get_device() == i and out.dtype is _I32 and out.shape == (B, hkv, max_sel) and out.is_contiguous()):
+        _refuse(("q", q, q.dtype, 3, None), ("out", out, _I32, 3, (B, hkv, max_sel)))
+    if ws is None:
+        ws = status_workspace(i)
+    else:
+        _check_ws(ws, i)
+    rc = load().bsattn_decode_select(q.data_ptr(), index[0].data_ptr(), index[1].data_ptr(), cache_seqlens.data_ptr(),
+                                     block_table.data_ptr(), sinks, recent, out.data_ptr(), B, q.shape[1], hkv, pages,
+                                     64 * per, block_table.shape[1], d, max_sel, dtype, ws.data_ptr(), ws.numel(),
+                                     _raw_stream(i))
+    if rc:
+        _check("bsattn_decode_select", rc)
+    return out
+
+
+def bsattn_mask_from_qk_workspace_size(B: int, Hq: int, Hkv: int, Sq: int, Sk: int, d: int) -> int:
+    return int(load().bsattn_mask_from_qk_workspace_size(B, Hq, Hkv, Sq, Sk, d))
+
+
+_Strides6 = ctypes.c_int64 * 6
+
+
+def bsattn_mask_from_qk(q, k, topk: int, is_causal: bool, sinks: int = 1, recent: int = 1,
+                        use_dense_for_last_block: bool = False, out=None, ws=None):
+    """The block mask [B,Hq,ceil(Sq/64),ceil(Sk/64)] uint8 of a prompt, for bsattn_prefill: of the key blocks that
+    a query block sees the first `sinks`, the last `recent` and those with the highest scores, topk in all (all
+    of them for the last two query blocks with use_dense_for_last_block).  q [B,Hq,Sq,d], k [B,Hkv,Sk,d]
+    fp16|bf16 CUDA views with contiguous channels and 16-byte aligned strides."""
+    i = q.get_device()
+    dtype = _dtype_code(q)
+    if not (i >= 0 and k.get_device() == i and k.dtype is q.dtype and q.dim() == 4 and k.dim() == 4
+            and q.shape[0] == k.shape[0] and q.shape[3] == k.shape[3]):
+        _refuse(("q", q.contiguous(), q.dtype, 4, None),
+                ("k", k.contiguous(), q.dtype, 4, (q.shape[0], *k.shape[1:-1], q.shape[-1])))
+    if _current_device() != i:
+        with torch.cuda.device(i):
+            return bsattn_mask_from_qk(q, k, topk, is_causal, sinks, recent, use_dense_for_last_block, out, ws)
+    B, Hq, Sq, d = q.shape
+    _, hkv, Sk, _ = k.shape
+    topk, (sinks, recent) = min(int(topk), _INT_MAX), _span(sinks, recent)
+    strides = None
+    if not (q.is_contiguous() and k.is_contiguous()):
+        qs, ks = q.stride(), k.stride()
+        if qs[3] != 1 and q.numel() or ks[3] != 1 and k.numel():
+            raise ValueError("channels (the last dimension) must be contiguous")
+        strides = _Strides6(*qs[:3], *ks[:3])
+    shape = (B, Hq, -(-Sq // 64), -(-Sk // 64))
+    if out is None:
+        out = torch.empty(shape, dtype=_U8, device=q.device)
+    elif not (out.get_device() == i and out.dtype is _U8 and out.shape == shape and out.is_contiguous()):
+        _refuse(("k", k.contiguous(), k.dtype, 4, None), ("out", out, _U8, 4, shape))
+    if ws is None:
+        ws = torch.empty(bsattn_mask_from_qk_workspace_size(B, Hq, hkv, Sq, Sk, d), dtype=_U8, device=q.device)
+    else:
+        _check_ws(ws, i)
+    rc = load().bsattn_mask_from_qk(q.data_ptr(), k.data_ptr(), max(topk, -1), sinks, recent,
+                                    int(bool(use_dense_for_last_block)), int(bool(is_causal)), out.data_ptr(), B, Hq,
+                                    hkv, Sq, Sk, d, strides, dtype, ws.data_ptr(), ws.numel(), _raw_stream(i))
+    if rc:
+        _check("bsattn_mask_from_qk", rc)
     return out

@@ -1,0 +1,714 @@
+// decode_shared.cu -- one query token per sequence over a prefix that sequences share and each one's own tokens,
+// 16-bit paged cache, sm_103a.
+//
+//     out = softmax_j(q . k_j / sqrt(d)) v_j,   j over the prefix's tokens and the sequence's own
+//
+// The softmax over both is joined from its parts: with (O, L) the result and log-sum-exp of a part,
+// out = sum O 2^(L - M) / sum 2^(L - M).  This file's kernel does the prefixes: the query heads of a kv head of
+// all sequences that share one are the rows of its products, so K and V of a prefix are read once for up to
+// 256 rows and not once a sequence.  decode_stream.cu then does the sequences' own tokens and joins.
+//
+// For few rows HBM bandwidth bounds this, for many the tensor core (256 rows of d = 128: 256 operations a
+// byte against the 280 that the two peaks divide to).  The rows stand in two tcgen05 tiles a CTA:
+//     S_x = Q_x K^T    M=128 N=128 K=d, fp32 in TMEM
+//     P_x              exp2 online softmax, one thread a row, written over S_x as the 16-bit type
+//     O_x += P_x V     M=128 N=d K=128, A = P_x from TMEM
+// as in prefill_window.cu, with its roles (warps 0-3 and 4-7 softmax of tile 0 and 1, warps 8 and 9 their
+// products, warp 10 the copies), its turns, its halves of P and its rule that the reference maximum moves only
+// when it has grown by 2^8.  Where a prefix has no more than 128 rows, both tiles are the same rows and take
+// every second key tile each, without turns.
+// The prefixes' keys, end to end, are cut into equal parts, one a CTA, so that one long prefix and many
+// short ones both fill the GPU (shared_prefix.cuh); a CTA goes from one piece to the next without a break.
+//
+// TMEM: S_0 0-127, S_1 128-255, O_0 256.., O_1 256 + d...  Every wait is bounded: on expiry the CTA records
+// BSATTN_ERR_TIMEOUT, hands its remaining pieces over as NaN, drains what is in flight and leaves.
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
+#include "host_internal.h"
+#include "shared_prefix.cuh"
+#include "tile128.cuh"
+
+namespace bsattn {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kMmaWarp = 8;              // and 9
+constexpr int kLoadWarp = 10;
+constexpr int kRegsSoftmax = 208, kRegsOther = 88;       // registers a thread: two warpgroups, and the third
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kOCol = 256;
+constexpr float kRescaleLog2 = 8.0f;
+// Notes of key tiles, in turn: the loader is never this many tiles ahead of the last warp of a softmax.
+constexpr int kNotes = 16;
+
+template <int D>
+struct Cfg {
+    static constexpr int kStages = D == 64 ? 10 : 5;             // one 128-row tile of K or V each
+    static constexpr uint32_t kTile = 128 * D * 2;
+    static constexpr uint32_t kKV = 2 * kTile;                   // after two query tiles
+    static constexpr uint32_t kBars = kKV + kStages * kTile;
+    // q_full[2] q_free[2] full[stages] empty[stages] s_full[2] p_half[2] p_full[2] o_full[2] o_free[2] fin[2] turn[2]
+    static constexpr uint32_t kNumBars = 4 + 2 * kStages + 14;
+    static constexpr uint32_t kMisc = (kBars + 8 * kNumBars + 15) & ~15u;   // tmem base, abort flag, first prefix
+    static constexpr uint32_t kMissing = kMisc + 16;             // [kNotes]: which halves of a key tile are not there
+    static constexpr uint32_t kBytes = 1024 + kMissing + 4 * kNotes;
+    static_assert(kBytes <= 226 * 1024, "shared memory");        // the scan's static arrays beside it
+};
+
+struct PrefixParams {
+    PrefixPieces s;
+    const int32_t* table;                // [P, max_pages]
+    int* status;
+    int page_size, max_pages, num_pages;
+    int q_bytes;                         // of a query tile
+    float scale_log2;
+    unsigned long long budget_ns;
+};
+
+// A CTA's walk over its units, from piece to piece.
+struct Walk {
+    long long at, end, base;             // units done, the last one, units before prefix p
+    int p;
+};
+
+struct Piece {
+    int p, b0, n;                        // prefix, first of its sequences, how many
+    int kvh, k0, k1, len;                // kv head, key tiles [k0, k1), keys of the prefix
+    int rows;                            // of the item
+    long long place;                     // rows of all items before it
+};
+
+__device__ __forceinline__ bool next_piece(const PrefixParams& prm, Walk& w, Piece& x) {
+    if (w.at >= w.end) return false;
+    PrefixGroup g = prefix_group(prm.s, w.p);
+    for (;;) {
+        const long long units = prefix_units(prm.s, g);
+        if (w.at < w.base + units) break;
+        w.base += units;
+        g = prefix_group(prm.s, ++w.p);
+    }
+    const long long local = w.at - w.base;
+    const long long item = local <= 0x7fffffffLL ? static_cast<int>(local) / g.tiles : local / g.tiles;
+    x.p = w.p;
+    x.k0 = static_cast<int>(local - item * g.tiles);
+    x.k1 = static_cast<int>(min(static_cast<long long>(g.tiles), x.k0 + (w.end - w.at)));
+    const int t = static_cast<int>(item / prm.s.Hkv);
+    x.kvh = static_cast<int>(item - static_cast<long long>(t) * prm.s.Hkv);
+    x.b0 = g.start + t * prm.s.seqs;
+    x.n = min(prm.s.seqs, g.n - t * prm.s.seqs);
+    x.len = g.len;
+    x.place = prefix_rows_before(prm.s, g, t, x.kvh, x.rows);
+    w.at += x.k1 - x.k0;
+    return true;
+}
+
+// HALVES: both query tiles are the same rows, tile 0 takes the even key tiles of a piece and tile 1 the odd ones.
+template <int D, bool BF16, bool HALVES>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v, const PrefixParams p) {
+    using C = Cfg<D>;
+    constexpr int kStages = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sq = sm;
+    uint8_t* skv = sm + C::kKV;
+    uint64_t* q_full = reinterpret_cast<uint64_t*>(sm + C::kBars);   // [2]
+    uint64_t* q_free = q_full + 2;                                    // [2]
+    uint64_t* full = q_free + 2;                                      // [stages]
+    uint64_t* empty = full + kStages;                                 // [stages] both query tiles
+    uint64_t* s_full = empty + kStages;                               // [2] the product, and its issuer
+    uint64_t* p_half = s_full + 2;                                    // [2] four warps: P of the first 64 keys
+    uint64_t* p_full = p_half + 2;                                    // [2] four warps
+    uint64_t* o_full = p_full + 2;                                    // [2] a piece's last P V
+    uint64_t* o_free = o_full + 2;                                    // [2] four warps
+    uint64_t* fin = o_free + 2;                                       // [2]
+    uint64_t* turn = fin + 2;                                         // [2] the other has issued
+    int* misc = reinterpret_cast<int*>(sm + C::kMisc);
+    int* missing = reinterpret_cast<int*>(sm + C::kMissing);
+    volatile int* abort_flag = &misc[1];
+    int* status = p.status;
+    __shared__ long long warp_sums[kThreads / 32];
+    __shared__ long long first_base;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    // the kernel that joins may start wherever there is room: it waits for this one by itself
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // ------------------------------------------------------------ this CTA's part of all units
+    Walk start;
+    {
+        const int per = (p.s.P + kThreads - 1) / kThreads;
+        long long sum = 0;
+        for (int k = 0; k < per; ++k) {
+            const int i = tid * per + k;
+            if (i >= p.s.P) break;
+            const PrefixGroup g = prefix_group(p.s, i);
+            sum += prefix_units(p.s, g);
+            if (g.bad && blockIdx.x == 0) atomicOr(status, BSATTN_ERR_BAD_INDEX);
+        }
+        long long upto = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += u;
+        }
+        if (lane == 31) warp_sums[warp] = upto;
+        __syncthreads();
+        long long total = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) upto += warp_sums[w];
+            total += warp_sums[w];
+        }
+        // two tiles a CTA at least where its two halves take one each
+        const long long chunk = max((total + gridDim.x - 1) / gridDim.x, HALVES ? 2LL : 1LL);
+        if (blockIdx.x == 0) {
+            long long before = upto - sum;
+            for (int k = 0; k < per; ++k) {
+                const int i = tid * per + k;
+                if (i >= p.s.P) break;
+                p.s.info[1 + i] = before;
+                before += prefix_units(p.s, prefix_group(p.s, i));
+            }
+            if (tid == 0) p.s.info[0] = chunk;
+        }
+        start.at = static_cast<long long>(blockIdx.x) * chunk;
+        start.end = min(start.at + chunk, total);
+        if (start.at >= total) return;                        // the whole CTA
+        if (upto - sum <= start.at && start.at < upto) {
+            int i = tid * per;
+            long long before = upto - sum;
+            for (;; ++i) {
+                const long long n = prefix_units(p.s, prefix_group(p.s, i));
+                if (start.at < before + n) break;
+                before += n;
+            }
+            misc[2] = i;
+            first_base = before;
+        }
+    }
+
+    if (tid == 0) {
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&q_full[x], 1);
+            mbar_init(&q_free[x], 1);
+            mbar_init(&s_full[x], 2);
+            mbar_init(&p_half[x], 4);
+            mbar_init(&p_full[x], 4);
+            mbar_init(&o_full[x], 1);
+            mbar_init(&o_free[x], 4);
+            mbar_init(&fin[x], 1);
+            mbar_init(&turn[x], 1);
+        }
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 2);
+        }
+        misc[1] = 0;
+        fence_barrier_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(reinterpret_cast<uint32_t*>(&misc[0]), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = static_cast<uint32_t>(misc[0]);
+    start.p = misc[2];
+    start.base = first_base;
+    // key tiles of query tile x in a piece of n
+    const auto tiles_of = [](int x, int n) { return HALVES ? (n + 1 - x) / 2 : n; };
+
+    // The softmax keeps a row of 128 scores a thread: its two warpgroups take 208 of the registers that the
+    // launch gave, the third is left 88.  (launch() has checked that the launch gave that many.)
+    if (warp >= kMmaWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+        Walk walk = start;
+        Piece piece;
+        if (warp == kLoadWarp) {
+            // ------------------------------------------------------------ TMA
+            if (lane == 0) {
+                tma_prefetch_desc(&tm_q);
+                tma_prefetch_desc(&tm_k);
+                tma_prefetch_desc(&tm_v);
+            }
+            int g = 0;                                   // tiles loaded, K and V counted apart
+            int nq[2] = {0, 0};                          // Q tiles loaded
+            bool ok = true, bad = false;
+            while (ok && next_piece(p, walk, piece)) {
+                const int n = piece.k1 - piece.k0;
+                int look = -1;
+                for (int i = 0; ok && i < n; ++i) {
+                    if ((i & 15) == 0) {
+                        // the cache rows of the next 32 blocks of 64 keys
+                        const int key = 2 * (piece.k0 + i) * 64 + 64 * lane;
+                        look = -1;
+                        if (key < piece.len && key < 128 * piece.k1) {
+                            const int lp = key / p.page_size;
+                            const int page = p.table[static_cast<size_t>(piece.p) * p.max_pages + lp];
+                            if (page >= 0 && page < p.num_pages) look = page * p.page_size + key - lp * p.page_size;
+                            else bad = true;
+                        }
+                    }
+                    const int r0 = __shfl_sync(0xffffffffu, look, 2 * (i & 15));
+                    const int r1 = __shfl_sync(0xffffffffu, look, 2 * (i & 15) + 1);
+                    // rows past the cache's end are filled with zeros
+                    const int none = p.num_pages * p.page_size;
+#pragma unroll 1
+                    for (int v = 0; ok && v < 2; ++v) {
+                        const int st = g % kStages;
+                        ok = g < kStages || warp_wait_within(&empty[st], (g / kStages - 1) & 1, p.budget_ns, abort_flag, status);
+                        if (!ok) break;
+                        if (lane == 0) {
+                            if (v == 0) missing[(g >> 1) % kNotes] = (r0 < 0 ? 1 : 0) | (r1 < 0 ? 2 : 0);
+                            mbar_arrive_expect_tx(&full[st], C::kTile);
+#pragma unroll
+                            for (int h = 0; h < D / 64; ++h) {
+                                uint8_t* dst = skv + st * C::kTile + h * 16384;
+                                tma_load_3d(dst, v ? &tm_v : &tm_k, &full[st], h * 64, piece.kvh, r0 < 0 ? none : r0);
+                                tma_load_3d(dst + 8192, v ? &tm_v : &tm_k, &full[st], h * 64, piece.kvh, r1 < 0 ? none : r1);
+                            }
+                        }
+                        ++g;
+                        if (i > 0 || v > 0) continue;
+                        for (int x = 0; ok && x < 2; ++x) {
+                            if (tiles_of(x, n) == 0) continue;
+                            ok = nq[x] == 0 || warp_wait_within(&q_free[x], (nq[x] - 1) & 1, p.budget_ns, abort_flag, status);
+                            if (!ok) break;
+                            if (lane == 0) {
+                                mbar_arrive_expect_tx(&q_full[x], static_cast<uint32_t>(p.q_bytes));
+                                const int b = piece.b0 + (HALVES ? 0 : x * (p.s.seqs / 2));
+#pragma unroll
+                                for (int h = 0; h < D / 64; ++h)
+                                    tma_load_4d(sq + x * C::kTile + h * 16384, &tm_q, &q_full[x], h * 64, 0, piece.kvh, b);
+                            }
+                            ++nq[x];
+                        }
+                    }
+                }
+            }
+            if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(status, BSATTN_ERR_BAD_INDEX);
+            // copies in flight land before the shared memory is released, whoever has given up on them
+            const uint64_t dl = global_timer_ns() + 200000000ull;
+            for (int x = 0; x < 2; ++x)
+                if (nq[x] > 0) wait_parity_drain(&q_full[x], (nq[x] - 1) & 1, dl);
+            for (int j = max(0, g - kStages); j < g; ++j) wait_parity_drain(&full[j % kStages], (j / kStages) & 1, dl);
+            __syncwarp();
+        } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+            // ------------------------------------------------------------ products of query tile x
+            const int x = static_cast<int>(uniform(static_cast<uint32_t>(warp - kMmaWarp)));
+            const bool lead = elect_one_sync();
+            constexpr uint32_t idS = idesc_f16(128, 128, BF16, false);
+            constexpr uint32_t idO = idesc_f16(128, D, BF16, true);
+            const uint64_t q_desc = uniform(sdesc_sw128(smem_u32(sq + x * C::kTile), 16, 1024));
+            const uint64_t k_desc = sdesc_sw128(smem_u32(skv), 16, 1024);
+            const uint64_t v_desc = sdesc_sw128(smem_u32(skv), 16384, 1024);
+            constexpr uint32_t kTileDesc = C::kTile >> 4;
+            const uint32_t ts = uniform(tbase + 128 * x), to = uniform(tbase + kOCol + D * x);
+            int blk = 0, items = 0, outs = 0;                // tiles, pieces (S begun, O begun) so far
+            bool ok = true;
+            const auto wait = [&](uint64_t* bar, int parity) {
+                return warp_wait_within(bar, static_cast<uint32_t>(parity & 1), p.budget_ns, abort_flag, status);
+            };
+            // rows of a V tile past the prefix's end may hold anything, and a weight of 0 must not meet a NaN
+            // (both issuers may clear them: they write the same)
+            const auto clear_tail = [&](int st, int valid) {
+                for (int e = lane; e < (128 - valid) * (D / 8); e += 32) {
+                    const int r = valid + e / (D / 8), c = e % (D / 8);
+                    *reinterpret_cast<uint4*>(skv + st * C::kTile + (c >> 3) * 16384 + r * 128 + (c & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+            };
+            const auto issue_s = [&](int st) {
+                const uint64_t kb = uniform(k_desc + static_cast<uint32_t>(st) * kTileDesc);
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+                    mma_f16_ss_if(lead, ts, q_desc + off, kb + off, idS, kk > 0 ? 1u : 0u);
+                }
+                mma_commit_if(lead, &s_full[x]);
+                // passes on what the loader has noted, which this warp has seen by its wait for the tile
+                mbar_arrive_if(lead, &s_full[x]);
+            };
+            // half of P V, which the softmax hands over while it works on the rest
+            const auto issue_pv = [&](uint64_t vb, int half, bool begins) {
+                tc_fence_after();
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int kk = 4 * half + e;
+                    mma_f16_ts_if(lead, to, ts + 8 * kk, vb + ((kk * 2048) >> 4), idO, (!begins || half > 0 || e > 0) ? 1u : 0u);
+                }
+            };
+            if constexpr (HALVES) {
+                // Every stage is waited for in turn, the other tile's too, which are given back here as they are
+                // not read.  V is given back by the product itself, so that the next tiles can come early.
+                int g = 0;                                   // ring position: K at g, V after it
+                while (ok && next_piece(p, walk, piece)) {
+                    const int n = piece.k1 - piece.k0, mine = tiles_of(x, n);
+                    int done = 0;
+                    for (int i = 0; ok && i < n; ++i, g += 2) {
+                        const int sk = g % kStages, sv = (g + 1) % kStages;
+                        if (!(ok = wait(&full[sk], g / kStages))) break;
+                        if ((i & 1) != x) {
+                            mbar_arrive_if(lead, &empty[sk]);
+                            if (!(ok = wait(&full[sv], (g + 1) / kStages))) break;
+                            mbar_arrive_if(lead, &empty[sv]);
+                            continue;
+                        }
+                        if (done == 0 && !(ok = wait(&q_full[x], items++))) break;
+                        issue_s(sk);
+                        ++blk;
+                        if (!(ok = wait(&full[sv], (g + 1) / kStages))) break;
+                        const int valid = piece.len - 128 * (piece.k0 + i);
+                        if (valid < 128) clear_tail(sv, valid);
+                        if (done == 0 && outs++ > 0 && !(ok = wait(&o_free[x], outs - 2))) break;
+                        const uint64_t vb = uniform(v_desc + static_cast<uint32_t>(sv) * kTileDesc);
+                        if (!(ok = wait(&p_half[x], blk - 1))) break;
+                        issue_pv(vb, 0, done == 0);
+                        if (!(ok = wait(&p_full[x], blk - 1))) break;
+                        issue_pv(vb, 1, done == 0);
+                        if (++done == mine) mma_commit_if(lead, &o_full[x]);
+                        mma_commit_if(lead, &empty[sv]);
+                    }
+                }
+            } else {
+                int g = 0, rounds = 0;
+                bool pend = false, begins = false, ends = false; // a tile awaits its P V, which begins / ends its O
+                int valid = 128;                                 // its rows of V that are the prefix's
+                // One round: P V of the tile before, be it of the piece before, and S of the tile at position g,
+                // if there is one.  None of its waits waits for what comes after it: K of position g takes
+                // the stage of position g - 5 or an earlier one, which the softmax gave back for a round before.
+                auto round = [&](bool tile, bool first, bool last, int rows) {
+                    const int sk = g % kStages, sv = (g + kStages - 1) % kStages;
+                    if (pend && !wait(&full[sv], (g - 1) / kStages)) return false;
+                    if (pend && valid < 128) clear_tail(sv, valid);
+                    if (tile && !wait(&full[sk], g / kStages)) return false;
+                    const uint64_t vb = uniform(v_desc + static_cast<uint32_t>(sv) * kTileDesc);
+                    if (tile && first && !wait(&q_full[x], items++)) return false;
+                    // tile 0's round comes after tile 1's round before, tile 1's after tile 0's
+                    if (rounds + x > 0 && !wait(&turn[x], rounds + x + 1)) return false;
+                    ++rounds;
+                    if (pend) {
+                        if (begins && outs++ > 0 && !wait(&o_free[x], outs - 2)) return false;
+                        if (!wait(&p_half[x], blk - 1)) return false;
+                        issue_pv(vb, 0, begins);
+                        if (!wait(&p_full[x], blk - 1)) return false;
+                        issue_pv(vb, 1, begins);
+                        if (ends) mma_commit_if(lead, &o_full[x]);
+                        pend = false;
+                    }
+                    if (tile) {
+                        issue_s(sk);
+                        ++blk;
+                        pend = true;
+                        begins = first;
+                        ends = last;
+                        valid = rows;
+                    }
+                    mbar_arrive_if(lead, &turn[1 - x]);
+                    return true;
+                };
+                while (ok && next_piece(p, walk, piece))
+                    for (int k = piece.k0; ok && k < piece.k1; ++k, g += 2)
+                        ok = round(true, k == piece.k0, k == piece.k1 - 1, piece.len - 128 * k);
+                if (ok) round(false, false, false, 0);
+            }
+            mma_commit_if(lead, &fin[x]);
+            wait_parity_drain(&fin[x], 0, global_timer_ns() + 200000000ull);
+            __syncwarp();
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+        // ------------------------------------------------------------ softmax of query tile x
+        const int x = warp >> 2;
+        const int lrow = 32 * (warp & 3) + lane;
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const uint32_t ts = tbase + lanes + 128 * x, to = tbase + lanes + kOCol + D * x;
+        const float c = p.scale_log2;
+        const bool speaks = (warp & 3) == 0 && lane == 0;
+        const int tile_rows = HALVES ? p.s.part_rows : p.s.part_rows / 2;
+        const int irow = HALVES ? lrow : x * tile_rows + lrow;       // row of the item
+        int blk = 0, items = 0, g = 0;
+        bool ok = true;
+        Walk walk = start;
+        Piece piece;
+        while (next_piece(p, walk, piece)) {
+            const int pieces = piece.k1 - piece.k0, n = tiles_of(x, pieces);
+            const int g0 = g;                            // ring position of the piece's first K tile
+            g += 2 * pieces;
+            const bool mine = lrow < tile_rows && irow < piece.rows;
+            const size_t at = HALVES
+                ? static_cast<size_t>(blockIdx.x) * 2 * p.s.part_rows + 2 * piece.place + x * piece.rows + irow
+                : static_cast<size_t>(blockIdx.x) * p.s.part_rows + piece.place + irow;
+            float m_used = -INFINITY, l = 0.f;
+            int v_read = -1;                             // stage of the V tile to give back when it is read
+            for (int i = 0; ok && i < n; ++i, ++blk) {
+                const int u = HALVES ? 2 * i + x : i;
+                const int st = (g0 + 2 * u) % kStages;
+                if (!warp_wait_within(&s_full[x], blk & 1, p.budget_ns, abort_flag, status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const int gone = missing[((g0 >> 1) + u) % kNotes];
+                if (speaks) {
+                    // S of this tile is there: its K tile has been read, and V of the tile before
+                    if (!HALVES && v_read >= 0) mbar_arrive(&empty[v_read]);
+                    mbar_arrive(&empty[st]);
+                    v_read = (g0 + 2 * u + 1) % kStages;
+                    if (i == n - 1) mbar_arrive(&q_free[x]);
+                }
+                __syncwarp();
+                float s[128];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) tmem_ld_row32(ts + 32 * h, reinterpret_cast<uint32_t*>(s) + 32 * h);
+                tmem_wait_ld();
+                const int valid = piece.len - 128 * (piece.k0 + u);
+                if (valid < 128 || gone != 0) {
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        const uint32_t on = gone >> (h >> 1) & 1 ? 0u : below(valid - 32 * h);
+                        if (on == 0xffffffffu) continue;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!((on >> e) & 1u)) s[32 * h + e] = -INFINITY;
+                    }
+                }
+                float mx;
+                {
+                    float m4[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        m4[j] = max3f(s[j], s[j + 4], s[j + 8]);
+#pragma unroll
+                        for (int e = 12; e + 4 < 128; e += 8) m4[j] = max3f(m4[j], s[j + e], s[j + e + 4]);
+                        m4[j] = fmaxf(m4[j], s[j + 124]);
+                    }
+                    mx = fmaxf(max3f(m4[0], m4[1], m4[2]), m4[3]);
+                }
+                const bool grow = mx * c > m_used * c + kRescaleLog2;
+                const float m_new = grow ? mx : m_used;
+                const float alpha = grow ? ex2_approx((m_used - m_new) * c) : 1.f;
+                const bool rescale = grow && m_used != -INFINITY;
+                m_used = m_new;
+                const float mc = m_new == -INFINITY ? 0.f : m_new * c;
+                if (__any_sync(0xffffffffu, rescale)) {
+                    // O holds every tile before this one: their P V ran before this tile's S
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t o[32];
+                        tmem_ld_row32(to + c0, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        tmem_st_row32(to + c0, o);
+                    }
+                }
+                float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                                 make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t pv[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 y = fma2f(make_float2(s[32 * h + 2 * e], s[32 * h + 2 * e + 1]), make_float2(c, c),
+                                               make_float2(-mc, -mc));
+                        const float2 ev = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                        acc[e & 3] = add2f(acc[e & 3], ev);
+                        pv[e] = pack2<BF16>(ev.x, ev.y);
+                    }
+                    tmem_st_row16(ts + 16 * h, pv);
+                    if (h == 1) {
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&p_half[x]);
+                    }
+                }
+                const float2 a2 = add2f(add2f(acc[0], acc[1]), add2f(acc[2], acc[3]));
+                l = l * alpha + (a2.x + a2.y);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[x]);
+            }
+            // ---- the piece's O / l and log-sum-exp (base 2)
+            if (ok && n > 0) {
+                ok = warp_wait_within(&o_full[x], items & 1, p.budget_ns, abort_flag, status);
+                ++items;
+            }
+            if (!ok) {
+                // (and so for the pieces after it: what lacks a part shows it)
+                if (mine) p.s.lse[at] = __int_as_float(0x7fffffff);
+                continue;
+            }
+            if (n == 0) {
+                if (mine) p.s.lse[at] = -INFINITY;
+                continue;
+            }
+            tc_fence_after();
+            if (!HALVES && speaks) mbar_arrive(&empty[v_read]);
+            __syncwarp();
+            uint32_t o[D];
+#pragma unroll
+            for (int c0 = 0; c0 < D; c0 += 32) tmem_ld_row32(to + c0, o + c0);
+            tmem_wait_ld();
+            // O is in registers: the next piece's first P V may overwrite it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&o_free[x]);
+            if (mine) {
+                // a row without a finite score has l = 0, or NaN if it met one
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                float4* out = reinterpret_cast<float4*>(p.s.o + at * D);
+#pragma unroll
+                for (int e = 0; e < D / 4; ++e)
+                    out[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                                         __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+                p.s.lse[at] = l == 0.f ? -INFINITY : m_used * c + log2f(l);
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tbase, kTmemCols);
+    }
+}
+
+template <int D, bool BF16, bool HALVES>
+int launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PrefixParams& prm, int sms,
+           cudaStream_t stream) {
+    auto kern = prefix_kernel<D, BF16, HALVES>;
+    static std::atomic<unsigned long long> raised{0};
+    const int rc = raise_smem_limit(reinterpret_cast<const void*>(kern), Cfg<D>::kBytes, raised);
+    if (rc) return rc;
+    // the warpgroups' register shares come out of the launch's: with fewer, the larger ones would never come
+    static const bool enough = [kern] {
+        cudaFuncAttributes a{};
+        return cudaFuncGetAttributes(&a, kern) == cudaSuccess &&
+               a.numRegs * kThreads >= 128 * (2 * kRegsSoftmax + kRegsOther);
+    }();
+    if (!enough) return BSATTN_ERR_CUDA;
+    kern<<<static_cast<unsigned>(sms), kThreads, Cfg<D>::kBytes, stream>>>(tq, tk, tv, prm);
+    return cudaGetLastError() == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
+}
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// The prefixes' share of the workspace, behind that of the stream decode.
+struct PrefixLayout {
+    size_t info, lse, o, total;
+    PrefixPieces s;
+};
+
+PrefixLayout prefix_layout(int B, int P, int Hq, int Hkv, int d, int sms) {
+    PrefixLayout w{};
+    const int G = Hq / Hkv, tile = 128 / G;              // sequences of a 128-row tile
+    // A prefix with no more than a tile of rows, on the average, has both query tiles of a CTA to itself.
+    w.s.halves = (static_cast<long long>(B) + P - 1) / P <= tile;
+    w.s.seqs = w.s.halves ? tile : 2 * tile;
+    w.s.part_rows = w.s.seqs * G;
+    w.s.P = P;
+    w.s.B = B;
+    w.s.Hq = Hq;
+    w.s.Hkv = Hkv;
+    w.s.rows = (static_cast<long long>(B) * Hq + static_cast<long long>(sms) * w.s.part_rows) * (w.s.halves ? 2 : 1);
+    w.info = bsattn_decode_window_workspace_size(Hq, Hkv, d);
+    w.lse = w.info + up256(sizeof(long long) * (static_cast<size_t>(P) + 1));
+    w.o = w.lse + up256(sizeof(float) * static_cast<size_t>(w.s.rows));
+    w.total = w.o + up256(sizeof(float) * static_cast<size_t>(w.s.rows) * d);
+    return w;
+}
+
+int sms_of_device() {
+    const int n = num_sms_of_current_device();
+    return n > 0 ? n : 148;
+}
+
+}  // namespace
+}  // namespace bsattn
+
+extern "C" size_t bsattn_decode_shared_workspace_size(int B, int P, int Hq, int Hkv, int d) {
+    using namespace bsattn;
+    if (B <= 0 || P <= 0 || Hq <= 0 || Hkv <= 0 || d <= 0 || Hq % Hkv || Hq / Hkv > 8)
+        return bsattn_decode_window_workspace_size(Hq, Hkv, d);
+    return prefix_layout(B, P, Hq, Hkv, d, sms_of_device()).total;
+}
+
+extern "C" int bsattn_decode_shared(const void* q, const void* k_pages, const void* v_pages,
+                                    const int32_t* prefix_lens, const int32_t* prefix_table,
+                                    const int32_t* group_starts, const int32_t* cache_seqlens,
+                                    const int32_t* block_table, void* out, int B, int P, int Hq, int Hkv,
+                                    int num_pages, int page_size, int max_pages_per_prefix, int max_pages_per_seq,
+                                    int d, bsattn_dtype dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    using namespace bsattn;
+    if (B < 0 || P <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || num_pages <= 0 || page_size <= 0 ||
+        max_pages_per_prefix <= 0 || max_pages_per_seq <= 0)
+        return BSATTN_ERR_INVALID_ARG;
+    if (Hq / Hkv > 8 || page_size % 64 || (d != 64 && d != 128)) return BSATTN_ERR_UNSUPPORTED;
+    if (dtype != BSATTN_F16 && dtype != BSATTN_BF16) return BSATTN_ERR_UNSUPPORTED;
+    if (!workspace || !aligned16(workspace)) return BSATTN_ERR_INVALID_ARG;
+    if (static_cast<long long>(num_pages) * page_size > 0x7fffffffLL - 128) return BSATTN_ERR_UNSUPPORTED;
+    if (B == 0) return BSATTN_OK;
+    if (!q || !out || !k_pages || !v_pages || !prefix_lens || !prefix_table || !group_starts || !cache_seqlens ||
+        !block_table)
+        return BSATTN_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(k_pages) || !aligned16(v_pages)) return BSATTN_ERR_INVALID_ARG;
+    // the prefix kernel has read all of q when the other writes out, as decode_stream() checks it
+    const int sms = sms_of_device();
+    PrefixLayout w = prefix_layout(B, P, Hq, Hkv, d, sms);
+    if (workspace_bytes < w.total) return BSATTN_ERR_INVALID_ARG;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    w.s.starts = group_starts;
+    w.s.lens = prefix_lens;
+    w.s.info = reinterpret_cast<long long*>(ws + w.info);
+    w.s.lse = reinterpret_cast<float*>(ws + w.lse);
+    w.s.o = reinterpret_cast<float*>(ws + w.o);
+    w.s.room = static_cast<int>(std::min(static_cast<long long>(max_pages_per_prefix) * page_size, 1LL << 30));
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const StreamCall own{q, k_pages, v_pages, cache_seqlens, block_table, out, B, Hq, Hkv, num_pages, page_size,
+                         max_pages_per_seq, d, dtype, workspace, w.info};
+    int rc = decode_stream_shared(own, w.s, true, st);           // checks alone
+    if (rc) return rc;
+    PrefixParams prm{};
+    prm.s = w.s;
+    prm.table = prefix_table;
+    prm.status = status_word(workspace);
+    prm.page_size = page_size;
+    prm.max_pages = max_pages_per_prefix;
+    prm.num_pages = num_pages;
+    prm.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(d)));
+    prm.budget_ns = wait_budget_ns();
+    const int G = Hq / Hkv, tile = 128 / G;
+    prm.q_bytes = tile * G * d * 2;
+    const bool bf16 = dtype == BSATTN_BF16;
+    CUtensorMap tq, tk, tv;
+    const uint64_t dq[4] = {uint64_t(d), uint64_t(G), uint64_t(Hkv), uint64_t(B)};
+    const uint64_t sq[3] = {d * 2ull, uint64_t(G) * d * 2, uint64_t(Hq) * d * 2};
+    const uint32_t bq[4] = {64, uint32_t(G), 1, uint32_t(tile)};
+    const uint64_t rows = uint64_t(num_pages) * page_size, row_bytes = uint64_t(Hkv) * d * 2;
+    rc = encode_4d(&tq, q, bf16, dq, sq, bq);
+    if (!rc) rc = encode_3d(&tk, k_pages, bf16, d, Hkv, rows, d * 2ull, row_bytes, 64, 1, 64, true);
+    if (!rc) rc = encode_3d(&tv, v_pages, bf16, d, Hkv, rows, d * 2ull, row_bytes, 64, 1, 64, true);
+    if (rc) return rc;
+    const auto run = [&](auto dim, auto halves) {
+        constexpr int D = decltype(dim)::value;
+        constexpr bool HALVES = decltype(halves)::value;
+        return bf16 ? launch<D, true, HALVES>(tq, tk, tv, prm, sms, st) : launch<D, false, HALVES>(tq, tk, tv, prm, sms, st);
+    };
+    using D64 = std::integral_constant<int, 64>;
+    using D128 = std::integral_constant<int, 128>;
+    if (w.s.halves) rc = d == 64 ? run(D64{}, std::true_type{}) : run(D128{}, std::true_type{});
+    else rc = d == 64 ? run(D64{}, std::false_type{}) : run(D128{}, std::false_type{});
+    return rc ? rc : decode_stream_shared(own, w.s, false, st);
+}

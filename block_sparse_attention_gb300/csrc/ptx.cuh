@@ -110,6 +110,27 @@ __device__ __forceinline__ bool warp_wait_parity(uint64_t* bar, uint32_t parity,
     return __all_sync(0xffffffffu, ok);
 }
 
+// warp_wait_parity with a budget that runs from the wait's own first poll: a call over a long cache may
+// itself take longer than any of its waits may.
+__device__ __forceinline__ bool warp_wait_within(uint64_t* bar, uint32_t parity, uint64_t budget_ns,
+                                                 volatile int* abort_flag, int* status) {
+    if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+    bool ok = true;
+    uint64_t deadline = 0;
+    for (uint32_t spins = 0; !mbar_try_wait(bar, parity); ++spins) {
+        if ((spins & 63u) != 0) continue;           // the clock is read after the first poll and every 64th
+        const uint64_t now = global_timer_ns();
+        if (spins == 0) deadline = now + budget_ns;
+        if (*abort_flag || now >= deadline) {
+            if (!*abort_flag) atomicOr(status, BSATTN_ERR_TIMEOUT);
+            *abort_flag = 1;
+            ok = false;
+            break;
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
 __device__ __forceinline__ float ex2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -388,6 +388,116 @@ int bsattn_prefill_window(const void* q, const void* k, const void* v, int windo
                           bsattn_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * ---------------------------------------------------------------------------------------------
+ * Choosing key blocks on the GPU.  The summary of a block of up to 64 rows is its mean in 8 bits: the rows'
+ * 32-bit sum, taken in halves (row i + row i + 32, then i + 16, ... i + 1, absent rows being 0), divided by
+ * their number; scale = max |mean| / 127 and code_c = mean_c / scale, each quotient rounded to nearest in 32
+ * bits, the code then to a whole number (ties to even, at most 127 in magnitude; 0 where the scale is 0).  A
+ * mean with a channel that is not finite has codes 0 and scale +infinity.  A query or a query block is
+ * summarised likewise (one row, or the block's).
+ * The score of a key block for query summaries h = 1 .. G is
+ *     (max_h ((sum_c code_hc code_c) scale_h)) scale,
+ * a whole number, exact, times two factors, each product rounded to nearest in 32 bits; +infinity where
+ * the key's scale is, and a query whose own scale is infinite counts as scale 0.  Nothing in it depends on the
+ * order of additions, and of blocks with equal scores the lower one comes first: a choice is the same
+ * wherever and however it is made.  These calls have no counterpart in the pages; the block scores stand for
+ * the given ones of bsattn_mask_from_topk.
+ */
+
+/*
+ * Summarises again, for every sequence b, each 64-token block that holds one of its last new_lens[b] tokens,
+ * from the rows in the cache (so tokens are appended first, in one step or in many).
+ *
+ *   k_pages        (device) [num_pages, page_size, Hkv, d] dtype, as in bsattn_decode_paged; page_size a
+ *                  multiple of 64
+ *   cache_seqlens  (device) [B] int32: lengths with the new tokens;  new_lens (device) [B] int32
+ *   block_table    (device) [B, max_pages_per_seq] int32
+ *   codes          (device) [num_pages, page_size / 64, Hkv, d] int8, updated
+ *   scales         (device) [num_pages, page_size / 64, Hkv] fp32, updated
+ * k_pages, codes and scales 16-byte aligned.  Entries of other blocks are left as they were; rows past a
+ * sequence's end have no effect.  Blocks on pages out of range and lengths past the table are skipped, a
+ * negative length or new_lens[b] counts as 0, one past the length as the length; all are flagged
+ * BSATTN_ERR_BAD_INDEX.  Sequences that share a block must agree about its rows.  codes and scales share no
+ * memory with the inputs (BSATTN_ERR_INVALID_ARG).  Workspace: a status word (256 bytes), as for the plan.
+ */
+int bsattn_index_update(const void* k_pages, const int32_t* cache_seqlens, const int32_t* new_lens,
+                        const int32_t* block_table, int8_t* codes, float* scales, int B, int Hkv, int num_pages,
+                        int page_size, int max_pages_per_seq, int d, bsattn_dtype dtype, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * The key blocks of one query token per sequence, for bsattn_decode_paged and bsattn_decode_paged_kv4 (or,
+ * with a table of consecutive pages, bsattn_decode_varlen): for sequence b and kv head g the first `sinks` and
+ * the last `recent` blocks of its cache_seqlens[b] tokens, then those with the highest scores for its
+ * G = Hq / Hkv query heads, max_sel in all or as many as there are.
+ *
+ *   q              (device) [B, Hq, d] dtype;  codes, scales, block_table as above
+ *   block_indices  (device) [B, Hkv, max_sel] int32, fully written: the chosen blocks in rising order, then -1
+ * sinks + recent <= max_sel (else BSATTN_ERR_INVALID_ARG).  Blocks on pages out of range are not chosen, a
+ * length past the table is taken as the table's, a negative one as 0; all are flagged BSATTN_ERR_BAD_INDEX.
+ * Requires Hq / Hkv <= 8, d in {64, 128}, max_pages_per_seq * page_size <= 3276800.  block_indices shares no
+ * memory with the inputs.  Workspace: a status word.
+ */
+int bsattn_decode_select(const void* q, const int8_t* codes, const float* scales, const int32_t* cache_seqlens,
+                         const int32_t* block_table, int sinks, int recent, int32_t* block_indices, int B, int Hq,
+                         int Hkv, int num_pages, int page_size, int max_pages_per_seq, int d, int max_sel,
+                         bsattn_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * A block mask for bsattn_prefill from the summaries of q's and k's 64-row blocks (of the rows there are, at the
+ * end).  Query block r sees the key blocks up to that of its last row's position min(64 r + 63, Sq - 1) + Sk -
+ * Sq (bottom-right alignment), or all of them if not is_causal.  Of these it gets the first `sinks` and the last
+ * `recent`, then those with the highest scores until it has topk (forced blocks stay, however many), or all of
+ * them if use_dense_for_last_block and r is one of the last two.  Under the causal rule `recent` 1 is the
+ * diagonal block; where Sk - Sq is not a multiple of 64 a block's rows begin in the block before it, and 2 has
+ * all of them see themselves.
+ *
+ *   q         (device) [B, Hq, Sq, d] dtype;  k (device) [B, Hkv, Sk, d] dtype; 16-byte aligned.  Query head h
+ *             is scored against kv head h / (Hq / Hkv)
+ *   strides   (host) 6 element strides: batch, head, row of q, of k (multiples of 8, not negative; any value
+ *             for a dimension of one entry; channels contiguous), or NULL for dense tensors
+ *   mask_out  (device) [B, Hq, ceil(Sq/64), ceil(Sk/64)] uint8, fully written with 0 / 1
+ *   workspace (device) >= bsattn_mask_from_qk_workspace_size bytes, 16-byte aligned; need not be zero-filled.
+ *             Calls that can overlap on the GPU need one each.
+ * d in {64, 128}; Sk <= 450560 (else BSATTN_ERR_UNSUPPORTED).  mask_out and workspace share no memory with one
+ * another, q or k (BSATTN_ERR_INVALID_ARG).
+ */
+int bsattn_mask_from_qk(const void* q, const void* k, int topk, int sinks, int recent,
+                        int use_dense_for_last_block, int is_causal, uint8_t* mask_out, int B, int Hq, int Hkv,
+                        int Sq, int Sk, int d, const int64_t* strides, bsattn_dtype dtype, void* workspace,
+                        size_t workspace_bytes, void* stream);
+size_t bsattn_mask_from_qk_workspace_size(int B, int Hq, int Hkv, int Sq, int Sk, int d);
+
+/*
+ * One query token per sequence over a prefix that sequences share and the sequence's own tokens after it, a
+ * stream decode over a 16-bit paged cache: out = softmax(q . k / sqrt(d)) v over both.  The prefix is read
+ * once for all the sequences that share it (for 256 query rows of a kv head at a time), not once for each.
+ *
+ *   q, out         (device) [B, Hq, d] dtype;  k_pages, v_pages (device) [num_pages, page_size, Hkv, d] dtype
+ *   prefix_lens    (device) [P] int32: tokens of prefix p, any number
+ *   prefix_table   (device) [P, max_pages_per_prefix] int32: its pages
+ *   group_starts   (device) [P + 1] int32: sequences group_starts[p] .. group_starts[p + 1] - 1 share prefix p;
+ *                  rising from 0 to B
+ *   cache_seqlens  (device) [B] int32: a sequence's own tokens, which may be none
+ *   block_table    (device) [B, max_pages_per_seq] int32: their pages
+ * No visible token gives 0.  Tokens on pages out of range, and any past a table, are skipped, a negative length
+ * is taken as 0; these and group_starts that do not rise from 0 to B are flagged BSATTN_ERR_BAD_INDEX (the
+ * rows of groups that overlap or run backwards are then undefined; a sequence outside all groups has no prefix).
+ * Rows past a length may hold anything.  P is rounded to dtype before the second product.  A wait that expires
+ * makes every row NaN that lacks some of its tokens, and leaves the workspace ready for the next call.
+ * P >= 1, Hq / Hkv <= 8, Hkv <= 1024, d in {64, 128}, page_size a multiple of 64, a prefix of at most 2^30
+ * tokens.  out may be q itself; otherwise it shares no memory with q or the cache.  Workspace:
+ * bsattn_decode_shared_workspace_size bytes, its first 4352 zero before the first use; one zeroed once serves every
+ * shape that fits it.
+ */
+int bsattn_decode_shared(const void* q, const void* k_pages, const void* v_pages, const int32_t* prefix_lens,
+                         const int32_t* prefix_table, const int32_t* group_starts, const int32_t* cache_seqlens,
+                         const int32_t* block_table, void* out, int B, int P, int Hq, int Hkv, int num_pages,
+                         int page_size, int max_pages_per_prefix, int max_pages_per_seq, int d, bsattn_dtype dtype,
+                         void* workspace, size_t workspace_bytes, void* stream);
+size_t bsattn_decode_shared_workspace_size(int B, int P, int Hq, int Hkv, int d);
+
+/*
  * Reads and clears the device status word at the start of `workspace` (device), after
  * synchronising `stream`.  Returns the OR of the BSATTN_ERR_* bits the kernels recorded
  * since the last read (0 = none), or BSATTN_ERR_CUDA if the read itself failed.  Only the
