@@ -6,7 +6,7 @@
 // The softmax over both is joined from its parts: with (O, L) the result and log-sum-exp of a part,
 // out = sum O 2^(L - M) / sum 2^(L - M).  This file's kernel does the prefixes: the query heads of a kv head of
 // all sequences that share one are the rows of its products, so K and V of a prefix are read once for up to
-// 256 rows and not once a sequence.  decode_stream.cu then does the sequences' own tokens and joins.
+// 256 rows and not once a sequence.  decode_shared_own.cu does the sequences' own tokens, and joins.
 //
 // For few rows HBM bandwidth bounds this, for many the tensor core (256 rows of d = 128: 256 operations a
 // byte against the 280 that the two peaks divide to).  The rows stand in two tcgen05 tiles a CTA:
@@ -18,7 +18,7 @@
 // when it has grown by 2^8.  Where a prefix has no more than 128 rows, both tiles are the same rows and take
 // every second key tile each, without turns.
 // The prefixes' keys, end to end, are cut into equal parts, one a CTA, so that one long prefix and many
-// short ones both fill the GPU (shared_prefix.cuh); a CTA goes from one piece to the next without a break.
+// short ones both fill the GPU (decode_shared.cuh); a CTA goes from one piece to the next without a break.
 //
 // TMEM: S_0 0-127, S_1 128-255, O_0 256.., O_1 256 + d...  Every wait is bounded: on expiry the CTA records
 // BSATTN_ERR_TIMEOUT, hands its remaining pieces over as NaN, drains what is in flight and leaves.
@@ -26,8 +26,8 @@
 #include <cmath>
 #include <type_traits>
 
+#include "decode_shared.cuh"
 #include "host_internal.h"
-#include "shared_prefix.cuh"
 #include "tile128.cuh"
 
 namespace bsattn {
@@ -58,13 +58,8 @@ struct Cfg {
 };
 
 struct PrefixParams {
-    PrefixPieces s;
-    const int32_t* table;                // [P, max_pages]
-    int* status;
-    int page_size, max_pages, num_pages;
+    SharedCall s;
     int q_bytes;                         // of a query tile
-    float scale_log2;
-    unsigned long long budget_ns;
 };
 
 // A CTA's walk over its units, from piece to piece.
@@ -129,13 +124,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     int* misc = reinterpret_cast<int*>(sm + C::kMisc);
     int* missing = reinterpret_cast<int*>(sm + C::kMissing);
     volatile int* abort_flag = &misc[1];
-    int* status = p.status;
+    int* status = p.s.status;
     __shared__ long long warp_sums[kThreads / 32];
     __shared__ long long first_base;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     // the kernel that joins may start wherever there is room: it waits for this one by itself
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // and this one ends no sooner than the one before it
+    const auto leave = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
 
     // ------------------------------------------------------------ this CTA's part of all units
     Walk start;
@@ -170,14 +167,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < per; ++k) {
                 const int i = tid * per + k;
                 if (i >= p.s.P) break;
-                p.s.info[1 + i] = before;
+                p.s.prefix_info[1 + i] = before;
                 before += prefix_units(p.s, prefix_group(p.s, i));
             }
-            if (tid == 0) p.s.info[0] = chunk;
+            if (tid == 0) p.s.prefix_info[0] = chunk;
         }
         start.at = static_cast<long long>(blockIdx.x) * chunk;
         start.end = min(start.at + chunk, total);
-        if (start.at >= total) return;                        // the whole CTA
+        if (start.at >= total) {                              // the whole CTA
+            leave();
+            return;
+        }
         if (upto - sum <= start.at && start.at < upto) {
             int i = tid * per;
             long long before = upto - sum;
@@ -248,20 +248,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int key = 2 * (piece.k0 + i) * 64 + 64 * lane;
                         look = -1;
                         if (key < piece.len && key < 128 * piece.k1) {
-                            const int lp = key / p.page_size;
-                            const int page = p.table[static_cast<size_t>(piece.p) * p.max_pages + lp];
-                            if (page >= 0 && page < p.num_pages) look = page * p.page_size + key - lp * p.page_size;
+                            const int lp = key / p.s.page_size;
+                            const int page = p.s.prefix_table[static_cast<size_t>(piece.p) * p.s.prefix_pages + lp];
+                            if (page >= 0 && page < p.s.num_pages) look = page * p.s.page_size + key - lp * p.s.page_size;
                             else bad = true;
                         }
                     }
                     const int r0 = __shfl_sync(0xffffffffu, look, 2 * (i & 15));
                     const int r1 = __shfl_sync(0xffffffffu, look, 2 * (i & 15) + 1);
                     // rows past the cache's end are filled with zeros
-                    const int none = p.num_pages * p.page_size;
+                    const int none = p.s.num_pages * p.s.page_size;
 #pragma unroll 1
                     for (int v = 0; ok && v < 2; ++v) {
                         const int st = g % kStages;
-                        ok = g < kStages || warp_wait_within(&empty[st], (g / kStages - 1) & 1, p.budget_ns, abort_flag, status);
+                        ok = g < kStages || warp_wait_within(&empty[st], (g / kStages - 1) & 1, p.s.budget_ns, abort_flag, status);
                         if (!ok) break;
                         if (lane == 0) {
                             if (v == 0) missing[(g >> 1) % kNotes] = (r0 < 0 ? 1 : 0) | (r1 < 0 ? 2 : 0);
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (i > 0 || v > 0) continue;
                         for (int x = 0; ok && x < 2; ++x) {
                             if (tiles_of(x, n) == 0) continue;
-                            ok = nq[x] == 0 || warp_wait_within(&q_free[x], (nq[x] - 1) & 1, p.budget_ns, abort_flag, status);
+                            ok = nq[x] == 0 || warp_wait_within(&q_free[x], (nq[x] - 1) & 1, p.s.budget_ns, abort_flag, status);
                             if (!ok) break;
                             if (lane == 0) {
                                 mbar_arrive_expect_tx(&q_full[x], static_cast<uint32_t>(p.q_bytes));
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int blk = 0, items = 0, outs = 0;                // tiles, pieces (S begun, O begun) so far
             bool ok = true;
             const auto wait = [&](uint64_t* bar, int parity) {
-                return warp_wait_within(bar, static_cast<uint32_t>(parity & 1), p.budget_ns, abort_flag, status);
+                return warp_wait_within(bar, static_cast<uint32_t>(parity & 1), p.s.budget_ns, abort_flag, status);
             };
             // rows of a V tile past the prefix's end may hold anything, and a weight of 0 must not meet a NaN
             // (both issuers may clear them: they write the same)
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int lrow = 32 * (warp & 3) + lane;
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t ts = tbase + lanes + 128 * x, to = tbase + lanes + kOCol + D * x;
-        const float c = p.scale_log2;
+        const float c = p.s.scale_log2;
         const bool speaks = (warp & 3) == 0 && lane == 0;
         const int tile_rows = HALVES ? p.s.part_rows : p.s.part_rows / 2;
         const int irow = HALVES ? lrow : x * tile_rows + lrow;       // row of the item
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; ok && i < n; ++i, ++blk) {
                 const int u = HALVES ? 2 * i + x : i;
                 const int st = (g0 + 2 * u) % kStages;
-                if (!warp_wait_within(&s_full[x], blk & 1, p.budget_ns, abort_flag, status)) {
+                if (!warp_wait_within(&s_full[x], blk & 1, p.s.budget_ns, abort_flag, status)) {
                     ok = false;
                     break;
                 }
@@ -541,16 +541,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // ---- the piece's O / l and log-sum-exp (base 2)
             if (ok && n > 0) {
-                ok = warp_wait_within(&o_full[x], items & 1, p.budget_ns, abort_flag, status);
+                ok = warp_wait_within(&o_full[x], items & 1, p.s.budget_ns, abort_flag, status);
                 ++items;
             }
             if (!ok) {
                 // (and so for the pieces after it: what lacks a part shows it)
-                if (mine) p.s.lse[at] = __int_as_float(0x7fffffff);
+                if (mine) p.s.prefix_lse[at] = __int_as_float(0x7fffffff);
                 continue;
             }
             if (n == 0) {
-                if (mine) p.s.lse[at] = -INFINITY;
+                if (mine) p.s.prefix_lse[at] = -INFINITY;
                 continue;
             }
             tc_fence_after();
@@ -567,12 +567,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (mine) {
                 // a row without a finite score has l = 0, or NaN if it met one
                 const float inv = l == 0.f ? 0.f : 1.f / l;
-                float4* out = reinterpret_cast<float4*>(p.s.o + at * D);
+                float4* out = reinterpret_cast<float4*>(p.s.prefix_o + at * D);
 #pragma unroll
                 for (int e = 0; e < D / 4; ++e)
                     out[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
                                          __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
-                p.s.lse[at] = l == 0.f ? -INFINITY : m_used * c + log2f(l);
+                p.s.prefix_lse[at] = l == 0.f ? -INFINITY : m_used * c + log2f(l);
             }
         }
     }
@@ -583,6 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tbase, kTmemCols);
     }
+    leave();
 }
 
 template <int D, bool BF16, bool HALVES>
@@ -599,34 +600,40 @@ int launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, 
                a.numRegs * kThreads >= 128 * (2 * kRegsSoftmax + kRegsOther);
     }();
     if (!enough) return BSATTN_ERR_CUDA;
-    kern<<<static_cast<unsigned>(sms), kThreads, Cfg<D>::kBytes, stream>>>(tq, tk, tv, prm);
-    return cudaGetLastError() == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
+    return launch_after(kern, static_cast<unsigned>(sms), kThreads, Cfg<D>::kBytes, stream, tq, tk, tv, prm);
 }
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// The prefixes' share of the workspace, behind that of the stream decode.
-struct PrefixLayout {
-    size_t info, lse, o, total;
-    PrefixPieces s;
+// Byte offsets of the workspace, behind the status word, and what depends on the shape and the GPU alone.
+struct Layout {
+    size_t prefix_info, own_info, prefix_lse, prefix_o, own_lse, own_o, total;
+    int halves, seqs, part_rows, own_parts;
 };
 
-PrefixLayout prefix_layout(int B, int P, int Hq, int Hkv, int d, int sms) {
-    PrefixLayout w{};
+Layout layout_of(int B, int P, int Hq, int Hkv, int d, int sms) {
+    Layout w{};
     const int G = Hq / Hkv, tile = 128 / G;              // sequences of a 128-row tile
     // A prefix with no more than a tile of rows, on the average, has both query tiles of a CTA to itself.
-    w.s.halves = (static_cast<long long>(B) + P - 1) / P <= tile;
-    w.s.seqs = w.s.halves ? tile : 2 * tile;
-    w.s.part_rows = w.s.seqs * G;
-    w.s.P = P;
-    w.s.B = B;
-    w.s.Hq = Hq;
-    w.s.Hkv = Hkv;
-    w.s.rows = (static_cast<long long>(B) * Hq + static_cast<long long>(sms) * w.s.part_rows) * (w.s.halves ? 2 : 1);
-    w.info = bsattn_decode_window_workspace_size(Hq, Hkv, d);
-    w.lse = w.info + up256(sizeof(long long) * (static_cast<size_t>(P) + 1));
-    w.o = w.lse + up256(sizeof(float) * static_cast<size_t>(w.s.rows));
-    w.total = w.o + up256(sizeof(float) * static_cast<size_t>(w.s.rows) * d);
+    w.halves = (static_cast<long long>(B) + P - 1) / P <= tile;
+    w.seqs = w.halves ? tile : 2 * tile;
+    w.part_rows = w.seqs * G;
+    w.own_parts = 4 * std::max(2 * sms / Hkv, 1);        // four warps a CTA, two CTAs an SM
+    const size_t rows = (static_cast<size_t>(B) * Hq + static_cast<size_t>(sms) * w.part_rows) * (w.halves ? 2 : 1);
+    const size_t own = (static_cast<size_t>(B) + w.own_parts) * Hq;
+    size_t at = 256;
+    const auto take = [&at](size_t bytes) {
+        const size_t here = at;
+        at += up256(bytes);
+        return here;
+    };
+    w.prefix_info = take(sizeof(long long) * (static_cast<size_t>(P) + 1));
+    w.own_info = take(sizeof(long long) * (static_cast<size_t>(B) + 1));
+    w.prefix_lse = take(sizeof(float) * rows);
+    w.prefix_o = take(sizeof(float) * rows * d);
+    w.own_lse = take(sizeof(float) * own);
+    w.own_o = take(sizeof(float) * own * d);
+    w.total = at;
     return w;
 }
 
@@ -640,9 +647,8 @@ int sms_of_device() {
 
 extern "C" size_t bsattn_decode_shared_workspace_size(int B, int P, int Hq, int Hkv, int d) {
     using namespace bsattn;
-    if (B <= 0 || P <= 0 || Hq <= 0 || Hkv <= 0 || d <= 0 || Hq % Hkv || Hq / Hkv > 8)
-        return bsattn_decode_window_workspace_size(Hq, Hkv, d);
-    return prefix_layout(B, P, Hq, Hkv, d, sms_of_device()).total;
+    if (B <= 0 || P <= 0 || Hq <= 0 || Hkv <= 0 || d <= 0 || Hq % Hkv || Hq / Hkv > 8) return 256;
+    return layout_of(B, P, Hq, Hkv, d, sms_of_device()).total;
 }
 
 extern "C" int bsattn_decode_shared(const void* q, const void* k_pages, const void* v_pages,
@@ -657,49 +663,70 @@ extern "C" int bsattn_decode_shared(const void* q, const void* k_pages, const vo
         return BSATTN_ERR_INVALID_ARG;
     if (Hq / Hkv > 8 || page_size % 64 || (d != 64 && d != 128)) return BSATTN_ERR_UNSUPPORTED;
     if (dtype != BSATTN_F16 && dtype != BSATTN_BF16) return BSATTN_ERR_UNSUPPORTED;
-    if (!workspace || !aligned16(workspace)) return BSATTN_ERR_INVALID_ARG;
     if (static_cast<long long>(num_pages) * page_size > 0x7fffffffLL - 128) return BSATTN_ERR_UNSUPPORTED;
+    if (static_cast<long long>(B) * Hq > 0x7fffffffLL || P > (1 << 24) || Hkv > 1024) return BSATTN_ERR_UNSUPPORTED;
+    if (!workspace || workspace_bytes < 256 || !aligned16(workspace)) return BSATTN_ERR_INVALID_ARG;
     if (B == 0) return BSATTN_OK;
     if (!q || !out || !k_pages || !v_pages || !prefix_lens || !prefix_table || !group_starts || !cache_seqlens ||
         !block_table)
         return BSATTN_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(out) || !aligned16(k_pages) || !aligned16(v_pages)) return BSATTN_ERR_INVALID_ARG;
-    // the prefix kernel has read all of q when the other writes out, as decode_stream() checks it
+    // out is written by the last kernel, which reads neither q nor the cache: it may be q itself
+    const size_t out_bytes = static_cast<size_t>(B) * Hq * d * 2;
+    const uint64_t rows = uint64_t(num_pages) * page_size, row_bytes = uint64_t(Hkv) * d * 2;
+    if ((out != q && overlap(out, out_bytes, q, out_bytes)) || overlap(out, out_bytes, k_pages, rows * row_bytes) ||
+        overlap(out, out_bytes, v_pages, rows * row_bytes))
+        return BSATTN_ERR_INVALID_ARG;
     const int sms = sms_of_device();
-    PrefixLayout w = prefix_layout(B, P, Hq, Hkv, d, sms);
+    const Layout w = layout_of(B, P, Hq, Hkv, d, sms);
     if (workspace_bytes < w.total) return BSATTN_ERR_INVALID_ARG;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    w.s.starts = group_starts;
-    w.s.lens = prefix_lens;
-    w.s.info = reinterpret_cast<long long*>(ws + w.info);
-    w.s.lse = reinterpret_cast<float*>(ws + w.lse);
-    w.s.o = reinterpret_cast<float*>(ws + w.o);
-    w.s.room = static_cast<int>(std::min(static_cast<long long>(max_pages_per_prefix) * page_size, 1LL << 30));
-    const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const StreamCall own{q, k_pages, v_pages, cache_seqlens, block_table, out, B, Hq, Hkv, num_pages, page_size,
-                         max_pages_per_seq, d, dtype, workspace, w.info};
-    int rc = decode_stream_shared(own, w.s, true, st);           // checks alone
-    if (rc) return rc;
     PrefixParams prm{};
-    prm.s = w.s;
-    prm.table = prefix_table;
-    prm.status = status_word(workspace);
-    prm.page_size = page_size;
-    prm.max_pages = max_pages_per_prefix;
-    prm.num_pages = num_pages;
-    prm.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(d)));
-    prm.budget_ns = wait_budget_ns();
+    SharedCall& s = prm.s;
+    s.q = q;
+    s.k = k_pages;
+    s.v = v_pages;
+    s.out = out;
+    s.starts = group_starts;
+    s.prefix_lens = prefix_lens;
+    s.own_lens = cache_seqlens;
+    s.prefix_table = prefix_table;
+    s.own_table = block_table;
+    s.prefix_info = reinterpret_cast<long long*>(ws + w.prefix_info);
+    s.own_info = reinterpret_cast<long long*>(ws + w.own_info);
+    s.prefix_lse = reinterpret_cast<float*>(ws + w.prefix_lse);
+    s.prefix_o = reinterpret_cast<float*>(ws + w.prefix_o);
+    s.own_lse = reinterpret_cast<float*>(ws + w.own_lse);
+    s.own_o = reinterpret_cast<float*>(ws + w.own_o);
+    s.status = status_word(workspace);
+    s.B = B;
+    s.P = P;
+    s.Hq = Hq;
+    s.Hkv = Hkv;
+    s.seqs = w.seqs;
+    s.part_rows = w.part_rows;
+    s.halves = w.halves;
+    s.own_parts = w.own_parts;
+    s.page_size = page_size;
+    s.num_pages = num_pages;
+    s.prefix_pages = max_pages_per_prefix;
+    s.own_pages = max_pages_per_seq;
+    s.prefix_room = static_cast<int>(std::min(static_cast<long long>(max_pages_per_prefix) * page_size, 1LL << 30));
+    s.own_room = static_cast<int>(std::min(static_cast<long long>(max_pages_per_seq) * page_size, 1LL << 30));
+    s.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(d)));
+    s.budget_ns = wait_budget_ns();
     const int G = Hq / Hkv, tile = 128 / G;
     prm.q_bytes = tile * G * d * 2;
     const bool bf16 = dtype == BSATTN_BF16;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
     CUtensorMap tq, tk, tv;
     const uint64_t dq[4] = {uint64_t(d), uint64_t(G), uint64_t(Hkv), uint64_t(B)};
     const uint64_t sq[3] = {d * 2ull, uint64_t(G) * d * 2, uint64_t(Hq) * d * 2};
     const uint32_t bq[4] = {64, uint32_t(G), 1, uint32_t(tile)};
-    const uint64_t rows = uint64_t(num_pages) * page_size, row_bytes = uint64_t(Hkv) * d * 2;
-    rc = encode_4d(&tq, q, bf16, dq, sq, bq);
+    int rc = encode_4d(&tq, q, bf16, dq, sq, bq);
     if (!rc) rc = encode_3d(&tk, k_pages, bf16, d, Hkv, rows, d * 2ull, row_bytes, 64, 1, 64, true);
     if (!rc) rc = encode_3d(&tv, v_pages, bf16, d, Hkv, rows, d * 2ull, row_bytes, 64, 1, 64, true);
+    if (!rc) rc = launch_own_tokens(s, d, bf16, st);
     if (rc) return rc;
     const auto run = [&](auto dim, auto halves) {
         constexpr int D = decltype(dim)::value;
@@ -708,7 +735,7 @@ extern "C" int bsattn_decode_shared(const void* q, const void* k_pages, const vo
     };
     using D64 = std::integral_constant<int, 64>;
     using D128 = std::integral_constant<int, 128>;
-    if (w.s.halves) rc = d == 64 ? run(D64{}, std::true_type{}) : run(D128{}, std::true_type{});
+    if (w.halves) rc = d == 64 ? run(D64{}, std::true_type{}) : run(D128{}, std::true_type{});
     else rc = d == 64 ? run(D64{}, std::false_type{}) : run(D128{}, std::false_type{});
-    return rc ? rc : decode_stream_shared(own, w.s, false, st);
+    return rc ? rc : launch_join(s, d, bf16, st);
 }

@@ -1,0 +1,517 @@
+// decode_shared_own.cu -- a decode over shared prefixes: the sequences' own tokens, and the joining of all
+// pieces, 16-bit paged cache, sm_103a.  (decode_shared.cu does the prefixes.)
+//
+// Each byte of a sequence's own K and V is used once, by the G <= 8 query heads of its kv head, so HBM bandwidth
+// bounds this; sequences have few own tokens or many.  Every warp is by itself: an equal part of all units of 32
+// keys, for one kv head, from one sequence to the next without a break (the next sequence's K, V and queries are
+// on their way before the one before is done), and what it has of a sequence goes to the workspace as a piece.
+// The products are those of decode_stream.cu, transposed, so that the G heads are the n = 8 side of mma.sync
+// m16n8k16: S^T [16 keys x 8] = K Q^T and O^T [d x 8] += V^T P^T.
+//
+// Joining is a warp a row: with (O, L) of each piece, out = sum O 2^(L - M) / sum 2^(L - M), in a fixed order.
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
+#include "decode_shared.cuh"
+#include "host_internal.h"
+#include "mma16.cuh"
+#include "ptx.cuh"
+
+namespace bsattn {
+namespace {
+
+using namespace mma16;
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kTok = 32, kTiles = kTok / 16;             // keys of a unit
+constexpr int kLeast = 2;                                // units of a part
+// exp2 is taken of x - max + 12: weights up to 4096, so that a weight 2^-24 of the largest is
+// still a normal fp16 number and 2^-36 the smallest one
+constexpr float kWeightLog2 = 12.f;
+
+template <int D>
+struct Ring {
+    static constexpr int kStages = 2 * (128 / D);        // K or V of a unit each
+    static constexpr uint32_t kStage = kTok * D * 2;
+    static constexpr uint32_t kRing = kStages * kStage;  // of one warp
+    static constexpr uint32_t kBars = kWarps * kRing;    // full[warp][stage]
+    static constexpr uint32_t kInfo = kBars + 8 * kWarps * kStages;       // (sequence, keys) of a stage
+    static constexpr uint32_t kBytes = 1024 + kInfo + 8 * kWarps * kStages;
+    static_assert(kStage % 1024 == 0, "swizzled tiles start on 1024 bytes");
+};
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads, 2)
+    own_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const SharedCall p) {
+    using R = Ring<D>;
+    using T = std::conditional_t<BF16, __nv_bfloat16, __half>;
+    constexpr int kStages = R::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ long long upto_of[kThreads];              // units up to the end of thread t's sequences
+    __shared__ long long warp_sums[kWarps];
+    __shared__ int aborted;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint8_t* ring = sm + warp * R::kRing;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + R::kBars) + warp * kStages;
+    volatile int2* info = reinterpret_cast<int2*>(sm + R::kInfo) + warp * kStages;
+    volatile int* abort_flag = &aborted;
+    const int G = p.Hq / p.Hkv;
+    const int g = blockIdx.x % p.Hkv, part = static_cast<int>(blockIdx.x / p.Hkv) * kWarps + warp;
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (lane == 0)
+        for (int s = 0; s < kStages; ++s) mbar_init(&full[s], 1);
+    if (tid == 0) aborted = 0;
+    fence_barrier_init();
+
+    // ------------------------------------------------------------ this warp's part of all units
+    const int per = (p.B + kThreads - 1) / kThreads;
+    long long upto = 0;
+    {
+        bool bad = false;
+        long long sum = 0;
+        for (int i = 0; i < per && tid * per + i < p.B; ++i) {
+            const int b = tid * per + i, len = p.own_lens[b];
+            bad = bad || len < 0 || len > p.own_room;
+            sum += own_units(own_len(p, b));
+        }
+        if (bad && blockIdx.x == 0) atomicOr(p.status, BSATTN_ERR_BAD_INDEX);
+        upto = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += u;
+        }
+        if (lane == 31) warp_sums[warp] = upto;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) upto += warp_sums[w];
+        upto_of[tid] = upto;
+        if (blockIdx.x == 0) {
+            long long before = upto - sum;
+            for (int i = 0; i < per && tid * per + i < p.B; ++i) {
+                const int b = tid * per + i;
+                p.own_info[1 + b] = before;
+                before += own_units(own_len(p, b));
+            }
+        }
+        __syncthreads();
+    }
+    const long long total = upto_of[kThreads - 1];
+    const long long chunk = max((total + p.own_parts - 1) / p.own_parts, static_cast<long long>(kLeast));
+    if (blockIdx.x == 0 && tid == 0) p.own_info[0] = chunk;
+    const long long x0 = part * chunk;
+    const int n = static_cast<int>(min(chunk, total - x0));     // units of this warp
+    if (x0 >= total) return;                                    // (no barrier of the CTA's comes after this)
+
+    // the next batch of units begins at unit `cu` of sequence `cb`
+    int cb, cu;
+    {
+        int t = 0;
+#pragma unroll
+        for (int step = kThreads / 2; step > 0; step >>= 1)
+            if (upto_of[t + step - 1] <= x0) t += step;
+        long long before = t > 0 ? upto_of[t - 1] : 0;
+        cb = t * per;
+        for (;; ++cb) {
+            const int u = own_units(own_len(p, cb));
+            if (x0 < before + u) break;
+            before += u;
+        }
+        cu = static_cast<int>(x0 - before);
+    }
+
+    // ---------------------------------------------------------------- feeding
+    // Lane i knows sequence, cache row and keys of the warp's unit base + i, for `count` of them.
+    int base = 0, count = 0;
+    int look_b = 0, look_row = -1, look_keys = 0;
+    bool bad = false;
+    const auto look_up = [&] {
+        base += count;
+        for (;;) {
+            // lane i: sequence cb + i; `ends`: units up to its end
+            const int len = cb + lane < p.B ? own_len(p, cb + lane) : 0;
+            int ends = own_units(len);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, ends, o);
+                if (lane >= o) ends += u;
+            }
+            const int have = __shfl_sync(0xffffffffu, ends, 31) - cu;
+            if (have <= 0) {
+                cb += 32;
+                cu = 0;
+                continue;
+            }
+            count = min(have, 32);
+            // the sequence that unit cu + lane is of, and (for the next batch) unit cu + count
+            const auto find = [&](int u) {
+                int s = 0;
+#pragma unroll
+                for (int half = 16; half > 0; half >>= 1)
+                    if (__shfl_sync(0xffffffffu, ends, s + half - 1) <= u) s += half;
+                if (__shfl_sync(0xffffffffu, ends, s) <= u) ++s;
+                return s;
+            };
+            const int s = find(cu + lane), next = find(cu + count);
+            const int before = __shfl_sync(0xffffffffu, ends, (s - 1) & 31), len_s = __shfl_sync(0xffffffffu, len, s & 31);
+            const int next_before = __shfl_sync(0xffffffffu, ends, (next - 1) & 31);
+            look_b = cb + s;
+            look_row = -1;
+            look_keys = 0;
+            if (lane < count) {
+                const int key = (cu + lane - (s > 0 ? before : 0)) * kTok, lp = key / p.page_size;
+                const int page = lp < p.own_pages ? p.own_table[static_cast<size_t>(look_b) * p.own_pages + lp] : -1;
+                if (page < 0 || page >= p.num_pages) {
+                    bad = true;
+                } else {
+                    look_row = page * p.page_size + key - lp * p.page_size;
+                    look_keys = min(len_s - key, kTok);
+                }
+            }
+            cu = cu + count - (next > 0 ? next_before : 0);
+            cb += next;
+            return;
+        }
+    };
+    int issued = 0;
+    // Half h is K of unit h / 2 if h is even, its V if it is odd.
+    const auto issue = [&](int h) {
+        ++issued;
+        const int k = h >> 1;
+        if (k >= base + count) look_up();
+        const int row = __shfl_sync(0xffffffffu, look_row, k - base);
+        const int keys = __shfl_sync(0xffffffffu, look_keys, k - base);
+        const int b = __shfl_sync(0xffffffffu, look_b, k - base);
+        const int st = h % kStages;
+        if (lane == 0) {
+            info[st].x = b;
+            info[st].y = keys;
+            if (row < 0) {
+                mbar_arrive(&full[st]);                             // nothing to load: the unit is skipped
+            } else {
+                mbar_arrive_expect_tx(&full[st], R::kStage);
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load_3d(ring + st * R::kStage + c * (kTok * 128), h & 1 ? &tm_v : &tm_k, &full[st], c * 64, g, row);
+            }
+        }
+        __syncwarp();
+    };
+    // the four channels of head lane / 4 that the lane's K registers hold in each k16 step
+    const auto queries = [&](int b, uint32_t (&to)[D / 16][2]) {
+        const T* qg = static_cast<const T*>(p.q) + (static_cast<size_t>(b) * p.Hq + g * G) * D;
+        const int hq = lane >> 2, j = lane & 3;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            const T* src = qg + hq * D + kk * 16 + 2 * j;
+            to[kk][0] = hq < G ? __ldg(reinterpret_cast<const uint32_t*>(src)) : 0u;
+            to[kk][1] = hq < G ? __ldg(reinterpret_cast<const uint32_t*>(src + 8)) : 0u;
+        }
+    };
+
+    const int r8 = lane >> 2, j4 = lane & 3;
+    for (int h = 0; h < kStages && h < 2 * n; ++h) issue(h);
+    uint32_t qb[D / 16][2], qn[D / 16][2];
+    float o[D / 16][4];
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;     // l of this lane's keys only
+    int cur = info[0].x;
+    queries(cur, qb);
+    const auto begin = [&] {
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
+        m0 = m1 = -INFINITY;
+        l0 = l1 = 0.f;
+    };
+    // The piece of sequence b to the workspace.
+    const auto end = [&](int b) {
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) {
+            l0 += __shfl_xor_sync(0xffffffffu, l0, w);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, w);
+        }
+        const size_t row = ((static_cast<size_t>(part) + b) * p.Hkv + g) * G + 2 * j4;
+        const float inv0 = l0 == 0.f ? 0.f : 1.f / l0, inv1 = l1 == 0.f ? 0.f : 1.f / l1;
+        if (r8 == 0) {
+            if (2 * j4 < G) p.own_lse[row] = l0 == 0.f ? -INFINITY : m0 + log2f(l0) - kWeightLog2;
+            if (2 * j4 + 1 < G) p.own_lse[row + 1] = l1 == 0.f ? -INFINITY : m1 + log2f(l1) - kWeightLog2;
+        }
+        float* to = p.own_o + row * D + r8;
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt) {
+            if (2 * j4 < G) {
+                to[16 * mt] = o[mt][0] * inv0;
+                to[16 * mt + 8] = o[mt][2] * inv0;
+            }
+            if (2 * j4 + 1 < G) {
+                to[D + 16 * mt] = o[mt][1] * inv1;
+                to[D + 16 * mt + 8] = o[mt][3] * inv1;
+            }
+        }
+    };
+    begin();
+    int done = 0, begun = 0;                                     // units
+    // Waits for half h; issues half h + kStages into its stage once it is read.
+    const auto arrived = [&](int h) {
+        const bool ok = warp_wait_within(&full[h % kStages], (h / kStages) & 1, p.budget_ns, abort_flag, p.status);
+        __syncwarp();
+        return ok;
+    };
+    const auto consumed = [&](int h) {
+        __syncwarp();
+        if (h + kStages < 2 * n) issue(h + kStages);
+    };
+    for (; done < n; ++done) {
+        const int hk = 2 * done;
+        if (!arrived(hk)) break;
+        const uint8_t* stage = ring + (hk % kStages) * R::kStage;
+        const int b = info[hk % kStages].x, keys = info[hk % kStages].y;
+        begun = done + 1;
+        if (b != cur) {
+            end(cur);
+            begin();
+            cur = b;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                qb[kk][0] = qn[kk][0];
+                qb[kk][1] = qn[kk][1];
+            }
+        }
+        // the queries of the sequence that begins with the next unit
+        const auto look_ahead = [&] {
+            if (done + 1 >= n) return;
+            const int next = info[(hk + 2) % kStages].x;
+            if (next != cur) queries(next, qn);
+        };
+        if (keys == 0) {                                            // no page
+            consumed(hk);
+            look_ahead();
+            if (!arrived(hk + 1)) break;
+            consumed(hk + 1);
+            continue;
+        }
+        float x[kTiles][4];
+        const uint32_t kbase = smem_u32(stage);
+        const int mat = lane >> 3;
+#pragma unroll
+        for (int mt = 0; mt < kTiles; ++mt) {
+            float sc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const int col = kk * 16 + (mat >> 1) * 8;
+                uint32_t a[4];
+                ldsm4(kbase + (col >> 6) * (kTok * 128) + sw128_offset(16 * mt + (mat & 1) * 8 + (lane & 7), col & 63), a);
+                mma16816<BF16>(sc, a, qb[kk][0], qb[kk][1]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                x[mt][e] = 16 * mt + r8 + 8 * (e >> 1) < keys ? sc[e] * p.scale_log2 : -INFINITY;
+        }
+        consumed(hk);
+        look_ahead();
+        float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+        for (int mt = 0; mt < kTiles; ++mt) {
+            t0 = fmaxf(t0, fmaxf(x[mt][0], x[mt][2]));
+            t1 = fmaxf(t1, fmaxf(x[mt][1], x[mt][3]));
+        }
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) {
+            t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, w));
+            t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, w));
+        }
+        if (__any_sync(0xffffffffu, t0 > m0 || t1 > m1)) {
+            const float n0 = fmaxf(m0, t0), n1 = fmaxf(m1, t1);
+            const float a0 = ex2_approx(m0 - (n0 == -INFINITY ? 0.f : n0));
+            const float a1 = ex2_approx(m1 - (n1 == -INFINITY ? 0.f : n1));
+            m0 = n0;
+            m1 = n1;
+            l0 *= a0;
+            l1 *= a1;
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt) {
+                o[mt][0] *= a0;
+                o[mt][1] *= a1;
+                o[mt][2] *= a0;
+                o[mt][3] *= a1;
+            }
+        }
+        const float z0 = m0 == -INFINITY ? 0.f : m0 - kWeightLog2;
+        const float z1 = m1 == -INFINITY ? 0.f : m1 - kWeightLog2;
+        uint32_t pb[kTiles][2];
+#pragma unroll
+        for (int mt = 0; mt < kTiles; ++mt) {
+            const float p0 = ex2_approx(x[mt][0] - z0), p1 = ex2_approx(x[mt][1] - z1);
+            const float p2 = ex2_approx(x[mt][2] - z0), p3 = ex2_approx(x[mt][3] - z1);
+            l0 += p0 + p2;
+            l1 += p1 + p3;
+            pb[mt][0] = transpose8x8(pack2<BF16>(p0, p1));
+            pb[mt][1] = transpose8x8(pack2<BF16>(p2, p3));
+        }
+        if (!arrived(hk + 1)) break;
+        uint8_t* vs = ring + ((hk + 1) % kStages) * R::kStage;
+        if (keys < kTok) {
+            // rows past the end may hold anything: a weight of 0 must not meet a NaN
+            for (int e = lane; e < (kTok - keys) * (D / 8); e += 32) {
+                const int r = keys + e / (D / 8), c = e % (D / 8);
+                *reinterpret_cast<uint4*>(vs + (c >> 3) * (kTok * 128) + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+        }
+        const uint32_t vbase = smem_u32(vs);
+#pragma unroll
+        for (int mt = 0; mt < kTiles; ++mt)
+#pragma unroll
+            for (int dt = 0; dt < D / 16; ++dt) {
+                const int col = dt * 16 + (mat & 1) * 8;
+                uint32_t a[4];
+                ldsm4_t(vbase + (col >> 6) * (kTok * 128) + sw128_offset(16 * mt + (mat >> 1) * 8 + (lane & 7), col & 63), a);
+                mma16816<BF16>(o[dt], a, pb[mt][0], pb[mt][1]);
+            }
+        consumed(hk + 1);
+    }
+    if (done < n) {
+        // After a wait that expired: copies in flight land, and every piece that lacks a unit is handed over as NaN.
+        const uint64_t dl = global_timer_ns() + 200000000ull;
+        for (int h = max(issued - kStages, 0); h < issued; ++h) wait_parity_drain(&full[h % kStages], (h / kStages) & 1, dl);
+        l0 = l1 = __int_as_float(0x7fffffff);
+        end(cur);
+        for (int k = begun; k < n; ++k) {
+            // units on their way are noted at their stages, the others come after them in the batch or in later ones
+            if (2 * k >= issued && k >= base + count) look_up();
+            const int b = 2 * k < issued ? info[2 * k % kStages].x : __shfl_sync(0xffffffffu, look_b, k - base);
+            if (b != cur) {
+                cur = b;
+                end(cur);
+            }
+        }
+    } else {
+        end(cur);
+    }
+    if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.status, BSATTN_ERR_BAD_INDEX);
+}
+
+// ------------------------------------------------------------------------------------------ joining
+
+constexpr int kBatch = 8;                // pieces joined in one trip to L2
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads) join_kernel(const SharedCall p) {
+    constexpr int kC = D / 32;                           // channels of a lane
+    using V = std::conditional_t<kC == 4, float4, float2>;
+    const int lane = threadIdx.x & 31;
+    const int row = static_cast<int>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const int b = row / p.Hq, h = row - b * p.Hq;
+    if (b >= p.B) return;
+    const int G = p.Hq / p.Hkv, kvh = h / G;
+    // the prefix whose sequences begin last before or at b
+    int prefix = 0;
+    for (int i = 1; i <= p.P; i += 32)
+        prefix += __reduce_add_sync(0xffffffffu, i + lane <= p.P && p.starts[i + lane] <= b ? 1 : 0);
+    PrefixGroup group{};
+    int i = -1;
+    if (prefix < p.P) {
+        group = prefix_group(p, prefix);
+        i = b - group.start;
+    }
+    const int mine = own_units(own_len(p, b));
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // pieces 0 .. shared - 1 are the prefix's, those up to `count` of the sequence's own tokens
+    int shared = 0, count = 0, other = 0;
+    long long first = 0, by = 0, own = 0;
+    if (i >= 0 && i < group.n && group.tiles > 0) {
+        const long long chunk = p.prefix_info[0], units = p.prefix_info[1 + prefix];
+        const int t = i / p.seqs, each = p.halves ? 2 : 1;
+        const long long place = prefix_rows_before(p, group, t, kvh, other);
+        const long long from = units + (static_cast<long long>(t) * p.Hkv + kvh) * group.tiles, c0 = from / chunk;
+        shared = static_cast<int>((from + group.tiles - 1) / chunk - c0 + 1) * each;
+        by = static_cast<long long>(p.part_rows) * each;
+        first = c0 * by + place * each + (i - t * p.seqs) * G + (h - kvh * G);
+    }
+    count = shared;
+    if (mine > 0) {
+        const long long chunk = p.own_info[0], from = p.own_info[1 + b], c0 = from / chunk;
+        count += static_cast<int>((from + mine - 1) / chunk - c0 + 1);
+        own = ((c0 + b) * p.Hkv + kvh) * G + (h - kvh * G);
+    }
+    float num[kC] = {};
+    float M = -INFINITY, den = 0.f;
+    for (int k0 = 0; k0 < count; k0 += kBatch) {
+        float lv[kBatch];
+        V ov[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int n = k0 + k;
+            lv[k] = -INFINITY;
+            ov[k] = V{};
+            if (n < count) {
+                const bool pre = n < shared;
+                const long long at = !pre ? own + static_cast<long long>(n - shared) * p.Hq
+                                     : p.halves ? first + (n >> 1) * by + (n & 1) * other : first + n * by;
+                lv[k] = __ldcg((pre ? p.prefix_lse : p.own_lse) + at);
+                ov[k] = __ldcg(reinterpret_cast<const V*>((pre ? p.prefix_o : p.own_o) + at * D) + lane);
+            }
+        }
+        float top = M;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) top = fmaxf(top, lv[k]);
+        const float ref = top == -INFINITY ? 0.f : top, down = ex2_approx(M - ref);
+        M = top;
+        den *= down;
+#pragma unroll
+        for (int e = 0; e < kC; ++e) num[e] *= down;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            // where a row has met no finite score O may not have been written
+            if (lv[k] == -INFINITY) continue;
+            const float w = ex2_approx(lv[k] - ref);
+            const float* v = reinterpret_cast<const float*>(&ov[k]);
+#pragma unroll
+            for (int e = 0; e < kC; ++e) num[e] = fmaf(w, v[e], num[e]);
+            den += w;
+        }
+    }
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    uint32_t w[kC / 2];
+#pragma unroll
+    for (int e = 0; e < kC / 2; ++e) w[e] = pack2<BF16>(num[2 * e] * inv, num[2 * e + 1] * inv);
+    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + static_cast<size_t>(row) * D + kC * lane);
+    if constexpr (kC == 4) *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+    else out[0] = w[0];
+}
+
+template <int D, bool BF16>
+int launch_own(const SharedCall& p, cudaStream_t st) {
+    CUtensorMap tk, tv;
+    const uint64_t rows = uint64_t(p.num_pages) * p.page_size, row_bytes = uint64_t(p.Hkv) * D * 2;
+    int rc = encode_3d(&tk, p.k, BF16, D, p.Hkv, rows, D * 2ull, row_bytes, 64, 1, kTok, true);
+    if (!rc) rc = encode_3d(&tv, p.v, BF16, D, p.Hkv, rows, D * 2ull, row_bytes, 64, 1, kTok, true);
+    if (rc) return rc;
+    auto kern = own_kernel<D, BF16>;
+    static std::atomic<unsigned long long> raised{0};
+    rc = raise_smem_limit(reinterpret_cast<const void*>(kern), Ring<D>::kBytes, raised);
+    if (rc) return rc;
+    kern<<<static_cast<unsigned>(p.own_parts / kWarps) * p.Hkv, kThreads, Ring<D>::kBytes, st>>>(tk, tv, p);
+    return cudaGetLastError() == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_own_tokens(const SharedCall& p, int d, bool bf16, cudaStream_t st) {
+    if (d == 64) return bf16 ? launch_own<64, true>(p, st) : launch_own<64, false>(p, st);
+    return bf16 ? launch_own<128, true>(p, st) : launch_own<128, false>(p, st);
+}
+
+int launch_join(const SharedCall& p, int d, bool bf16, cudaStream_t st) {
+    const unsigned grid = static_cast<unsigned>((static_cast<long long>(p.B) * p.Hq + kWarps - 1) / kWarps);
+    if (d == 64)
+        return bf16 ? launch_after(join_kernel<64, true>, grid, kThreads, 0, st, p)
+                    : launch_after(join_kernel<64, false>, grid, kThreads, 0, st, p);
+    return bf16 ? launch_after(join_kernel<128, true>, grid, kThreads, 0, st, p)
+                : launch_after(join_kernel<128, false>, grid, kThreads, 0, st, p);
+}
+
+}  // namespace bsattn

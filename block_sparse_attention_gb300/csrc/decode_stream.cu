@@ -46,11 +46,13 @@
 
 #include "host_internal.h"
 #include "kv4.cuh"
+#include "mma16.cuh"
 #include "ptx.cuh"
-#include "shared_prefix.cuh"
 
 namespace bsattn {
 namespace {
+
+using namespace mma16;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
@@ -83,11 +85,6 @@ struct StreamParams {
     float score_log2;               // log2(e) / sqrt(d), and the keys' unit
     float v_unit;
     unsigned long long budget_ns;
-};
-
-// A call over shared prefixes: the results over those too.
-struct SharedStreamParams : StreamParams {
-    PrefixPieces pre;
 };
 
 // Shared memory of one CTA: rings first (1024-byte aligned for the swizzle), then barriers.  The
@@ -125,68 +122,13 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                  : "memory");
 }
 
-template <bool BF16>
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    if constexpr (BF16) {
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-            "{%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    } else {
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-            "{%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    }
-}
-
-__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
-}
-
-__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
-}
-
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
-    uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
-}
-
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    if constexpr (BF16) {
-        __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<uint32_t*>(&v);
-    } else {
-        __half2 v = __floats2half2_rn(a, b);
-        return *reinterpret_cast<uint32_t*>(&v);
-    }
-}
-
-template <bool BF16>
-__device__ __forceinline__ float2 unpack2(uint32_t w) {
-    if constexpr (BF16) {
-        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-    } else {
-        return __half22float2(*reinterpret_cast<__half2*>(&w));
-    }
-}
-
 // The visible units of one sequence: `near` units from unit `from`, after `head` sink units.
 struct Span {
     int len;          // tokens
     int head, from, n;
 };
 
-template <int TOK, bool SHARED>
+template <int TOK>
 __device__ __forceinline__ Span span_of(const StreamParams& p, int b) {
     Span s;
     int len = p.seqlens[b];
@@ -207,51 +149,13 @@ __device__ __forceinline__ Span span_of(const StreamParams& p, int b) {
         s.from = first - s.head;                    // unit of the i-th visible one past the sinks: i + from
     }
     s.n = all - s.from;
-    // a sequence without a token of its own still has its prefix: one unit, of nothing
-    if (SHARED && s.n == 0) s.n = 1;
     return s;
 }
 
-// The results over sequence b's prefix for kv head g's query heads: `count` pieces.
-struct PrefixRows {
-    int count;
-    long long first, by;            // place of the first piece's first row, and from a piece to the next
-    int other;                      // where a piece has two halves: from the one to the other
-};
-
-// By a whole warp.
-__device__ __forceinline__ PrefixRows prefix_rows(const PrefixPieces& s, int b, int g) {
-    PrefixRows r;
-    r.count = 0;
-    r.first = r.by = 0;
-    r.other = 0;
-    // the prefix whose sequences begin last before or at b
-    int p = 0;
-    for (int i = 1 + (threadIdx.x & 31); i - static_cast<int>(threadIdx.x & 31) <= s.P; i += 32)
-        p += __reduce_add_sync(0xffffffffu, i <= s.P && s.starts[i] <= b);
-    if (p >= s.P) return r;
-    const PrefixGroup group = prefix_group(s, p);
-    const int i = b - group.start;
-    if (i < 0 || i >= group.n || group.tiles == 0) return r;
-    const long long chunk = s.info[0];
-    const int t = i / s.seqs;
-    int rows;
-    const long long place = prefix_rows_before(s, group, t, g, rows);
-    const long long unit = s.info[1 + p] + (static_cast<long long>(t) * s.Hkv + g) * group.tiles;
-    const long long c0 = unit / chunk, c1 = (unit + group.tiles - 1) / chunk;
-    const int each = s.halves ? 2 : 1;
-    r.count = static_cast<int>(c1 - c0 + 1) * each;
-    r.by = static_cast<long long>(s.part_rows) * each;
-    r.first = c0 * r.by + place * each + (i - t * s.seqs) * (s.Hq / s.Hkv);
-    r.other = rows;
-    return r;
-}
-
-// SHARED: out is joined with the results over the sequences' prefixes (decode_shared.cu).
-template <int D, bool BF16, bool KV4, bool SHARED>
+template <int D, bool BF16, bool KV4>
 __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
     stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                  const std::conditional_t<SHARED, SharedStreamParams, StreamParams> p) {
+                  const StreamParams p) {
     using R = Ring<D, KV4>;
     using T = std::conditional_t<BF16, __nv_bfloat16, __half>;
     // At 4 bits both products run in fp16 (the cache's values are exact there, bf16 queries are scaled)
@@ -285,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
     for (int k = 0; k < per; ++k) {
         const int b = tid * per + k;
         if (b >= p.B) break;
-        const Span s = span_of<kTok, SHARED>(p, b);
+        const Span s = span_of<kTok>(p, b);
         sum += s.n;
         if (g == 0 && part == b % p.parts) {
             const int len = p.seqlens[b];
@@ -361,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
             int b = tid * per;
             long long before = upto - sum;
             for (;; ++b) {
-                const int n = span_of<kTok, SHARED>(p, b).n;
+                const int n = span_of<kTok>(p, b).n;
                 if (x0 < before + n) break;
                 before += n;
             }
@@ -384,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
     // no row comes out that lacks a piece and does not show it.
     bool lost = false;
     for (long long x = x0; x < x1;) {
-        const Span s = span_of<kTok, SHARED>(p, b);
+        const Span s = span_of<kTok>(p, b);
         if (s.n == 0) {
             ++b;
             continue;
@@ -417,7 +321,6 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
                 if (key >= s.len) return;                           // second half past the end
             } else {
                 key = (i < s.head ? i : i + s.from) * kTok;
-                if (SHARED && key >= s.len) return;                 // the unit of nothing
             }
             look_key = key;
             if (p.table) {
@@ -772,58 +675,6 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
         }
         __syncthreads();
         const bool whole = i0 == 0 && i1 == s.n;
-        // A row's value and log-sum-exp joined with those over its prefix, kBatch pieces at a time.
-        PrefixRows prefix{};
-        if constexpr (SHARED) {
-            if (whole) {
-                asm volatile("griddepcontrol.wait;" ::: "memory");
-                prefix = prefix_rows(p.pre, b, g);
-            }
-        }
-        const auto with_prefix = [&](float4 val, float lse, int row, int c4) {
-            if constexpr (SHARED) {
-                // (this kernel's weights, and so its sums, are scaled by 2^kWeightLog2)
-                float M = lse - kWeightLog2, den = lse == -INFINITY ? 0.f : 1.f;
-                float4 num = val;
-                for (int k0 = 0; k0 < prefix.count; k0 += kBatch) {
-                    float lv[kBatch];
-                    float4 ov[kBatch];
-#pragma unroll
-                    for (int k = 0; k < kBatch; ++k) {
-                        const int i = k0 + k;
-                        const bool in = i < prefix.count;
-                        const long long at = prefix.first + row + (p.pre.halves ? (i >> 1) * prefix.by + (i & 1) * prefix.other
-                                                                                 : i * prefix.by);
-                        lv[k] = in ? __ldcg(p.pre.lse + at) : -INFINITY;
-                        ov[k] = in ? __ldcg(reinterpret_cast<const float4*>(p.pre.o + at * D) + c4)
-                                   : make_float4(0.f, 0.f, 0.f, 0.f);
-                    }
-                    float top = M;
-#pragma unroll
-                    for (int k = 0; k < kBatch; ++k) top = fmaxf(top, lv[k]);
-                    const float ref = top == -INFINITY ? 0.f : top;
-                    const float r = ex2_approx(M - ref);
-                    num = make_float4(num.x * r, num.y * r, num.z * r, num.w * r);
-                    den *= r;
-#pragma unroll
-                    for (int k = 0; k < kBatch; ++k) {
-                        // where a piece has no key nothing has been written but that
-                        if (lv[k] == -INFINITY) continue;
-                        const float wt = ex2_approx(lv[k] - ref);
-                        num.x += wt * ov[k].x;
-                        num.y += wt * ov[k].y;
-                        num.z += wt * ov[k].z;
-                        num.w += wt * ov[k].w;
-                        den += wt;
-                    }
-                    M = top;
-                }
-                const float inv = den == 0.f ? 0.f : 1.f / den;
-                return make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
-            } else {
-                return val;
-            }
-        };
         const size_t slot = (static_cast<size_t>(part) * 2 + (i0 == 0 ? 1 : 0)) * p.Hkv + g;
         const size_t row_base = static_cast<size_t>(b) * p.Hq + g * G;
         const float* join = reinterpret_cast<const float*>(sm);
@@ -859,9 +710,8 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
             }
             // den is 0 only for a row with no visible token (NaN stays NaN)
             const float inv = den == 0.f ? 0.f : 1.f / den;
-            float4 val = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+            const float4 val = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
             if (whole) {
-                if constexpr (SHARED) val = with_prefix(val, den == 0.f ? -INFINITY : M + log2f(den), row, c4);
                 const float u = p.v_unit;
                 uint2 w2;
                 w2.x = pack2<BF16>(val.x * u, val.y * u);
@@ -889,10 +739,6 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
             }
             __syncthreads();
             if (misc[1]) {
-                if constexpr (SHARED) {
-                    asm volatile("griddepcontrol.wait;" ::: "memory");
-                    prefix = prefix_rows(p.pre, b, g);
-                }
                 // read through L2 (an SM's L1 may hold an earlier call's lines), kBatch pieces at a time
                 for (int e = tid; e < G * (D / 4); e += kThreads) {
                     const int row = e / (D / 4), c4 = e % (D / 4);
@@ -932,15 +778,9 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KV4>::kCtas)
                         M = Mc;
                     }
                     const float inv = (den == 0.f ? 0.f : 1.f / den) * p.v_unit;
-                    if constexpr (SHARED) {
-                        num = with_prefix(make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv),
-                                          den == 0.f ? -INFINITY : M + log2f(den), row, c4);
-                    } else {
-                        num = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
-                    }
                     uint2 w2;
-                    w2.x = pack2<BF16>(num.x, num.y);
-                    w2.y = pack2<BF16>(num.z, num.w);
+                    w2.x = pack2<BF16>(num.x * inv, num.y * inv);
+                    w2.y = pack2<BF16>(num.z * inv, num.w * inv);
                     *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + (row_base + row) * D + 4 * c4) = w2;
                 }
                 if (tid == 0) p.tickets[c_first * p.Hkv + g] = 0;         // ready for the next call
@@ -980,33 +820,9 @@ WsLayout ws_layout(int Hq, int Hkv, int d, int parts) {
 }
 
 template <int D, bool BF16, bool KV4>
-int launch(const CUtensorMap& tk, const CUtensorMap& tv, const StreamParams& prm, const PrefixPieces* pre,
-           cudaStream_t stream) {
+int launch(const CUtensorMap& tk, const CUtensorMap& tv, const StreamParams& prm, cudaStream_t stream) {
     using R = Ring<D, KV4>;
-    if constexpr (!KV4) {
-        if (pre) {
-            auto kern = stream_kernel<D, BF16, false, true>;
-            static std::atomic<unsigned long long> raised_shared{0};
-            const int rc = raise_smem_limit(reinterpret_cast<const void*>(kern), R::kBytes, raised_shared);
-            if (rc) return rc;
-            SharedStreamParams both;
-            static_cast<StreamParams&>(both) = prm;
-            both.pre = *pre;
-            // its CTAs start where the kernel over the prefixes leaves room, and wait for it when they join
-            cudaLaunchConfig_t cfg{};
-            cfg.gridDim = dim3(static_cast<unsigned>(prm.parts) * prm.Hkv);
-            cfg.blockDim = dim3(kThreads);
-            cfg.dynamicSmemBytes = R::kBytes;
-            cfg.stream = stream;
-            cudaLaunchAttribute at{};
-            at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-            at.val.programmaticStreamSerializationAllowed = 1;
-            cfg.attrs = &at;
-            cfg.numAttrs = 1;
-            return cudaLaunchKernelEx(&cfg, kern, tk, tv, both) == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
-        }
-    }
-    auto kern = stream_kernel<D, BF16, KV4, false>;
+    auto kern = stream_kernel<D, BF16, KV4>;
     static std::atomic<unsigned long long> raised{0};
     const int rc = raise_smem_limit(reinterpret_cast<const void*>(kern), R::kBytes, raised);
     if (rc) return rc;
@@ -1014,11 +830,9 @@ int launch(const CUtensorMap& tk, const CUtensorMap& tv, const StreamParams& prm
     return cudaGetLastError() == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
 }
 
-// Checks, workspace and launch shared by the entry points.  `k16` / `v16`: 16-bit caches, or null; `pre`: where
-// the results over shared prefixes are, or null; `check`: the checks alone.
+// Checks, workspace and launch shared by the entry points.  `k16` / `v16`: 16-bit caches, or null.
 int decode_stream(StreamParams prm, const void* k16, const void* v16, int d, bsattn_dtype dtype,
-                  void* workspace, size_t workspace_bytes, cudaStream_t st, const PrefixPieces* pre = nullptr,
-                  bool check = false) {
+                  void* workspace, size_t workspace_bytes, cudaStream_t st) {
     const bool kv4 = prm.kc != nullptr;
     if (prm.B < 0 || prm.Hq <= 0 || prm.Hkv <= 0 || prm.window < 0 || prm.sinks < 0 || prm.max_sel < 0)
         return BSATTN_ERR_INVALID_ARG;
@@ -1049,7 +863,6 @@ int decode_stream(StreamParams prm, const void* k16, const void* v16, int d, bsa
     if (static_cast<long long>(parts) * prm.Hkv > kMaxTickets) return BSATTN_ERR_UNSUPPORTED;
     const WsLayout w = ws_layout(prm.Hq, prm.Hkv, d, parts);
     if (workspace_bytes < w.total || !aligned16(workspace)) return BSATTN_ERR_INVALID_ARG;
-    if (check) return BSATTN_OK;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     prm.parts = parts;
     prm.status = status_word(ws);
@@ -1065,11 +878,11 @@ int decode_stream(StreamParams prm, const void* k16, const void* v16, int d, bsa
         int rc = encode_3d(&tk, k16, bf16, d, prm.Hkv, rows, d * 2ull, row_bytes, 64, 1, Ring<128, false>::kTok, true);
         rc |= encode_3d(&tv, v16, bf16, d, prm.Hkv, rows, d * 2ull, row_bytes, 64, 1, Ring<128, false>::kTok, true);
         if (rc) return rc;
-        if (d == 64) return bf16 ? launch<64, true, false>(tk, tv, prm, pre, st) : launch<64, false, false>(tk, tv, prm, pre, st);
-        return bf16 ? launch<128, true, false>(tk, tv, prm, pre, st) : launch<128, false, false>(tk, tv, prm, pre, st);
+        if (d == 64) return bf16 ? launch<64, true, false>(tk, tv, prm, st) : launch<64, false, false>(tk, tv, prm, st);
+        return bf16 ? launch<128, true, false>(tk, tv, prm, st) : launch<128, false, false>(tk, tv, prm, st);
     }
-    if (d == 64) return bf16 ? launch<64, true, true>(tk, tv, prm, pre, st) : launch<64, false, true>(tk, tv, prm, pre, st);
-    return bf16 ? launch<128, true, true>(tk, tv, prm, pre, st) : launch<128, false, true>(tk, tv, prm, pre, st);
+    if (d == 64) return bf16 ? launch<64, true, true>(tk, tv, prm, st) : launch<64, false, true>(tk, tv, prm, st);
+    return bf16 ? launch<128, true, true>(tk, tv, prm, st) : launch<128, false, true>(tk, tv, prm, st);
 }
 
 int page_check(int num_pages, int page_size, int max_pages) {
@@ -1079,24 +892,6 @@ int page_check(int num_pages, int page_size, int max_pages) {
 }
 
 }  // namespace
-
-int decode_stream_shared(const StreamCall& c, const PrefixPieces& pieces, bool check, cudaStream_t stream) {
-    StreamParams prm{};
-    prm.q = c.q;
-    prm.seqlens = c.seqlens;
-    prm.table = c.table;
-    prm.out = c.out;
-    prm.B = c.B;
-    prm.Hq = c.Hq;
-    prm.Hkv = c.Hkv;
-    prm.num_pages = c.num_pages;
-    prm.page_size = c.page_size;
-    prm.max_pages = c.max_pages;
-    prm.score_log2 = 1.f;
-    prm.v_unit = 1.f;
-    return decode_stream(prm, c.k, c.v, c.d, c.dtype, c.workspace, c.workspace_bytes, stream, &pieces, check);
-}
-
 }  // namespace bsattn
 
 extern "C" size_t bsattn_decode_window_workspace_size(int Hq, int Hkv, int d) {

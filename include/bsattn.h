@@ -469,9 +469,9 @@ int bsattn_mask_from_qk(const void* q, const void* k, int topk, int sinks, int r
 size_t bsattn_mask_from_qk_workspace_size(int B, int Hq, int Hkv, int Sq, int Sk, int d);
 
 /*
- * One query token per sequence over a prefix that sequences share and the sequence's own tokens after it, a
- * stream decode over a 16-bit paged cache: out = softmax(q . k / sqrt(d)) v over both.  The prefix is read
- * once for all the sequences that share it (for 256 query rows of a kv head at a time), not once for each.
+ * One query token per sequence over a prefix that sequences share and the sequence's own tokens after it, from a
+ * 16-bit paged cache: out = softmax(q . k / sqrt(d)) v over both.  The prefix is read once for all the
+ * sequences that share it (for 256 query rows of a kv head at a time), not once for each.
  *
  *   q, out         (device) [B, Hq, d] dtype;  k_pages, v_pages (device) [num_pages, page_size, Hkv, d] dtype
  *   prefix_lens    (device) [P] int32: tokens of prefix p, any number
@@ -484,11 +484,11 @@ size_t bsattn_mask_from_qk_workspace_size(int B, int Hq, int Hkv, int Sq, int Sk
  * is taken as 0; these and group_starts that do not rise from 0 to B are flagged BSATTN_ERR_BAD_INDEX (the
  * rows of groups that overlap or run backwards are then undefined; a sequence outside all groups has no prefix).
  * Rows past a length may hold anything.  P is rounded to dtype before the second product.  A wait that expires
- * makes every row NaN that lacks some of its tokens, and leaves the workspace ready for the next call.
- * P >= 1, Hq / Hkv <= 8, Hkv <= 1024, d in {64, 128}, page_size a multiple of 64, a prefix of at most 2^30
- * tokens.  out may be q itself; otherwise it shares no memory with q or the cache.  Workspace:
- * bsattn_decode_shared_workspace_size bytes, its first 4352 zero before the first use; one zeroed once serves every
- * shape that fits it.
+ * makes every row NaN that lacks some of its tokens.  The result does not depend on the order in which CTAs run.
+ * P >= 1, Hq / Hkv <= 8, Hkv <= 1024, d in {64, 128}, page_size a multiple of 64, at most 2^30 tokens a prefix or
+ * sequence.  out may be q itself; otherwise it shares no memory with q or the cache.  Workspace:
+ * bsattn_decode_shared_workspace_size bytes, 16-byte aligned; its first 256 bytes are the status word's, the rest
+ * need not be zero and serves any shape that fits.  Calls that can overlap on the GPU need one each.
  */
 int bsattn_decode_shared(const void* q, const void* k_pages, const void* v_pages, const int32_t* prefix_lens,
                          const int32_t* prefix_table, const int32_t* group_starts, const int32_t* cache_seqlens,

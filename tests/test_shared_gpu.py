@@ -117,14 +117,34 @@ def test_nothing_to_see(bsa):
 
 
 def test_agrees_with_the_window_decode(bsa):
-    """No prefix: each sequence's own tokens, to the last bit; a prefix of whole pages in front of them: as if
-    each sequence had it for itself."""
+    """No prefix: each sequence's own tokens; a prefix of whole pages in front of them: as if each sequence had it
+    for itself.  Both within the bound of the one statement."""
     c = Case([9, 11], [0, 0], [(77 * b) % 3000 for b in range(20)], 8, 2, 128, BF16, seed=3)
-    assert torch.equal(c.call(bsa), bsa.bsattn_decode_window_paged(c.q, c.k, c.v, c.lens, c.table, 1 << 20))
+    c.check(bsa)
+    serving.check(bsa.bsattn_decode_window_paged(c.q, c.k, c.v, c.lens, c.table, 1 << 20), *c.want())
     c = Case([5], [640], [100, 1, 64, 0, 300], 8, 2, 128, BF16, seed=4)
     joined = torch.cat((c.ptable.expand(5, -1), c.table), 1).contiguous()
-    got, alone = c.check(bsa), bsa.bsattn_decode_window_paged(c.q, c.k, c.v, c.lens + 640, joined, 1 << 20)
-    assert (got.double() - alone.double()).abs().max() < 2e-2
+    c.check(bsa)
+    serving.check(bsa.bsattn_decode_window_paged(c.q, c.k, c.v, c.lens + 640, joined, 1 << 20), *c.want())
+
+
+@pytest.mark.parametrize("d,dtype", [(64, F16), (128, BF16)])
+@pytest.mark.parametrize("sizes", [[1], [30], [70], [129]])
+def test_own_tokens_of_any_lengths(bsa, sizes, d, dtype):
+    """Ragged own lengths, none among them, one sequence far longer than the others, with prefixes of few tokens and
+    of many: every mix of steps."""
+    B = sum(sizes)
+    for plen, longest in ((0, 700), (64, 5000), (900, 64), (3001, 3003)):
+        lens = [(longest * (b * b + 3) // 7) % 200 * (b % 4 != 1) for b in range(B)]
+        lens[B // 2] = longest
+        Case(sizes, [plen], lens, 8, 2, d, dtype, page=128, seed=plen + B).check(bsa)
+
+
+def test_more_row_tiles_than_a_part_keeps(bsa):
+    """One long prefix and hundreds of groups of one or two sequences: parts that go through many row tiles."""
+    sizes = [3] + [1 + p % 2 for p in range(500)]
+    B = sum(sizes)
+    Case(sizes, [30_000] + [p % 2 for p in range(500)], [5 * (b % 2) for b in range(B)], 2, 1, 64, BF16, seed=6).check(bsa)
 
 
 @pytest.mark.parametrize("d,dtype", [(64, F16), (128, BF16)])
@@ -146,11 +166,37 @@ def test_nan_reaches_those_that_see_it(bsa):
     want = torch.zeros_like(lost)
     want[:3, 4:] = True
     assert torch.equal(lost, want) and torch.equal(got[~lost], clean[~lost])
-    c = Case([3, 40], [400, 500], [50] * 43, 8, 2, 64, F16, seed=6)
-    c.v[c.table[20, 0], 3, 0, 9] = float("inf")                # one channel of one sequence's head 0
+    # in one channel of one sequence's head 0: its rows alone, whoever is worked on with it
+    for at in (2, 20):
+        for bad in (float("inf"), float("nan"), -float("inf")):
+            c = Case([3, 40], [400, 500], [50] * 43, 8, 2, 64, F16, seed=6)
+            clean = c.call(bsa)
+            c.v[c.table[at, 0], 3, 0, 9] = bad
+            got = c.call(bsa)
+            off = ~torch.isfinite(got)
+            assert off[at, :4, 9].all() and off.sum() == 4 and torch.equal(got[~off], clean[~off])
+    # in the prefix: all rows of the group's head
+    c = Case([3, 40], [400, 500], [50] * 43, 8, 2, 128, BF16, seed=7)
+    out, bound = c.want()
+    c.v[c.ptable[1, 1], 3, 1, 100] = float("inf")
     got = c.call(bsa)
-    bad = ~torch.isfinite(got)
-    assert bad[20, :4, 9].all() and bad.sum() == 4 and torch.equal(got[~bad], clean[~bad])
+    assert not torch.isfinite(got[3:, 4:, 100]).any()
+    rest = torch.ones_like(got, dtype=torch.bool)
+    rest[3:, 4:] = False
+    serving.check(got[rest], out[rest], bound[rest])
+
+
+def test_nan_beside_bad_pages(bsa):
+    c = Case([40], [500], [150] * 40, 8, 2, 128, BF16, page=64, seed=8)
+    c.ptable[0, 2] = -1
+    c.table[7, 1] = c.k.shape[0]
+    c.table[9, 0] = 2 ** 31 - 1
+    out, bound = c.want()
+    c.v[c.table[20, 0], 3] = float("nan")
+    got = c.call(bsa)
+    rest = torch.arange(40, device="cuda") != 20
+    serving.check(got[rest], out[rest], bound[rest])
+    assert got[20].isnan().all()
 
 
 @pytest.mark.parametrize("B", [5, 70])
@@ -184,8 +230,10 @@ def test_bad_groups(bsa):
     """Groups that do not rise from 0 to B are reported; sequences outside all of them have no prefix."""
     c = Case([2, 3], [300, 200], [40] * 5, 8, 2, 64, BF16, seed=8)
     ws = torch.zeros(bsa.bsattn_decode_shared_workspace_size(5, 2, 8, 2, 64), dtype=torch.uint8, device="cuda")
-    own = bsa.bsattn_decode_window_paged(c.q, c.k, c.v, c.lens, c.table, 1 << 20)
-    whole = c.call(bsa, ws=ws)
+    whole, plens = c.call(bsa, ws=ws), c.plens
+    c.plens = torch.zeros_like(plens)
+    own = c.check(bsa, ws=ws)
+    c.plens = plens
     assert bsa.bsattn_get_device_status(ws) == 0
     for starts, outside in (([1, 2, 5], [0]), ([0, 2, 4], [4]), ([0, 2, 2], [2, 3, 4]), ([5, 5, 5], range(5))):
         c.starts = _i32(starts)
@@ -216,7 +264,6 @@ def test_expired_waits(bsa, B, plen, lens):
                 status = bsa.bsattn_get_device_status(ws)
                 seen |= status
                 assert status in (0, bsa.BSATTN_ERR_TIMEOUT)
-                assert not ws[256:4352].any()
                 lost = got.isnan().all(-1)
                 assert torch.equal(got[~lost], want[~lost])
                 assert status or not lost.any()
@@ -232,7 +279,7 @@ def test_one_workspace_for_all_shapes(bsa):
     ws = torch.zeros(bsa.bsattn_decode_shared_workspace_size(300, 9, 32, 8, 128), dtype=torch.uint8, device="cuda")
     for seed, (B, plen, d) in enumerate([(70, 900, 128), (3, 2000, 64), (130, 64, 64), (5, 1, 128), (64, 5000, 128)]):
         Case([B], [plen], [9 * b % 130 for b in range(B)], 16, 4, d, BF16, seed=seed).check(bsa, ws=ws)
-    ws[4352:] = 0xff
+    ws[256:] = 0xff
     Case([6, 80], [100, 900], [3] * 86, 16, 4, 64, F16, seed=9).check(bsa, ws=ws)
 
 
