@@ -40,6 +40,7 @@ constexpr int kRegsSoftmax = 208, kRegsOther = 88;       // registers a thread: 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 256;
 constexpr float kRescaleLog2 = 8.0f;
+constexpr long long kShortBytes = 12 << 20;              // K and V of all prefixes that their tables have room for
 // Notes of key tiles, in turn: the loader is never this many tiles ahead of the last warp of a softmax.
 constexpr int kNotes = 16;
 
@@ -69,13 +70,13 @@ struct Walk {
 };
 
 struct Piece {
-    int p, b0, n;                        // prefix, first of its sequences, how many
-    int kvh, k0, k1, len;                // kv head, key tiles [k0, k1), keys of the prefix
+    int p, b0, kvh;                      // prefix, first of the item's sequences, kv head
+    int k0, k1, len;                     // key tiles [k0, k1), keys of the prefix
     int rows;                            // of the item
-    long long place;                     // rows of all items before it
+    long long place;                     // of the first one
 };
 
-__device__ __forceinline__ bool next_piece(const PrefixParams& prm, Walk& w, Piece& x) {
+__device__ __forceinline__ bool next_piece(const PrefixParams& prm, int part, int beside, Walk& w, Piece& x) {
     if (w.at >= w.end) return false;
     PrefixGroup g = prefix_group(prm.s, w.p);
     for (;;) {
@@ -89,12 +90,11 @@ __device__ __forceinline__ bool next_piece(const PrefixParams& prm, Walk& w, Pie
     x.p = w.p;
     x.k0 = static_cast<int>(local - item * g.tiles);
     x.k1 = static_cast<int>(min(static_cast<long long>(g.tiles), x.k0 + (w.end - w.at)));
-    const int t = static_cast<int>(item / prm.s.Hkv);
-    x.kvh = static_cast<int>(item - static_cast<long long>(t) * prm.s.Hkv);
+    const int along = prm.s.Hkv / prm.s.side, t = static_cast<int>(item / along);
+    x.kvh = static_cast<int>(item - static_cast<long long>(t) * along) * prm.s.side + beside;
     x.b0 = g.start + t * prm.s.seqs;
-    x.n = min(prm.s.seqs, g.n - t * prm.s.seqs);
     x.len = g.len;
-    x.place = prefix_rows_before(prm.s, g, t, x.kvh, x.rows);
+    x.place = prefix_place(prm.s, g, part, t, x.kvh, x.rows);
     w.at += x.k1 - x.k0;
     return true;
 }
@@ -128,11 +128,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ long long warp_sums[kThreads / 32];
     __shared__ long long first_base;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int part = static_cast<int>(blockIdx.x) / p.s.side, beside = static_cast<int>(blockIdx.x) - part * p.s.side;
 
-    // the kernel that joins may start wherever there is room: it waits for this one by itself
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    // and this one ends no sooner than the one before it
-    const auto leave = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
+    // The kernel that joins may start wherever there is room (and waits for this one by itself); this one ends no
+    // sooner than that of the sequences' own tokens.  (With the leave to start given at the top, that kernel's CTAs
+    // come to wait beside this one's: 72 us for 70.5, 64 sequences over 32768 tokens.)
+    const auto leave = [] {
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+    };
 
     // ------------------------------------------------------------ this CTA's part of all units
     Walk start;
@@ -161,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             total += warp_sums[w];
         }
         // two tiles a CTA at least where its two halves take one each
-        const long long chunk = max((total + gridDim.x - 1) / gridDim.x, HALVES ? 2LL : 1LL);
+        const long long chunk = max((total + p.s.prefix_parts - 1) / p.s.prefix_parts, HALVES ? 2LL : 1LL);
         if (blockIdx.x == 0) {
             long long before = upto - sum;
             for (int k = 0; k < per; ++k) {
@@ -172,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (tid == 0) p.s.prefix_info[0] = chunk;
         }
-        start.at = static_cast<long long>(blockIdx.x) * chunk;
+        start.at = part * chunk;
         start.end = min(start.at + chunk, total);
         if (start.at >= total) {                              // the whole CTA
             leave();
@@ -239,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int g = 0;                                   // tiles loaded, K and V counted apart
             int nq[2] = {0, 0};                          // Q tiles loaded
             bool ok = true, bad = false;
-            while (ok && next_piece(p, walk, piece)) {
+            while (ok && next_piece(p, part, beside, walk, piece)) {
                 const int n = piece.k1 - piece.k0;
                 int look = -1;
                 for (int i = 0; ok && i < n; ++i) {
@@ -350,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Every stage is waited for in turn, the other tile's too, which are given back here as they are
                 // not read.  V is given back by the product itself, so that the next tiles can come early.
                 int g = 0;                                   // ring position: K at g, V after it
-                while (ok && next_piece(p, walk, piece)) {
+                while (ok && next_piece(p, part, beside, walk, piece)) {
                     const int n = piece.k1 - piece.k0, mine = tiles_of(x, n);
                     int done = 0;
                     for (int i = 0; ok && i < n; ++i, g += 2) {
@@ -415,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive_if(lead, &turn[1 - x]);
                     return true;
                 };
-                while (ok && next_piece(p, walk, piece))
+                while (ok && next_piece(p, part, beside, walk, piece))
                     for (int k = piece.k0; ok && k < piece.k1; ++k, g += 2)
                         ok = round(true, k == piece.k0, k == piece.k1 - 1, piece.len - 128 * k);
                 if (ok) round(false, false, false, 0);
@@ -439,14 +443,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         Walk walk = start;
         Piece piece;
-        while (next_piece(p, walk, piece)) {
+        while (next_piece(p, part, beside, walk, piece)) {
             const int pieces = piece.k1 - piece.k0, n = tiles_of(x, pieces);
             const int g0 = g;                            // ring position of the piece's first K tile
             g += 2 * pieces;
             const bool mine = lrow < tile_rows && irow < piece.rows;
-            const size_t at = HALVES
-                ? static_cast<size_t>(blockIdx.x) * 2 * p.s.part_rows + 2 * piece.place + x * piece.rows + irow
-                : static_cast<size_t>(blockIdx.x) * p.s.part_rows + piece.place + irow;
+            const size_t at = piece.place + (HALVES ? x * piece.rows + lrow : irow);
             float m_used = -INFINITY, l = 0.f;
             int v_read = -1;                             // stage of the V tile to give back when it is read
             for (int i = 0; ok && i < n; ++i, ++blk) {
@@ -556,22 +558,55 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             if (!HALVES && speaks) mbar_arrive(&empty[v_read]);
             __syncwarp();
-            uint32_t o[D];
+            // a lane holds rows lane / 4 + 8 {0, 1} of 16 (twice), two neighbouring columns of every eight
+            uint32_t o[2][D / 2];
 #pragma unroll
-            for (int c0 = 0; c0 < D; c0 += 32) tmem_ld_row32(to + c0, o + c0);
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                for (int c0 = 0; c0 < D; c0 += 64)
+                    tmem_ld_16x256b_x8(to + (static_cast<uint32_t>(16 * hf) << 16) + c0, o[hf] + c0 / 2);
             tmem_wait_ld();
             // O is in registers: the next piece's first P V may overwrite it
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&o_free[x]);
-            if (mine) {
-                // a row without a finite score has l = 0, or NaN if it met one
-                const float inv = l == 0.f ? 0.f : 1.f / l;
-                float4* out = reinterpret_cast<float4*>(p.s.prefix_o + at * D);
+            // a row without a finite score has l = 0, or NaN if it met one
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const uint32_t rows = __ballot_sync(0xffffffffu, mine);
+            if (rows != 0u) {
+                // Four lanes exchange their pairs of columns, so that they write 64 bytes of a row (a row a lane would
+                // be 32 lines a store: 4.3 us for 256 rows of 128, against 1.3).
+                float* out = p.s.prefix_o + (at - lane) * D + 4 * (lane & 1) + 8 * (lane >> 1 & 1);
+                const bool upper = (lane & 2) != 0, odd = (lane & 1) != 0;
 #pragma unroll
-                for (int e = 0; e < D / 4; ++e)
-                    out[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
-                                         __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+                for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const int row = 16 * hf + 8 * r + (lane >> 2);
+                        const float by = __shfl_sync(0xffffffffu, inv, row);
+                        const bool there = (rows >> row & 1u) != 0u;
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) {
+                            float f[2], g2[2];           // the lane's first and second pair
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float a = __uint_as_float(o[hf][8 * i + 2 * r + e]) * by;
+                                const float b = __uint_as_float(o[hf][8 * i + 4 + 2 * r + e]) * by;
+                                const float got = __shfl_xor_sync(0xffffffffu, upper ? a : b, 2);
+                                f[e] = upper ? got : a;
+                                g2[e] = upper ? b : got;
+                            }
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float got = __shfl_xor_sync(0xffffffffu, odd ? f[e] : g2[e], 1);
+                                if (odd) f[e] = got;
+                                else g2[e] = got;
+                            }
+                            if (there) *reinterpret_cast<float4*>(out + row * D + 16 * i) = make_float4(f[0], f[1], g2[0], g2[1]);
+                        }
+                    }
+            }
+            if (mine) {
                 p.s.prefix_lse[at] = l == 0.f ? -INFINITY : m_used * c + log2f(l);
             }
         }
@@ -587,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D, bool BF16, bool HALVES>
-int launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PrefixParams& prm, int sms,
+int launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PrefixParams& prm,
            cudaStream_t stream) {
     auto kern = prefix_kernel<D, BF16, HALVES>;
     static std::atomic<unsigned long long> raised{0};
@@ -600,7 +635,12 @@ int launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, 
                a.numRegs * kThreads >= 128 * (2 * kRegsSoftmax + kRegsOther);
     }();
     if (!enough) return BSATTN_ERR_CUDA;
-    return launch_after(kern, static_cast<unsigned>(sms), kThreads, Cfg<D>::kBytes, stream, tq, tk, tv, prm);
+    // Beside the kernel of the own tokens where the prefixes are short (4 sequences over 2000 tokens: 16.6 us for
+    // 20.4), after it otherwise: begun beside it, the first two key tiles take 4 us each instead of 1.5, all CTAs alike,
+    // as if their instructions came from memory (64 sequences over 32768 tokens: 77 us for 70.5).
+    const unsigned grid = static_cast<unsigned>(prm.s.prefix_parts) * prm.s.side;
+    const long long bytes = static_cast<long long>(prm.s.P) * prm.s.prefix_room * prm.s.Hkv * D * 4;
+    return launch_on(bytes <= kShortBytes, kern, grid, kThreads, Cfg<D>::kBytes, stream, tq, tk, tv, prm);
 }
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -608,7 +648,7 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 // Byte offsets of the workspace, behind the status word, and what depends on the shape and the GPU alone.
 struct Layout {
     size_t prefix_info, own_info, prefix_lse, prefix_o, own_lse, own_o, total;
-    int halves, seqs, part_rows, own_parts;
+    int halves, seqs, part_rows, side, prefix_parts, own_parts;
 };
 
 Layout layout_of(int B, int P, int Hq, int Hkv, int d, int sms) {
@@ -619,7 +659,12 @@ Layout layout_of(int B, int P, int Hq, int Hkv, int d, int sms) {
     w.seqs = w.halves ? tile : 2 * tile;
     w.part_rows = w.seqs * G;
     w.own_parts = 4 * std::max(2 * sms / Hkv, 1);        // four warps a CTA, two CTAs an SM
-    const size_t rows = (static_cast<size_t>(B) * Hq + static_cast<size_t>(sms) * w.part_rows) * (w.halves ? 2 : 1);
+    // A prefix with no more rows than a CTA has is read once: all its kv heads at the same keys at the same time, as
+    // those lie next to each other in the cache (64 sequences over 32768 tokens: 76 us for 85).  One with more is
+    // read several times and bound by its products: there all CTAs get equal work whatever Hkv is.
+    w.side = (static_cast<long long>(B) + P - 1) / P <= w.seqs && Hkv <= sms ? Hkv : 1;
+    w.prefix_parts = std::max(sms / w.side, 1);          // a CTA an SM
+    const size_t rows = (static_cast<size_t>(B) * Hq + static_cast<size_t>(w.prefix_parts) * w.side * w.part_rows) * (w.halves ? 2 : 1);
     const size_t own = (static_cast<size_t>(B) + w.own_parts) * Hq;
     size_t at = 256;
     const auto take = [&at](size_t bytes) {
@@ -706,6 +751,8 @@ extern "C" int bsattn_decode_shared(const void* q, const void* k_pages, const vo
     s.seqs = w.seqs;
     s.part_rows = w.part_rows;
     s.halves = w.halves;
+    s.side = w.side;
+    s.prefix_parts = w.prefix_parts;
     s.own_parts = w.own_parts;
     s.page_size = page_size;
     s.num_pages = num_pages;
@@ -731,7 +778,7 @@ extern "C" int bsattn_decode_shared(const void* q, const void* k_pages, const vo
     const auto run = [&](auto dim, auto halves) {
         constexpr int D = decltype(dim)::value;
         constexpr bool HALVES = decltype(halves)::value;
-        return bf16 ? launch<D, true, HALVES>(tq, tk, tv, prm, sms, st) : launch<D, false, HALVES>(tq, tk, tv, prm, sms, st);
+        return bf16 ? launch<D, true, HALVES>(tq, tk, tv, prm, st) : launch<D, false, HALVES>(tq, tk, tv, prm, st);
     };
     using D64 = std::integral_constant<int, 64>;
     using D128 = std::integral_constant<int, 128>;

@@ -14,12 +14,14 @@ namespace bsattn {
 // A piece is the result over some keys: for each of its rows O / l (fp32) and the base-2 log-sum-exp, -infinity
 // where the row has met no finite score (O is not written then, or is 0).
 //
-// Prefixes.  Sequences starts[p] .. starts[p + 1] - 1 share prefix p.  An item is a kv head's query rows of up to
-// `seqs` of them; a unit is 128 keys of an item.  The units of all items, in the order prefix, sequences, kv
-// head, keys, are cut into equal parts, one a CTA.  What part c has of an item is a piece; its row r stands at
-//     c * part_rows + (rows of all items before) + r
-// or twice as far apart where `halves`: a piece is then two, of every second key tile each.  (Going from a piece
-// to the next one moves on by the item's rows or by part_rows, which is no less, or by both: no two share a place.)
+// Prefixes.  Sequences starts[p] .. starts[p + 1] - 1 share prefix p.  A CTA's kv head is its lane among `side` kv
+// heads side by side, plus a multiple of `side`.  An item is up to `seqs` sequences and one such multiple; a unit is
+// 128 keys of an item.  The units of all items, in the order prefix, sequences, kv heads, keys, are cut into equal
+// parts, one a (CTA, lane).  What part c has of an item is a piece; its row r stands at
+//     c * part_rows + (the lane's rows of all items before) + r
+// of the lane's, or twice as far apart where `halves`: a piece is then two, of every second key tile each.  (Going
+// from a piece to the next one moves on by the item's rows or by part_rows, which is no less, or by both: no two
+// share a place.)
 //
 // Own tokens.  A unit is 32 keys of a sequence.  The units of all sequences, end to end, are cut into equal parts,
 // one a (warp, kv head).  What part c has of sequence b is a piece at c + b: [kv head][its query heads].
@@ -42,7 +44,7 @@ struct SharedCall {
     int* status;
     int B, P, Hq, Hkv;
     int seqs, part_rows, halves;
-    int own_parts;
+    int side, prefix_parts, own_parts;
     int page_size, num_pages, prefix_pages, own_pages;
     int prefix_room, own_room;   // tokens that a table has room for
     float scale_log2;
@@ -69,13 +71,17 @@ __device__ __forceinline__ PrefixGroup prefix_group(const SharedCall& s, int p) 
 }
 
 __device__ __forceinline__ long long prefix_units(const SharedCall& s, const PrefixGroup& g) {
-    return static_cast<long long>((g.n + s.seqs - 1) / s.seqs) * s.Hkv * g.tiles;
+    return static_cast<long long>((g.n + s.seqs - 1) / s.seqs) * (s.Hkv / s.side) * g.tiles;
 }
 
-// Rows of all items before item (sequences t, kv head h) of a group, and the item's own.
-__device__ __forceinline__ long long prefix_rows_before(const SharedCall& s, const PrefixGroup& g, int t, int h, int& rows) {
-    rows = min(s.seqs, g.n - t * s.seqs) * (s.Hq / s.Hkv);
-    return (static_cast<long long>(g.start) + static_cast<long long>(t) * s.seqs) * s.Hq + static_cast<long long>(h) * rows;
+// Where part c's rows of an item (the t-th sequences of a group, kv head h) begin, and how many there are.
+__device__ __forceinline__ long long prefix_place(const SharedCall& s, const PrefixGroup& g, int c, int t, int h, int& rows) {
+    const int G = s.Hq / s.Hkv, lane = h % s.side, along = s.Hkv / s.side;
+    rows = min(s.seqs, g.n - t * s.seqs) * G;
+    const long long of_lane = static_cast<long long>(s.prefix_parts) * s.part_rows + static_cast<long long>(s.B) * G * along;
+    return (lane * of_lane + static_cast<long long>(c) * s.part_rows +
+            (static_cast<long long>(g.start) + t * s.seqs) * G * along + static_cast<long long>(h / s.side) * rows) *
+           (s.halves ? 2 : 1);
 }
 
 __device__ __forceinline__ int own_len(const SharedCall& s, int b) { return max(min(s.own_lens[b], s.own_room), 0); }
@@ -86,9 +92,10 @@ __device__ __forceinline__ int own_units(int len) { return len / 32 + (len % 32 
 int launch_own_tokens(const SharedCall& call, int d, bool bf16, cudaStream_t stream);
 int launch_join(const SharedCall& call, int d, bool bf16, cudaStream_t stream);
 
-// Launches a kernel that may start while the one before it on the stream still runs (and waits for it by itself).
+// Launches a kernel; `early`: it may start while the one before it on the stream still runs, and waits for that one
+// by itself.
 template <typename Kernel, typename... Args>
-int launch_after(Kernel kern, unsigned grid, int threads, size_t smem, cudaStream_t stream, const Args&... args) {
+int launch_on(bool early, Kernel kern, unsigned grid, int threads, size_t smem, cudaStream_t stream, const Args&... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
@@ -98,7 +105,7 @@ int launch_after(Kernel kern, unsigned grid, int threads, size_t smem, cudaStrea
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = early ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
 }
 
