@@ -12,6 +12,7 @@
 #include <algorithm>
 
 #include "host_internal.h"
+#include "mma16.cuh"
 #include "ptx.cuh"
 #include "summary.cuh"
 
@@ -20,15 +21,20 @@ namespace {
 
 // ------------------------------------------------------------------------------------------ decode
 //
-// One CTA a (sequence, kv head).  An index row (codes of a block of one head) is read by d / 16 lanes, 16
-// bytes each, against the query heads' codes in registers: four whole-number products an instruction
-// (dp4a), and the lanes' sums added by exchanging halves (V values over L lanes in V - V / L exchanges).
-// The index is read once, which bounds a large batch; a small one is a chain of latencies: lengths, table,
-// index, then the counts.
+// A CTA a (sequence, kv head), of as many threads as leave room for all of them at once.
+// A warp scores 16 blocks at a time, S [16 blocks x 8 heads] = K Q^T by mma.sync m16n8k16 in fp16: a code c enters
+// as 1152 + c, which takes one byte permutation for two codes (1024 + byte is an fp16 number with that byte for its
+// lowest), and the sums begin at -1152 times the query's codes.  Whole numbers below 2^23 in magnitude throughout, 32
+// channels a sum: exact.  (8-bit products of the tensor core are slow here, an m16n8k32 in 17 cycles an SM; by dp4a,
+// which is not, the adding of eight lanes' sums made it three times the instructions: 28 us for 64 sequences.)
+// Which channel a matrix index stands for is free, so a lane reads D / 4 consecutive codes of a row.  Keys stay in
+// shared memory, the first kHeld of a thread in registers.  A trip of the search counts at four thresholds at once:
+// a count is mostly the way through the barrier.
+// The index is read once, which bounds a large batch; a small one is a chain of latencies: lengths, table, index,
+// then the counts.
 
-constexpr int kSelThreads = 256;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kMaxBlocks = 51200;               // of a sequence: their keys lie in shared memory
+constexpr int kMaxBlocks = 46875;               // of a sequence: their keys lie in shared memory
+constexpr int kHeld = 8;                        // keys of a thread in registers
 
 struct SelectParams {
     const void* q;
@@ -41,57 +47,43 @@ struct SelectParams {
     int Hq, Hkv, page_size, max_pages, num_pages, max_sel, sinks, recent;
 };
 
-// The sum of `mine` over the CTA, the same in all threads.  Counters are used in turn, `nth` counting the calls.
-__device__ __forceinline__ int cta_sum(int mine, int (&counter)[3], int nth) {
-    const int w = __reduce_add_sync(0xffffffffu, mine);
-    if ((threadIdx.x & 31) == 0 && w) atomicAdd(&counter[nth % 3], w);
-    __syncthreads();
-    // everybody has read the counter of the call before, which is the one of the call after next
-    if (threadIdx.x == 0) counter[(nth + 2) % 3] = 0;
-    return *static_cast<volatile int*>(&counter[nth % 3]);
+// What the CTA's warps add up.
+struct Shares {
+    uint32_t range[2];                          // largest of ~key, and of key
+    int there, forced;                          // blocks that may be chosen, blocks that have to be
+    int counts[3][4];
+};
+
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t to, const void* from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
 }
 
-// GP: query heads of a kv head, rounded up to a power of two.
-template <int D, bool BF16, int GP>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p) {
-    constexpr int kLanes = D / 16;                          // of an index row
-    constexpr int kRows = 32 / kLanes;                      // that a warp reads at once
-    constexpr int kPasses = kLanes > GP ? kLanes / GP : 1;  // reads whose sums are added together
-    constexpr int kV = kPasses * GP, kR = kV / kLanes;      // values, and those a lane is left with
-    constexpr int kUnroll = kPasses >= 4 ? 1 : (kPasses == 2 ? 2 : 4);
-    extern __shared__ uint32_t keys[];                      // first each block's index row, then its key
-    __shared__ __align__(16) int8_t qcodes[8][D];
-    __shared__ float qscale[8];
-    __shared__ int counter[3];
-    __shared__ uint32_t range[2];                           // smallest and largest key
-    __shared__ int above[kSelWarps], level[kSelWarps];
+// Times 16 blocks whose index rows a warp has on their way.
+__host__ __device__ constexpr int depth_of(int threads) { return threads > 512 ? 2 : 4; }
+
+template <int D, bool BF16, int TH>
+__global__ void __launch_bounds__(TH, TH == 128 ? 4 : 1) select_kernel(const SelectParams p) {
+    constexpr int kWarps = TH / 32, kDepth = depth_of(TH);
+    constexpr bool kLean = TH > 512;                        // no registers for the queries' operands
+    constexpr int kSteps = D / 16, kSums = kSteps / 2;      // k16 steps, and sums of two of them
+    constexpr uint32_t kGroup = 16 * D + 64;                // 16 index rows: codes, scales
+    extern __shared__ __align__(16) uint8_t sel_smem[];
+    uint32_t* keys = reinterpret_cast<uint32_t*>(sel_smem + kWarps * kDepth * kGroup);   // of the CTA's blocks; first their index rows
+    __shared__ uint2 qb[kSteps][32];                        // the queries' codes as a lane's operands, head lane / 4
+    __shared__ float qscale[8], qbase[kSums][8];            // of the query heads: scale, where sums begin
+    __shared__ Shares sh;
+    __shared__ int above[kWarps], level[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int b = blockIdx.x / p.Hkv, g = blockIdx.x - b * p.Hkv, G = p.Hq / p.Hkv;
+    const int row = static_cast<int>(blockIdx.x), b = row / p.Hkv, g = row - b * p.Hkv, G = p.Hq / p.Hkv;
 
     const int asked = p.seqlens[b];
-    const int blocks_a_page = p.page_size / kBlockRows;
-    const int room = p.max_pages * blocks_a_page;
-    const bool far = asked < 0 || asked > static_cast<long long>(p.max_pages) * p.page_size;
-    const int n = asked <= 0 ? 0 : min(asked / kBlockRows + (asked % kBlockRows != 0), room);
-    if (tid < 3) counter[tid] = 0;
-    if (tid == 0) {
-        range[0] = 0xffffffffu;
-        range[1] = 0;
-    }
-    // the index row of each block, or -1
-    bool bad = far;
-    for (int j = tid; j < n; j += kSelThreads) {
-        const int lp = j / blocks_a_page;
-        const int page = p.table[static_cast<size_t>(b) * p.max_pages + lp];
-        const bool in = page >= 0 && page < p.num_pages;
-        bad = bad || !in;
-        keys[j] = in ? static_cast<uint32_t>(page * blocks_a_page + j - lp * blocks_a_page) : 0xffffffffu;
-    }
-    if (bad && (lane == 0 || !far)) atomicOr(p.status, BSATTN_ERR_BAD_INDEX);
     // a warp a query head: its codes and scale
-    if (warp < G) {
+    for (int head = warp; head < G; head += kWarps) {
         const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.q) +
-                                                                (static_cast<size_t>(b) * p.Hq + g * G + warp) * D);
+                                                                (static_cast<size_t>(b) * p.Hq + g * G + head) * D);
         float x[D / 32], top = 0.f;
         bool finite = true;
 #pragma unroll
@@ -110,138 +102,232 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
         const float scale = scale8(top, finite);
+        int sum = 0;
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) qcodes[warp][lane * (D / 32) + e] = static_cast<int8_t>(code8(x[e], scale, finite));
-        if (lane == 0) qscale[warp] = finite ? scale : 0.f;         // a query that is not finite scores 0
+        for (int e = 0; e < D / 32; ++e) {
+            const int c = code8(x[e], scale, finite);
+            x[e] = static_cast<float>(c);
+            sum += c;
+        }
+        // (channels 2 i, 2 i + 1 of head h: half of the operands of lane 4 h + j in step k, as below)
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e) {
+            const int ch = lane * (D / 32) + 2 * e, k = ch / 64 * 4 + ch % 16 / 4;
+            reinterpret_cast<uint32_t*>(&qb[k][4 * head + ch % 64 / 16])[ch % 4 / 2] = mma16::pack2<false>(x[2 * e], x[2 * e + 1]);
+        }
+        // Step k has channels 64 (k / 4) + 16 j + 4 (k % 4) + 0 .. 3 of a lane j of a quad, a sum two steps: those of
+        // lanes with the same bit 4 and bit 1 (d = 128: four channels a lane) or the same bit 2 (d = 64: two).
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1)
+            if (D == 128 ? m != 16 && m != 2 : m != 4) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+        if (D == 128 ? (lane & ~18) == 0 : (lane & ~4) == 0)
+            qbase[D == 128 ? lane >> 4 << 1 | (lane >> 1 & 1) : lane >> 2][head] = -1152.f * static_cast<float>(sum);
+        if (lane == 0) qscale[head] = finite ? scale : 0.f;         // a query that is not finite scores 0
     }
+    const int blocks_a_page = p.page_size / kBlockRows;
+    const int room = p.max_pages * blocks_a_page;
+    const bool far = asked < 0 || asked > static_cast<long long>(p.max_pages) * p.page_size;
+    const int n = asked <= 0 ? 0 : min(asked / kBlockRows + (asked % kBlockRows != 0), room);
+    for (int i = tid; i < static_cast<int>(sizeof(Shares) / 4); i += TH) reinterpret_cast<uint32_t*>(&sh)[i] = 0;
+    // (heads that there are not: codes 0)
+    for (int i = tid; i < kSteps * 32; i += TH)
+        if (i % 32 / 4 >= G) qb[i / 32][i % 32] = make_uint2(0, 0);
+    if (tid < 8 * kSums && tid % 8 >= G) qbase[tid / 8][tid % 8] = 0.f;
+    // the index row of each block, or -1
+    bool bad = far;
+    for (int i = tid; i < n; i += TH) {
+        const int j = i, lp = j / blocks_a_page;
+        const int page = __ldg(p.table + static_cast<size_t>(b) * p.max_pages + lp);
+        const bool in = page >= 0 && page < p.num_pages;
+        bad = bad || !in;
+        keys[i] = in ? static_cast<uint32_t>(page * blocks_a_page + j - lp * blocks_a_page) : 0xffffffffu;
+    }
+    if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.status, BSATTN_ERR_BAD_INDEX);
     __syncthreads();
 
     // ---------------------------------------------------------------- scores
-    const int first_recent = max(n - p.recent, 0);
     {
-        const int sub = lane / kLanes, part = lane % kLanes;
-        int4 qc[GP];
+        const int first_recent = max(n - p.recent, 0);
+        const int r8 = lane >> 2, j4 = lane & 3, h0 = 2 * j4;
+        float sq[2];
 #pragma unroll
-        for (int h = 0; h < GP; ++h)
-            qc[h] = h < G ? *reinterpret_cast<const int4*>(&qcodes[h][16 * part]) : make_int4(0, 0, 0, 0);
-        // after the exchanges a lane has values kR part + {0 .. kR - 1}: value v is head v % GP of read v / GP
-        const int my_pass = kR * part / GP, my_head = kR * part % GP;
-        float sq[kR];
+        for (int e = 0; e < 2; ++e) sq[e] = h0 + e < G ? qscale[h0 + e] : 0.f;
+        uint32_t least = 0, most = 0;                       // of ~key, and of key
+        int there = 0;                                      // and the forced ones, 2^16 each
+        // Groups of 16 blocks in turn: the warp's m-th is group kWarps m + warp.  Where rows are 128 bytes, the two
+        // halves of every second one change places, so that a quad's 16-byte reads of two rows meet no bank twice.
+        uint8_t* ring = sel_smem + warp * kDepth * kGroup;
+        const int groups = ((n + 15) / 16 - warp + kWarps - 1) / kWarps;
+        const auto fetch = [&](int m) {
+            if (m < groups) {
+                const uint32_t to = smem_u32(ring + (m % kDepth) * kGroup);
+                const int base = (m * kWarps + warp) * 16;
+                constexpr int kChunks = D / 16;                     // of 16 bytes in a row
 #pragma unroll
-        for (int r = 0; r < kR; ++r) sq[r] = my_head + r < G ? qscale[my_head + r] : 0.f;
-        uint32_t least = 0xffffffffu, most = 0;
-        constexpr int kStep = kRows * kPasses;              // blocks of a warp at a time
-        for (int base = warp * kStep; base < n; base += kSelWarps * kStep * kUnroll) {
-            int4 kc[kUnroll][kPasses];
-            float sk[kUnroll];
-            uint32_t row_of_mine[kUnroll];
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int at = base + u * kSelWarps * kStep;
-#pragma unroll
-                for (int i = 0; i < kPasses; ++i) {
-                    const int j = at + i * kRows + sub;
-                    const uint32_t row = j < n ? keys[j] : 0xffffffffu;
-                    kc[u][i] = make_int4(0, 0, 0, 0);
-                    if (row != 0xffffffffu)
-                        kc[u][i] = __ldg(reinterpret_cast<const int4*>(p.codes + (static_cast<size_t>(row) * p.Hkv + g) * D) + part);
+                for (int e = 0; e < kChunks / 2; ++e) {
+                    const int r = (32 / kChunks) * e + lane / kChunks, c = lane % kChunks;
+                    const uint32_t row = base + r < n ? keys[base + r] : 0u;
+                    const size_t place = static_cast<size_t>(row == 0xffffffffu ? 0u : row) * p.Hkv + g;
+                    copy16(to + r * D + (D == 128 ? c ^ (r & 1) << 2 : c) * 16, p.codes + place * D + c * 16);
                 }
-                const int j = at + my_pass * kRows + sub;
-                row_of_mine[u] = j < n ? keys[j] : 0xffffffffu;
-                sk[u] = row_of_mine[u] != 0xffffffffu ? __ldg(p.scales + static_cast<size_t>(row_of_mine[u]) * p.Hkv + g) : 0.f;
-            }
-            __syncwarp();                                   // the rows are read: keys may take their places
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                int v[kV];
-#pragma unroll
-                for (int i = 0; i < kPasses; ++i)
-#pragma unroll
-                    for (int h = 0; h < GP; ++h) {
-                        int s = __dp4a(kc[u][i].x, qc[h].x, 0);
-                        s = __dp4a(kc[u][i].y, qc[h].y, s);
-                        s = __dp4a(kc[u][i].z, qc[h].z, s);
-                        v[i * GP + h] = __dp4a(kc[u][i].w, qc[h].w, s);
-                    }
-#pragma unroll
-                for (int m = kLanes / 2, half = kV / 2; m > 0; m >>= 1, half >>= 1) {
-                    const bool upper = (lane & m) != 0;
-#pragma unroll
-                    for (int i = 0; i < half; ++i) {
-                        const int keep = upper ? v[i + half] : v[i], give = upper ? v[i] : v[i + half];
-                        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, m);
-                    }
-                }
-                float best = -INFINITY;
-#pragma unroll
-                for (int r = 0; r < kR; ++r)
-                    if (my_head + r < G) best = fmaxf(best, __fmul_rn(static_cast<float>(v[r]), sq[r]));
-#pragma unroll
-                for (int m = 1; m < GP / kR; m <<= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, m));
-                const int j = base + u * kSelWarps * kStep + my_pass * kRows + sub;
-                if (my_head == 0 && j < n) {
-                    uint32_t key = 0;
-                    if (row_of_mine[u] != 0xffffffffu) {
-                        key = key_of(sk[u] == INFINITY ? INFINITY : __fmul_rn(best, sk[u]));
-                        if (j < p.sinks || j >= first_recent) {
-                            key = kForced;
-                        } else {
-                            least = min(least, key);
-                            most = max(most, key);
-                        }
-                    }
-                    keys[j] = key;
+                if (lane < 16) {
+                    const uint32_t row = base + lane < n ? keys[base + lane] : 0u;
+                    copy4(to + 16 * D + 4 * lane, p.scales + static_cast<size_t>(row == 0xffffffffu ? 0u : row) * p.Hkv + g);
                 }
             }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        uint2 q2[kLean ? 1 : kSteps];
+        float2 begin[kSums];
+#pragma unroll
+        for (int k = 0; k < (kLean ? 1 : kSteps); ++k) q2[k] = qb[k][lane];
+#pragma unroll
+        for (int k = 0; k < kSums; ++k) begin[k] = *reinterpret_cast<const float2*>(&qbase[k][h0]);
+#pragma unroll
+        for (int m = 0; m < kDepth; ++m) fetch(m);
+        for (int m = 0; m < groups; ++m) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+            __syncwarp();
+            const uint8_t* stage = ring + (m % kDepth) * kGroup;
+            uint4 kc[2][D / 64];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int w = 0; w < D / 64; ++w) {
+                    const int c = D == 128 ? (j4 + 4 * w) ^ (r8 & 1) << 2 : j4;
+                    kc[e][w] = *reinterpret_cast<const uint4*>(stage + (8 * e + r8) * D + 16 * c);
+                }
+            // lanes 0 and 1 of a quad have its two blocks
+            const int i = (m * kWarps + warp) * 16 + 8 * (j4 & 1) + r8;
+            const float sk = *reinterpret_cast<const float*>(stage + 16 * D + 4 * (8 * (j4 & 1) + r8));
+            float c[kSums][4];
+#pragma unroll
+            for (int k = 0; k < kSums; ++k) {
+                c[k][0] = c[k][2] = begin[k].x;
+                c[k][1] = c[k][3] = begin[k].y;
+            }
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+                uint32_t a[4];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint4 v = kc[e][k / 4];
+                    const uint32_t w = (k % 4 == 0 ? v.x : k % 4 == 1 ? v.y : k % 4 == 2 ? v.z : v.w) ^ 0x80808080u;
+                    a[e] = __byte_perm(w, 0x64646464u, 0x4140);
+                    a[e + 2] = __byte_perm(w, 0x64646464u, 0x4342);
+                }
+                if constexpr (kLean) q2[0] = qb[k][lane];
+                mma16::mma16816<false>(c[k / 2], a, q2[kLean ? 0 : k].x, q2[kLean ? 0 : k].y);
+            }
+            float best[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float dot[2] = {c[0][2 * e], c[0][2 * e + 1]};
+#pragma unroll
+                for (int k = 1; k < kSums; ++k) {
+                    dot[0] += c[k][2 * e];
+                    dot[1] += c[k][2 * e + 1];
+                }
+                best[e] = h0 < G ? __fmul_rn(dot[0], sq[0]) : -INFINITY;
+                if (h0 + 1 < G) best[e] = fmaxf(best[e], __fmul_rn(dot[1], sq[1]));
+                best[e] = fmaxf(best[e], __shfl_xor_sync(0xffffffffu, best[e], 1));
+                best[e] = fmaxf(best[e], __shfl_xor_sync(0xffffffffu, best[e], 2));
+            }
+            if (j4 < 2 && i < n) {
+                uint32_t key = 0;
+                if (keys[i] != 0xffffffffu) {
+                    ++there;
+                    if (i < p.sinks || i >= first_recent) {
+                        key = kForced;
+                        there += 1 << 16;
+                    } else {
+                        key = key_of(sk == INFINITY ? INFINITY : __fmul_rn(j4 ? best[1] : best[0], sk));
+                        least = max(least, ~key);
+                        most = max(most, key);
+                    }
+                }
+                keys[i] = key;
+            }
+            __syncwarp();                                           // the stage is read
+            fetch(m + kDepth);
         }
-        least = __reduce_min_sync(0xffffffffu, least);
+        // (a warp has fewer than 2^16 blocks)
+        there = __reduce_add_sync(0xffffffffu, there);
+        least = __reduce_max_sync(0xffffffffu, least);
         most = __reduce_max_sync(0xffffffffu, most);
         if (lane == 0) {
-            atomicMin(&range[0], least);
-            atomicMax(&range[1], most);
+            atomicMax(&sh.range[0], least);
+            atomicMax(&sh.range[1], most);
+            atomicAdd(&sh.there, there & 0xffff);
+            atomicAdd(&sh.forced, there >> 16);
         }
     }
     __syncthreads();
 
     // ---------------------------------------------------------------- the score that max_sel blocks reach
-    int nth = 0;
-    const auto count = [&](uint32_t t) {
-        int c = 0;
-        for (int j = tid; j < n; j += kSelThreads) c += keys[j] >= t;
-        return cta_sum(c, counter, nth++);
-    };
     uint32_t lo = 1;
     int spare = n;                                          // places for blocks whose score is lo itself
-    if (n > p.max_sel) {
-        int c_lo = count(1);
-        if (c_lo > p.max_sel) {
-            // count(lo) >= max_sel > count(hi), hi = most + 1 (there are no more forced blocks than places)
-            lo = range[0];
-            uint32_t hi = range[1] + 1;
-            int c_hi = count(hi);
-            if (c_hi >= p.max_sel) {                        // the forced blocks take all places
-                lo = hi;
-                c_lo = c_hi;
-            }
+    const int there = sh.there;
+    if (there > p.max_sel) {
+        int c_hi = sh.forced;
+        if (c_hi >= p.max_sel) {
+            lo = kForced;                                   // the forced blocks take all places
+        } else {
+            uint32_t held[kHeld];
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) held[i] = i * TH + tid < n ? keys[i * TH + tid] : 0u;
+            // count(lo) > max_sel > count(hi)
+            lo = ~sh.range[0];
+            uint32_t hi = sh.range[1] + 1;
+            int c_lo = there;
             for (int step = 0; c_lo != p.max_sel && hi - lo > 1; ++step) {
-                const uint32_t mid = between(lo, hi, step);
-                const int c = count(mid);
-                if (c >= p.max_sel) {
-                    lo = mid;
-                    c_lo = c;
-                } else {
-                    hi = mid;
-                    c_hi = c;
+                uint32_t t[4];
+                thresholds(lo, hi, step, t);
+                int c[2] = {0, 0};                          // two counts each, 2^16 apart
+                const auto count = [&](uint32_t k) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) c[i] += (k >= t[2 * i] ? 1 : 0) + (k >= t[2 * i + 1] ? 0x10000 : 0);
+                };
+#pragma unroll
+                for (int i = 0; i < kHeld; ++i) {
+                    if (i * TH >= n) break;
+                    count(held[i]);
                 }
+                for (int i = kHeld * TH + tid; i < n; i += TH) count(keys[i]);
+                int* to = sh.counts[step % 3];
+                const int s0 = __reduce_add_sync(0xffffffffu, c[0]), s1 = __reduce_add_sync(0xffffffffu, c[1]);
+                if (lane < 4) {
+                    const int s = lane & 2 ? s1 : s0, v = lane & 1 ? s >> 16 : s & 0xffff;
+                    if (v) atomicAdd(&to[lane], v);
+                }
+                __syncthreads();
+                // the last threshold that max_sel blocks reach, and the first that fewer do
+                int now[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) now[i] = static_cast<volatile int*>(to)[i];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (now[i] >= p.max_sel) {
+                        lo = t[i];
+                        c_lo = now[i];
+                    }
+#pragma unroll
+                for (int i = 3; i >= 0; --i)
+                    if (now[i] < p.max_sel) {
+                        hi = t[i];
+                        c_hi = now[i];
+                    }
+                // everybody has read the counts of the trip before, which are those of the trip after next
+                if (tid < 4) sh.counts[(step + 2) % 3][tid] = 0;
             }
             if (c_lo != p.max_sel) spare = p.max_sel - c_hi;
         }
     }
 
     // ---------------------------------------------------------------- the chosen blocks in order
-    // warp w has the blocks [w * each, (w + 1) * each)
-    const int each = ((n + kSelWarps - 1) / kSelWarps + 31) & ~31;
-    const int j0 = min(warp * each, n), j1 = min(j0 + each, n);
+    // warp w has the blocks [w * span, (w + 1) * span)
+    const int span = ((n + kWarps - 1) / kWarps + 31) & ~31;
+    const int j0 = min(warp * span, n), j1 = min(j0 + span, n);
     int over = 0, equal = 0;
     for (int j = j0 + lane; j < j1; j += 32) {
         over += keys[j] > lo;
@@ -254,17 +340,12 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         level[warp] = equal;
     }
     __syncthreads();
-    int over_before = 0, equal_before = 0, all = 0, all_equal = 0;
-#pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) {
-        if (w == warp) {
-            over_before = all;
-            equal_before = all_equal;
-        }
-        all += above[w];
-        all_equal += level[w];
+    int over_before = 0, equal_before = 0;
+    for (int w = 0; w < warp; ++w) {
+        over_before += above[w];
+        equal_before += level[w];
     }
-    int32_t* out = p.out + static_cast<size_t>(blockIdx.x) * p.max_sel;
+    int32_t* out = p.out + static_cast<size_t>(row) * p.max_sel;
     const uint32_t below = (1u << lane) - 1u;
     for (int j = j0; j < j1; j += 32) {
         const uint32_t key = j + lane < j1 ? keys[j + lane] : 0u;
@@ -276,18 +357,33 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         over_before += __popc(is_over);
         equal_before += __popc(is_equal);
     }
-    for (int j = all + min(all_equal, spare) + tid; j < p.max_sel; j += kSelThreads) out[j] = -1;
+    // (the last warp has passed all blocks)
+    if (warp == kWarps - 1)
+        for (int j = over_before + min(equal_before, spare) + lane; j < p.max_sel; j += 32) out[j] = -1;
 }
 
-template <int D, bool BF16, int GP>
-int launch_select(const SelectParams& prm, int B, cudaStream_t st) {
-    auto kern = select_kernel<D, BF16, GP>;
+template <int D, bool BF16, int TH>
+int launch_select(const SelectParams& prm, long long rows, cudaStream_t st) {
+    auto kern = select_kernel<D, BF16, TH>;
     const int blocks = prm.max_pages * (prm.page_size / kBlockRows);
     static std::atomic<unsigned long long> raised{0};
-    const int rc = raise_smem_limit(reinterpret_cast<const void*>(kern), 4 * kMaxBlocks, raised);
+    int rc = raise_smem_limit(reinterpret_cast<const void*>(kern), 224 * 1024, raised);
     if (rc) return rc;
-    kern<<<static_cast<unsigned>(B) * prm.Hkv, kSelThreads, 4 * static_cast<size_t>(blocks), st>>>(prm);
+    const size_t smem = TH / 32 * depth_of(TH) * (16 * D + 64) + 4 * static_cast<size_t>(blocks);
+    kern<<<static_cast<unsigned>(rows), TH, smem, st>>>(prm);
     return cudaGetLastError() == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
+}
+
+template <int D, bool BF16>
+int select(const SelectParams& prm, int B, cudaStream_t st) {
+    int sms = num_sms_of_current_device();
+    if (sms <= 0) sms = 148;
+    const long long rows = static_cast<long long>(B) * prm.Hkv;
+    const int blocks = prm.max_pages * (prm.page_size / kBlockRows);
+    // many threads where a row has an SM to itself; the rings of many and the keys of many blocks do not both fit
+    if (rows <= sms && blocks <= 16384) return launch_select<D, BF16, 1024>(prm, rows, st);
+    if (rows <= 2 * sms && blocks <= 16384) return launch_select<D, BF16, 512>(prm, rows, st);
+    return launch_select<D, BF16, 128>(prm, rows, st);
 }
 
 // ------------------------------------------------------------------------------------------ prompts
@@ -596,19 +692,9 @@ extern "C" int bsattn_decode_select(const void* q, const int8_t* codes, const fl
     prm.sinks = sinks;
     prm.recent = recent;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const auto run = [&](auto dim, auto bf16) {
-        constexpr int D = decltype(dim)::value;
-        constexpr bool BF16 = decltype(bf16)::value;
-        const int G = Hq / Hkv;
-        if (G == 1) return launch_select<D, BF16, 1>(prm, B, st);
-        if (G == 2) return launch_select<D, BF16, 2>(prm, B, st);
-        if (G <= 4) return launch_select<D, BF16, 4>(prm, B, st);
-        return launch_select<D, BF16, 8>(prm, B, st);
-    };
-    using D64 = std::integral_constant<int, 64>;
-    using D128 = std::integral_constant<int, 128>;
-    if (d == 64) return dtype == BSATTN_BF16 ? run(D64{}, std::true_type{}) : run(D64{}, std::false_type{});
-    return dtype == BSATTN_BF16 ? run(D128{}, std::true_type{}) : run(D128{}, std::false_type{});
+    const bool bf16 = dtype == BSATTN_BF16;
+    if (d == 64) return bf16 ? select<64, true>(prm, B, st) : select<64, false>(prm, B, st);
+    return bf16 ? select<128, true>(prm, B, st) : select<128, false>(prm, B, st);
 }
 
 extern "C" size_t bsattn_mask_from_qk_workspace_size(int B, int Hq, int Hkv, int Sq, int Sk, int d) {

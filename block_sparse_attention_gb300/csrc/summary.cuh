@@ -62,6 +62,22 @@ __device__ __forceinline__ uint32_t between(uint32_t lo, uint32_t hi, int step) 
     return max(min(mid, hi - 1), lo + 1);
 }
 
+// NT rising keys between lo and hi at which the next counts are taken, likewise: equal parts of the scores' range for
+// the first eight steps, then of the keys'.  Where fewer lie between, some are given twice.
+template <int NT>
+__device__ __forceinline__ void thresholds(uint32_t lo, uint32_t hi, int step, uint32_t (&t)[NT]) {
+    const float a = score_of(lo), b = score_of(hi), by = (b - a) * (1.f / (NT + 1));
+    const bool even = step < 8 && isfinite(a) && isfinite(b) && isfinite(by);
+    const uint32_t gap = hi - lo;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const uint32_t mid = even ? key_of(fmaf(by, static_cast<float>(i + 1), a))
+                                  : lo + gap / (NT + 1) * (i + 1) + gap % (NT + 1) * (i + 1) / (NT + 1);
+        t[i] = max(min(mid, hi - 1), lo + 1);
+        if (i > 0) t[i] = max(t[i], t[i - 1]);
+    }
+}
+
 // A warp's sum of a block's rows: lane l holds channels 8 (l % (D / 8)) + 0 .. 7 of it, all lanes with the
 // same channels the same.  `row(r)` gives the address of the lane's 16 bytes of row r < count.
 template <int D, bool BF16, typename Row>

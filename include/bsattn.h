@@ -435,7 +435,7 @@ int bsattn_index_update(const void* k_pages, const int32_t* cache_seqlens, const
  *   block_indices  (device) [B, Hkv, max_sel] int32, fully written: the chosen blocks in rising order, then -1
  * sinks + recent <= max_sel (else BSATTN_ERR_INVALID_ARG).  Blocks on pages out of range are not chosen, a
  * length past the table is taken as the table's, a negative one as 0; all are flagged BSATTN_ERR_BAD_INDEX.
- * Requires Hq / Hkv <= 8, d in {64, 128}, max_pages_per_seq * page_size <= 3276800.  block_indices shares no
+ * Requires Hq / Hkv <= 8, d in {64, 128}, max_pages_per_seq * page_size <= 3000000.  block_indices shares no
  * memory with the inputs.  Workspace: a status word.
  */
 int bsattn_decode_select(const void* q, const int8_t* codes, const float* scales, const int32_t* cache_seqlens,

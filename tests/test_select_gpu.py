@@ -228,6 +228,25 @@ def test_select_extreme_scores(bsa):
                 assert (got[b] == 3).any(-1).all() and (got[b] == 41).any(-1).all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_select_largest_products(bsa, d):
+    """Codes at both ends of their range, so that sums are as large as they get, and scores one apart."""
+    g = torch.Generator().manual_seed(d)
+    codes = torch.full((60, 1, 2, d), 127, dtype=torch.int8)
+    codes[20:40] = -127
+    codes[40:] = torch.where(torch.rand(20, 1, 2, d, generator=g) < 0.5, 127, -127).to(torch.int8)
+    for j in range(60):                                     # one less in one channel
+        codes[j, 0, :, j % d] -= torch.sign(codes[j, 0, :, j % d]) * (j % 3)
+    index = bsa.BlockIndex(codes.cuda(), torch.ones(60, 1, 2, device="cuda"))
+    table = _i32([list(range(60))] * 3)
+    q = torch.ones(3, 16, d, dtype=BF16, device="cuda")
+    q[1] = -1
+    q[2] = torch.where(_rand(16, d, dtype=BF16, seed=d) < 0, -1.0, 1.0).to(BF16)
+    q[:, 3, ::2] *= 0.5
+    for k in (1, 7, 10, 21, 33, 59):
+        _check_select(bsa, q, index, [60 * 64] * 3, table, k, 0, 0)
+
+
 def test_select_reports_what_is_out_of_range(bsa):
     index = _random_index(bsa, 20, 1, 2, 64, seed=5)
     q = _rand(4, 4, 64, dtype=F16, seed=6)
@@ -252,14 +271,14 @@ def test_select_long(bsa, d, page):
     index = _random_index(bsa, pages, page // 64, 2, d, seed=7)
     q = _rand(2, 8, d, dtype=BF16, seed=8)
     _check_select(bsa, q, index, lens, _table(lens, page, pages, 6), 200, 1, 4)
-    width = 51200 * 64 // page
+    width = 3_000_000 // page
     wide = torch.arange(width, dtype=torch.int32, device="cuda").remainder(pages).repeat(2, 1)
     got = bsa.bsattn_decode_select(q, index, _i32([width * page, 10]), wide, 100, 1, 1)
     # every summary is there many times: of equal scores the lower block
     whole = ref.select(q[:1].cpu(), index.codes.cpu(), index.scales.cpu(), [pages * page], wide[:1, :pages].cpu(), 100, 0, 0, page)
     times = -(-width // pages)
     best = [j for j in whole[0, 0].tolist()]
-    assert got[0, 0, 0] == 0 and got[0, 0, -1] == 51199
+    assert got[0, 0, 0] == 0 and got[0, 0, -1] == width * page // 64 - 1
     assert {int(j) % (pages * page // 64) for j in got[0, 0, 1:-1].tolist()} <= set(best) | {0} and times > 1
     assert got[1, 0].tolist() == [0] + [-1] * 99
 

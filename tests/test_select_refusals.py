@@ -57,8 +57,8 @@ def test_select_refuses(kw):
     assert _call("select", **kw) == INVALID
 
 
-@pytest.mark.parametrize("kw", [dict(Hq=18), dict(page=32), dict(d=32), dict(dtype=-1), dict(max_pages=51201),
-                                dict(page=128, max_pages=25601), dict(max_sel=1 << 27)])
+@pytest.mark.parametrize("kw", [dict(Hq=18), dict(page=32), dict(d=32), dict(dtype=-1), dict(max_pages=46876),
+                                dict(page=128, max_pages=23438), dict(max_sel=1 << 27)])
 def test_select_does_not_support(kw):
     assert _call("select", **kw) == UNSUPPORTED
 
