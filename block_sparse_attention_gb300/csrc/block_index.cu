@@ -4,9 +4,11 @@
 // rows in the cache (summary.cuh): codes [pages, page_size / 64, Hkv, d] and a scale for each block and head.
 //
 // Each row is read once and 1/128 of it written, so HBM bandwidth bounds this, and for the few blocks of a
-// decode step a chain of latencies.  A warp takes a (block, kv head), a warp's next to its neighbour's head,
-// as rows of neighbouring heads lie next to each other: sixteen 16-byte loads a lane in flight.
+// decode step a chain of latencies.  A warp takes a (block, kv head), its neighbour the next head, as rows of
+// neighbouring heads lie next to each other.  The lanes look up where 32 of a warp's blocks lie at once, and the
+// warp has the rows of two (d = 64: four) on their way while it adds up another's.
 #include <algorithm>
+#include <climits>
 
 #include "host_internal.h"
 #include "summary.cuh"
@@ -14,8 +16,10 @@
 namespace bsattn {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kWarps = 7;                       // 32 KB of shared memory each
+constexpr int kThreads = 32 * kWarps;
+constexpr int kStretches = 256;                 // of sequences, a thread each; the last ones are empty
+static_assert(kThreads <= kStretches, "a thread a stretch");
 
 struct UpdateParams {
     const void* k;
@@ -50,10 +54,12 @@ __device__ __forceinline__ Touched touched(const UpdateParams& p, int b) {
 }
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kThreads) update_kernel(const UpdateParams p) {
+__global__ void __launch_bounds__(kThreads, 1) update_kernel(const UpdateParams p) {
+    using Ring = BlockRing<D>;
+    extern __shared__ __align__(128) uint8_t ring_smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // thread t has the blocks of its stretch of sequences; upto[t]: of all stretches to its end
-    __shared__ long long upto[kThreads];
+    __shared__ long long upto[kStretches];
     __shared__ long long warp_sums[kWarps];
     const int per = (p.B + kThreads - 1) / kThreads;
     long long sum = 0;
@@ -73,69 +79,100 @@ __global__ void __launch_bounds__(kThreads) update_kernel(const UpdateParams p) 
     __syncthreads();
     for (int w = 0; w < warp; ++w) sum += warp_sums[w];
     upto[tid] = sum;
+    if (tid + kThreads < kStretches) upto[tid + kThreads] = LLONG_MAX;
     __syncthreads();
     const long long tasks = upto[kThreads - 1] * p.Hkv;
     const int blocks_a_page = p.page_size / kBlockRows;
+    const long long stride = static_cast<long long>(gridDim.x) * kWarps;
+    const long long step = static_cast<long long>(p.Hkv) * D * 2;
+    const Ring ring(ring_smem + warp * Ring::kBytes);
     bool bad = false;
-    for (long long task = static_cast<long long>(blockIdx.x) * kWarps + warp; task < tasks;
-         task += static_cast<long long>(gridDim.x) * kWarps) {
-        long long nth;
-        int g;
-        if (tasks <= 0xffffffffLL) {
-            const uint32_t q = static_cast<uint32_t>(task) / static_cast<uint32_t>(p.Hkv);
-            nth = q;
-            g = static_cast<int>(static_cast<uint32_t>(task) - q * static_cast<uint32_t>(p.Hkv));
-        } else {
-            nth = task / p.Hkv;
-            g = static_cast<int>(task - nth * p.Hkv);
-        }
-        // the first stretch that ends past it
-        int at = 0;
+    for (long long base = static_cast<long long>(blockIdx.x) * kWarps + warp; base < tasks; base += 32 * stride) {
+        // ---------------------------------------------------------------- lane l: where the warp's l-th block lies
+        const long long task = base + lane * stride;
+        int of_block = -1, count = 0;                       // its place in the index over Hkv, and its rows
+        int g = 0;
+        if (task < tasks) {
+            long long nth;
+            if (tasks <= 0xffffffffLL) {
+                const uint32_t q = static_cast<uint32_t>(task) / static_cast<uint32_t>(p.Hkv);
+                nth = q;
+                g = static_cast<int>(static_cast<uint32_t>(task) - q * static_cast<uint32_t>(p.Hkv));
+            } else {
+                nth = task / p.Hkv;
+                g = static_cast<int>(task - nth * p.Hkv);
+            }
+            // the first stretch that ends past it
+            int at = 0;
 #pragma unroll
-        for (int step = kThreads / 2; step > 0; step >>= 1)
-            if (upto[at + step - 1] <= nth) at += step;
-        long long before = at > 0 ? upto[at - 1] : 0;
-        int b = at * per;
-        Touched t = touched(p, b);
-        while (nth >= before + t.n) {
-            before += t.n;
-            t = touched(p, ++b);
+            for (int half = kStretches / 2; half > 0; half >>= 1)
+                if (upto[at + half - 1] <= nth) at += half;
+            long long before = at > 0 ? upto[at - 1] : 0;
+            int b = at * per;
+            Touched t = touched(p, b);
+            while (nth >= before + t.n) {
+                before += t.n;
+                t = touched(p, ++b);
+            }
+            const int block = t.first + static_cast<int>(nth - before);
+            const int lp = block / blocks_a_page, sub = block - lp * blocks_a_page;
+            const int page = p.table[static_cast<size_t>(b) * p.max_pages + lp];
+            if (page < 0 || page >= p.num_pages) {
+                bad = true;
+            } else {
+                of_block = page * blocks_a_page + sub;
+                count = min(t.len - block * kBlockRows, kBlockRows);
+            }
         }
-        const int block = t.first + static_cast<int>(nth - before);
-        const int lp = block / blocks_a_page, sub = block - lp * blocks_a_page;
-        const int page = p.table[static_cast<size_t>(b) * p.max_pages + lp];
-        if (page < 0 || page >= p.num_pages) {
-            bad = true;
-            continue;
-        }
-        const int count = min(t.len - block * kBlockRows, kBlockRows);
-        const size_t row0 = static_cast<size_t>(page) * p.page_size + sub * kBlockRows;
-        const uint16_t* src = static_cast<const uint16_t*>(p.k) + (row0 * p.Hkv + g) * D + 8 * (lane % (D / 8));
-        float s[8];
-        block_sum<D, BF16>([&](int r) { return reinterpret_cast<const uint4*>(src + static_cast<size_t>(r) * p.Hkv * D); },
-                           count, s);
-        int code[8];
-        const float scale = summarise<D>(s, count, code);
-        const size_t to = (static_cast<size_t>(page) * blocks_a_page + sub) * p.Hkv + g;
-        if (lane < D / 8) {
-            uint32_t w[2];
+        const int n = static_cast<int>(min((tasks - base + stride - 1) / stride, 32LL));
+        // ---------------------------------------------------------------- the blocks one after another
+        const auto fetch = [&](int m) {
+            const int at = __shfl_sync(0xffffffffu, of_block, m & 31), head = __shfl_sync(0xffffffffu, g, m & 31);
+            const int rows = __shfl_sync(0xffffffffu, count, m & 31);
+            if (m < n && at >= 0)
+                ring.fetch(m % Ring::kDepth, static_cast<const char*>(p.k) +
+                           (static_cast<size_t>(at) * kBlockRows * p.Hkv + head) * (D * 2) + 16 * (lane % (D / 8)), step, rows);
+            Ring::commit();
+        };
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                w[h] = (code[4 * h] & 255) | (code[4 * h + 1] & 255) << 8 | (code[4 * h + 2] & 255) << 16 |
-                       static_cast<uint32_t>(code[4 * h + 3]) << 24;
-            *reinterpret_cast<uint2*>(p.codes + to * D + 8 * lane) = make_uint2(w[0], w[1]);
-            if (lane == 0) p.scales[to] = scale;
+        for (int m = 0; m < Ring::kDepth; ++m) fetch(m);
+        for (int m = 0; m < n; ++m) {
+            const int at = __shfl_sync(0xffffffffu, of_block, m), head = __shfl_sync(0xffffffffu, g, m);
+            const int rows = __shfl_sync(0xffffffffu, count, m);
+            Ring::wait();
+            if (at >= 0) {
+                float s[8];
+                ring.template sum<BF16>(m % Ring::kDepth, s);
+                int code[8];
+                const float scale = summarise<D>(s, rows, code);
+                const size_t to = static_cast<size_t>(at) * p.Hkv + head;
+                if (lane < D / 8) {
+                    uint32_t w[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        w[h] = (code[4 * h] & 255) | (code[4 * h + 1] & 255) << 8 | (code[4 * h + 2] & 255) << 16 |
+                               static_cast<uint32_t>(code[4 * h + 3]) << 24;
+                    *reinterpret_cast<uint2*>(p.codes + to * D + 8 * lane) = make_uint2(w[0], w[1]);
+                    if (lane == 0) p.scales[to] = scale;
+                }
+            }
+            fetch(m + Ring::kDepth);
         }
     }
-    if (bad && lane == 0) atomicOr(p.status, BSATTN_ERR_BAD_INDEX);
+    if (bad) atomicOr(p.status, BSATTN_ERR_BAD_INDEX);
 }
 
 template <int D, bool BF16>
 int launch(const UpdateParams& prm, int sms, cudaStream_t st) {
-    // a warp a task, and no more CTAs than the GPU holds at once (three an SM)
+    auto kern = update_kernel<D, BF16>;
+    constexpr int kSmem = kWarps * BlockRing<D>::kBytes;
+    static std::atomic<unsigned long long> raised{0};
+    const int rc = raise_smem_limit(reinterpret_cast<const void*>(kern), kSmem, raised);
+    if (rc) return rc;
+    // a warp a task, and no more CTAs than the GPU holds at once
     const long long most = static_cast<long long>(prm.B) * prm.max_pages * (prm.page_size / kBlockRows) * prm.Hkv;
-    const long long grid = std::min<long long>((most + kWarps - 1) / kWarps, 3LL * sms);
-    update_kernel<D, BF16><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(prm);
+    const long long grid = std::min<long long>((most + kWarps - 1) / kWarps, sms);
+    kern<<<static_cast<unsigned>(grid), kThreads, kSmem, st>>>(prm);
     return cudaGetLastError() == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
 }
 

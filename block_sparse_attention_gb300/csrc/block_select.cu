@@ -21,7 +21,7 @@ namespace {
 
 // ------------------------------------------------------------------------------------------ decode
 //
-// A CTA a (sequence, kv head), of as many threads as leave room for all of them at once.
+// A (sequence, kv head) is a CTA's, or that of a cluster whose CTAs have a stretch of its blocks each.
 // A warp scores 16 blocks at a time, S [16 blocks x 8 heads] = K Q^T by mma.sync m16n8k16 in fp16: a code c enters
 // as 1152 + c, which takes one byte permutation for two codes (1024 + byte is an fp16 number with that byte for its
 // lowest), and the sums begin at -1152 times the query's codes.  Whole numbers below 2^23 in magnitude throughout, 32
@@ -30,8 +30,8 @@ namespace {
 // Which channel a matrix index stands for is free, so a lane reads D / 4 consecutive codes of a row.  Keys stay in
 // shared memory, the first kHeld of a thread in registers.  A trip of the search counts at four thresholds at once:
 // a count is mostly the way through the barrier.
-// The index is read once, which bounds a large batch; a small one is a chain of latencies: lengths, table, index,
-// then the counts.
+// The index is read once, but instructions bound a batch and the SMs that work a few long sequences; a single short
+// one is a chain of latencies: lengths, table, index, then the counts.
 
 constexpr int kMaxBlocks = 46875;               // of a sequence: their keys lie in shared memory
 constexpr int kHeld = 8;                        // keys of a thread in registers
@@ -47,12 +47,32 @@ struct SelectParams {
     int Hq, Hkv, page_size, max_pages, num_pages, max_sel, sinks, recent;
 };
 
-// What the CTA's warps add up.
+// What the CTA's warps add up, or the cluster's CTAs.
 struct Shares {
     uint32_t range[2];                          // largest of ~key, and of key
     int there, forced;                          // blocks that may be chosen, blocks that have to be
     int counts[3][4];
 };
+
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t n;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+    return n;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// The word of CTA `rank` that stands where `mine` does here.
+__device__ __forceinline__ uint32_t word_of(const void* mine, uint32_t rank) {
+    uint32_t at;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(mine)), "r"(rank));
+    return at;
+}
+__device__ __forceinline__ void add_to(uint32_t at, uint32_t v) {
+    asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+__device__ __forceinline__ void max_to(uint32_t at, uint32_t v) {
+    asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
 
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
@@ -61,23 +81,24 @@ __device__ __forceinline__ void copy4(uint32_t to, const void* from) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
 }
 
-// Times 16 blocks whose index rows a warp has on their way.
-__host__ __device__ constexpr int depth_of(int threads) { return threads > 512 ? 2 : 4; }
+constexpr int kDepth = 4;                       // times 16 blocks whose index rows a warp has on their way
+constexpr int kMaxCluster = 8;
 
 template <int D, bool BF16, int TH>
 __global__ void __launch_bounds__(TH, TH == 128 ? 4 : 1) select_kernel(const SelectParams p) {
-    constexpr int kWarps = TH / 32, kDepth = depth_of(TH);
-    constexpr bool kLean = TH > 512;                        // no registers for the queries' operands
+    constexpr int kWarps = TH / 32;
     constexpr int kSteps = D / 16, kSums = kSteps / 2;      // k16 steps, and sums of two of them
     constexpr uint32_t kGroup = 16 * D + 64;                // 16 index rows: codes, scales
     extern __shared__ __align__(16) uint8_t sel_smem[];
     uint32_t* keys = reinterpret_cast<uint32_t*>(sel_smem + kWarps * kDepth * kGroup);   // of the CTA's blocks; first their index rows
     __shared__ uint2 qb[kSteps][32];                        // the queries' codes as a lane's operands, head lane / 4
     __shared__ float qscale[8], qbase[kSums][8];            // of the query heads: scale, where sums begin
-    __shared__ Shares sh;
+    __shared__ Shares own, all;                             // the CTA's, the cluster's
     __shared__ int above[kWarps], level[kWarps];
+    __shared__ int at_rank[2][kMaxCluster];                 // chosen blocks of each CTA: above the threshold, at it
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int row = static_cast<int>(blockIdx.x), b = row / p.Hkv, g = row - b * p.Hkv, G = p.Hq / p.Hkv;
+    const int CL = static_cast<int>(cluster_size()), rank = static_cast<int>(blockIdx.x) % CL;
+    const int row = static_cast<int>(blockIdx.x) / CL, b = row / p.Hkv, g = row - b * p.Hkv, G = p.Hq / p.Hkv;
 
     const int asked = p.seqlens[b];
     // a warp a query head: its codes and scale
@@ -127,8 +148,15 @@ __global__ void __launch_bounds__(TH, TH == 128 ? 4 : 1) select_kernel(const Sel
     const int blocks_a_page = p.page_size / kBlockRows;
     const int room = p.max_pages * blocks_a_page;
     const bool far = asked < 0 || asked > static_cast<long long>(p.max_pages) * p.page_size;
-    const int n = asked <= 0 ? 0 : min(asked / kBlockRows + (asked % kBlockRows != 0), room);
-    for (int i = tid; i < static_cast<int>(sizeof(Shares) / 4); i += TH) reinterpret_cast<uint32_t*>(&sh)[i] = 0;
+    const int all_n = asked <= 0 ? 0 : min(asked / kBlockRows + (asked % kBlockRows != 0), room);
+    // the CTA's blocks: n from block0 on
+    const int each = ((all_n + CL - 1) / CL + 15) & ~15;
+    const int block0 = min(rank * each, all_n), n = min(each, all_n - block0);
+    if (tid < static_cast<int>(sizeof(Shares) / 4)) {
+        reinterpret_cast<uint32_t*>(&own)[tid] = 0;
+        reinterpret_cast<uint32_t*>(&all)[tid] = 0;
+    }
+    if (CL > 1) cluster_arrive();                           // what the others add to is 0
     // (heads that there are not: codes 0)
     for (int i = tid; i < kSteps * 32; i += TH)
         if (i % 32 / 4 >= G) qb[i / 32][i % 32] = make_uint2(0, 0);
@@ -136,7 +164,7 @@ __global__ void __launch_bounds__(TH, TH == 128 ? 4 : 1) select_kernel(const Sel
     // the index row of each block, or -1
     bool bad = far;
     for (int i = tid; i < n; i += TH) {
-        const int j = i, lp = j / blocks_a_page;
+        const int j = block0 + i, lp = j / blocks_a_page;
         const int page = __ldg(p.table + static_cast<size_t>(b) * p.max_pages + lp);
         const bool in = page >= 0 && page < p.num_pages;
         bad = bad || !in;
@@ -147,7 +175,7 @@ __global__ void __launch_bounds__(TH, TH == 128 ? 4 : 1) select_kernel(const Sel
 
     // ---------------------------------------------------------------- scores
     {
-        const int first_recent = max(n - p.recent, 0);
+        const int first_recent = max(all_n - p.recent, 0);
         const int r8 = lane >> 2, j4 = lane & 3, h0 = 2 * j4;
         float sq[2];
 #pragma unroll
@@ -177,10 +205,10 @@ __global__ void __launch_bounds__(TH, TH == 128 ? 4 : 1) select_kernel(const Sel
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        uint2 q2[kLean ? 1 : kSteps];
+        uint2 q2[kSteps];
         float2 begin[kSums];
 #pragma unroll
-        for (int k = 0; k < (kLean ? 1 : kSteps); ++k) q2[k] = qb[k][lane];
+        for (int k = 0; k < kSteps; ++k) q2[k] = qb[k][lane];
 #pragma unroll
         for (int k = 0; k < kSums; ++k) begin[k] = *reinterpret_cast<const float2*>(&qbase[k][h0]);
 #pragma unroll
@@ -216,8 +244,7 @@ __global__ void __launch_bounds__(TH, TH == 128 ? 4 : 1) select_kernel(const Sel
                     a[e] = __byte_perm(w, 0x64646464u, 0x4140);
                     a[e + 2] = __byte_perm(w, 0x64646464u, 0x4342);
                 }
-                if constexpr (kLean) q2[0] = qb[k][lane];
-                mma16::mma16816<false>(c[k / 2], a, q2[kLean ? 0 : k].x, q2[kLean ? 0 : k].y);
+                mma16::mma16816<false>(c[k / 2], a, q2[k].x, q2[k].y);
             }
             float best[2];
 #pragma unroll
@@ -237,7 +264,7 @@ __global__ void __launch_bounds__(TH, TH == 128 ? 4 : 1) select_kernel(const Sel
                 uint32_t key = 0;
                 if (keys[i] != 0xffffffffu) {
                     ++there;
-                    if (i < p.sinks || i >= first_recent) {
+                    if (block0 + i < p.sinks || block0 + i >= first_recent) {
                         key = kForced;
                         there += 1 << 16;
                     } else {
@@ -256,17 +283,30 @@ __global__ void __launch_bounds__(TH, TH == 128 ? 4 : 1) select_kernel(const Sel
         least = __reduce_max_sync(0xffffffffu, least);
         most = __reduce_max_sync(0xffffffffu, most);
         if (lane == 0) {
-            atomicMax(&sh.range[0], least);
-            atomicMax(&sh.range[1], most);
-            atomicAdd(&sh.there, there & 0xffff);
-            atomicAdd(&sh.forced, there >> 16);
+            atomicMax(&own.range[0], least);
+            atomicMax(&own.range[1], most);
+            atomicAdd(&own.there, there & 0xffff);
+            atomicAdd(&own.forced, there >> 16);
         }
     }
     __syncthreads();
+    Shares& sh = CL > 1 ? all : own;
+    if (CL > 1) {
+        cluster_wait();
+        // a lane a word of a CTA
+        if (warp == 0 && lane / 4 < CL) {
+            const uint32_t v = reinterpret_cast<const uint32_t*>(&own)[lane & 3];
+            const uint32_t to = word_of(reinterpret_cast<const uint32_t*>(&all) + (lane & 3), lane / 4);
+            if (lane & 2) add_to(to, v);
+            else max_to(to, v);
+        }
+        cluster_arrive();
+        cluster_wait();
+    }
 
     // ---------------------------------------------------------------- the score that max_sel blocks reach
     uint32_t lo = 1;
-    int spare = n;                                          // places for blocks whose score is lo itself
+    int spare = all_n;                                      // places for blocks whose score is lo itself
     const int there = sh.there;
     if (there > p.max_sel) {
         int c_hi = sh.forced;
@@ -294,13 +334,19 @@ __global__ void __launch_bounds__(TH, TH == 128 ? 4 : 1) select_kernel(const Sel
                     count(held[i]);
                 }
                 for (int i = kHeld * TH + tid; i < n; i += TH) count(keys[i]);
-                int* to = sh.counts[step % 3];
+                int* to = own.counts[step % 3];
                 const int s0 = __reduce_add_sync(0xffffffffu, c[0]), s1 = __reduce_add_sync(0xffffffffu, c[1]);
                 if (lane < 4) {
                     const int s = lane & 2 ? s1 : s0, v = lane & 1 ? s >> 16 : s & 0xffff;
                     if (v) atomicAdd(&to[lane], v);
                 }
                 __syncthreads();
+                if (CL > 1) {
+                    if (warp == 0 && lane / 4 < CL) add_to(word_of(&all.counts[step % 3][lane & 3], lane / 4), to[lane & 3]);
+                    cluster_arrive();
+                    cluster_wait();
+                    to = all.counts[step % 3];
+                }
                 // the last threshold that max_sel blocks reach, and the first that fewer do
                 int now[4];
 #pragma unroll
@@ -318,7 +364,7 @@ __global__ void __launch_bounds__(TH, TH == 128 ? 4 : 1) select_kernel(const Sel
                         c_hi = now[i];
                     }
                 // everybody has read the counts of the trip before, which are those of the trip after next
-                if (tid < 4) sh.counts[(step + 2) % 3][tid] = 0;
+                if (tid < 4) own.counts[(step + 2) % 3][tid] = all.counts[(step + 2) % 3][tid] = 0;
             }
             if (c_lo != p.max_sel) spare = p.max_sel - c_hi;
         }
@@ -341,6 +387,21 @@ __global__ void __launch_bounds__(TH, TH == 128 ? 4 : 1) select_kernel(const Sel
     }
     __syncthreads();
     int over_before = 0, equal_before = 0;
+    if (CL > 1) {
+        if (warp == 0) {
+            const int o = __reduce_add_sync(0xffffffffu, lane < kWarps ? above[lane] : 0);
+            const int e = __reduce_add_sync(0xffffffffu, lane < kWarps ? level[lane] : 0);
+            if (lane < 2 * CL)
+                asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(word_of(&at_rank[lane & 1][rank], lane >> 1)), "r"(lane & 1 ? e : o)
+                             : "memory");
+        }
+        cluster_arrive();
+        cluster_wait();
+        for (int r = 0; r < rank; ++r) {
+            over_before += at_rank[0][r];
+            equal_before += at_rank[1][r];
+        }
+    }
     for (int w = 0; w < warp; ++w) {
         over_before += above[w];
         equal_before += level[w];
@@ -353,25 +414,34 @@ __global__ void __launch_bounds__(TH, TH == 128 ? 4 : 1) select_kernel(const Sel
         const uint32_t is_equal = __ballot_sync(0xffffffffu, key == lo);
         const int eq = equal_before + __popc(is_equal & below);
         const int at = over_before + __popc(is_over & below) + min(eq, spare);
-        if (key > lo || (key == lo && eq < spare)) out[at] = j + lane;
+        if (key > lo || (key == lo && eq < spare)) out[at] = block0 + j + lane;
         over_before += __popc(is_over);
         equal_before += __popc(is_equal);
     }
     // (the last warp has passed all blocks)
-    if (warp == kWarps - 1)
+    if (rank == CL - 1 && warp == kWarps - 1)
         for (int j = over_before + min(equal_before, spare) + lane; j < p.max_sel; j += 32) out[j] = -1;
 }
 
 template <int D, bool BF16, int TH>
-int launch_select(const SelectParams& prm, long long rows, cudaStream_t st) {
+int launch_select(const SelectParams& prm, long long rows, int cluster, cudaStream_t st) {
     auto kern = select_kernel<D, BF16, TH>;
     const int blocks = prm.max_pages * (prm.page_size / kBlockRows);
     static std::atomic<unsigned long long> raised{0};
     int rc = raise_smem_limit(reinterpret_cast<const void*>(kern), 224 * 1024, raised);
     if (rc) return rc;
-    const size_t smem = TH / 32 * depth_of(TH) * (16 * D + 64) + 4 * static_cast<size_t>(blocks);
-    kern<<<static_cast<unsigned>(rows), TH, smem, st>>>(prm);
-    return cudaGetLastError() == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(rows * cluster));
+    cfg.blockDim = dim3(TH);
+    cfg.dynamicSmemBytes = TH / 32 * kDepth * (16 * D + 64) + 4 * static_cast<size_t>(((blocks + cluster - 1) / cluster + 15) & ~15);
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = static_cast<unsigned>(cluster);
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, prm) == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
 }
 
 template <int D, bool BF16>
@@ -380,10 +450,20 @@ int select(const SelectParams& prm, int B, cudaStream_t st) {
     if (sms <= 0) sms = 148;
     const long long rows = static_cast<long long>(B) * prm.Hkv;
     const int blocks = prm.max_pages * (prm.page_size / kBlockRows);
-    // many threads where a row has an SM to itself; the rings of many and the keys of many blocks do not both fit
-    if (rows <= sms && blocks <= 16384) return launch_select<D, BF16, 1024>(prm, rows, st);
-    if (rows <= 2 * sms && blocks <= 16384) return launch_select<D, BF16, 512>(prm, rows, st);
-    return launch_select<D, BF16, 128>(prm, rows, st);
+    // Where a row can have an SM to itself, a CTA has 512 threads, and a cluster as many SMs as there are, with 512
+    // blocks a CTA at least (1 sequence of 8192 blocks, 8 kv heads: 13.6 us by 8 CTAs, 35.3 by one; of 1024 blocks
+    // 11.2 by two, 10.3 by one, and 11.4 to 13.9 at 2048).  With few blocks the way through its barriers is longer
+    // than the counts (100 blocks: 6.6 us, 5.5 by 128 threads; 257: 7.3 and 7.0; 512: 8.7 and 9.4).
+    int cluster = 1;
+    if (rows <= sms && blocks > 384) {
+        while (cluster < kMaxCluster && rows * cluster * 2 <= sms && blocks >= 1024 * cluster) cluster *= 2;
+        // (the rings of many warps and the keys of more blocks do not both fit)
+        if (blocks <= 16384 * cluster) return launch_select<D, BF16, 512>(prm, rows, cluster, st);
+    }
+    // Small CTAs, four an SM: 192 rows of 512 blocks take 11.3 us, 15.5 by 512 threads.  Two to a row where they are
+    // at once on the GPU and long (192 rows of 2048 blocks: 23.8 us, 29.5 by one; but 304 of 1024 19.9 and 18.3).
+    cluster = rows * 2 <= 4 * sms && blocks >= 2048 ? 2 : 1;
+    return launch_select<D, BF16, 128>(prm, rows, cluster, st);
 }
 
 // ------------------------------------------------------------------------------------------ prompts
@@ -393,7 +473,8 @@ int select(const SelectParams& prm, int B, cudaStream_t st) {
 // numbers: exact), keys of the 16 rows in shared memory, then a warp a row to find its threshold and write
 // its bytes.  Under the causal rule a CTA goes no further than its rows see.
 
-constexpr int kMaskThreads = 512;
+constexpr int kSumThreads = 7 * 32;      // 32 KB of shared memory a warp
+constexpr int kMaskThreads = 256;
 constexpr int kMaskWarps = kMaskThreads / 32;
 
 struct MaskParams {
@@ -405,42 +486,67 @@ struct MaskParams {
     uint8_t* mask;
     int B, topk, sinks, recent, dense, causal;
     int rows;                            // query blocks of a CTA: 16, or 8 where 16 rows of keys do not fit
-    int pitch;                           // keys of a row, a multiple of 128
+    int pitch;                           // keys of a row: a multiple of 128, and 8 for the banks
+    int wide;                            // four bytes of the mask can be written at once
 };
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(256) summarise_kernel(const MaskParams p) {
+__global__ void __launch_bounds__(kSumThreads, 1) summarise_kernel(const MaskParams p) {
+    using Ring = BlockRing<D>;
+    extern __shared__ __align__(128) uint8_t ring_smem[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int lane = threadIdx.x & 31;
-    long long task = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const long long of_q = static_cast<long long>(p.B) * p.H[0] * p.n[0];
-    const int t = task < of_q ? 0 : 1;
-    if (t) task -= of_q;
-    const int H = p.H[t], n = p.n[t];
-    if (task >= static_cast<long long>(p.B) * H * n) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t of_q = static_cast<uint32_t>(p.B) * p.H[0] * p.n[0];
+    const uint32_t tasks = of_q + static_cast<uint32_t>(p.B) * p.H[1] * p.n[1];
+    const uint32_t stride = gridDim.x * (kSumThreads / 32);
+    const Ring ring(ring_smem + warp * Ring::kBytes);
+    struct Task {
+        int t, b, h, j, count;
+    };
     // neighbouring heads next to each other: in a projection's output their rows are neighbours
-    const uint32_t u = static_cast<uint32_t>(task);
-    const int h = static_cast<int>(u % static_cast<uint32_t>(H));
-    const uint32_t r = u / static_cast<uint32_t>(H);
-    const int j = static_cast<int>(r % static_cast<uint32_t>(n)), b = static_cast<int>(r / static_cast<uint32_t>(n));
-    const int count = min(p.S[t] - j * kBlockRows, kBlockRows);
-    const uint16_t* src = static_cast<const uint16_t*>(p.x[t]) + b * p.sb[t] + h * p.sh[t] +
-                          static_cast<long long>(j) * kBlockRows * p.ss[t] + 8 * (lane % (D / 8));
-    const long long step = p.ss[t];
-    float s[8];
-    block_sum<D, BF16>([&](int row) { return reinterpret_cast<const uint4*>(src + row * step); }, count, s);
-    int code[8];
-    const float scale = summarise<D>(s, count, code);
-    const size_t to = (static_cast<size_t>(b) * H + h) * n + j;
-    if (lane < D / 8) {
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 v = __floats2bfloat162_rn(static_cast<float>(code[2 * e]), static_cast<float>(code[2 * e + 1]));
-            w[e] = *reinterpret_cast<const uint32_t*>(&v);
+    const auto task_of = [&](uint32_t u) {
+        Task k;
+        k.t = u < of_q ? 0 : 1;
+        if (k.t) u -= of_q;
+        const uint32_t r = u / static_cast<uint32_t>(p.H[k.t]);
+        k.h = static_cast<int>(u - r * p.H[k.t]);
+        k.b = static_cast<int>(r / static_cast<uint32_t>(p.n[k.t]));
+        k.j = static_cast<int>(r - static_cast<uint32_t>(k.b) * p.n[k.t]);
+        k.count = min(p.S[k.t] - k.j * kBlockRows, kBlockRows);
+        return k;
+    };
+    const auto fetch = [&](uint32_t u, int stage) {
+        if (u < tasks) {
+            const Task k = task_of(u);
+            const uint16_t* src = static_cast<const uint16_t*>(p.x[k.t]) + k.b * p.sb[k.t] + k.h * p.sh[k.t] +
+                                  static_cast<long long>(k.j) * kBlockRows * p.ss[k.t] + 8 * (lane % (D / 8));
+            ring.fetch(stage, reinterpret_cast<const char*>(src), 2 * p.ss[k.t], k.count);
         }
-        *reinterpret_cast<uint4*>(p.codes[t] + to * D + 8 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
-        if (lane == 0) p.scales[t][to] = scale;
+        Ring::commit();
+    };
+    // (fewer than 2^31 tasks, and a stride below 2^16: nothing wraps)
+    uint32_t u = blockIdx.x + gridDim.x * warp, ahead = u;
+#pragma unroll
+    for (int m = 0; m < Ring::kDepth; ++m, ahead += stride) fetch(ahead, m);
+    for (int stage = 0; u < tasks; u += stride, ahead += stride, stage = (stage + 1) % Ring::kDepth) {
+        Ring::wait();
+        const Task k = task_of(u);
+        float s[8];
+        ring.template sum<BF16>(stage, s);
+        fetch(ahead, stage);
+        int code[8];
+        const float scale = summarise<D>(s, k.count, code);
+        const size_t to = (static_cast<size_t>(k.b) * p.H[k.t] + k.h) * p.n[k.t] + k.j;
+        if (lane < D / 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 v = __floats2bfloat162_rn(static_cast<float>(code[2 * e]), static_cast<float>(code[2 * e + 1]));
+                w[e] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            *reinterpret_cast<uint4*>(p.codes[k.t] + to * D + 8 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (lane == 0) p.scales[k.t][to] = scale;
+        }
     }
 }
 
@@ -452,7 +558,7 @@ __device__ __forceinline__ void mma_whole(float (&c)[4], const uint32_t (&a)[4],
 }
 
 template <int D>
-__global__ void __launch_bounds__(kMaskThreads) mask_kernel(const MaskParams p) {
+__global__ void __launch_bounds__(kMaskThreads, 2) mask_kernel(const MaskParams p) {
     extern __shared__ __align__(16) uint32_t keys[];        // [rows][pitch]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int nq = p.n[0], nk = p.n[1];
@@ -494,20 +600,30 @@ __global__ void __launch_bounds__(kMaskThreads) mask_kernel(const MaskParams p) 
             sq[half] = s == INFINITY ? 0.f : s;             // a query block that is not finite scores 0
         }
         const size_t kbase = (static_cast<size_t>(b) * p.H[1] + kvh) * nk;
-        const int tiles = p.pitch / 8;
+        // (the padding of a row stays unwritten)
+        const int tiles = p.pitch / 8 - 1;
+        uint4 next[D / 32];                                 // the next tile's codes and scales, on their way
+        float next_scale[2];
+        const auto fetch = [&](int tile) {
+            const int c0 = 8 * tile;
+            if (c0 >= widest) return;
+            const uint4* src = reinterpret_cast<const uint4*>(p.codes[1] + (kbase + min(c0 + r8, nk - 1)) * D + j4 * (D / 4));
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) next[w] = src[w];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) next_scale[e] = p.scales[1][kbase + min(c0 + 2 * j4 + e, nk - 1)];
+        };
+        fetch(warp);
         for (int tile = warp; tile < tiles; tile += kMaskWarps) {
             const int c0 = 8 * tile;
             uint2 put[2] = {};
             if (c0 < widest) {
-                const int col = min(c0 + r8, nk - 1);
-                const uint4* src = reinterpret_cast<const uint4*>(p.codes[1] + (kbase + col) * D + j4 * (D / 4));
+                float c[4] = {};
+                const float sk[2] = {next_scale[0], next_scale[1]};
                 uint4 kv[D / 32];
 #pragma unroll
-                for (int w = 0; w < D / 32; ++w) kv[w] = src[w];
-                float sk[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) sk[e] = p.scales[1][kbase + min(c0 + 2 * j4 + e, nk - 1)];
-                float c[4] = {};
+                for (int w = 0; w < D / 32; ++w) kv[w] = next[w];
+                fetch(tile + kMaskWarps);
 #pragma unroll
                 for (int w = 0; w < D / 32; ++w) {
                     mma_whole(c, a[2 * w], kv[w].x, kv[w].y);
@@ -541,24 +657,30 @@ __global__ void __launch_bounds__(kMaskThreads) mask_kernel(const MaskParams p) 
         const int n = seen(row0 + i);
         uint32_t lo = 1;
         int spare = nk;
+        // the lane's keys: four of every 128, those of the first 256 in registers; 0 where there is none
+        uint4 held[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+            held[c] = 128 * c < n ? *reinterpret_cast<const uint4*>(mine + 128 * c + 4 * lane) : make_uint4(0, 0, 0, 0);
+        const auto every = [&](const auto& f) {
+            f(held[0]);
+            if (n > 128) f(held[1]);
+            for (int j = 256 + 4 * lane; j < n; j += 128) f(*reinterpret_cast<const uint4*>(mine + j));
+        };
         if (n > p.topk) {
             uint32_t least = 0xffffffffu, most = 0;
             int forced = 0;
-            for (int j = 4 * lane; j < n; j += 128) {
-                const uint4 k4 = *reinterpret_cast<const uint4*>(mine + j);
+            every([&](const uint4& k4) {
                 const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    if (k[e] == kForced) {
-                        ++forced;
-                    } else if (k[e] != 0) {
-                        least = min(least, k[e]);
-                        most = max(most, k[e]);
-                    }
+                    forced += k[e] == kForced;
+                    if (k[e] != kForced) most = max(most, k[e]);
+                    least = min(least, k[e] - 1u);          // (0 becomes the largest)
                 }
-            }
+            });
             forced = __reduce_add_sync(0xffffffffu, forced);
-            least = __reduce_min_sync(0xffffffffu, least);
+            least = __reduce_min_sync(0xffffffffu, least) + 1u;
             most = __reduce_max_sync(0xffffffffu, most);
             if (forced >= p.topk) {
                 lo = kForced;
@@ -568,20 +690,32 @@ __global__ void __launch_bounds__(kMaskThreads) mask_kernel(const MaskParams p) 
                 uint32_t hi = most + 1;
                 int c_lo = n, c_hi = forced;
                 for (int step = 0; c_lo != p.topk && hi - lo > 1; ++step) {
-                    const uint32_t mid = between(lo, hi, step);
-                    int c = 0;
-                    for (int j = 4 * lane; j < n; j += 128) {
-                        const uint4 k4 = *reinterpret_cast<const uint4*>(mine + j);
-                        c += (k4.x >= mid) + (k4.y >= mid) + (k4.z >= mid) + (k4.w >= mid);
-                    }
-                    c = __reduce_add_sync(0xffffffffu, c);
-                    if (c >= p.topk) {
-                        lo = mid;
-                        c_lo = c;
-                    } else {
-                        hi = mid;
-                        c_hi = c;
-                    }
+                    uint32_t t[4];
+                    thresholds(lo, hi, step, t);
+                    int c[2] = {0, 0};                      // two counts each, 2^16 apart
+                    every([&](const uint4& k4) {
+                        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) c[i] += (k[e] >= t[2 * i] ? 1 : 0) + (k[e] >= t[2 * i + 1] ? 0x10000 : 0);
+                    });
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) c[i] = __reduce_add_sync(0xffffffffu, c[i]);
+                    const int now[4] = {c[0] & 0xffff, c[0] >> 16, c[1] & 0xffff, c[1] >> 16};
+                    // the last threshold that topk blocks reach, and the first that fewer do
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (now[i] >= p.topk) {
+                            lo = t[i];
+                            c_lo = now[i];
+                        }
+#pragma unroll
+                    for (int i = 3; i >= 0; --i)
+                        if (now[i] < p.topk) {
+                            hi = t[i];
+                            c_hi = now[i];
+                        }
                 }
                 if (c_lo != p.topk) spare = p.topk - c_hi;
             }
@@ -589,12 +723,30 @@ __global__ void __launch_bounds__(kMaskThreads) mask_kernel(const MaskParams p) 
         uint8_t* out = p.mask + (static_cast<size_t>(bh) * nq + row0 + i) * nk;
         const uint32_t below = (1u << lane) - 1u;
         int equal_before = 0;
-        for (int j = 0; j < nk; j += 32) {
-            const uint32_t key = j + lane < n ? mine[j + lane] : 0u;
-            const uint32_t is_equal = __ballot_sync(0xffffffffu, key == lo);
-            const bool on = key > lo || (key == lo && equal_before + __popc(is_equal & below) < spare);
-            if (j + lane < nk) out[j + lane] = on ? 1 : 0;
-            equal_before += __popc(is_equal);
+        for (int j = 4 * lane; j - 4 * lane < nk; j += 128) {
+            const uint4 k4 = j < 128 ? held[0] : j < 256 ? held[1] : j < n ? *reinterpret_cast<const uint4*>(mine + j) : make_uint4(0, 0, 0, 0);
+            const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+            uint32_t equal[4];
+            int rank = equal_before;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                equal[e] = __ballot_sync(0xffffffffu, k[e] == lo);
+                rank += __popc(equal[e] & below);
+                equal_before += __popc(equal[e]);
+            }
+            uint32_t on = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (k[e] > lo || (k[e] == lo && rank < spare)) on |= 1u << 8 * e;
+                rank += k[e] == lo;
+            }
+            if (p.wide) {
+                if (j < nk) *reinterpret_cast<uint32_t*>(out + j) = on;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (j + e < nk) out[j + e] = static_cast<uint8_t>(on >> 8 * e);
+            }
         }
     }
 }
@@ -625,11 +777,17 @@ template <int D, bool BF16>
 int launch_mask(const MaskParams& prm, cudaStream_t st) {
     const long long tasks = static_cast<long long>(prm.B) * (static_cast<long long>(prm.H[0]) * prm.n[0] +
                                                              static_cast<long long>(prm.H[1]) * prm.n[1]);
-    summarise_kernel<D, BF16><<<static_cast<unsigned>((tasks + 7) / 8), 256, 0, st>>>(prm);
-    if (cudaGetLastError() != cudaSuccess) return BSATTN_ERR_CUDA;
-    static std::atomic<unsigned long long> raised{0};
-    const int rc = raise_smem_limit(reinterpret_cast<const void*>(mask_kernel<D>), 220 * 1024, raised);
+    auto summarise = summarise_kernel<D, BF16>;
+    constexpr int kWarps = kSumThreads / 32, kSmem = kWarps * BlockRing<D>::kBytes;
+    static std::atomic<unsigned long long> raised{0}, raised_mask{0};
+    int rc = raise_smem_limit(reinterpret_cast<const void*>(summarise), kSmem, raised);
+    if (!rc) rc = raise_smem_limit(reinterpret_cast<const void*>(mask_kernel<D>), 224 * 1024, raised_mask);
     if (rc) return rc;
+    int sms = num_sms_of_current_device();
+    if (sms <= 0) sms = 148;
+    // a task a CTA first, then more
+    summarise<<<static_cast<unsigned>(std::min<long long>(tasks, sms)), kSumThreads, kSmem, st>>>(prm);
+    if (cudaGetLastError() != cudaSuccess) return BSATTN_ERR_CUDA;
     const int strips = (prm.n[0] + prm.rows - 1) / prm.rows;
     // launched while the summaries are still being made: it waits for them itself
     cudaLaunchConfig_t cfg{};
@@ -754,10 +912,11 @@ extern "C" int bsattn_mask_from_qk(const void* q, const void* k, int topk, int s
     prm.recent = recent;
     prm.dense = use_dense_for_last_block != 0;
     prm.causal = is_causal != 0;
-    prm.pitch = (prm.n[1] + 127) & ~127;
+    prm.pitch = ((prm.n[1] + 127) & ~127) + 8;
+    prm.wide = prm.n[1] % 4 == 0 && reinterpret_cast<uintptr_t>(mask_out) % 4 == 0;
     // 16 rows of keys, or 8 where they do not fit
-    prm.rows = 16 * 4LL * prm.pitch <= 220 * 1024 ? 16 : 8;
-    if (static_cast<long long>(prm.rows) * 4 * prm.pitch > 220 * 1024) return BSATTN_ERR_UNSUPPORTED;
+    prm.rows = 16 * 4LL * prm.pitch <= 224 * 1024 ? 16 : 8;
+    if (static_cast<long long>(prm.rows) * 4 * prm.pitch > 224 * 1024) return BSATTN_ERR_UNSUPPORTED;
     const long long tasks = static_cast<long long>(B) * (static_cast<long long>(Hq) * prm.n[0] + static_cast<long long>(Hkv) * prm.n[1]);
     if (tasks > 0x7fffffffLL) return BSATTN_ERR_UNSUPPORTED;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);

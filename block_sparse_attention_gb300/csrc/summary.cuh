@@ -52,18 +52,9 @@ __device__ __forceinline__ float score_of(uint32_t key) {
     return __int_as_float(k < 0 ? k ^ static_cast<int>(0x80000000u) : ~k);
 }
 
-// A key between lo and hi (hi - lo > 1) at which the next count is taken: the mean of the two scores for
-// the first steps, which halves what lies between them wherever the scores are spread evenly, then the
-// middle of the keys, which ends after 32 steps whatever they are.
-__device__ __forceinline__ uint32_t between(uint32_t lo, uint32_t hi, int step) {
-    const float a = score_of(lo), b = score_of(hi);
-    uint32_t mid = lo + (hi - lo) / 2;
-    if (step < 16 && isfinite(a) && isfinite(b)) mid = key_of(0.5f * a + 0.5f * b);
-    return max(min(mid, hi - 1), lo + 1);
-}
-
-// NT rising keys between lo and hi at which the next counts are taken, likewise: equal parts of the scores' range for
-// the first eight steps, then of the keys'.  Where fewer lie between, some are given twice.
+// NT rising keys between lo and hi (hi - lo > 1) at which the next counts are taken: equal parts of the scores' range
+// for the first eight steps, which is quick wherever the scores are spread evenly, then of the keys', which ends within
+// log 2^32 to the base NT + 1 more whatever they are.  Where fewer lie between, some are given twice.
 template <int NT>
 __device__ __forceinline__ void thresholds(uint32_t lo, uint32_t hi, int step, uint32_t (&t)[NT]) {
     const float a = score_of(lo), b = score_of(hi), by = (b - a) * (1.f / (NT + 1));
@@ -78,47 +69,82 @@ __device__ __forceinline__ void thresholds(uint32_t lo, uint32_t hi, int step, u
     }
 }
 
-// A warp's sum of a block's rows: lane l holds channels 8 (l % (D / 8)) + 0 .. 7 of it, all lanes with the
-// same channels the same.  `row(r)` gives the address of the lane's 16 bytes of row r < count.
-template <int D, bool BF16, typename Row>
-__device__ __forceinline__ void block_sum(Row row, int count, float (&sum)[8]) {
-    constexpr int kAt = 256 / D;              // rows that a warp reads at once: 2 or 4
-    constexpr int kEach = kBlockRows / kAt;   // rows of a lane: 32 or 16, row kAt j + sub
-    const int sub = (threadIdx.x & 31) / (D / 8);
-    // 16 rows in flight a lane: with row kAt j + sub the halves of 32, 16, 8 (and 4) rows are a lane's own
+// A warp's blocks on their way to it: stages of 64 rows in shared memory, of which a lane copies and adds up the same
+// 16-byte pieces, so that it waits for its own copies only and 32 KB a warp are on their way whatever the registers
+// hold.  Lane l has channels 8 (l % (D / 8)) + 0 .. 7 of rows kAt j + l / (D / 8).
+template <int D>
+struct BlockRing {
+    static constexpr int kAt = 256 / D;              // rows that a warp copies at once: 2 or 4
+    static constexpr int kEach = kBlockRows / kAt;   // rows of a lane: 32 or 16
+    static constexpr int kStage = kBlockRows * D * 2;
+    static constexpr int kBytes = 32768;
+    static constexpr int kDepth = kBytes / kStage;   // 2 or 4 blocks
+    uint8_t* at;                                     // the stages from the lane's first piece on
+
+    __device__ __forceinline__ explicit BlockRing(uint8_t* base) : at(base + (threadIdx.x & 31) * 16) {}
+
+    // The block whose first row begins, for the lane's channels, at `first`, a row `step` bytes after another, of
+    // which `count` are there; the others come as 0.
+    __device__ __forceinline__ void fetch(int stage, const char* first, long long step, int count) const {
+        const int sub = (threadIdx.x & 31) / (D / 8);
+        const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(at)) + stage * kStage;
+        const char* from = first + sub * step;
 #pragma unroll
-    for (int batch = 0; batch < kEach / 16; ++batch) {
-        uint4 raw[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int r = kAt * (i * (kEach / 16) + batch) + sub;
-            raw[i] = r < count ? __ldg(row(r)) : make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < kEach; ++j) {
+            const bool on = kAt * j + sub < count;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + j * 512), "l"(on ? from : first),
+                         "r"(on ? 16 : 0)
+                         : "memory");
+            from += kAt * step;
         }
-        float x[8];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            float2 v[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                v[i] = two_floats<BF16>(c == 0 ? raw[i].x : c == 1 ? raw[i].y : c == 2 ? raw[i].z : raw[i].w);
-#pragma unroll
-            for (int half = 8; half > 0; half >>= 1)
-#pragma unroll
-                for (int i = 0; i < half; ++i) {
-                    v[i].x = __fadd_rn(v[i].x, v[i + half].x);
-                    v[i].y = __fadd_rn(v[i].y, v[i + half].y);
-                }
-            x[2 * c] = v[0].x;
-            x[2 * c + 1] = v[0].y;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e] = batch == 0 ? x[e] : __fadd_rn(sum[e], x[e]);
     }
+    __device__ __forceinline__ static void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    // All but the last kDepth - 1 groups are there.
+    __device__ __forceinline__ static void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory"); }
+
+    // The sums of the lane's channels, all lanes with the same channels the same.
+    template <bool BF16>
+    __device__ __forceinline__ void sum(int stage, float (&s)[8]) const {
+        // with row kAt j + sub the halves of 32, 16, 8, 4 (and 2) rows are a lane's own: eight rows at a time
+        constexpr int kParts = kEach / 8;
+        const uint8_t* from = at + stage * kStage;
+        float y[kParts][8];
 #pragma unroll
-    for (int m = 16; m >= D / 8; m >>= 1)
+        for (int part = 0; part < kParts; ++part) {
+            uint4 raw[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e] = __fadd_rn(sum[e], __shfl_xor_sync(0xffffffffu, sum[e], m));
-}
+            for (int i = 0; i < 8; ++i) raw[i] = *reinterpret_cast<const uint4*>(from + (i * kParts + part) * 512);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                float2 v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[i] = two_floats<BF16>(c == 0 ? raw[i].x : c == 1 ? raw[i].y : c == 2 ? raw[i].z : raw[i].w);
+#pragma unroll
+                for (int half = 4; half > 0; half >>= 1)
+#pragma unroll
+                    for (int i = 0; i < half; ++i) {
+                        v[i].x = __fadd_rn(v[i].x, v[i + half].x);
+                        v[i].y = __fadd_rn(v[i].y, v[i + half].y);
+                    }
+                y[part][2 * c] = v[0].x;
+                y[part][2 * c + 1] = v[0].y;
+            }
+        }
+#pragma unroll
+        for (int half = kParts / 2; half > 0; half >>= 1)
+#pragma unroll
+            for (int i = 0; i < half; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[i][e] = __fadd_rn(y[i][e], y[i + half][e]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] = y[0][e];
+#pragma unroll
+        for (int m = 16; m >= D / 8; m >>= 1)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] = __fadd_rn(s[e], __shfl_xor_sync(0xffffffffu, s[e], m));
+    }
+};
 
 // The mean of `count` rows with that sum, and from it the lane's eight codes and the block's scale.
 template <int D>
