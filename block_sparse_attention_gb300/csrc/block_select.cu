@@ -468,14 +468,13 @@ int select(const SelectParams& prm, int B, cudaStream_t st) {
 
 // ------------------------------------------------------------------------------------------ prompts
 //
-// Two kernels: one summarises the blocks of q and k (a warp each, HBM-bound), codes kept as 16-bit whole
-// numbers for the second, which takes 16 query blocks of a head a CTA: products by mma.sync m16n8k16 (whole
-// numbers: exact), keys of the 16 rows in shared memory, then a warp a row to find its threshold and write
-// its bytes.  Under the causal rule a CTA goes no further than its rows see.
+// Two kernels.  One summarises the blocks of q and k, a warp each, HBM-bound (32 heads of 16384 tokens, d = 128, 268
+// MB: 47 us, 5.7 TB/s); codes are kept as 16-bit whole numbers for the other, which takes 16 query blocks of a head a
+// CTA: products by mma.sync m16n8k16 (whole numbers: exact), keys of the 16 rows in shared memory, then a warp a row
+// to find its threshold and write its bytes (19 us there, a chain of latencies).  Under the causal rule a CTA goes no
+// further than its rows see.
 
 constexpr int kSumThreads = 7 * 32;      // 32 KB of shared memory a warp
-constexpr int kMaskThreads = 256;
-constexpr int kMaskWarps = kMaskThreads / 32;
 
 struct MaskParams {
     const void* x[2];                    // q, k
@@ -557,8 +556,9 @@ __device__ __forceinline__ void mma_whole(float (&c)[4], const uint32_t (&a)[4],
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D>
-__global__ void __launch_bounds__(kMaskThreads, 2) mask_kernel(const MaskParams p) {
+template <int D, int TH>
+__global__ void __launch_bounds__(TH, TH == 256 ? 2 : 1) mask_kernel(const MaskParams p) {
+    constexpr int kMaskWarps = TH / 32;
     extern __shared__ __align__(16) uint32_t keys[];        // [rows][pitch]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int nq = p.n[0], nk = p.n[1];
@@ -773,26 +773,17 @@ MaskLayout mask_layout(int B, int Hq, int Hkv, int Sq, int Sk, int d) {
     return w;
 }
 
-template <int D, bool BF16>
-int launch_mask(const MaskParams& prm, cudaStream_t st) {
-    const long long tasks = static_cast<long long>(prm.B) * (static_cast<long long>(prm.H[0]) * prm.n[0] +
-                                                             static_cast<long long>(prm.H[1]) * prm.n[1]);
-    auto summarise = summarise_kernel<D, BF16>;
-    constexpr int kWarps = kSumThreads / 32, kSmem = kWarps * BlockRing<D>::kBytes;
-    static std::atomic<unsigned long long> raised{0}, raised_mask{0};
-    int rc = raise_smem_limit(reinterpret_cast<const void*>(summarise), kSmem, raised);
-    if (!rc) rc = raise_smem_limit(reinterpret_cast<const void*>(mask_kernel<D>), 224 * 1024, raised_mask);
+template <int D, int TH>
+int launch_rows(const MaskParams& prm, cudaStream_t st) {
+    auto kern = mask_kernel<D, TH>;
+    static std::atomic<unsigned long long> raised{0};
+    const int rc = raise_smem_limit(reinterpret_cast<const void*>(kern), 224 * 1024, raised);
     if (rc) return rc;
-    int sms = num_sms_of_current_device();
-    if (sms <= 0) sms = 148;
-    // a task a CTA first, then more
-    summarise<<<static_cast<unsigned>(std::min<long long>(tasks, sms)), kSumThreads, kSmem, st>>>(prm);
-    if (cudaGetLastError() != cudaSuccess) return BSATTN_ERR_CUDA;
     const int strips = (prm.n[0] + prm.rows - 1) / prm.rows;
     // launched while the summaries are still being made: it waits for them itself
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(strips) * prm.B * prm.H[0]);
-    cfg.blockDim = dim3(kMaskThreads);
+    cfg.blockDim = dim3(TH);
     cfg.dynamicSmemBytes = static_cast<size_t>(prm.rows) * prm.pitch * 4;
     cfg.stream = st;
     cudaLaunchAttribute at{};
@@ -800,7 +791,27 @@ int launch_mask(const MaskParams& prm, cudaStream_t st) {
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, mask_kernel<D>, prm) == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kern, prm) == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
+}
+
+template <int D, bool BF16>
+int launch_mask(const MaskParams& prm, cudaStream_t st) {
+    const long long tasks = static_cast<long long>(prm.B) * (static_cast<long long>(prm.H[0]) * prm.n[0] +
+                                                             static_cast<long long>(prm.H[1]) * prm.n[1]);
+    auto summarise = summarise_kernel<D, BF16>;
+    constexpr int kWarps = kSumThreads / 32, kSmem = kWarps * BlockRing<D>::kBytes;
+    static std::atomic<unsigned long long> raised{0};
+    const int rc = raise_smem_limit(reinterpret_cast<const void*>(summarise), kSmem, raised);
+    if (rc) return rc;
+    int sms = num_sms_of_current_device();
+    if (sms <= 0) sms = 148;
+    // a task a CTA first, then more
+    summarise<<<static_cast<unsigned>(std::min<long long>(tasks, sms)), kSumThreads, kSmem, st>>>(prm);
+    if (cudaGetLastError() != cudaSuccess) return BSATTN_ERR_CUDA;
+    // 16 rows by 16 warps where every CTA has an SM to itself (64 CTAs of 64 key blocks: 13.5 us for both kernels, 15.5
+    // by 8 warps), by 8 where there are more (512 CTAs of 256 key blocks: 64 us, 69 by 16 warps)
+    const long long ctas = static_cast<long long>((prm.n[0] + prm.rows - 1) / prm.rows) * prm.B * prm.H[0];
+    return ctas <= sms ? launch_rows<D, 512>(prm, st) : launch_rows<D, 256>(prm, st);
 }
 
 }  // namespace
