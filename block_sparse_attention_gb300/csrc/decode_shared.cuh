@@ -1,5 +1,6 @@
 // decode_shared.cuh -- what the kernels of a decode over shared prefixes know of a call, and where its pieces lie:
-// decode_shared.cu makes those of the prefixes, decode_shared_own.cu those of the sequences' own tokens, and joins.
+// decode_shared.cu makes them (those of the sequences' own tokens by decode_shared_own.cuh), decode_shared_join.cu
+// joins them.
 #pragma once
 
 #include <cstddef>
@@ -11,13 +12,16 @@
 
 namespace bsattn {
 
+constexpr int kSharedThreads = 384;
+
 // A piece is the result over some keys: for each of its rows O / l (fp32) and the base-2 log-sum-exp, -infinity
 // where the row has met no finite score (O is not written then, or is 0).
 //
-// Prefixes.  Sequences starts[p] .. starts[p + 1] - 1 share prefix p.  A CTA's kv head is its lane among `side` kv
-// heads side by side, plus a multiple of `side`.  An item is up to `seqs` sequences and one such multiple; a unit is
-// 128 keys of an item.  The units of all items, in the order prefix, sequences, kv heads, keys, are cut into equal
-// parts, one a (CTA, lane).  What part c has of an item is a piece; its row r stands at
+// Prefixes.  Sequences starts[p] .. starts[p + 1] - 1 share prefix p.  `side` kv heads and `deep` times up to `seqs`
+// sequences are worked side by side at the same keys, by CTAs of their own, the lanes.  An item is up to `seqs`
+// sequences and one kv head, those of a lane: a multiple of `deep` or `side` on from the lane's first.  A unit is 128
+// keys of an item.  A lane's units, in the order prefix, sequences, kv heads, keys, are cut into equal parts, one a CTA.
+// What part c has of an item is a piece; its row r stands at
 //     c * part_rows + (the lane's rows of all items before) + r
 // of the lane's, or twice as far apart where `halves`: a piece is then two, of every second key tile each.  (Going
 // from a piece to the next one moves on by the item's rows or by part_rows, which is no less, or by both: no two
@@ -44,7 +48,8 @@ struct SharedCall {
     int* status;
     int B, P, Hq, Hkv;
     int seqs, part_rows, halves;
-    int side, prefix_parts, own_parts;
+    long long lane_rows;         // of all pieces of a lane
+    int side, deep;
     int page_size, num_pages, prefix_pages, own_pages;
     int prefix_room, own_room;   // tokens that a table has room for
     float scale_log2;
@@ -71,42 +76,25 @@ __device__ __forceinline__ PrefixGroup prefix_group(const SharedCall& s, int p) 
 }
 
 __device__ __forceinline__ long long prefix_units(const SharedCall& s, const PrefixGroup& g) {
-    return static_cast<long long>((g.n + s.seqs - 1) / s.seqs) * (s.Hkv / s.side) * g.tiles;
+    const int times = (g.n + s.seqs - 1) / s.seqs;
+    return static_cast<long long>((times + s.deep - 1) / s.deep) * (s.Hkv / s.side) * g.tiles;
 }
 
 // Where part c's rows of an item (the t-th sequences of a group, kv head h) begin, and how many there are.
 __device__ __forceinline__ long long prefix_place(const SharedCall& s, const PrefixGroup& g, int c, int t, int h, int& rows) {
-    const int G = s.Hq / s.Hkv, lane = h % s.side, along = s.Hkv / s.side;
+    const int G = s.Hq / s.Hkv, lane = t % s.deep * s.side + h % s.side, along = s.Hkv / s.side;
     rows = min(s.seqs, g.n - t * s.seqs) * G;
-    const long long of_lane = static_cast<long long>(s.prefix_parts) * s.part_rows + static_cast<long long>(s.B) * G * along;
-    return (lane * of_lane + static_cast<long long>(c) * s.part_rows +
-            (static_cast<long long>(g.start) + t * s.seqs) * G * along + static_cast<long long>(h / s.side) * rows) *
+    // (there is one prefix only where deep > 1)
+    const long long before = (s.deep > 1 ? 0LL : g.start) + t / s.deep * s.seqs;
+    return (lane * s.lane_rows + static_cast<long long>(c) * s.part_rows + before * G * along +
+            static_cast<long long>(h / s.side) * rows) *
            (s.halves ? 2 : 1);
 }
 
 __device__ __forceinline__ int own_len(const SharedCall& s, int b) { return max(min(s.own_lens[b], s.own_room), 0); }
 __device__ __forceinline__ int own_units(int len) { return len / 32 + (len % 32 != 0); }
 
-// Launches of decode_shared_own.cu.  The own tokens' kernel comes first on the stream; that of the prefixes does
-// not end before it (so that the joining one, launched third, need only wait for the second).
-int launch_own_tokens(const SharedCall& call, int d, bool bf16, cudaStream_t stream);
+// The launch of decode_shared_join.cu, second on the stream.
 int launch_join(const SharedCall& call, int d, bool bf16, cudaStream_t stream);
-
-// Launches a kernel; `early`: it may start while the one before it on the stream still runs, and waits for that one
-// by itself.
-template <typename Kernel, typename... Args>
-int launch_on(bool early, Kernel kern, unsigned grid, int threads, size_t smem, cudaStream_t stream, const Args&... args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = early ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
-}
 
 }  // namespace bsattn

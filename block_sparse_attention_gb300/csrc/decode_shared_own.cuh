@@ -1,5 +1,4 @@
-// decode_shared_own.cu -- a decode over shared prefixes: the sequences' own tokens, and the joining of all
-// pieces, 16-bit paged cache, sm_103a.  (decode_shared.cu does the prefixes.)
+// decode_shared_own.cuh -- a decode over shared prefixes: the sequences' own tokens (decode_shared.cu calls this).
 //
 // Each byte of a sequence's own K and V is used once, by the G <= 8 query heads of its kv head, so HBM bandwidth
 // bounds this; sequences have few own tokens or many.  Every warp is by itself: an equal part of all units of 32
@@ -7,111 +6,64 @@
 // on their way before the one before is done), and what it has of a sequence goes to the workspace as a piece.
 // The products are those of decode_stream.cu, transposed, so that the G heads are the n = 8 side of mma.sync
 // m16n8k16: S^T [16 keys x 8] = K Q^T and O^T [d x 8] += V^T P^T.
-//
-// Joining is a warp a row: with (O, L) of each piece, out = sum O 2^(L - M) / sum 2^(L - M), in a fixed order.
-#include <algorithm>
+#pragma once
+
+#include <climits>
 #include <cmath>
 #include <type_traits>
 
 #include "decode_shared.cuh"
-#include "host_internal.h"
 #include "mma16.cuh"
 #include "ptx.cuh"
 
 namespace bsattn {
-namespace {
 
-using namespace mma16;
-
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
+constexpr int kOwnWarps = kSharedThreads / 32;           // of a CTA, 16 KB of shared memory each
+constexpr int kStretches = 512;                          // of sequences, a thread each; the last ones are empty
+static_assert(kSharedThreads <= kStretches, "a thread a stretch");
 constexpr int kTok = 32, kTiles = kTok / 16;             // keys of a unit
-constexpr int kLeast = 2;                                // units of a part
 // exp2 is taken of x - max + 12: weights up to 4096, so that a weight 2^-24 of the largest is
 // still a normal fp16 number and 2^-36 the smallest one
 constexpr float kWeightLog2 = 12.f;
 
 template <int D>
-struct Ring {
+struct OwnRing {
     static constexpr int kStages = 2 * (128 / D);        // K or V of a unit each
     static constexpr uint32_t kStage = kTok * D * 2;
     static constexpr uint32_t kRing = kStages * kStage;  // of one warp
-    static constexpr uint32_t kBars = kWarps * kRing;    // full[warp][stage]
-    static constexpr uint32_t kInfo = kBars + 8 * kWarps * kStages;       // (sequence, keys) of a stage
-    static constexpr uint32_t kBytes = 1024 + kInfo + 8 * kWarps * kStages;
+    static constexpr uint32_t kBars = kOwnWarps * kRing; // full[warp][stage]
+    static constexpr uint32_t kInfo = kBars + 8 * kOwnWarps * kStages;    // (sequence, keys) of a stage
+    static constexpr uint32_t kUpto = kInfo + 8 * kOwnWarps * kStages;    // [kStretches] units up to a stretch's end
+    static constexpr uint32_t kBytes = kUpto + 8 * kStretches;
     static_assert(kStage % 1024 == 0, "swizzled tiles start on 1024 bytes");
 };
 
+// One warp's part, for kv head g, of the units of all sequences.  `sm` is on 1024 bytes; the CTA has written upto_of
+// there, set up the barriers, and met at a barrier since.  Parts from the last unit on are empty.
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kThreads, 2)
-    own_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const SharedCall p) {
-    using R = Ring<D>;
+__device__ __forceinline__ void own_tokens(const CUtensorMap* tm_k, const CUtensorMap* tm_v, const SharedCall& p, uint8_t* sm,
+                                           volatile int* abort_flag, int part, int g, long long chunk, long long total) {
+    using namespace mma16;
+    using R = OwnRing<D>;
     using T = std::conditional_t<BF16, __nv_bfloat16, __half>;
     constexpr int kStages = R::kStages;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ long long upto_of[kThreads];              // units up to the end of thread t's sequences
-    __shared__ long long warp_sums[kWarps];
-    __shared__ int aborted;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint8_t* ring = sm + warp * R::kRing;
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + R::kBars) + warp * kStages;
     volatile int2* info = reinterpret_cast<int2*>(sm + R::kInfo) + warp * kStages;
-    volatile int* abort_flag = &aborted;
+    const long long* upto_of = reinterpret_cast<const long long*>(sm + R::kUpto);
     const int G = p.Hq / p.Hkv;
-    const int g = blockIdx.x % p.Hkv, part = static_cast<int>(blockIdx.x / p.Hkv) * kWarps + warp;
-
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (lane == 0)
-        for (int s = 0; s < kStages; ++s) mbar_init(&full[s], 1);
-    if (tid == 0) aborted = 0;
-    fence_barrier_init();
-
-    // ------------------------------------------------------------ this warp's part of all units
-    const int per = (p.B + kThreads - 1) / kThreads;
-    long long upto = 0;
-    {
-        bool bad = false;
-        long long sum = 0;
-        for (int i = 0; i < per && tid * per + i < p.B; ++i) {
-            const int b = tid * per + i, len = p.own_lens[b];
-            bad = bad || len < 0 || len > p.own_room;
-            sum += own_units(own_len(p, b));
-        }
-        if (bad && blockIdx.x == 0) atomicOr(p.status, BSATTN_ERR_BAD_INDEX);
-        upto = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long u = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += u;
-        }
-        if (lane == 31) warp_sums[warp] = upto;
-        __syncthreads();
-        for (int w = 0; w < warp; ++w) upto += warp_sums[w];
-        upto_of[tid] = upto;
-        if (blockIdx.x == 0) {
-            long long before = upto - sum;
-            for (int i = 0; i < per && tid * per + i < p.B; ++i) {
-                const int b = tid * per + i;
-                p.own_info[1 + b] = before;
-                before += own_units(own_len(p, b));
-            }
-        }
-        __syncthreads();
-    }
-    const long long total = upto_of[kThreads - 1];
-    const long long chunk = max((total + p.own_parts - 1) / p.own_parts, static_cast<long long>(kLeast));
-    if (blockIdx.x == 0 && tid == 0) p.own_info[0] = chunk;
+    const int per = (p.B + kSharedThreads - 1) / kSharedThreads;        // sequences of a stretch
     const long long x0 = part * chunk;
     const int n = static_cast<int>(min(chunk, total - x0));     // units of this warp
-    if (x0 >= total) return;                                    // (no barrier of the CTA's comes after this)
+    if (x0 >= total) return;
 
     // the next batch of units begins at unit `cu` of sequence `cb`
     int cb, cu;
     {
         int t = 0;
 #pragma unroll
-        for (int step = kThreads / 2; step > 0; step >>= 1)
+        for (int step = kStretches / 2; step > 0; step >>= 1)
             if (upto_of[t + step - 1] <= x0) t += step;
         long long before = t > 0 ? upto_of[t - 1] : 0;
         cb = t * per;
@@ -195,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 mbar_arrive_expect_tx(&full[st], R::kStage);
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c)
-                    tma_load_3d(ring + st * R::kStage + c * (kTok * 128), h & 1 ? &tm_v : &tm_k, &full[st], c * 64, g, row);
+                    tma_load_3d(ring + st * R::kStage + c * (kTok * 128), h & 1 ? tm_v : tm_k, &full[st], c * 64, g, row);
             }
         }
         __syncwarp();
@@ -392,175 +344,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         end(cur);
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.status, BSATTN_ERR_BAD_INDEX);
-}
-
-// ------------------------------------------------------------------------------------------ joining
-
-constexpr int kBatch = 8;                // pieces that a warp joins in one trip to L2
-
-// WARPS: of a row, each with every WARPS-th piece: four where the rows are few, as a trip more costs more than joining
-// their four results.
-template <int D, bool BF16, int WARPS>
-__global__ void __launch_bounds__(kThreads) join_kernel(const SharedCall p) {
-    constexpr int kC = D / 32;                           // channels of a lane
-    using V = std::conditional_t<kC == 4, float4, float2>;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int row = static_cast<int>(blockIdx.x) * (kWarps / WARPS) + warp / WARPS, share = warp % WARPS;
-    const int b = row / p.Hq, h = row - b * p.Hq;
-    if (b >= p.B) return;                                // (with four warps a row, none or all)
-    const int G = p.Hq / p.Hkv, kvh = h / G;
-    // the prefix whose sequences begin last before or at b
-    int prefix = 0;
-    for (int i = 1; i <= p.P; i += 32)
-        prefix += __reduce_add_sync(0xffffffffu, i + lane <= p.P && p.starts[i + lane] <= b ? 1 : 0);
-    PrefixGroup group{};
-    int i = -1;
-    if (prefix < p.P) {
-        group = prefix_group(p, prefix);
-        i = b - group.start;
-    }
-    const int mine = own_units(own_len(p, b));
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    // pieces 0 .. shared - 1 are the prefix's, those up to `count` of the sequence's own tokens
-    int shared = 0, count = 0, other = 0;
-    long long first = 0, by = 0, own = 0;
-    if (i >= 0 && i < group.n && group.tiles > 0) {
-        const long long chunk = p.prefix_info[0], units = p.prefix_info[1 + prefix];
-        const int t = i / p.seqs, each = p.halves ? 2 : 1;
-        const long long from = units + (static_cast<long long>(t) * (p.Hkv / p.side) + kvh / p.side) * group.tiles;
-        const long long c0 = from / chunk;
-        shared = static_cast<int>((from + group.tiles - 1) / chunk - c0 + 1) * each;
-        by = static_cast<long long>(p.part_rows) * each;
-        first = prefix_place(p, group, static_cast<int>(c0), t, kvh, other) + (i - t * p.seqs) * G + (h - kvh * G);
-    }
-    count = shared;
-    if (mine > 0) {
-        const long long chunk = p.own_info[0], from = p.own_info[1 + b], c0 = from / chunk;
-        count += static_cast<int>((from + mine - 1) / chunk - c0 + 1);
-        own = ((c0 + b) * p.Hkv + kvh) * G + (h - kvh * G);
-    }
-    float num[kC] = {};
-    float M = -INFINITY, den = 0.f;
-    const auto place = [&](int n) -> long long {
-        return n >= shared ? own + static_cast<long long>(n - shared) * p.Hq
-               : p.halves  ? first + (n >> 1) * by + (n & 1) * other
-                           : first + n * by;
-    };
-    // 32 pieces at a time: first their L, one a lane, so that all that is read of O after that is on its way together
-    for (int k0 = share; k0 < count; k0 += 32 * WARPS) {
-        const int n = k0 + lane * WARPS;
-        const float mine_l = n < count ? __ldcg((n < shared ? p.prefix_lse : p.own_lse) + place(n)) : -INFINITY;
-        float top = mine_l;
-#pragma unroll
-        for (int w = 1; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-        top = fmaxf(top, M);
-        const float ref = top == -INFINITY ? 0.f : top, down = ex2_approx(M - ref);
-        M = top;
-        den *= down;
-#pragma unroll
-        for (int e = 0; e < kC; ++e) num[e] *= down;
-        // (where a row has met no finite score O may not have been written)
-        const float weight = mine_l == -INFINITY ? 0.f : ex2_approx(mine_l - ref);
-        den += weight;                                   // of this lane's pieces
-        const int here = min((count - k0 + WARPS - 1) / WARPS, 32);
-        for (int k1 = 0; k1 < here; k1 += kBatch) {
-            V ov[kBatch];
-            float w[kBatch];
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                w[k] = __shfl_sync(0xffffffffu, weight, (k1 + k) & 31);
-                ov[k] = V{};
-                if (k1 + k < here && w[k] != 0.f) {
-                    const int at = k0 + (k1 + k) * WARPS;
-                    ov[k] = __ldcg(reinterpret_cast<const V*>((at < shared ? p.prefix_o : p.own_o) + place(at) * D) + lane);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                if (k1 + k >= here) w[k] = 0.f;
-                const float* v = reinterpret_cast<const float*>(&ov[k]);
-#pragma unroll
-                for (int e = 0; e < kC; ++e) num[e] = fmaf(w[k], v[e], num[e]);
-            }
-        }
-    }
-#pragma unroll
-    for (int w = 1; w < 32; w <<= 1) den += __shfl_xor_sync(0xffffffffu, den, w);
-    if constexpr (WARPS > 1) {
-        __shared__ float top_of[WARPS], den_of[WARPS];
-        __shared__ V num_of[WARPS][32];
-        V* to = &num_of[share][lane];
-#pragma unroll
-        for (int e = 0; e < kC; ++e) reinterpret_cast<float*>(to)[e] = num[e];
-        if (lane == 0) {
-            top_of[share] = M;
-            den_of[share] = den;
-        }
-        __syncthreads();
-        if (share > 0) return;
-        float top = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) top = fmaxf(top, top_of[w]);
-        const float ref = top == -INFINITY ? 0.f : top;
-        den = 0.f;
-#pragma unroll
-        for (int e = 0; e < kC; ++e) num[e] = 0.f;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
-            // a warp without a finite L has a sum of 0, or NaN if it met one: either way it counts
-            const float by = top_of[w] == -INFINITY ? 1.f : ex2_approx(top_of[w] - ref);
-            const V v = num_of[w][lane];
-#pragma unroll
-            for (int e = 0; e < kC; ++e) num[e] = fmaf(by, reinterpret_cast<const float*>(&v)[e], num[e]);
-            den = fmaf(by, den_of[w], den);
-        }
-    }
-    const float inv = den == 0.f ? 0.f : 1.f / den;
-    uint32_t w[kC / 2];
-#pragma unroll
-    for (int e = 0; e < kC / 2; ++e) w[e] = pack2<BF16>(num[2 * e] * inv, num[2 * e + 1] * inv);
-    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + static_cast<size_t>(row) * D + kC * lane);
-    if constexpr (kC == 4) *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
-    else out[0] = w[0];
-}
-
-template <int D, bool BF16>
-int launch_own(const SharedCall& p, cudaStream_t st) {
-    CUtensorMap tk, tv;
-    const uint64_t rows = uint64_t(p.num_pages) * p.page_size, row_bytes = uint64_t(p.Hkv) * D * 2;
-    int rc = encode_3d(&tk, p.k, BF16, D, p.Hkv, rows, D * 2ull, row_bytes, 64, 1, kTok, true);
-    if (!rc) rc = encode_3d(&tv, p.v, BF16, D, p.Hkv, rows, D * 2ull, row_bytes, 64, 1, kTok, true);
-    if (rc) return rc;
-    auto kern = own_kernel<D, BF16>;
-    static std::atomic<unsigned long long> raised{0};
-    rc = raise_smem_limit(reinterpret_cast<const void*>(kern), Ring<D>::kBytes, raised);
-    if (rc) return rc;
-    kern<<<static_cast<unsigned>(p.own_parts / kWarps) * p.Hkv, kThreads, Ring<D>::kBytes, st>>>(tk, tv, p);
-    return cudaGetLastError() == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
-}
-
-}  // namespace
-
-int launch_own_tokens(const SharedCall& p, int d, bool bf16, cudaStream_t st) {
-    if (d == 64) return bf16 ? launch_own<64, true>(p, st) : launch_own<64, false>(p, st);
-    return bf16 ? launch_own<128, true>(p, st) : launch_own<128, false>(p, st);
-}
-
-int launch_join(const SharedCall& p, int d, bool bf16, cudaStream_t st) {
-    const long long rows = static_cast<long long>(p.B) * p.Hq;
-    // (16 x 32 rows with 40 pieces each: 25.0 us for 28.5 in all; 64 x 32 rows: 18.2 for 15.2)
-    const bool few = rows <= 1024;
-    const unsigned grid = static_cast<unsigned>(few ? rows : (rows + kWarps - 1) / kWarps);
-    const auto run = [&](auto dim, auto type) {
-        constexpr int D = decltype(dim)::value;
-        constexpr bool BF16 = decltype(type)::value;
-        return few ? launch_on(true, join_kernel<D, BF16, kWarps>, grid, kThreads, 0, st, p)
-                   : launch_on(true, join_kernel<D, BF16, 1>, grid, kThreads, 0, st, p);
-    };
-    using D64 = std::integral_constant<int, 64>;
-    using D128 = std::integral_constant<int, 128>;
-    if (d == 64) return bf16 ? run(D64{}, std::true_type{}) : run(D64{}, std::false_type{});
-    return bf16 ? run(D128{}, std::true_type{}) : run(D128{}, std::false_type{});
 }
 
 }  // namespace bsattn

@@ -94,6 +94,28 @@ def test_groups(bsa, d, dtype):
     Case([90, 120], [333, 900], [5] * 210, 8, 4, d, dtype, seed=3).check(bsa)
 
 
+@pytest.mark.parametrize("B", [33, 65, 257, 290])
+def test_one_prefix_read_several_times(bsa, B):
+    """32 sequences of eight heads a reading: two at a time and more, and of nine and ten some CTAs have one less."""
+    lens = [(11 * b) % 70 for b in range(B)]
+    Case([B], [2000], lens, 16, 2, 64, BF16, seed=B).check(bsa)
+    Case([B], [130], [0] * B, 16, 2, 128, F16, seed=B + 1).check(bsa)
+
+
+@pytest.mark.parametrize("Hkv", [75, 76, 77, 160, 700])
+def test_many_kv_heads(bsa, Hkv):
+    """As many as half the SMs and more."""
+    Case([5], [300], [0, 3, 64, 65, 200], Hkv, Hkv, 64, F16, seed=Hkv).check(bsa)
+    Case([2, 3], [0, 200], [0, 3, 64, 65, 200], Hkv, Hkv, 64, BF16, seed=Hkv).check(bsa)
+
+
+@pytest.mark.parametrize("plen,own", [(5000, 1), (1, 3000), (40_000, 0), (0, 6000)])
+def test_shares_of_the_gpu(bsa, plen, own):
+    """Prefixes and own tokens that cost very different amounts, or nothing."""
+    for B in (3, 100):
+        Case([B], [plen], [own if b % 3 == 0 else 0 for b in range(B)], 8, 2, 128, BF16, seed=B).check(bsa)
+
+
 def test_many_pieces_a_cta(bsa):
     """More items than CTAs, and items of many CTAs: barriers, rings and accumulators are used again and again."""
     Case([2] * 100, [200 + 3 * p for p in range(100)], [1] * 200, 16, 8, 64, F16, seed=1).check(bsa)
