@@ -57,8 +57,10 @@ struct Cfg {
     static constexpr uint32_t kMissing = kMisc + 16;             // [kNotes]: which halves of a key tile are not there
     static constexpr uint32_t kBytes = 1024 + kMissing + 4 * kNotes;
     static_assert(kBytes <= 226 * 1024, "shared memory");        // the scan's static arrays beside it
-    // What a unit of a prefix costs, in units of own tokens (one of 12 warps): 1.7 us against 0.1.
-    static constexpr float kCost = 16.f;
+    // What a unit of a prefix costs, in units of own tokens: 1.6 us a CTA, while its 12 warps would have that many of the
+    // others.  (256 sequences of 1000 own tokens over 65521: 282 us with 16, 262 with 13, 285 with 10; d = 64, 192 over
+    // 6 prefixes: 85 with 16, 79 with 20, 87 with 24.)
+    static constexpr float kCost = D == 128 ? 13.f : 20.f;
 };
 
 struct PrefixParams {
@@ -169,6 +171,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The kernel that joins may start wherever there is room (and waits for this one by itself).  With the leave to
     // start given at the top, its CTAs come to wait beside this one's.
     const auto leave = [] { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); };
+
+    if (tid == 32 * kLoadWarp) {
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+        tma_prefetch_desc(&own_k);
+        tma_prefetch_desc(&own_v);
+    }
 
     // ------------------------------------------------------------ this CTA's part of all units
     Walk start;
@@ -312,16 +322,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         Piece piece;
         if (warp == kLoadWarp) {
             // ------------------------------------------------------------ TMA
-            if (lane == 0) {
-                tma_prefetch_desc(&tm_q);
-                tma_prefetch_desc(&tm_k);
-                tma_prefetch_desc(&tm_v);
-            }
             int g = 0;                                   // tiles loaded, K and V counted apart
             int nq[2] = {0, 0};                          // Q tiles loaded
             bool ok = true, bad = false;
             while (ok && next_piece(p, part, beside, walk, piece)) {
                 const int n = piece.k1 - piece.k0;
+                const auto queries = [&] {
+                    for (int x = 0; ok && x < 2; ++x) {
+                        if (tiles_of(x, n) == 0) continue;
+                        ok = nq[x] == 0 || warp_wait_within(&q_free[x], (nq[x] - 1) & 1, p.s.budget_ns, abort_flag, status);
+                        if (!ok) break;
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(&q_full[x], static_cast<uint32_t>(p.q_bytes));
+                            const int b = piece.b0 + (HALVES ? 0 : x * (p.s.seqs / 2));
+#pragma unroll
+                            for (int h = 0; h < D / 64; ++h)
+                                tma_load_4d(sq + x * C::kTile + h * 16384, &tm_q, &q_full[x], h * 64, 0, piece.kvh, b);
+                        }
+                        ++nq[x];
+                    }
+                };
+                // (of a later piece they come after its first K, as they wait for the tiles before it)
+                const bool at_once = nq[0] == 0 && nq[1] == 0;
+                if (at_once) queries();
                 int look = -1;
                 for (int i = 0; ok && i < n; ++i) {
                     if ((i & 15) == 0) {
@@ -355,20 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                         ++g;
-                        if (i > 0 || v > 0) continue;
-                        for (int x = 0; ok && x < 2; ++x) {
-                            if (tiles_of(x, n) == 0) continue;
-                            ok = nq[x] == 0 || warp_wait_within(&q_free[x], (nq[x] - 1) & 1, p.s.budget_ns, abort_flag, status);
-                            if (!ok) break;
-                            if (lane == 0) {
-                                mbar_arrive_expect_tx(&q_full[x], static_cast<uint32_t>(p.q_bytes));
-                                const int b = piece.b0 + (HALVES ? 0 : x * (p.s.seqs / 2));
-#pragma unroll
-                                for (int h = 0; h < D / 64; ++h)
-                                    tma_load_4d(sq + x * C::kTile + h * 16384, &tm_q, &q_full[x], h * 64, 0, piece.kvh, b);
-                            }
-                            ++nq[x];
-                        }
+                        if (i > 0 || v > 0 || at_once) continue;
+                        queries();
                     }
                 }
             }
@@ -391,10 +402,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t kTileDesc = C::kTile >> 4;
             const uint32_t ts = uniform(tbase + 128 * x), to = uniform(tbase + kOCol + D * x);
             int blk = 0, items = 0, outs = 0;                // tiles, pieces (S begun, O begun) so far
-            bool ok = true;
             const auto wait = [&](uint64_t* bar, int parity) {
                 return warp_wait_within(bar, static_cast<uint32_t>(parity & 1), p.s.budget_ns, abort_flag, status);
             };
+            bool ok = true;
             // rows of a V tile past the prefix's end may hold anything, and a weight of 0 must not meet a NaN
             // (both issuers may clear them: they write the same)
             const auto clear_tail = [&](int st, int valid) {
@@ -635,53 +646,51 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             if (!HALVES && speaks) mbar_arrive(&empty[v_read]);
             __syncwarp();
-            // a lane holds rows lane / 4 + 8 {0, 1} of 16 (twice), two neighbouring columns of every eight
-            uint32_t o[2][D / 2];
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                for (int c0 = 0; c0 < D; c0 += 64)
-                    tmem_ld_16x256b_x8(to + (static_cast<uint32_t>(16 * hf) << 16) + c0, o[hf] + c0 / 2);
-            tmem_wait_ld();
-            // O is in registers: the next piece's first P V may overwrite it
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&o_free[x]);
             // a row without a finite score has l = 0, or NaN if it met one
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const uint32_t rows = __ballot_sync(0xffffffffu, mine);
-            if (rows != 0u) {
-                // Four lanes exchange their pairs of columns, so that they write 64 bytes of a row (a row a lane would
-                // be 32 lines a store: 4.3 us for 256 rows of 128, against 1.3).
-                float* out = p.s.prefix_o + (at - lane) * D + 4 * (lane & 1) + 8 * (lane >> 1 & 1);
-                const bool upper = (lane & 2) != 0, odd = (lane & 1) != 0;
+            // Four lanes exchange their pairs of columns, so that they write 64 bytes of a row (a row a lane would
+            // be 32 lines a store: 4.3 us for 256 rows of 128, against 1.3).
+            float* out = p.s.prefix_o + (at - lane) * D + 4 * (lane & 1) + 8 * (lane >> 1 & 1);
+            const bool upper = (lane & 2) != 0, odd = (lane & 1) != 0;
+#pragma unroll 1
+            for (int hf = 0; hf < 2; ++hf) {
+                // a lane holds rows lane / 4 + 8 {0, 1} of 16, two neighbouring columns of every eight
+                uint32_t o[D / 2];
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf)
+                for (int c0 = 0; c0 < D; c0 += 64) tmem_ld_16x256b_x8(to + (static_cast<uint32_t>(16 * hf) << 16) + c0, o + c0 / 2);
+                tmem_wait_ld();
+                if (hf == 1) {
+                    // O is in registers: the next piece's first P V may overwrite it
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&o_free[x]);
+                }
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const int row = 16 * hf + 8 * r + (lane >> 2);
-                        const float by = __shfl_sync(0xffffffffu, inv, row);
-                        const bool there = (rows >> row & 1u) != 0u;
+                for (int r = 0; r < 2; ++r) {
+                    const int row = 16 * hf + 8 * r + (lane >> 2);
+                    const float by = __shfl_sync(0xffffffffu, inv, row);
+                    const bool there = (rows >> row & 1u) != 0u;
 #pragma unroll
-                        for (int i = 0; i < D / 16; ++i) {
-                            float f[2], g2[2];           // the lane's first and second pair
+                    for (int i = 0; i < D / 16; ++i) {
+                        float f[2], g2[2];               // the lane's first and second pair
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const float a = __uint_as_float(o[hf][8 * i + 2 * r + e]) * by;
-                                const float b = __uint_as_float(o[hf][8 * i + 4 + 2 * r + e]) * by;
-                                const float got = __shfl_xor_sync(0xffffffffu, upper ? a : b, 2);
-                                f[e] = upper ? got : a;
-                                g2[e] = upper ? b : got;
-                            }
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const float got = __shfl_xor_sync(0xffffffffu, odd ? f[e] : g2[e], 1);
-                                if (odd) f[e] = got;
-                                else g2[e] = got;
-                            }
-                            if (there) *reinterpret_cast<float4*>(out + row * D + 16 * i) = make_float4(f[0], f[1], g2[0], g2[1]);
+                        for (int e = 0; e < 2; ++e) {
+                            const float a = __uint_as_float(o[8 * i + 2 * r + e]) * by;
+                            const float b = __uint_as_float(o[8 * i + 4 + 2 * r + e]) * by;
+                            const float got = __shfl_xor_sync(0xffffffffu, upper ? a : b, 2);
+                            f[e] = upper ? got : a;
+                            g2[e] = upper ? b : got;
                         }
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float got = __shfl_xor_sync(0xffffffffu, odd ? f[e] : g2[e], 1);
+                            if (odd) f[e] = got;
+                            else g2[e] = got;
+                        }
+                        if (there) *reinterpret_cast<float4*>(out + row * D + 16 * i) = make_float4(f[0], f[1], g2[0], g2[1]);
                     }
+                }
             }
             if (mine) {
                 p.s.prefix_lse[at] = l == 0.f ? -INFINITY : m_used * c + log2f(l);
