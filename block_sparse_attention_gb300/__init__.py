@@ -450,9 +450,9 @@ def _device_index(device) -> int:
 
 
 def call_workspace(device, purpose: str, nbytes: int) -> torch.Tensor:
-    """A workspace for the stream decodes that no other call in flight uses: one per (stream, purpose),
-    "decode_kv4", "decode_window" or "decode_shared", and a new one for every call captured into a CUDA graph (graphs may be
-    replayed side by side).  With nbytes 0 outside a capture, the one that such calls on the current stream
+    """A workspace that no other call in flight uses: one per (stream, purpose), "decode_kv4", "decode_window",
+    "decode_shared" or "mask", and a new one for every call captured into a CUDA graph (graphs may be replayed side
+    by side).  With nbytes 0 outside a capture, the one that such calls on the current stream
     use, for bsattn_get_device_status; what captured calls find is in status_workspace(device)."""
     return _call_workspace(_device_index(device), purpose, nbytes, _capturing())
 
@@ -1047,7 +1047,9 @@ def bsattn_mask_from_qk(q, k, topk: int, is_causal: bool, sinks: int = 1, recent
     elif not (out.get_device() == i and out.dtype is _U8 and out.shape == shape and out.is_contiguous()):
         _refuse(("k", k.contiguous(), k.dtype, 4, None), ("out", out, _U8, 4, shape))
     if ws is None:
-        ws = torch.empty(bsattn_mask_from_qk_workspace_size(B, Hq, hkv, Sq, Sk, d), dtype=_U8, device=q.device)
+        need = bsattn_mask_from_qk_workspace_size(B, Hq, hkv, Sq, Sk, d)
+        # (a captured call's need not start at zero: no memset in the graph)
+        ws = torch.empty(need, dtype=_U8, device=q.device) if _capturing() else _call_workspace(i, "mask", need, False)
     else:
         _check_ws(ws, i)
     rc = load().bsattn_mask_from_qk(q.data_ptr(), k.data_ptr(), max(topk, -1), sinks, recent,
