@@ -22,16 +22,17 @@ namespace {
 // ------------------------------------------------------------------------------------------ decode
 //
 // A (sequence, kv head) is a CTA's, or that of a cluster whose CTAs have a stretch of its blocks each.
-// A warp scores 16 blocks at a time, S [16 blocks x 8 heads] = K Q^T by mma.sync m16n8k16 in fp16: a code c enters
+// A warp scores 32 blocks at a time, S [16 blocks x 8 heads] = K Q^T twice by mma.sync m16n8k16 in fp16: a code c enters
 // as 1152 + c, which takes one byte permutation for two codes (1024 + byte is an fp16 number with that byte for its
 // lowest), and the sums begin at -1152 times the query's codes.  Whole numbers below 2^23 in magnitude throughout, 32
-// channels a sum: exact.  (8-bit products of the tensor core are slow here, an m16n8k32 in 17 cycles an SM; by dp4a,
-// which is not, the adding of eight lanes' sums made it three times the instructions: 28 us for 64 sequences.)
-// Which channel a matrix index stands for is free, so a lane reads D / 4 consecutive codes of a row.  Keys stay in
-// shared memory, the first kHeld of a thread in registers.  A trip of the search counts at four thresholds at once:
-// a count is mostly the way through the barrier.
-// The index is read once, but instructions bound a batch and the SMs that work a few long sequences; a single short
-// one is a chain of latencies: lengths, table, index, then the counts.
+// channels a sum: exact.  (64 sequences of up to 1024 blocks, d = 128: 17.6 us; 16 blocks at a time 21.1, as the way from
+// the products to a key is a chain of latencies; by 8-bit products, which the tensor core does at an m16n8k32 in 17
+// cycles an SM, 21.3; by dp4a, with the adding of eight lanes' sums, 28.)
+// Which channel a matrix index stands for is free, so a lane reads 16 consecutive codes of a row.  Keys stay in shared
+// memory, the first kHeld of a thread in registers.  A trip of the search counts at four thresholds at once: a count is
+// mostly the way through the barrier.
+// The index is read once (41 MB there, 5.9 us at the copy rate); what bounds this is the longest row's chain: lengths,
+// table and index 4 us, then 16 times 32 blocks a warp, six counts, the writing.
 
 constexpr int kMaxBlocks = 46875;               // of a sequence: their keys lie in shared memory
 constexpr int kHeld = 8;                        // keys of a thread in registers
@@ -81,14 +82,21 @@ __device__ __forceinline__ void copy4(uint32_t to, const void* from) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
 }
 
-constexpr int kDepth = 4;                       // times 16 blocks whose index rows a warp has on their way
+__device__ __forceinline__ void mma_codes(int (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+constexpr int kDepth = 2;                       // times 32 blocks whose index rows a warp has on their way
 constexpr int kMaxCluster = 8;
 
 template <int D, bool BF16, int TH>
 __global__ void __launch_bounds__(TH, TH == 128 ? 4 : 1) select_kernel(const SelectParams p) {
     constexpr int kWarps = TH / 32;
     constexpr int kSteps = D / 16, kSums = kSteps / 2;      // k16 steps, and sums of two of them
-    constexpr uint32_t kGroup = 16 * D + 64;                // 16 index rows: codes, scales
+    constexpr uint32_t kGroup = 32 * D + 128;               // 32 index rows: codes, scales
     extern __shared__ __align__(16) uint8_t sel_smem[];
     uint32_t* keys = reinterpret_cast<uint32_t*>(sel_smem + kWarps * kDepth * kGroup);   // of the CTA's blocks; first their index rows
     __shared__ uint2 qb[kSteps][32];                        // the queries' codes as a lane's operands, head lane / 4
@@ -150,7 +158,7 @@ __global__ void __launch_bounds__(TH, TH == 128 ? 4 : 1) select_kernel(const Sel
     const bool far = asked < 0 || asked > static_cast<long long>(p.max_pages) * p.page_size;
     const int all_n = asked <= 0 ? 0 : min(asked / kBlockRows + (asked % kBlockRows != 0), room);
     // the CTA's blocks: n from block0 on
-    const int each = ((all_n + CL - 1) / CL + 15) & ~15;
+    const int each = ((all_n + CL - 1) / CL + 31) & ~31;
     const int block0 = min(rank * each, all_n), n = min(each, all_n - block0);
     if (tid < static_cast<int>(sizeof(Shares) / 4)) {
         reinterpret_cast<uint32_t*>(&own)[tid] = 0;
@@ -177,38 +185,37 @@ __global__ void __launch_bounds__(TH, TH == 128 ? 4 : 1) select_kernel(const Sel
     {
         const int first_recent = max(all_n - p.recent, 0);
         const int r8 = lane >> 2, j4 = lane & 3, h0 = 2 * j4;
-        float sq[2];
+        float sq[2];                                        // (NaN of a head that there is not: no maximum takes it)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) sq[e] = h0 + e < G ? qscale[h0 + e] : 0.f;
+        for (int e = 0; e < 2; ++e) sq[e] = h0 + e < G ? qscale[h0 + e] : __int_as_float(0x7fffffff);
         uint32_t least = 0, most = 0;                       // of ~key, and of key
         int there = 0;                                      // and the forced ones, 2^16 each
-        // Groups of 16 blocks in turn: the warp's m-th is group kWarps m + warp.  Where rows are 128 bytes, the two
+        // Groups of 32 blocks in turn: the warp's m-th is group kWarps m + warp.  Where rows are 128 bytes, the two
         // halves of every second one change places, so that a quad's 16-byte reads of two rows meet no bank twice.
         uint8_t* ring = sel_smem + warp * kDepth * kGroup;
-        const int groups = ((n + 15) / 16 - warp + kWarps - 1) / kWarps;
+        const int groups = ((n + 31) / 32 - warp + kWarps - 1) / kWarps;
+        constexpr int kChunks = D / 16, kRows = 32 / kChunks;       // of 16 bytes in a row; rows that a warp copies at once
+        const int r_in = lane / kChunks, chunk = lane % kChunks;
+        const int8_t* codes = p.codes + static_cast<size_t>(g) * D + chunk * 16;
+        const size_t row_bytes = static_cast<size_t>(p.Hkv) * D;
+        const uint32_t put = r_in * D + (D == 128 ? chunk ^ (r_in & 1) << 2 : chunk) * 16;
         const auto fetch = [&](int m) {
             if (m < groups) {
                 const uint32_t to = smem_u32(ring + (m % kDepth) * kGroup);
-                const int base = (m * kWarps + warp) * 16;
-                constexpr int kChunks = D / 16;                     // of 16 bytes in a row
+                const int at = (m * kWarps + warp) * 32 + lane;
+                uint32_t row = at < n ? keys[at] : 0u;
+                if (row == 0xffffffffu) row = 0u;
 #pragma unroll
-                for (int e = 0; e < kChunks / 2; ++e) {
-                    const int r = (32 / kChunks) * e + lane / kChunks, c = lane % kChunks;
-                    const uint32_t row = base + r < n ? keys[base + r] : 0u;
-                    const size_t place = static_cast<size_t>(row == 0xffffffffu ? 0u : row) * p.Hkv + g;
-                    copy16(to + r * D + (D == 128 ? c ^ (r & 1) << 2 : c) * 16, p.codes + place * D + c * 16);
-                }
-                if (lane < 16) {
-                    const uint32_t row = base + lane < n ? keys[base + lane] : 0u;
-                    copy4(to + 16 * D + 4 * lane, p.scales + static_cast<size_t>(row == 0xffffffffu ? 0u : row) * p.Hkv + g);
-                }
+                for (int e = 0; e < kChunks; ++e)
+                    copy16(to + e * kRows * D + put, codes + __shfl_sync(0xffffffffu, row, kRows * e + r_in) * row_bytes);
+                copy4(to + 32 * D + 4 * lane, p.scales + static_cast<size_t>(row) * p.Hkv + g);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
         uint2 q2[kSteps];
-        float2 begin[kSums];
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) q2[k] = qb[k][lane];
+        float2 begin[kSums];
 #pragma unroll
         for (int k = 0; k < kSums; ++k) begin[k] = *reinterpret_cast<const float2*>(&qbase[k][h0]);
 #pragma unroll
@@ -217,50 +224,55 @@ __global__ void __launch_bounds__(TH, TH == 128 ? 4 : 1) select_kernel(const Sel
             asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
             __syncwarp();
             const uint8_t* stage = ring + (m % kDepth) * kGroup;
-            uint4 kc[2][D / 64];
+            float best[2][2];                                       // of blocks 16 t + 8 e + r8, over two heads
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+            for (int t = 0; t < 2; ++t) {
+                uint4 kc[2][D / 64];
 #pragma unroll
-                for (int w = 0; w < D / 64; ++w) {
-                    const int c = D == 128 ? (j4 + 4 * w) ^ (r8 & 1) << 2 : j4;
-                    kc[e][w] = *reinterpret_cast<const uint4*>(stage + (8 * e + r8) * D + 16 * c);
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int w = 0; w < D / 64; ++w) {
+                        const int c = D == 128 ? (j4 + 4 * w) ^ (r8 & 1) << 2 : j4;
+                        kc[e][w] = *reinterpret_cast<const uint4*>(stage + (16 * t + 8 * e + r8) * D + 16 * c);
+                    }
+                float c[kSums][4];
+#pragma unroll
+                for (int k = 0; k < kSums; ++k) {
+                    c[k][0] = c[k][2] = begin[k].x;
+                    c[k][1] = c[k][3] = begin[k].y;
                 }
-            // lanes 0 and 1 of a quad have its two blocks
-            const int i = (m * kWarps + warp) * 16 + 8 * (j4 & 1) + r8;
-            const float sk = *reinterpret_cast<const float*>(stage + 16 * D + 4 * (8 * (j4 & 1) + r8));
-            float c[kSums][4];
 #pragma unroll
-            for (int k = 0; k < kSums; ++k) {
-                c[k][0] = c[k][2] = begin[k].x;
-                c[k][1] = c[k][3] = begin[k].y;
-            }
+                for (int k = 0; k < kSteps; ++k) {
+                    uint32_t a[4];
 #pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-                uint32_t a[4];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint4 v = kc[e][k / 4];
-                    const uint32_t w = (k % 4 == 0 ? v.x : k % 4 == 1 ? v.y : k % 4 == 2 ? v.z : v.w) ^ 0x80808080u;
-                    a[e] = __byte_perm(w, 0x64646464u, 0x4140);
-                    a[e + 2] = __byte_perm(w, 0x64646464u, 0x4342);
+                    for (int e = 0; e < 2; ++e) {
+                        const uint4 v = kc[e][k / 4];
+                        const uint32_t w = (k % 4 == 0 ? v.x : k % 4 == 1 ? v.y : k % 4 == 2 ? v.z : v.w) ^ 0x80808080u;
+                        a[e] = __byte_perm(w, 0x64646464u, 0x4140);
+                        a[e + 2] = __byte_perm(w, 0x64646464u, 0x4342);
+                    }
+                    mma16::mma16816<false>(c[k / 2], a, q2[k].x, q2[k].y);
                 }
-                mma16::mma16816<false>(c[k / 2], a, q2[k].x, q2[k].y);
+#pragma unroll
+                for (int k = 1; k < kSums; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) c[0][e] += c[k][e];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    best[t][e] = fmaxf(__fmul_rn(c[0][2 * e], sq[0]), __fmul_rn(c[0][2 * e + 1], sq[1]));
             }
-            float best[2];
+            // over all heads, lane j of a quad block 16 (j / 2) + 8 (j % 2) + r8
+            float top[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float dot[2] = {c[0][2 * e], c[0][2 * e + 1]};
-#pragma unroll
-                for (int k = 1; k < kSums; ++k) {
-                    dot[0] += c[k][2 * e];
-                    dot[1] += c[k][2 * e + 1];
-                }
-                best[e] = h0 < G ? __fmul_rn(dot[0], sq[0]) : -INFINITY;
-                if (h0 + 1 < G) best[e] = fmaxf(best[e], __fmul_rn(dot[1], sq[1]));
-                best[e] = fmaxf(best[e], __shfl_xor_sync(0xffffffffu, best[e], 1));
-                best[e] = fmaxf(best[e], __shfl_xor_sync(0xffffffffu, best[e], 2));
+                const float got = __shfl_xor_sync(0xffffffffu, j4 & 2 ? best[0][e] : best[1][e], 2);
+                top[e] = fmaxf(j4 & 2 ? best[1][e] : best[0][e], got);
             }
-            if (j4 < 2 && i < n) {
+            const float last = __shfl_xor_sync(0xffffffffu, j4 & 1 ? top[0] : top[1], 1);
+            const float score = fmaxf(j4 & 1 ? top[1] : top[0], last);
+            const int in_group = 8 * j4 + r8, i = (m * kWarps + warp) * 32 + in_group;
+            const float sk = *reinterpret_cast<const float*>(stage + 32 * D + 4 * in_group);
+            if (i < n) {
                 uint32_t key = 0;
                 if (keys[i] != 0xffffffffu) {
                     ++there;
@@ -268,7 +280,7 @@ __global__ void __launch_bounds__(TH, TH == 128 ? 4 : 1) select_kernel(const Sel
                         key = kForced;
                         there += 1 << 16;
                     } else {
-                        key = key_of(sk == INFINITY ? INFINITY : __fmul_rn(j4 ? best[1] : best[0], sk));
+                        key = key_of(sk == INFINITY ? INFINITY : __fmul_rn(score, sk));
                         least = max(least, ~key);
                         most = max(most, key);
                     }
@@ -433,7 +445,7 @@ int launch_select(const SelectParams& prm, long long rows, int cluster, cudaStre
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(rows * cluster));
     cfg.blockDim = dim3(TH);
-    cfg.dynamicSmemBytes = TH / 32 * kDepth * (16 * D + 64) + 4 * static_cast<size_t>(((blocks + cluster - 1) / cluster + 15) & ~15);
+    cfg.dynamicSmemBytes = TH / 32 * kDepth * (32 * D + 128) + 4 * static_cast<size_t>(((blocks + cluster - 1) / cluster + 31) & ~31);
     cfg.stream = st;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
@@ -450,18 +462,18 @@ int select(const SelectParams& prm, int B, cudaStream_t st) {
     if (sms <= 0) sms = 148;
     const long long rows = static_cast<long long>(B) * prm.Hkv;
     const int blocks = prm.max_pages * (prm.page_size / kBlockRows);
-    // Where a row can have an SM to itself, a CTA has 512 threads, and a cluster as many SMs as there are, with 512
-    // blocks a CTA at least (1 sequence of 8192 blocks, 8 kv heads: 13.6 us by 8 CTAs, 35.3 by one; of 1024 blocks
-    // 11.2 by two, 10.3 by one, and 11.4 to 13.9 at 2048).  With few blocks the way through its barriers is longer
-    // than the counts (100 blocks: 6.6 us, 5.5 by 128 threads; 257: 7.3 and 7.0; 512: 8.7 and 9.4).
+    // Where a row can have an SM to itself, a CTA has 512 threads, and a long row a cluster of as many SMs as there are,
+    // with 512 blocks a CTA at least (1 sequence of 8192 blocks, 8 kv heads: 12.9 us by clusters of eight, 35 by one
+    // CTA; 2048 blocks: 11.1 by four, 12.5 by two; but 1024: 10.9 by two, 9.7 by one).  With few blocks the way through
+    // its barriers is longer than the counts (512 blocks: 8.4 us, 7.9 by 128 threads; 257: 7.3 and 6.2).
     int cluster = 1;
-    if (rows <= sms && blocks > 384) {
-        while (cluster < kMaxCluster && rows * cluster * 2 <= sms && blocks >= 1024 * cluster) cluster *= 2;
+    if (rows <= sms && blocks > 768) {
+        while (cluster < kMaxCluster && rows * cluster * 2 <= sms && blocks >= std::max(1024 * cluster, 2048)) cluster *= 2;
         // (the rings of many warps and the keys of more blocks do not both fit)
         if (blocks <= 16384 * cluster) return launch_select<D, BF16, 512>(prm, rows, cluster, st);
     }
-    // Small CTAs, four an SM: 192 rows of 512 blocks take 11.3 us, 15.5 by 512 threads.  Two to a row where they are
-    // at once on the GPU and long (192 rows of 2048 blocks: 23.8 us, 29.5 by one; but 304 of 1024 19.9 and 18.3).
+    // Small CTAs, four an SM: 192 rows of 512 blocks take 9.8 us, 15.5 by 512 threads.  Two to a row where they are at
+    // once on the GPU and long (192 rows of 2048 blocks: 21.4 us, 23.5 by one; but 304 of 1024 18.8 and 16.3).
     cluster = rows * 2 <= 4 * sms && blocks >= 2048 ? 2 : 1;
     return launch_select<D, BF16, 128>(prm, rows, cluster, st);
 }
