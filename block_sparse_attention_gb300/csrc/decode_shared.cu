@@ -4,12 +4,16 @@
 //     out = softmax_j(q . k_j / sqrt(d)) v_j,   j over the prefix's tokens and the sequence's own
 //
 // The softmax over both is joined from its parts: with (O, L) the result and log-sum-exp of a part,
-// out = sum O 2^(L - M) / sum 2^(L - M).  This file's kernel does the prefixes: the query heads of a kv head of
-// all sequences that share one are the rows of its products, so K and V of a prefix are read once for up to
-// 256 rows and not once a sequence.  decode_shared_own.cuh does the sequences' own tokens.
+// out = sum O 2^(L - M) / sum 2^(L - M).  One kernel makes the parts, and each of its CTAs has one of two roles.
+// Some have the sequences' own tokens (decode_shared_own.cuh).  The others have the prefixes: the query heads of a kv
+// head of all sequences that share one are the rows of its products, so K and V of a prefix are read once for up to
+// 256 rows and not once a sequence.  Own tokens are bound by HBM bandwidth, prefixes with many rows by the tensor core
+// (256 rows of d = 128: 256 operations a byte against the 280 that the two peaks divide to), so they run beside each
+// other: 256 sequences of 1000 own tokens on the average over 65521, 32 / 8 heads, take 262 us; 189 with prefixes alone,
+// 170 with own tokens alone, and 363 by two kernels one after the other.  A CTA learns its role from the lengths, which
+// every CTA adds up for itself (3 us).
 //
-// For few rows HBM bandwidth bounds this, for many the tensor core (256 rows of d = 128: 256 operations a
-// byte against the 280 that the two peaks divide to).  The rows stand in two tcgen05 tiles a CTA:
+// The rows of a prefix stand in two tcgen05 tiles a CTA:
 //     S_x = Q_x K^T    M=128 N=128 K=d, fp32 in TMEM
 //     P_x              exp2 online softmax, one thread a row, written over S_x as the 16-bit type
 //     O_x += P_x V     M=128 N=d K=128, A = P_x from TMEM
@@ -18,7 +22,9 @@
 // when it has grown by 2^8.  Where a prefix has no more than 128 rows, both tiles are the same rows and take
 // every second key tile each, without turns.
 // The prefixes' keys, end to end, are cut into equal parts, one a CTA, so that one long prefix and many
-// short ones both fill the GPU (decode_shared.cuh); a CTA goes from one piece to the next without a break.
+// short ones both fill their share of the GPU (decode_shared.cuh); a CTA goes from one piece to the next without a
+// break.  With few rows the way to the first tile's end (14 us of 68 for 64 sequences over 32768 tokens: lengths, page
+// table, queries and keys, and this code, which comes from memory too) and the joining (9 us) are what shows.
 //
 // TMEM: S_0 0-127, S_1 128-255, O_0 256.., O_1 256 + d...  Every wait is bounded: on expiry the CTA records
 // BSATTN_ERR_TIMEOUT, hands its remaining pieces over as NaN, drains what is in flight and leaves.
@@ -736,13 +742,15 @@ struct Layout {
 Layout layout_of(int B, int P, int Hq, int Hkv, int d, int sms) {
     Layout w{};
     const int G = Hq / Hkv, tile = 128 / G;              // sequences of a 128-row tile
-    // A prefix with no more than a tile of rows, on the average, has both query tiles of a CTA to itself.
+    // A prefix with no more than a tile of rows, on the average, has both query tiles of a CTA to itself (192 sequences
+    // over 6 prefixes, d = 64: 79 us, 100 with one of the tiles empty).
     w.halves = (static_cast<long long>(B) + P - 1) / P <= tile;
     w.seqs = w.halves ? tile : 2 * tile;
     w.part_rows = w.seqs * G;
     // A prefix with no more rows than a CTA has is read once: all its kv heads at the same keys at the same time, as
-    // those lie next to each other in the cache (64 sequences over 32768 tokens: 76 us for 85).  One prefix with more is
-    // read several times: at the same time, so that all but one reading comes from L2.
+    // those lie next to each other in the cache (64 sequences over 32768 tokens: 68 us for 74).  One prefix with more is
+    // read several times: at the same time, so that all but one reading comes from L2 (256 sequences over 65521: 262 us
+    // for 345).
     const int times = (B + w.seqs - 1) / w.seqs;
     w.side = (static_cast<long long>(B) + P - 1) / P <= w.seqs && 2 * Hkv <= sms ? Hkv : 1;
     w.deep = P == 1 && times > 1 ? (times + (times + 7) / 8 - 1) / ((times + 7) / 8) : 1;
