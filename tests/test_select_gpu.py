@@ -84,6 +84,11 @@ def test_update_many_sequences(bsa):
     _check_update(bsa, k, lens, new, _table(lens, 64, 2900, 2))
 
 
+def test_update_more_blocks_than_all_warps_look_up_at_once(bsa):
+    k = _rand(2300, 64, 17, 64, dtype=F16, seed=5)
+    _check_update(bsa, k, [2200 * 64 - 3, 70], [2200 * 64 - 3, 70], _table([2200 * 64 - 3, 70], 64, 2300, 4))
+
+
 def test_update_one_token_at_a_time(bsa):
     """Token by token is the same as all at once; what stands past the end has no effect."""
     k = _rand(4, 64, 2, 128, dtype=BF16, seed=5)
@@ -283,6 +288,19 @@ def test_select_long(bsa, d, page):
     assert got[1, 0].tolist() == [0] + [-1] * 99
 
 
+@pytest.mark.parametrize("B,hkv,width", [(1, 8, 768), (1, 8, 769), (2, 8, 2047), (2, 8, 2048), (9, 8, 2300), (1, 8, 4500),
+                                         (19, 8, 2050), (25, 8, 2100), (40, 8, 2047), (80, 8, 2048), (50, 3, 900)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_select_rows_of_one_cta_and_of_several(bsa, B, hkv, width, d):
+    """Tables of few and many blocks, rows that fill the GPU or do not, sequences much shorter than the table."""
+    lens = [(width * 64, 1, 33 * 64 + 1, 0, 517 * 64, 1024 * 64 - 5)[b % 6] if b < 12 else 64 * (b % 50) for b in range(B)]
+    lens = [min(n, width * 64) for n in lens]
+    pages = sum(-(-n // 64) for n in lens) + 1
+    index = _random_index(bsa, pages, 1, hkv, d, seed=width)
+    q = _rand(B, 2 * hkv, d, dtype=BF16, seed=B)
+    _check_select(bsa, q, index, lens, _table(lens, 64, pages, 9, most=width), 70, 1, 3)
+
+
 # ------------------------------------------------------------------------- masks
 
 def _check_mask(bsa, q, k, topk, causal, sinks, recent, dense):
@@ -331,6 +349,24 @@ def test_mask_long_rows(bsa, Sk):
     q, k = _rand(1, 1, 600, 64, dtype=BF16, seed=3), _rand(1, 1, Sk, 64, dtype=BF16, seed=4)
     _check_mask(bsa, q, k, 50, True, 1, 2, True)
     _check_mask(bsa, q, k, 700, False, 0, 0, False)
+
+
+def test_mask_of_many_heads(bsa):
+    """More CTAs than SMs."""
+    q, k = _rand(2, 40, 1100, 64, dtype=BF16, seed=3), _rand(2, 8, 1300, 64, dtype=BF16, seed=4)
+    _check_mask(bsa, q, k, 5, True, 1, 1, True)
+    _check_mask(bsa, q[:, :, :1030], k[:, :, :1030], 3, False, 0, 2, False)
+
+
+def test_mask_output_at_any_address(bsa):
+    q, k = _rand(1, 2, 300, 64, dtype=F16, seed=3), _rand(1, 2, 1024, 64, dtype=F16, seed=4)
+    want = bsa.bsattn_mask_from_qk(q, k, 5, True)
+    flat = torch.full((want.numel() + 3,), 9, dtype=torch.uint8, device="cuda")
+    for at in range(4):
+        flat.fill_(9)
+        out = flat[at:at + want.numel()].view(want.shape)
+        assert torch.equal(bsa.bsattn_mask_from_qk(q, k, 5, True, out=out), want)
+        assert (flat[:at] == 9).all() and (flat[at + want.numel():] == 9).all()
 
 
 def test_mask_extreme_values(bsa):
