@@ -9,7 +9,7 @@
 // head of all sequences that share one are the rows of its products, so K and V of a prefix are read once for up to
 // 256 rows and not once a sequence.  Own tokens are bound by HBM bandwidth, prefixes with many rows by the tensor core
 // (256 rows of d = 128: 256 operations a byte against the 280 that the two peaks divide to), so they run beside each
-// other: 256 sequences of 1000 own tokens on the average over 65521, 32 / 8 heads, take 262 us; 189 with prefixes alone,
+// other: 256 sequences of 1000 own tokens on the average over 65521, 32 / 8 heads, take 250 us; 180 with prefixes alone,
 // 170 with own tokens alone, and 363 by two kernels one after the other.  A CTA learns its role from the lengths, which
 // every CTA adds up for itself (3 us).
 //
@@ -23,8 +23,8 @@
 // every second key tile each, without turns.
 // The prefixes' keys, end to end, are cut into equal parts, one a CTA, so that one long prefix and many
 // short ones both fill their share of the GPU (decode_shared.cuh); a CTA goes from one piece to the next without a
-// break.  With few rows the way to the first tile's end (14 us of 68 for 64 sequences over 32768 tokens: lengths, page
-// table, queries and keys, and this code, which comes from memory too) and the joining (9 us) are what shows.
+// break.  With few rows the way to the first tile's end (lengths, page table, queries and keys, and this code, which has
+// to come to every SM too: 10 us of 58 for 64 sequences over 32768 tokens) and the joining (9 us) are what shows.
 //
 // TMEM: S_0 0-127, S_1 128-255, O_0 256.., O_1 256 + d...  Every wait is bounded: on expiry the CTA records
 // BSATTN_ERR_TIMEOUT, hands its remaining pieces over as NaN, drains what is in flight and leaves.
@@ -64,9 +64,9 @@ struct Cfg {
     static constexpr uint32_t kBytes = 1024 + kMissing + 4 * kNotes;
     static_assert(kBytes <= 226 * 1024, "shared memory");        // the scan's static arrays beside it
     // What a unit of a prefix costs, in units of own tokens: 1.6 us a CTA, while its 12 warps would have that many of the
-    // others.  (256 sequences of 1000 own tokens over 65521: 282 us with 16, 262 with 13, 285 with 10; d = 64, 192 over
-    // 6 prefixes: 85 with 16, 79 with 20, 87 with 24.)
-    static constexpr float kCost = D == 128 ? 13.f : 20.f;
+    // others.  (256 sequences of 1000 own tokens over 65521: 258 us with 12, 250 with 13, 274 with 14; d = 64, 192 over
+    // 6 prefixes: 75 with 17 to 20, 86 with 22.)
+    static constexpr float kCost = D == 128 ? 13.f : 18.f;
 };
 
 struct PrefixParams {
@@ -328,6 +328,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         Piece piece;
         if (warp == kLoadWarp) {
             // ------------------------------------------------------------ TMA
+            // K and V of the prefixes and of the own tokens are streamed past what is in L2 and read again: this code,
+            // which every SM fetches at the start, the pieces, the tables (64 sequences over 32768 tokens: 58.7 us, 67.7
+            // without; a few tokens' worth only: the same).
+            const uint64_t once = l2_evict_first();
             int g = 0;                                   // tiles loaded, K and V counted apart
             int nq[2] = {0, 0};                          // Q tiles loaded
             bool ok = true, bad = false;
@@ -379,8 +383,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int h = 0; h < D / 64; ++h) {
                                 uint8_t* dst = skv + st * C::kTile + h * 16384;
-                                tma_load_3d(dst, v ? &tm_v : &tm_k, &full[st], h * 64, piece.kvh, r0 < 0 ? none : r0);
-                                tma_load_3d(dst + 8192, v ? &tm_v : &tm_k, &full[st], h * 64, piece.kvh, r1 < 0 ? none : r1);
+                                tma_load_3d(dst, v ? &tm_v : &tm_k, &full[st], h * 64, piece.kvh, r0 < 0 ? none : r0, once);
+                                tma_load_3d(dst + 8192, v ? &tm_v : &tm_k, &full[st], h * 64, piece.kvh, r1 < 0 ? none : r1, once);
                             }
                         }
                         ++g;
@@ -743,12 +747,12 @@ Layout layout_of(int B, int P, int Hq, int Hkv, int d, int sms) {
     Layout w{};
     const int G = Hq / Hkv, tile = 128 / G;              // sequences of a 128-row tile
     // A prefix with no more than a tile of rows, on the average, has both query tiles of a CTA to itself (192 sequences
-    // over 6 prefixes, d = 64: 79 us, 100 with one of the tiles empty).
+    // over 6 prefixes, d = 64: 79 us, and 100 with one of the tiles empty).
     w.halves = (static_cast<long long>(B) + P - 1) / P <= tile;
     w.seqs = w.halves ? tile : 2 * tile;
     w.part_rows = w.seqs * G;
     // A prefix with no more rows than a CTA has is read once: all its kv heads at the same keys at the same time, as
-    // those lie next to each other in the cache (64 sequences over 32768 tokens: 68 us for 74).  One prefix with more is
+    // those lie next to each other in the cache (64 sequences over 32768 tokens: 68 us for 74, before the streams passed L2 by).  One prefix with more is
     // read several times: at the same time, so that all but one reading comes from L2 (256 sequences over 65521: 262 us
     // for 345).
     const int times = (B + w.seqs - 1) / w.seqs;

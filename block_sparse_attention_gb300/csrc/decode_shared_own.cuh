@@ -6,8 +6,9 @@
 // on their way before the one before is done), and what it has of a sequence goes to the workspace as a piece.
 // The products are those of decode_stream.cu, transposed, so that the G heads are the n = 8 side of mma.sync
 // m16n8k16: S^T [16 keys x 8] = K Q^T and O^T [d x 8] += V^T P^T.
-// An SM does 124 GB/s so (d = 128, its 12 warps, 192 KB on their way), set by the warps' instructions: the whole GPU is
-// at 6.2 TB/s, a quarter of it at 4.7.  Units of 64 keys by six warps: the same; of 16 keys: half of it.
+// An SM does 124 GB/s so (d = 128, its 12 warps, 192 KB on their way): each byte is written to shared memory and read
+// from it once, and 128 bytes a cycle allow no more than 130.  The whole GPU is at 6.2 TB/s, a quarter of it at 4.7.
+// Units of 64 keys by six warps: the same; of 16 keys: half of it.
 #pragma once
 
 #include <climits>
@@ -130,6 +131,7 @@ __device__ __forceinline__ void own_tokens(const CUtensorMap* tm_k, const CUtens
             return;
         }
     };
+    const uint64_t once = l2_evict_first();
     int issued = 0;
     // Half h is K of unit h / 2 if h is even, its V if it is odd.
     const auto issue = [&](int h) {
@@ -149,7 +151,7 @@ __device__ __forceinline__ void own_tokens(const CUtensorMap* tm_k, const CUtens
                 mbar_arrive_expect_tx(&full[st], R::kStage);
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c)
-                    tma_load_3d(ring + st * R::kStage + c * (kTok * 128), h & 1 ? tm_v : tm_k, &full[st], c * 64, g, row);
+                    tma_load_3d(ring + st * R::kStage + c * (kTok * 128), h & 1 ? tm_v : tm_k, &full[st], c * 64, g, row, once);
             }
         }
         __syncwarp();
