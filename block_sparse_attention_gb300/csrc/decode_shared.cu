@@ -9,8 +9,8 @@
 // head of all sequences that share one are the rows of its products, so K and V of a prefix are read once for up to
 // 256 rows and not once a sequence.  Own tokens are bound by HBM bandwidth, prefixes with many rows by the tensor core
 // (256 rows of d = 128: 256 operations a byte against the 280 that the two peaks divide to), so they run beside each
-// other: 256 sequences of 1000 own tokens on the average over 65521, 32 / 8 heads, take 250 us; 180 with prefixes alone,
-// 170 with own tokens alone, and 363 by two kernels one after the other.  A CTA learns its role from the lengths, which
+// other: 256 sequences of 1000 own tokens on the average over 65521, 32 / 8 heads, take 250 us; 177 with prefixes alone,
+// 165 with own tokens alone, and 363 by two kernels one after the other.  A CTA learns its role from the lengths, which
 // every CTA adds up for itself (3 us).
 //
 // The rows of a prefix stand in two tcgen05 tiles a CTA:

@@ -1,7 +1,7 @@
 // decode_shared_join.cu -- a decode over shared prefixes: the joining of all pieces, sm_103a.
 //
 // A warp a row: with (O, L) of each piece, out = sum O 2^(L - M) / sum 2^(L - M), in a fixed order.  What there is to
-// read is in L2, so a chain of latencies bounds this: the L of 32 pieces come at once, then the O of eight.
+// read is in L2, so a chain of latencies bounds this: the L of 32 pieces come at once, and the O of eight with them.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -68,10 +68,23 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const SharedCall p) {
                : p.halves  ? first + (n >> 1) * by + (n & 1) * other
                            : first + n * by;
     };
-    // 32 pieces at a time: first their L, one a lane, so that all that is read of O after that is on its way together
+    // 32 pieces at a time: their L, one a lane, and with them the O of the first eight
     for (int k0 = share; k0 < count; k0 += 32 * WARPS) {
+        const int here = min((count - k0 + WARPS - 1) / WARPS, 32);
+        V ov[kBatch];
+        const auto fetch = [&](int k1) {
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                ov[k] = V{};
+                if (k1 + k < here) {
+                    const int at = k0 + (k1 + k) * WARPS;
+                    ov[k] = __ldcg(reinterpret_cast<const V*>((at < shared ? p.prefix_o : p.own_o) + place(at) * D) + lane);
+                }
+            }
+        };
         const int n = k0 + lane * WARPS;
         const float mine_l = n < count ? __ldcg((n < shared ? p.prefix_lse : p.own_lse) + place(n)) : -INFINITY;
+        fetch(0);
         float top = mine_l;
 #pragma unroll
         for (int w = 1; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
@@ -81,29 +94,21 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const SharedCall p) {
         den *= down;
 #pragma unroll
         for (int e = 0; e < kC; ++e) num[e] *= down;
-        // (where a row has met no finite score O may not have been written)
         const float weight = mine_l == -INFINITY ? 0.f : ex2_approx(mine_l - ref);
         den += weight;                                   // of this lane's pieces
-        const int here = min((count - k0 + WARPS - 1) / WARPS, 32);
-        for (int k1 = 0; k1 < here; k1 += kBatch) {
-            V ov[kBatch];
-            float w[kBatch];
+        for (int k1 = 0;;) {
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
-                w[k] = __shfl_sync(0xffffffffu, weight, (k1 + k) & 31);
-                ov[k] = V{};
-                if (k1 + k < here && w[k] != 0.f) {
-                    const int at = k0 + (k1 + k) * WARPS;
-                    ov[k] = __ldcg(reinterpret_cast<const V*>((at < shared ? p.prefix_o : p.own_o) + place(at) * D) + lane);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                if (k1 + k >= here) w[k] = 0.f;
+                const float w = __shfl_sync(0xffffffffu, weight, (k1 + k) & 31);
+                // (where a row has met no finite score O may not have been written)
+                if (k1 + k >= here || w == 0.f) continue;
                 const float* v = reinterpret_cast<const float*>(&ov[k]);
 #pragma unroll
-                for (int e = 0; e < kC; ++e) num[e] = fmaf(w[k], v[e], num[e]);
+                for (int e = 0; e < kC; ++e) num[e] = fmaf(w, v[e], num[e]);
             }
+            k1 += kBatch;
+            if (k1 >= here) break;
+            fetch(k1);
         }
     }
 #pragma unroll
