@@ -8,7 +8,8 @@
 // neighbouring heads lie next to each other.  The lanes look up where 32 of a warp's blocks lie at once, and the
 // warp has the rows of two (d = 64: four) on their way while it adds up another's.  16 prompts of 512 to 8191 tokens, 8
 // heads, d = 128: 144 MB in 29 us (31.4 with sixteen 16-byte loads a lane in registers instead), 5 of them until
-// the first rows are on their way; a step of 64 sequences: 5.0 us.
+// the first rows are on their way; a step of 64 sequences: 4.5 us (5.0 with
+// its 512 blocks on half of the SMs).
 #include <algorithm>
 #include <climits>
 
@@ -89,7 +90,8 @@ __global__ void __launch_bounds__(kThreads, 1) update_kernel(const UpdateParams 
     const long long step = static_cast<long long>(p.Hkv) * D * 2;
     const Ring ring(ring_smem + warp * Ring::kBytes);
     bool bad = false;
-    for (long long base = static_cast<long long>(blockIdx.x) * kWarps + warp; base < tasks; base += 32 * stride) {
+    // (few tasks: one a CTA first)
+    for (long long base = blockIdx.x + static_cast<long long>(gridDim.x) * warp; base < tasks; base += 32 * stride) {
         // ---------------------------------------------------------------- lane l: where the warp's l-th block lies
         const long long task = base + lane * stride;
         int of_block = -1, count = 0;                       // its place in the index over Hkv, and its rows

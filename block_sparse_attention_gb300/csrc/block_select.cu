@@ -481,12 +481,11 @@ int select(const SelectParams& prm, int B, cudaStream_t st) {
 // ------------------------------------------------------------------------------------------ prompts
 //
 // Two kernels.  One summarises the blocks of q and k, a warp each, HBM-bound (32 heads of 16384 tokens, d = 128, 268
-// MB: 47 us, 5.7 TB/s); codes are kept as 16-bit whole numbers for the other, which takes 16 query blocks of a head a
+// MB: 45 us, 6 TB/s); codes are kept as 16-bit whole numbers for the other, which takes 16 query blocks of a head a
 // CTA: products by mma.sync m16n8k16 (whole numbers: exact), keys of the 16 rows in shared memory, then a warp a row
-// to find its threshold and write its bytes (19 us there, a chain of latencies).  Under the causal rule a CTA goes no
+// to find its threshold and write its bytes (16 us there, a chain of latencies).  Under the causal rule a CTA goes no
 // further than its rows see.
 
-constexpr int kSumThreads = 7 * 32;      // 32 KB of shared memory a warp
 
 struct MaskParams {
     const void* x[2];                    // q, k
@@ -501,15 +500,15 @@ struct MaskParams {
     int wide;                            // four bytes of the mask can be written at once
 };
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kSumThreads, 1) summarise_kernel(const MaskParams p) {
-    using Ring = BlockRing<D>;
+template <int D, bool BF16, int WARPS, int BYTES>
+__global__ void __launch_bounds__(32 * WARPS, 1) summarise_kernel(const MaskParams p) {
+    using Ring = BlockRing<D, BYTES>;
     extern __shared__ __align__(128) uint8_t ring_smem[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t of_q = static_cast<uint32_t>(p.B) * p.H[0] * p.n[0];
     const uint32_t tasks = of_q + static_cast<uint32_t>(p.B) * p.H[1] * p.n[1];
-    const uint32_t stride = gridDim.x * (kSumThreads / 32);
+    const uint32_t stride = gridDim.x * WARPS;
     const Ring ring(ring_smem + warp * Ring::kBytes);
     struct Task {
         int t, b, h, j, count;
@@ -569,7 +568,7 @@ __device__ __forceinline__ void mma_whole(float (&c)[4], const uint32_t (&a)[4],
 }
 
 template <int D, int TH>
-__global__ void __launch_bounds__(TH, TH == 256 ? 2 : 1) mask_kernel(const MaskParams p) {
+__global__ void __launch_bounds__(TH, TH == 256 ? 3 : 1) mask_kernel(const MaskParams p) {
     constexpr int kMaskWarps = TH / 32;
     extern __shared__ __align__(16) uint32_t keys[];        // [rows][pitch]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -806,22 +805,30 @@ int launch_rows(const MaskParams& prm, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, kern, prm) == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
 }
 
+template <int D, bool BF16, int WARPS, int BYTES>
+int launch_summaries(const MaskParams& prm, long long tasks, int sms, cudaStream_t st) {
+    auto kern = summarise_kernel<D, BF16, WARPS, BYTES>;
+    static std::atomic<unsigned long long> raised{0};
+    const int rc = raise_smem_limit(reinterpret_cast<const void*>(kern), WARPS * BYTES, raised);
+    if (rc) return rc;
+    // a task a CTA first, then more
+    kern<<<static_cast<unsigned>(std::min<long long>(tasks, sms)), 32 * WARPS, WARPS * BYTES, st>>>(prm);
+    return cudaGetLastError() == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
+}
+
 template <int D, bool BF16>
 int launch_mask(const MaskParams& prm, cudaStream_t st) {
     const long long tasks = static_cast<long long>(prm.B) * (static_cast<long long>(prm.H[0]) * prm.n[0] +
                                                              static_cast<long long>(prm.H[1]) * prm.n[1]);
-    auto summarise = summarise_kernel<D, BF16>;
-    constexpr int kWarps = kSumThreads / 32, kSmem = kWarps * BlockRing<D>::kBytes;
-    static std::atomic<unsigned long long> raised{0};
-    const int rc = raise_smem_limit(reinterpret_cast<const void*>(summarise), kSmem, raised);
-    if (rc) return rc;
     int sms = num_sms_of_current_device();
     if (sms <= 0) sms = 148;
-    // a task a CTA first, then more
-    summarise<<<static_cast<unsigned>(std::min<long long>(tasks, sms)), kSumThreads, kSmem, st>>>(prm);
-    if (cudaGetLastError() != cudaSuccess) return BSATTN_ERR_CUDA;
+    // Seven warps with 32 KB each where a warp has few blocks, and the way of the last one counts (2048 blocks: 13.4 us
+    // for both kernels, 14.7 by four warps), four with 48 KB where it has many (16384 blocks: 60.8 us, 62.7 by seven).
+    const int rc = tasks < 32LL * sms ? launch_summaries<D, BF16, 7, 32768>(prm, tasks, sms, st)
+                                      : launch_summaries<D, BF16, 4, 49152>(prm, tasks, sms, st);
+    if (rc) return rc;
     // 16 rows by 16 warps where every CTA has an SM to itself (64 CTAs of 64 key blocks: 13.5 us for both kernels, 15.5
-    // by 8 warps), by 8 where there are more (512 CTAs of 256 key blocks: 64 us, 69 by 16 warps)
+    // by 8 warps), by 8 where there are more (512 CTAs of 256 key blocks: 61 us, 69 by 16 warps)
     const long long ctas = static_cast<long long>((prm.n[0] + prm.rows - 1) / prm.rows) * prm.B * prm.H[0];
     return ctas <= sms ? launch_rows<D, 512>(prm, st) : launch_rows<D, 256>(prm, st);
 }

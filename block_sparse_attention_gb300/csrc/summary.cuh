@@ -70,15 +70,15 @@ __device__ __forceinline__ void thresholds(uint32_t lo, uint32_t hi, int step, u
 }
 
 // A warp's blocks on their way to it: stages of 64 rows in shared memory, of which a lane copies and adds up the same
-// 16-byte pieces, so that it waits for its own copies only and 32 KB a warp are on their way whatever the registers
+// 16-byte pieces, so that it waits for its own copies only and BYTES a warp are on their way whatever the registers
 // hold.  Lane l has channels 8 (l % (D / 8)) + 0 .. 7 of rows kAt j + l / (D / 8).
-template <int D>
+template <int D, int BYTES = 32768>
 struct BlockRing {
     static constexpr int kAt = 256 / D;              // rows that a warp copies at once: 2 or 4
     static constexpr int kEach = kBlockRows / kAt;   // rows of a lane: 32 or 16
     static constexpr int kStage = kBlockRows * D * 2;
-    static constexpr int kBytes = 32768;
-    static constexpr int kDepth = kBytes / kStage;   // 2 or 4 blocks
+    static constexpr int kBytes = BYTES;
+    static constexpr int kDepth = kBytes / kStage;   // 2 or 4 blocks of 32 KB
     uint8_t* at;                                     // the stages from the lane's first piece on
 
     __device__ __forceinline__ explicit BlockRing(uint8_t* base) : at(base + (threadIdx.x & 31) * 16) {}

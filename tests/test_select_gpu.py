@@ -358,6 +358,13 @@ def test_mask_of_many_heads(bsa):
     _check_mask(bsa, q[:, :, :1030], k[:, :, :1030], 3, False, 0, 2, False)
 
 
+@pytest.mark.parametrize("d,dtype", [(64, F16), (128, BF16)])
+def test_mask_of_many_blocks(bsa, d, dtype):
+    """Dozens of blocks for every SM."""
+    q, k = _rand(1, 50, 3300, d, dtype=dtype, seed=5), _rand(1, 50, 3201, d, dtype=dtype, seed=6)
+    _check_mask(bsa, q, k, 6, True, 1, 1, False)
+
+
 def test_mask_output_at_any_address(bsa):
     q, k = _rand(1, 2, 300, 64, dtype=F16, seed=3), _rand(1, 2, 1024, 64, dtype=F16, seed=4)
     want = bsa.bsattn_mask_from_qk(q, k, 5, True)
