@@ -534,6 +534,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t ts = tbase + lanes + 128 * x, to = tbase + lanes + kOCol + D * x;
         const float c = p.s.scale_log2;
+        // A weight is exp2(x c - reference(m)), m the maximum that the row goes by.  fp16 ones are taken 2^kUp times as large,
+        // so that those down to 2^-32 of the largest (2^-25, half of the smallest subnormal, for 2^7) count in O as they
+        // do in l: ten thousand keys of 2^-25 each would else be lost from O alone.  m may lag by kRescaleLog2, so none
+        // passes 2^15; where scores are so large that their rounding shows, m does not lag and the reference is
+        // rounded up.  bf16 reaches far enough as it is.
+        constexpr float kUp = BF16 ? 0.f : 7.f, kLagBelow = 1048576.f;
+        static_assert(BF16 || kUp + kRescaleLog2 <= 15.f, "weights below 65504");
+        const auto reference = [c](float m) { return BF16 ? m * c : __fmaf_ru(m, c, -kUp); };
         const bool speaks = (warp & 3) == 0 && lane == 0;
         const int tile_rows = HALVES ? p.s.part_rows : p.s.part_rows / 2;
         const int irow = HALVES ? lrow : x * tile_rows + lrow;       // row of the item
@@ -593,12 +601,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     mx = fmaxf(max3f(m4[0], m4[1], m4[2]), m4[3]);
                 }
-                const bool grow = mx * c > m_used * c + kRescaleLog2;
+                const float used = m_used * c;
+                const bool grow = mx * c > used + kRescaleLog2 || (!BF16 && mx > m_used && !(fabsf(used) < kLagBelow));
                 const float m_new = grow ? mx : m_used;
                 const float alpha = grow ? ex2_approx((m_used - m_new) * c) : 1.f;
                 const bool rescale = grow && m_used != -INFINITY;
                 m_used = m_new;
-                const float mc = m_new == -INFINITY ? 0.f : m_new * c;
+                const float mc = m_new == -INFINITY ? 0.f : reference(m_new);
                 if (__any_sync(0xffffffffu, rescale)) {
                     // O holds every tile before this one: their P V ran before this tile's S
 #pragma unroll 1
@@ -703,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (mine) {
-                p.s.prefix_lse[at] = l == 0.f ? -INFINITY : m_used * c + log2f(l);
+                p.s.prefix_lse[at] = l == 0.f ? -INFINITY : reference(m_used) + log2f(l);
             }
         }
     }

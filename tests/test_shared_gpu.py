@@ -1,4 +1,6 @@
 """Decoding over a shared prefix, against its 64-bit statement."""
+import math
+
 import pytest
 import torch
 
@@ -367,3 +369,57 @@ def test_far_pages(bsa):
     small.ptable = _i32([at[:10]])
     small.table = _i32([at[10:14], at[14:15] + [-1] * 3, at[15:16] + [-1] * 3])
     small.check(bsa)
+
+
+@pytest.mark.parametrize("at", [0, 13_000, 19_999])
+@pytest.mark.parametrize("B,group", [(1, 1), (20, 8)])
+def test_small_weights_of_a_long_prefix(bsa, B, group, at):
+    """One key that has all but a little of the weight and a value of 0, and thousands with 2^-24 to 2^-30 of it each,
+    which are all that there is of the result: fp16 weights have to keep them.  80 kv heads: a CTA has some ten
+    thousand keys of a head, with the large weight among them.  The largest weight of a row is 2^7 or more."""
+    n, hkv, d = 20_000, 80, 64
+    c = Case([B], [n], [0] * B, hkv * group, hkv, d, F16, page=64, seed=at)
+    j = torch.arange(n, device="cuda")
+    where = c.ptable[0].long()[j // 64], j % 64
+    g = torch.Generator(device="cuda").manual_seed(at + 1)
+    score = -math.log(2.0) * (24 + 6 * torch.rand(n, hkv, generator=g, device="cuda"))
+    score[at] = 0
+    k, v = torch.zeros(n, hkv, d, device="cuda"), 0.5 + torch.rand(n, hkv, d, generator=g, device="cuda")
+    k[..., 0], v[at] = score, 0
+    c.k[where], c.v[where] = k.to(F16), v.to(F16)
+    c.q.zero_()
+    c.q[..., 0] = math.sqrt(d)
+    got = c.call(bsa).view(B, hkv, group, d)
+    on = torch.ones(1, n, dtype=torch.bool, device="cuda")
+    for h in range(hkv):
+        out, bound = serving.attend(c.q[0, :1], c.k[where][:, h], c.v[where][:, h], on, F16, F16, 2.0 ** 7)
+        assert out.min() > 30 * bound.max()
+        serving.check(got[:, h], out, bound)
+
+
+@pytest.mark.parametrize("B", [3, 70])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_weights_above_the_reference(bsa, B, dtype):
+    """Scores just under 2^8 times the first tiles' ones: as much as the reference maximum may lag behind."""
+    c = Case([B], [3000], [20] * B, 8, 2, 64, dtype, seed=1)
+    c.q.zero_()
+    c.q[..., 0] = 8
+    for i, page in enumerate(c.ptable[0].tolist()):
+        c.k[page, :, :, 0] = 0.0 if i < 4 else 5.53125             # 2^7.98
+    c.check(bsa)
+
+
+@pytest.mark.parametrize("B", [3, 70])
+def test_scores_of_which_the_rounding_shows(bsa, B):
+    """fp16 scores of some 2^26 in base 2, which 32 bits have to the nearest 8, with maxima that move on by 6: no weight
+    passes the largest fp16 number."""
+    c = Case([B], [3000], [0] * B, 8, 2, 64, F16, seed=1)
+    c.q.zero_()
+    c.q[..., 0], c.q[..., 1] = 16384, 1
+    c.k[..., 0] = 22_704
+    for i, page in enumerate(c.ptable[0].tolist()):
+        c.k[page, :, :, 1] = 0 if i < 4 else 32 if i < 20 else 64
+    got = c.call(bsa)
+    top = c.v[c.ptable[0].long()].nan_to_num(0.0).abs().amax((0, 1)).repeat_interleave(4, 0)[None]
+    # a mean of values: weights of one row add up to 1, up to the rounding of each
+    assert torch.isfinite(got).all() and (got.abs() <= top * (1 + 2.0 ** -9)).all()
