@@ -538,6 +538,13 @@ def _span(window, sinks):
     return max(min(int(window), _INT_MAX), -1), max(min(int(sinks), _INT_MAX), -1)
 
 
+def _check_sizes(*tensors):
+    """Sizes of views as C ints: a broadcast one may have any."""
+    for t in tensors:
+        if t.numel() > _INT_MAX and max(t.shape) > _INT_MAX:
+            raise ValueError(f"sizes {tuple(t.shape)} do not fit 32 bits")
+
+
 def _check_out(out, q, contiguous):
     if out.get_device() != q.get_device() or out.dtype is not q.dtype or out.shape != q.shape:
         raise ValueError("out must have the queries' device, dtype and shape")
@@ -1032,6 +1039,7 @@ def bsattn_mask_from_qk(q, k, topk: int, is_causal: bool, sinks: int = 1, recent
     if _current_device() != i:
         with torch.cuda.device(i):
             return bsattn_mask_from_qk(q, k, topk, is_causal, sinks, recent, use_dense_for_last_block, out, ws)
+    _check_sizes(q, k)
     B, Hq, Sq, d = q.shape
     _, hkv, Sk, _ = k.shape
     topk, (sinks, recent) = min(int(topk), _INT_MAX), _span(sinks, recent)

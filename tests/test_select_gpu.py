@@ -506,3 +506,18 @@ def test_calls_on_other_streams_and_in_graphs(bsa):
     again = calls(bsa.bsattn_block_index(130, 2, 64, 64))
     assert all(torch.equal(a, b) for a, b in zip(captured, again))
     assert not torch.equal(captured[0], want[0]) and not torch.equal(captured[2], want[2])
+
+
+@pytest.mark.parametrize("big", [2 ** 32 + 64, 2 ** 31, 2 ** 32])
+def test_mask_sizes_past_32_bits(bsa, big):
+    """Broadcast views whose sizes a C int would cut off."""
+    x = _rand(1, 1, 64, 64, dtype=BF16, seed=1)
+    one = x[:, :, :1]
+    with pytest.raises(ValueError):
+        bsa.bsattn_mask_from_qk(x, one.expand(1, 1, big, 64), 4, True)
+    with pytest.raises(ValueError):
+        bsa.bsattn_mask_from_qk(one.expand(1, 1, big, 64), x, 4, True)
+    with pytest.raises(ValueError):
+        bsa.bsattn_mask_from_qk(one.expand(big, 1, 1, 64), one.expand(big, 1, 1, 64), 4, True)
+    with pytest.raises(ValueError):
+        bsa.bsattn_mask_from_qk(one.expand(1, big, 1, 64), one, 4, True)
