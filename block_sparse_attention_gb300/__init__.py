@@ -852,6 +852,7 @@ def bsattn_prefill_window(q, k, v, window: int, sinks: int = 0, out=None, ws=Non
     if _current_device() != i:
         with torch.cuda.device(i):
             return bsattn_prefill_window(q, k, v, window, sinks, out, ws)
+    _check_sizes(q, k)
     if out is None:
         out = torch.empty_like(q)
     else:

@@ -485,3 +485,18 @@ def test_prefill_rows_past_32_bit_offsets(bsa):
     k, v = _rand(2, 2, 40, 64, dtype=F16, seed=2), _rand(2, 2, 40, 64, dtype=F16, seed=3)
     bsa.bsattn_prefill_window(q, k, v, 9, 1, out=out)
     ref.check(out, *ref.window_prefill(q, k, v, 9, 1))
+
+
+@pytest.mark.parametrize("big", [2 ** 32 + 64, 2 ** 31, 2 ** 32])
+def test_sizes_past_32_bits(bsa, big):
+    """Broadcast views whose sizes a C int would cut off."""
+    x = torch.zeros(1, 1, 64, 64, dtype=torch.float16, device="cuda")
+    one = x[:, :, :1]
+    many = one.expand(1, 1, big, 64)
+    with pytest.raises(ValueError):
+        bsa.bsattn_prefill_window(x, many, many, 100)
+    with pytest.raises(ValueError):
+        bsa.bsattn_prefill_window(many, x, x, 100, out=many)
+    with pytest.raises(ValueError):
+        bsa.bsattn_prefill_window(one.expand(big, 1, 1, 64), one.expand(big, 1, 1, 64), one.expand(big, 1, 1, 64), 100,
+                                  out=one.expand(big, 1, 1, 64))
