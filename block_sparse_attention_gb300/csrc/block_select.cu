@@ -766,8 +766,8 @@ struct MaskLayout {
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 MaskLayout mask_layout(int B, int Hq, int Hkv, int Sq, int Sk, int d) {
-    const size_t n[2] = {static_cast<size_t>(B) * Hq * ((Sq + kBlockRows - 1) / kBlockRows),
-                         static_cast<size_t>(B) * Hkv * ((Sk + kBlockRows - 1) / kBlockRows)};
+    const auto blocks = [](int rows) { return (static_cast<size_t>(rows) + kBlockRows - 1) / kBlockRows; };
+    const size_t n[2] = {static_cast<size_t>(B) * Hq * blocks(Sq), static_cast<size_t>(B) * Hkv * blocks(Sk)};
     MaskLayout w{};
     size_t at = 256;
     for (int t = 0; t < 2; ++t) {

@@ -139,3 +139,10 @@ def test_reference_choice():
     codes, scale = ref.summary(torch.tensor([[1.0, -2.0], [3.0, -6.0]]))
     assert codes.tolist() == [64.0, -127.0] and scale == torch.tensor(4.0 / 127).double()      # 63.5 to even
     assert ref.quantise(torch.tensor([float("inf"), 1.0]).double())[1] == float("inf")
+
+
+def test_workspace_sizes_of_lengths_near_32_bits():
+    most = 2 ** 31 - 1
+    mask = bsa.bsattn_mask_from_qk_workspace_size
+    assert mask(1, 1, 1, 1 << 30, 64, 64) < mask(1, 1, 1, most - 63, 64, 64) <= mask(1, 1, 1, most, 64, 64) < 1 << 33
+    assert mask(1, 1, 1, 64, 1 << 30, 64) < mask(1, 1, 1, 64, most - 63, 64) <= mask(1, 1, 1, 64, most, 64) < 1 << 33
