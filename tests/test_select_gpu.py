@@ -508,6 +508,48 @@ def test_calls_on_other_streams_and_in_graphs(bsa):
     assert not torch.equal(captured[0], want[0]) and not torch.equal(captured[2], want[2])
 
 
+# ------------------------------------------------------------------------- ties between CTAs, the widest tables
+
+@pytest.mark.parametrize("B,hkv,width", [(5, 8, 2048), (1, 8, 2048), (1, 8, 4096), (25, 8, 2048), (50, 8, 2048)])
+def test_select_equal_scores_of_several_ctas(bsa, B, hkv, width):
+    """Rows of two, four and eight CTAs, and of one for long tables: of equal scores the lower block comes first, across
+    the places where one CTA's blocks end and the next one's begin."""
+    index = _random_index(bsa, width, 1, hkv, 64, seed=width + B)
+    table = torch.arange(width, dtype=torch.int32, device="cuda").repeat(B, 1)
+    lens = [width * 64 if b == 0 else 64 * 700 - 3 if b == 1 else 64 * (b % 40) for b in range(B)]
+    q = _rand(B, 2 * hkv, 64, dtype=BF16, seed=B)
+    zero = bsa.BlockIndex(torch.zeros_like(index.codes), torch.ones_like(index.scales))
+    for k in (1, 255, 256, 257, 511, 512, 513, 1024, 1025, 2047):
+        got = bsa.bsattn_decode_select(q, zero, _i32(lens), table, k, 0, 0).cpu()
+        for b, n in enumerate(lens):
+            n = min(-(-n // 64), k)
+            want = torch.tensor(list(range(n)) + [-1] * (k - n), dtype=torch.int32)
+            assert torch.equal(got[b], want.expand(hkv, k))
+    runs = torch.arange(width, device="cuda") // 100 * 100
+    some = bsa.BlockIndex(index.codes[runs].contiguous(), index.scales[runs].contiguous())
+    turns = torch.arange(width, device="cuda") % 3
+    few = bsa.BlockIndex(index.codes[turns].contiguous(), index.scales[turns].contiguous())
+    for k in (130, 512, 777):
+        _check_select(bsa, q, some, lens, table, k, 1, 2)
+        _check_select(bsa, q, few, lens, table, k, 0, 1)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_select_widest_table(bsa, d):
+    """More rows than two CTAs an SM each, in a table for 3000000 tokens, one of them as long as that."""
+    width, hkv, B = 46875, 8, 39
+    lens = [width * 64 - 5 if b == 7 else 3000 * 64 if b == 20 else 64 * (b % 9) for b in range(B)]
+    pages = sum(-(-n // 64) for n in lens) + 1
+    index = _random_index(bsa, pages, 1, hkv, d, seed=d)
+    q = _rand(B, hkv, d, dtype=BF16, seed=d)
+    table = _table(lens, 64, pages, 11, most=width)
+    _check_select(bsa, q, index, lens, table, 90, 1, 3)
+    same = bsa.BlockIndex(torch.zeros_like(index.codes), torch.ones_like(index.scales))
+    got = bsa.bsattn_decode_select(q, same, _i32(lens), table, 40_000, 0, 1)
+    want = torch.tensor(list(range(39_999)) + [width - 1], dtype=torch.int32)
+    assert torch.equal(got[7].cpu(), want.expand(hkv, 40_000))
+
+
 @pytest.mark.parametrize("big", [2 ** 32 + 64, 2 ** 31, 2 ** 32])
 def test_mask_sizes_past_32_bits(bsa, big):
     """Broadcast views whose sizes a C int would cut off."""

@@ -423,3 +423,33 @@ def test_scores_of_which_the_rounding_shows(bsa, B):
     top = c.v[c.ptable[0].long()].nan_to_num(0.0).abs().amax((0, 1)).repeat_interleave(4, 0)[None]
     # a mean of values: weights of one row add up to 1, up to the rounding of each
     assert torch.isfinite(got).all() and (got.abs() <= top * (1 + 2.0 ** -9)).all()
+
+
+@pytest.mark.parametrize("sizes,plens", [([150, 150], [900, 1300]), ([70, 300, 40], [2000, 129, 640]), ([257, 256], [64, 3001])])
+@pytest.mark.parametrize("d,dtype,group", [(64, F16, 4), (128, BF16, 4), (128, F16, 8)])
+def test_several_large_groups(bsa, sizes, plens, d, dtype, group):
+    """Groups of more than 256 rows a kv head each, several items a group."""
+    lens = [(13 * b) % 90 for b in range(sum(sizes))]
+    Case(sizes, plens, lens, 2 * group, 2, d, dtype, seed=sizes[0]).check(bsa)
+
+
+@pytest.mark.parametrize("B", [4, 70])
+def test_lengths_past_the_tables(bsa, B):
+    """What is past a table is left out, and the rest is as if the length ended with it."""
+    c = Case([B - 2, 2], [1024, 1024], [192] * B, 8, 2, 128, BF16, seed=12)
+    ws = torch.zeros(bsa.bsattn_decode_shared_workspace_size(B, 2, 8, 2, 128), dtype=torch.uint8, device="cuda")
+    whole, want = c.call(bsa, ws=ws), c.want()
+    serving.check(whole, *want)
+    assert bsa.bsattn_get_device_status(ws) == 0
+    plens, lens = c.plens, c.lens
+    for past in (1, 129, 2 ** 31 - 1 - 1024):
+        for p in range(2):
+            c.plens, c.lens = plens.clone(), lens
+            c.plens[p] += past
+            got = c.call(bsa, ws=ws)
+            assert torch.equal(got, whole) and bsa.bsattn_get_device_status(ws) == bsa.BSATTN_ERR_BAD_INDEX
+        for b in (0, B - 1):
+            c.plens, c.lens = plens, lens.clone()
+            c.lens[b] += past
+            got = c.call(bsa, ws=ws)
+            assert torch.equal(got, whole) and bsa.bsattn_get_device_status(ws) == bsa.BSATTN_ERR_BAD_INDEX
