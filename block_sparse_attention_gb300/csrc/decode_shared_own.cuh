@@ -28,6 +28,17 @@ constexpr int kTok = 32, kTiles = kTok / 16;             // keys of a unit
 // exp2 is taken of x - max + 12: weights up to 4096, so that a weight 2^-24 of the largest is
 // still a normal fp16 number and 2^-36 the smallest one
 constexpr float kWeightLog2 = 12.f;
+// What is taken off x.  In fp16 rounded up, so that no weight passes 2^12 where scores are so large that 32 bits have them
+// to the nearest 8 or more; bf16 has room for that.
+template <bool BF16>
+__device__ __forceinline__ float weight_reference(float top) {
+    return BF16 ? top - kWeightLog2 : __fadd_ru(top, -kWeightLog2);
+}
+template <bool BF16>
+__device__ __forceinline__ float log_sum(float top, float sum) {
+    if (sum == 0.f) return -INFINITY;
+    return BF16 ? top + log2f(sum) - kWeightLog2 : weight_reference<BF16>(top) + log2f(sum);
+}
 
 template <int D>
 struct OwnRing {
@@ -191,8 +202,8 @@ __device__ __forceinline__ void own_tokens(const CUtensorMap* tm_k, const CUtens
         const size_t row = ((static_cast<size_t>(part) + b) * p.Hkv + g) * G + 2 * j4;
         const float inv0 = l0 == 0.f ? 0.f : 1.f / l0, inv1 = l1 == 0.f ? 0.f : 1.f / l1;
         if (r8 == 0) {
-            if (2 * j4 < G) p.own_lse[row] = l0 == 0.f ? -INFINITY : m0 + log2f(l0) - kWeightLog2;
-            if (2 * j4 + 1 < G) p.own_lse[row + 1] = l1 == 0.f ? -INFINITY : m1 + log2f(l1) - kWeightLog2;
+            if (2 * j4 < G) p.own_lse[row] = log_sum<BF16>(m0, l0);
+            if (2 * j4 + 1 < G) p.own_lse[row + 1] = log_sum<BF16>(m1, l1);
         }
         float* to = p.own_o + row * D + r8;
 #pragma unroll
@@ -294,8 +305,8 @@ __device__ __forceinline__ void own_tokens(const CUtensorMap* tm_k, const CUtens
                 o[mt][3] *= a1;
             }
         }
-        const float z0 = m0 == -INFINITY ? 0.f : m0 - kWeightLog2;
-        const float z1 = m1 == -INFINITY ? 0.f : m1 - kWeightLog2;
+        const float z0 = m0 == -INFINITY ? 0.f : weight_reference<BF16>(m0);
+        const float z1 = m1 == -INFINITY ? 0.f : weight_reference<BF16>(m1);
         uint32_t pb[kTiles][2];
 #pragma unroll
         for (int mt = 0; mt < kTiles; ++mt) {

@@ -453,3 +453,17 @@ def test_lengths_past_the_tables(bsa, B):
             c.lens[b] += past
             got = c.call(bsa, ws=ws)
             assert torch.equal(got, whole) and bsa.bsattn_get_device_status(ws) == bsa.BSATTN_ERR_BAD_INDEX
+
+
+@pytest.mark.parametrize("plen,own", [(3000, 0), (0, 700), (500, 300)])
+@pytest.mark.parametrize("B", [3, 70])
+def test_largest_scores_of_either_part(bsa, B, plen, own):
+    """fp16 scores of 2^26 to 2^28 in base 2, which 32 bits have to the nearest 8 or 16: a mean of values all the same."""
+    c = Case([B], [plen], [own] * B, 32, 8, 64, F16, seed=plen + B)
+    c.q.zero_()
+    c.q[..., 0], c.q[..., 1] = 16384, 1
+    c.k[..., 0] = torch.tensor([30_000, 30_016, 30_032, 30_048, 44_000, 44_032, 60_000, 60_032], device="cuda").to(F16)
+    c.k[..., 1] = (_rand(*c.k.shape[:2], dtype=F16, seed=3).abs() * 32).to(F16)[..., None]
+    got = c.call(bsa)
+    values = c.v.nan_to_num(0.0).abs().amax((0, 1)).repeat_interleave(4, 0)[None]
+    assert torch.isfinite(got).all() and (got.abs() <= values * (1 + 2.0 ** -9)).all()
