@@ -7,8 +7,8 @@
 // up to the wanted number, the lower block first among equals.
 //
 // The choice is a search for the score that the wanted number of blocks reach: counts of blocks at or above
-// a threshold, halving what lies between, until the count is right or one score is left.  With scores spread
-// evenly it takes about as many counts as the number of blocks has bits.
+// four thresholds a trip, which cut what lies between into five, until a count is right or one score is left.  With
+// scores spread evenly it takes some six trips for a thousand blocks.
 #include <algorithm>
 
 #include "host_internal.h"
@@ -32,7 +32,7 @@ namespace {
 // memory, the first kHeld of a thread in registers.  A trip of the search counts at four thresholds at once: a count is
 // mostly the way through the barrier.
 // The index is read once (41 MB there, 5.9 us at the copy rate); what bounds this is the longest row's chain: lengths,
-// table and index 4 us, then 16 times 32 blocks a warp, six counts, the writing.
+// table and index 4 us, then 8 times 32 blocks a warp, six counts, the writing.
 
 constexpr int kMaxBlocks = 46875;               // of a sequence: their keys lie in shared memory
 constexpr int kHeld = 8;                        // keys of a thread in registers
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(TH, TH == 128 ? 4 : 1) select_kernel(const Sel
         bool finite = true;
 #pragma unroll
         for (int w = 0; w < D / 64; ++w) {
-            const float2 f = two_floats<BF16>(src[lane * (D / 64) + w]);
+            const float2 f = mma16::unpack2<BF16>(src[lane * (D / 64) + w]);
             x[2 * w] = f.x;
             x[2 * w + 1] = f.y;
         }
@@ -556,13 +556,6 @@ __global__ void __launch_bounds__(32 * WARPS, 1) summarise_kernel(const MaskPara
     }
 }
 
-__device__ __forceinline__ void mma_whole(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 template <int D, int TH>
 __global__ void __launch_bounds__(TH, TH == 256 ? 3 : 1) mask_kernel(const MaskParams p) {
     constexpr int kMaskWarps = TH / 32;
@@ -633,8 +626,8 @@ __global__ void __launch_bounds__(TH, TH == 256 ? 3 : 1) mask_kernel(const MaskP
                 fetch(tile + kMaskWarps);
 #pragma unroll
                 for (int w = 0; w < D / 32; ++w) {
-                    mma_whole(c, a[2 * w], kv[w].x, kv[w].y);
-                    mma_whole(c, a[2 * w + 1], kv[w].z, kv[w].w);
+                    mma16::mma16816<true>(c, a[2 * w], kv[w].x, kv[w].y);
+                    mma16::mma16816<true>(c, a[2 * w + 1], kv[w].z, kv[w].w);
                 }
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
@@ -762,8 +755,6 @@ __global__ void __launch_bounds__(TH, TH == 256 ? 3 : 1) mask_kernel(const MaskP
 struct MaskLayout {
     size_t codes[2], scales[2], total;
 };
-
-size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 MaskLayout mask_layout(int B, int Hq, int Hkv, int Sq, int Sk, int d) {
     const auto blocks = [](int rows) { return (static_cast<size_t>(rows) + kBlockRows - 1) / kBlockRows; };

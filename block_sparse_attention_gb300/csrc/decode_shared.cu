@@ -9,9 +9,9 @@
 // head of all sequences that share one are the rows of its products, so K and V of a prefix are read once for up to
 // 256 rows and not once a sequence.  Own tokens are bound by HBM bandwidth, prefixes with many rows by the tensor core
 // (256 rows of d = 128: 256 operations a byte against the 280 that the two peaks divide to), so they run beside each
-// other: 256 sequences of 1000 own tokens on the average over 65521, 32 / 8 heads, take 250 us; 177 with prefixes alone,
-// 165 with own tokens alone, and 363 by two kernels one after the other.  A CTA learns its role from the lengths, which
-// every CTA adds up for itself (3 us).
+// other: 256 sequences of 1000 own tokens on the average over 65521, 32 / 8 heads, take 259 us (276 once the GPU is warm);
+// 178 to 193 with prefixes alone, 169 with own tokens alone, and 363 by two kernels one after the other.  A CTA learns its
+// role from the lengths, which every CTA adds up for itself (3 us).
 //
 // The rows of a prefix stand in two tcgen05 tiles a CTA:
 //     S_x = Q_x K^T    M=128 N=128 K=d, fp32 in TMEM
@@ -64,8 +64,9 @@ struct Cfg {
     static constexpr uint32_t kBytes = 1024 + kMissing + 4 * kNotes;
     static_assert(kBytes <= 226 * 1024, "shared memory");        // the scan's static arrays beside it
     // What a unit of a prefix costs, in units of own tokens: 1.6 us a CTA, while its 12 warps would have that many of the
-    // others.  (256 sequences of 1000 own tokens over 65521: 258 us with 12, 250 with 13, 274 with 14; d = 64, 192 over
-    // 6 prefixes: 75 with 17 to 20, 86 with 22.)
+    // others.  (256 sequences of 1000 own tokens over 65521: 267 us with 12, 273 with 13, 277 with 14, 292 with 15, where two
+    // runs of the same are 5 apart; 64 over 32768: 59.0, 57.5, 57.1, 57.0; d = 64, 192 over 6 prefixes: 70.6 with 16, 69.4
+    // with 18, 71.3 with 20, 74.2 with 22.)
     static constexpr float kCost = D == 128 ? 13.f : 18.f;
 };
 
@@ -329,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == kLoadWarp) {
             // ------------------------------------------------------------ TMA
             // K and V of the prefixes and of the own tokens are streamed past what is in L2 and read again: this code,
-            // which every SM fetches at the start, the pieces, the tables (64 sequences over 32768 tokens: 58.7 us, 67.7
+            // which every SM fetches at the start, the pieces, the tables (64 sequences over 32768 tokens: 57.5 us, 68.0
             // without; a few tokens' worth only: the same).
             const uint64_t once = l2_evict_first();
             int g = 0;                                   // tiles loaded, K and V counted apart
@@ -743,8 +744,6 @@ int launch(const CUtensorMap (&maps)[5], const PrefixParams& prm, int grid, cuda
     return cudaGetLastError() == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
 }
 
-size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
-
 // Byte offsets of the workspace, behind the status word, and what depends on the shape and the GPU alone.
 struct Layout {
     size_t prefix_info, own_info, prefix_lse, prefix_o, own_lse, own_o, total;
@@ -756,14 +755,14 @@ Layout layout_of(int B, int P, int Hq, int Hkv, int d, int sms) {
     Layout w{};
     const int G = Hq / Hkv, tile = 128 / G;              // sequences of a 128-row tile
     // A prefix with no more than a tile of rows, on the average, has both query tiles of a CTA to itself (192 sequences
-    // over 6 prefixes, d = 64: 79 us, and 100 with one of the tiles empty).
+    // over 6 prefixes, d = 64: 69 us, and 88 with one of the tiles empty).
     w.halves = (static_cast<long long>(B) + P - 1) / P <= tile;
     w.seqs = w.halves ? tile : 2 * tile;
     w.part_rows = w.seqs * G;
     // A prefix with no more rows than a CTA has is read once: all its kv heads at the same keys at the same time, as
-    // those lie next to each other in the cache (64 sequences over 32768 tokens: 68 us for 74, before the streams passed L2 by).  One prefix with more is
-    // read several times: at the same time, so that all but one reading comes from L2 (256 sequences over 65521: 262 us
-    // for 345).
+    // those lie next to each other in the cache (64 sequences over 32768 tokens: 57.5 us for 62.4).  One prefix with more is
+    // read several times: at the same time, so that all but one reading comes from L2 (256 sequences over 65521: 273 us
+    // for 335).
     const int times = (B + w.seqs - 1) / w.seqs;
     w.side = (static_cast<long long>(B) + P - 1) / P <= w.seqs && 2 * Hkv <= sms ? Hkv : 1;
     w.deep = P == 1 && times > 1 ? (times + (times + 7) / 8 - 1) / ((times + 7) / 8) : 1;
@@ -839,8 +838,6 @@ extern "C" int bsattn_decode_shared(const void* q, const void* k_pages, const vo
     PrefixParams prm{};
     SharedCall& s = prm.s;
     s.q = q;
-    s.k = k_pages;
-    s.v = v_pages;
     s.out = out;
     s.starts = group_starts;
     s.prefix_lens = prefix_lens;

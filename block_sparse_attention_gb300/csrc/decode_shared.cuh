@@ -31,8 +31,6 @@ constexpr int kSharedThreads = 384;
 // one a (warp, kv head).  What part c has of sequence b is a piece at c + b: [kv head][its query heads].
 struct SharedCall {
     const void* q;
-    const void* k;
-    const void* v;
     void* out;
     const int32_t* starts;       // [P + 1]
     const int32_t* prefix_lens;  // [P]

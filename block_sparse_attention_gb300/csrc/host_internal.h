@@ -37,6 +37,8 @@ int num_sms_of_current_device();
 // (`done` is the kernel's own record: a bit a device).  Returns a bsattn_status.
 int raise_smem_limit(const void* kernel, int bytes, std::atomic<unsigned long long>& done);
 
+inline size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Whether na bytes at a and nb bytes at b share any.

@@ -17,19 +17,11 @@
 #include <cstdint>
 
 #include "bsattn.h"
+#include "mma16.cuh"
 
 namespace bsattn {
 
 constexpr int kBlockRows = 64;
-
-template <bool BF16>
-__device__ __forceinline__ float2 two_floats(uint32_t w) {
-    if constexpr (BF16) {
-        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-    } else {
-        return __half22float2(*reinterpret_cast<__half2*>(&w));
-    }
-}
 
 // The scale of values whose largest magnitude is `top` (infinity or NaN: not finite).
 __device__ __forceinline__ float scale8(float top, bool finite) { return finite ? __fdiv_rn(top, 127.f) : INFINITY; }
@@ -78,7 +70,7 @@ struct BlockRing {
     static constexpr int kEach = kBlockRows / kAt;   // rows of a lane: 32 or 16
     static constexpr int kStage = kBlockRows * D * 2;
     static constexpr int kBytes = BYTES;
-    static constexpr int kDepth = kBytes / kStage;   // 2 or 4 blocks of 32 KB
+    static constexpr int kDepth = kBytes / kStage;   // blocks of 16 or 8 KB: 2 or 4 in 32 KB, 3 or 6 in 48
     uint8_t* at;                                     // the stages from the lane's first piece on
 
     __device__ __forceinline__ explicit BlockRing(uint8_t* base) : at(base + (threadIdx.x & 31) * 16) {}
@@ -119,7 +111,7 @@ struct BlockRing {
                 float2 v[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    v[i] = two_floats<BF16>(c == 0 ? raw[i].x : c == 1 ? raw[i].y : c == 2 ? raw[i].z : raw[i].w);
+                    v[i] = mma16::unpack2<BF16>(c == 0 ? raw[i].x : c == 1 ? raw[i].y : c == 2 ? raw[i].z : raw[i].w);
 #pragma unroll
                 for (int half = 4; half > 0; half >>= 1)
 #pragma unroll

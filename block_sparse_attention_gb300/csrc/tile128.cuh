@@ -2,9 +2,7 @@
 // 32-bit arithmetic.  sm_103a.
 #pragma once
 
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
+#include "mma16.cuh"
 #include "ptx.cuh"
 
 namespace bsattn {
@@ -45,16 +43,7 @@ __device__ __forceinline__ float2 add2f(float2 a, float2 b) {
     return d;
 }
 
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    if constexpr (BF16) {
-        __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<uint32_t*>(&v);
-    } else {
-        __half2 v = __floats2half2_rn(a, b);
-        return *reinterpret_cast<uint32_t*>(&v);
-    }
-}
+using mma16::pack2;
 
 // 32 TMEM lanes x 32 columns, one accumulator row a thread.
 __device__ __forceinline__ void tmem_ld_row32(uint32_t taddr, uint32_t* r) {
