@@ -563,3 +563,29 @@ def test_mask_sizes_past_32_bits(bsa, big):
         bsa.bsattn_mask_from_qk(one.expand(big, 1, 1, 64), one.expand(big, 1, 1, 64), 4, True)
     with pytest.raises(ValueError):
         bsa.bsattn_mask_from_qk(one.expand(1, big, 1, 64), one, 4, True)
+
+
+def test_index_of_a_4bit_cache(bsa):
+    """Pages gathered from a 4-bit cache and summarised as pages of their own, each as a sequence."""
+    pages, page, hkv, d, lens = 12, 128, 2, 64, [300, 128, 61]
+    table, cache = _table(lens, page, pages, 5), bsa.bsattn_kv4_cache(pages, hkv, page, d)
+    slots = torch.cat([table[b].long()[torch.arange(n, device="cuda") // page] * page + torch.arange(n, device="cuda") % page
+                       for b, n in enumerate(lens)])
+    k, v = (_rand(len(slots), hkv, d, dtype=BF16, seed=s) for s in (1, 2))
+    bsa.bsattn_kv4_append(k, v, slots, cache)
+    mine = torch.tensor([int(p) for b, n in enumerate(lens) for p in table[b, :-(-n // page)]], device="cuda")
+    rows = _i32([min(page, n - at) for n in lens for at in range(0, n, page)])
+    whole = (mine[:, None] * page + torch.arange(page, device="cuda")).view(-1)
+    got, _ = bsa.bsattn_kv4_gather(whole, cache, BF16)
+    got = got.view(len(mine), page, hkv, d)
+    scratch = bsa.bsattn_block_index(len(mine), hkv, page, d)
+    bsa.bsattn_index_update(got, rows, rows, torch.arange(len(mine), dtype=torch.int32, device="cuda")[:, None].contiguous(), scratch)
+    index = bsa.bsattn_block_index(pages, hkv, page, d)
+    index.codes[mine], index.scales[mine] = scratch.codes, scratch.scales
+    for i, n in enumerate(rows.tolist()):
+        for sub in range(-(-n // 64)):
+            codes, scales = ref.summary(got[i, 64 * sub:min(64 * sub + 64, n)].transpose(0, 1))
+            assert _same(index.codes[mine[i], sub], codes) and _same(index.scales[mine[i], sub], scales)
+    q = _rand(3, 4, d, dtype=BF16, seed=3)
+    blocks = _check_select(bsa, q, index, lens, table, 2, 0, 1)
+    assert torch.isfinite(bsa.bsattn_decode_paged_kv4(q, cache, _i32(lens), table, blocks)).all()
